@@ -68,10 +68,25 @@ typedef int32_t kv_status;
 #define KV_PLAN_NARROW_TILES 8    /* tcgen05 tiles of 128 rows only (no
                                      256-row items; used to compare the two
                                      tile kernels) */
+#define KV_PLAN_LATENT 16         /* the step reads a latent pool
+                                     (paged_latent_decode_attn); goes with
+                                     KV_PLAN_IGNORE_GROUPS alone */
 
 /* Element type of a pool's K and V. */
 #define KV_DTYPE_BF16 0
 #define KV_DTYPE_E4M3 1
+#define KV_DTYPE_LATENT 2 /* one latent vector and one rotated key a token */
+
+/* Sizes of a latent cache and of the heads expanded from it. */
+#define KV_LATENT_RANK 512 /* values of a token's latent vector */
+#define KV_LATENT_ROPE 64  /* values of a token's rotated position key */
+#define KV_LATENT_HEAD 128 /* an expanded key's part without position, and an
+                              expanded value */
+
+/* Which dimensions a position rotation pairs (rot_dim = rotated dimensions,
+ * the first ones of a head; the others pass unchanged). */
+#define KV_ROPE_HALVES 0 /* (j, j + rot_dim / 2) */
+#define KV_ROPE_PAIRS 1  /* (2 j, 2 j + 1) */
 
 typedef struct kv_pool kv_pool; /* opaque */
 
@@ -80,7 +95,7 @@ typedef struct kv_pool_desc {
   int32_t block_size;   /* tokens per block; must be 16 ([DMW]) */
   int32_t num_layers;   /* >= 1 */
   int32_t num_kv_heads; /* Hkv >= 1 */
-  int32_t head_dim;     /* d: 64 or 128 */
+  int32_t head_dim;     /* d: 64 or 128 (latent pools: 512) */
   /* Device pools, caller-owned, each (bf16 pools)
    * [num_layers][num_blocks][num_kv_heads][block_size][head_dim] bf16,
    * 16-byte aligned.  Both NULL: a metadata-only pool (the allocator, tables
@@ -110,7 +125,16 @@ typedef struct kv_pool_desc {
    * stored are re-encoded from their stored values under the new scale.
    * Each value is coded as the nearest e4m3 value of x / scale, ties to the
    * even mantissa.  Non-finite inputs give unspecified codes.  kv_scales
-   * must be NULL for bf16 pools and for metadata-only pools. */
+   * must be NULL for bf16 pools and for metadata-only pools.
+   *
+   * KV_DTYPE_LATENT: latent attention's cache, shared by every query head.
+   * num_kv_heads must be 1 and head_dim 512; k_pool holds the latent vectors
+   * ([num_layers][num_blocks][16][512] bf16), v_pool the position keys, rotated
+   * already ([num_layers][num_blocks][16][64] bf16).  kv_append and
+   * kv_append_batch take k_new [..][n][512] and v_new [..][n][64] as they are
+   * to be stored; forks, frees, eviction, the host tier (host pools in the
+   * same layouts) and the radix index work as for other pools.  Read by
+   * paged_latent_decode_attn and paged_latent_prefill_attn only. */
   int32_t kv_dtype;
   void* kv_scales;
 } kv_pool_desc;
@@ -374,6 +398,75 @@ kv_status kv_build_batch(kv_pool* pool, int32_t nb, const int32_t* ids,
                          int32_t* seq_lens, int32_t groups_cap,
                          int32_t* out_n_groups, int32_t* groups);
 
+/* ---- position rotation on the way into the cache -------------------------- */
+
+/* One layer's new tokens of every branch: rotate the queries, rotate the keys
+ * and write them to their slots, write the values to theirs.  The slots were
+ * reserved beforehand (kv_reserve) and are included in block_tables and
+ * seq_lens.  Branch b's new tokens are rows [row_offsets[b], row_offsets[b + 1])
+ * of q, k_new and v_new (row_offsets[0] = 0, row_offsets[nb] = total; a branch
+ * may have none); row_offsets NULL: one new token a branch (total = nb).  New
+ * token i of the n_b of branch b has position p = seq_lens[b] - n_b + i, and
+ * every rotated pair (x_a, x_b) of its query and key heads becomes
+ *   x_a c - x_b s,  x_b c + x_a s,   (c, s) = rope[p][j], j = pair index,
+ * computed in fp32 and rounded once to bf16.  rope: device fp32
+ * [rope_len][rot_dim / 2][2], (cos, sin) of every position, any scaling of the
+ * angles in it; rot_dim a multiple of 16 in [16, head_dim]; rope_style
+ * KV_ROPE_*.
+ * q (nullable with q_out), q_out: [total][Hq][head_dim] bf16; q_out may be q.
+ * k_new, v_new: [total][Hkv][head_dim] bf16.  The strides are the distance
+ * between tokens in values (a slice of a fused projection needs no copy):
+ * multiples of 8, no less than a token's row; pointers 16-byte aligned.
+ * k_pool, v_pool, block_tables, seq_lens: as for paged_decode_attn.
+ * workspace: device, 256-byte aligned, >= 256 bytes, of which the status word
+ * is used; the caller zeroes it once, calls do not clear it, and
+ * kv_check_device_status reads and clears it.  A token whose position lies
+ * outside [0, min(rope_len, 16 max_blocks)), or whose block lies outside the
+ * pool, is recorded there and nothing is written for it.  Two branches must
+ * not write the same slot.  total = 0 does nothing.  Launches only (no host
+ * copy, capturable).  Errors: INVALID_ARG, CUDA. */
+kv_status paged_rope_append(
+    const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+    const void* v_new, int64_t v_stride, const float* rope, int32_t rope_len,
+    int32_t rot_dim, int32_t rope_style, void* q_out, int64_t q_out_stride,
+    void* k_pool, void* v_pool, int64_t num_blocks,
+    const int32_t* block_tables, const int32_t* seq_lens,
+    const int32_t* row_offsets, int32_t total, int32_t nb, int32_t max_blocks,
+    int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t block_size,
+    void* workspace, size_t ws_bytes, void* stream);
+
+/* paged_rope_append into an e4m3 pool (kv_scales: this layer's scale records).
+ * The new tokens of one branch that fall in one block are one write under the
+ * block rule of kv_pool_desc; keys are rotated in fp32 and coded from there
+ * (rounded once).  Queries stay bf16. */
+kv_status paged_rope_append_e4m3(
+    const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+    const void* v_new, int64_t v_stride, const float* rope, int32_t rope_len,
+    int32_t rot_dim, int32_t rope_style, void* q_out, int64_t q_out_stride,
+    void* k_pool, void* v_pool, void* kv_scales, int64_t num_blocks,
+    const int32_t* block_tables, const int32_t* seq_lens,
+    const int32_t* row_offsets, int32_t total, int32_t nb, int32_t max_blocks,
+    int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t block_size,
+    void* workspace, size_t ws_bytes, void* stream);
+
+/* The same for one layer of a latent pool: c_new [total][512] copied to its
+ * slots of c_pool, r_new [total][64] rotated (rot_dim = 64) into r_pool, and the
+ * position part of every query head rotated from q_rope to q_rope_out
+ * ([total][Hq][64] with the given distances between tokens and between heads,
+ * so that both may be slices of wider rows; in place where they are the same
+ * rows; both NULL: keys only).  c_pool, r_pool: this layer's [num_blocks][16][512]
+ * and [num_blocks][16][64] bf16.  rank must be 512 and rope_dim 64.  Everything
+ * else as for paged_rope_append. */
+kv_status paged_latent_append(
+    const void* c_new, int64_t c_stride, const void* r_new, int64_t r_stride,
+    const void* q_rope, int64_t q_stride, int64_t q_head_stride,
+    const float* rope, int32_t rope_len, int32_t rope_style, void* q_rope_out,
+    int64_t q_out_stride, int64_t q_out_head_stride, void* c_pool,
+    void* r_pool, int64_t num_blocks, const int32_t* block_tables,
+    const int32_t* seq_lens, const int32_t* row_offsets, int32_t total,
+    int32_t nb, int32_t max_blocks, int32_t Hq, int32_t rank, int32_t rope_dim,
+    int32_t block_size, void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- decode attention ---------------------------------------------------- */
 
 typedef struct kv_decode_plan_info {
@@ -404,7 +497,10 @@ typedef struct kv_decode_plan_info {
  * blocks in range and full; each row's segments tiling [0, end).  Writes
  * the plan to host `plan` (plan_cap int32 entries; pass plan = NULL to query
  * the size in info->plan_ints).  num_sms = the device's SM count (used to
- * size splits).  flags: KV_PLAN_*.  Errors: INVALID_ARG. */
+ * size splits).  flags: KV_PLAN_*.  With KV_PLAN_LATENT (Hkv = 1, head_dim =
+ * 512): n_tile_items = work items, n_tile_wide_items = the pairs of CTAs that
+ * run them, n_merge_rows = branches whose partial results are merged, the
+ * other counts 0.  Errors: INVALID_ARG. */
 kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
                             int32_t head_dim, int32_t block_size,
                             int32_t max_blocks, const int32_t* seq_lens,
@@ -500,6 +596,27 @@ kv_status paged_decode_append_attn_e4m3(
     const int32_t* block_tables, const int32_t* seq_lens,
     const int32_t* prefix_groups, int32_t n_groups, int32_t nb,
     int32_t max_blocks, int32_t Hq, int32_t Hkv, int32_t head_dim,
+    int32_t block_size, float scale, void* out, const int32_t* plan,
+    const kv_decode_plan_info* info, void* workspace, size_t ws_bytes,
+    void* stream);
+
+/* Decode attention over a latent pool, absorbed form: every query head attends
+ * to the latents themselves,
+ *   out[b][h] = sum_t softmax_t(scale * q[b][h] . [c_t ; r_t]) c_t,
+ * t over the seq_lens[b] tokens of branch b, c_t the token's latent vector
+ * (512) and r_t its rotated position key (64).  q [nb][Hq][576] bf16: the query
+ * carried into the latent space (W_uk^T q), then its rotated position part.
+ * out [nb][Hq][512] bf16, still in the latent space.  c_pool
+ * [num_blocks][16][512], r_pool [num_blocks][16][64] bf16: this layer's pools.
+ * The plan comes from paged_decode_plan with Hkv = 1, head_dim = 512 and
+ * KV_PLAN_LATENT; blocks of a shared segment are read once per 128 of its rows
+ * (branches x heads).  Everything else (segments, workspace, status, streams,
+ * errors) as for paged_decode_attn; all launches are on `stream`. */
+kv_status paged_latent_decode_attn(
+    const void* q, const void* c_pool, const void* r_pool, int64_t num_blocks,
+    const int32_t* block_tables, const int32_t* seq_lens,
+    const int32_t* prefix_groups, int32_t n_groups, int32_t nb,
+    int32_t max_blocks, int32_t Hq, int32_t rank, int32_t rope_dim,
     int32_t block_size, float scale, void* out, const int32_t* plan,
     const kv_decode_plan_info* info, void* workspace, size_t ws_bytes,
     void* stream);

@@ -32,8 +32,15 @@ KV_PLAN_NO_TENSOR_CORES = 1
 KV_PLAN_IGNORE_GROUPS = 2
 KV_PLAN_KV_E4M3 = 4
 KV_PLAN_NARROW_TILES = 8
+KV_PLAN_LATENT = 16
 KV_DTYPE_BF16 = 0
 KV_DTYPE_E4M3 = 1
+KV_DTYPE_LATENT = 2
+KV_LATENT_RANK = 512
+KV_LATENT_ROPE = 64
+KV_LATENT_HEAD = 128
+KV_ROPE_HALVES = 0
+KV_ROPE_PAIRS = 1
 
 _NAMES = {0: "OK", 1: "OOM", 2: "INVALID_ARG", 3: "NOT_FOUND", 4: "CUDA",
           5: "DEVICE", 6: "TIMEOUT", 7: "INTERNAL"}
@@ -155,6 +162,27 @@ _SIGS = {
                                                   _vp,
                                                   C.POINTER(kv_decode_plan_info),
                                                   _vp, C.c_size_t, _vp]),
+    "paged_rope_append": (C.c_int32, [_vp, C.c_int64, _vp, C.c_int64, _vp,
+                                      C.c_int64, _vp, C.c_int32, C.c_int32,
+                                      C.c_int32, _vp, C.c_int64, _vp, _vp,
+                                      C.c_int64, _vp, _vp, _vp] +
+                          [C.c_int32] * 7 + [_vp, C.c_size_t, _vp]),
+    "paged_rope_append_e4m3": (C.c_int32, [_vp, C.c_int64, _vp, C.c_int64, _vp,
+                                           C.c_int64, _vp, C.c_int32,
+                                           C.c_int32, C.c_int32, _vp,
+                                           C.c_int64, _vp, _vp, _vp, C.c_int64,
+                                           _vp, _vp, _vp] +
+                               [C.c_int32] * 7 + [_vp, C.c_size_t, _vp]),
+    "paged_latent_append": (C.c_int32, [_vp, C.c_int64, _vp, C.c_int64, _vp,
+                                        C.c_int64, C.c_int64, _vp, C.c_int32,
+                                        C.c_int32, _vp, C.c_int64, C.c_int64,
+                                        _vp, _vp, C.c_int64, _vp, _vp, _vp] +
+                            [C.c_int32] * 7 + [_vp, C.c_size_t, _vp]),
+    "paged_latent_decode_attn": (C.c_int32, [_vp, _vp, _vp, C.c_int64, _vp,
+                                             _vp, _vp] + [C.c_int32] * 7 +
+                                 [C.c_float, _vp, _vp,
+                                  C.POINTER(kv_decode_plan_info), _vp,
+                                  C.c_size_t, _vp]),
     "kv_check_device_status": (C.c_int32, [_vp, _vp, _i32p, _i32p]),
     "kv_selftest_timeout": (C.c_int32, [_vp, C.c_int64, _vp]),
     "kv_offload_attach": (C.c_int32, [_vp, _vp, _vp, _vp, C.c_int64]),
@@ -482,6 +510,107 @@ def paged_decode_append_attn_e4m3(q, k_step, v_step, k_pool, v_pool,
         _ptr(prefix_groups), n_groups, nb, max_blocks, Hq, Hkv, head_dim,
         block_size, scale, _ptr(out), _ptr(plan), C.byref(info),
         _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def _token_rows(t, width):
+    """(pointer, distance between tokens in values) of a bf16 tensor whose
+    tokens (dimension 0) are rows of `width` contiguous values."""
+    if t is None:
+        return None, 0
+    if t.element_size() != 2 or t.numel() != t.shape[0] * width or \
+            (t.shape[0] > 0 and not t[0].is_contiguous()):
+        raise KVError(KV_ERR_INVALID_ARG,
+                      f"a token is {width} contiguous bf16 values, got "
+                      f"{tuple(t.shape)} of {t.dtype}, strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+
+
+def _rope_table(rope):
+    """(pointer, rope_len, rot_dim) of an fp32 table [rope_len][rot/2][2]."""
+    if rope.dim() != 3 or rope.shape[2] != 2 or rope.element_size() != 4 or \
+            not rope.is_contiguous():
+        raise KVError(KV_ERR_INVALID_ARG,
+                      "rope is a contiguous fp32 [rope_len][rot_dim / 2][2], "
+                      f"got {tuple(rope.shape)} of {rope.dtype}")
+    return rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
+
+
+def paged_rope_append(q, k_new, v_new, rope, rope_style, q_out, k_pool, v_pool,
+                      num_blocks, block_tables, seq_lens, row_offsets, total,
+                      nb, max_blocks, Hq, Hkv, head_dim, workspace, stream=None,
+                      block_size=16):
+    """q, k_new, v_new, q_out: tensors [total][heads][head_dim], the distance
+    between tokens free (slices of one projection); rope [rope_len][rot/2][2];
+    workspace: a zeroed uint8 tensor of >= 256 bytes."""
+    rp, rlen, rot = _rope_table(rope)
+    _check(_lib.paged_rope_append(
+        *_token_rows(q, Hq * head_dim), *_token_rows(k_new, Hkv * head_dim),
+        *_token_rows(v_new, Hkv * head_dim), rp, rlen, rot, rope_style,
+        *_token_rows(q_out, Hq * head_dim), _ptr(k_pool), _ptr(v_pool),
+        num_blocks, _ptr(block_tables), _ptr(seq_lens), _ptr(row_offsets),
+        total, nb, max_blocks, Hq, Hkv, head_dim, block_size, _ptr(workspace),
+        workspace.numel(), _stream(stream)))
+
+
+def paged_rope_append_e4m3(q, k_new, v_new, rope, rope_style, q_out, k_pool,
+                           v_pool, kv_scales, num_blocks, block_tables,
+                           seq_lens, row_offsets, total, nb, max_blocks, Hq,
+                           Hkv, head_dim, workspace, stream=None,
+                           block_size=16):
+    """As paged_rope_append, into an e4m3 pool."""
+    rp, rlen, rot = _rope_table(rope)
+    _check(_lib.paged_rope_append_e4m3(
+        *_token_rows(q, Hq * head_dim), *_token_rows(k_new, Hkv * head_dim),
+        *_token_rows(v_new, Hkv * head_dim), rp, rlen, rot, rope_style,
+        *_token_rows(q_out, Hq * head_dim), _ptr(k_pool), _ptr(v_pool),
+        _ptr(kv_scales), num_blocks, _ptr(block_tables), _ptr(seq_lens),
+        _ptr(row_offsets), total, nb, max_blocks, Hq, Hkv, head_dim,
+        block_size, _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def _head_rows(t, heads, width):
+    """(pointer, distance between tokens, between heads) of a bf16 tensor
+    [total][heads][width] with contiguous values in a head."""
+    if t is None:
+        return None, 0, 0
+    if t.element_size() != 2 or t.dim() != 3 or \
+            tuple(t.shape[1:]) != (heads, width) or t.stride(2) != 1:
+        raise KVError(KV_ERR_INVALID_ARG,
+                      f"expected bf16 [total][{heads}][{width}], got "
+                      f"{tuple(t.shape)} of {t.dtype}, strides {t.stride()}")
+    hs = t.stride(1) if heads > 1 else width
+    ts = t.stride(0) if t.shape[0] > 1 else (heads - 1) * hs + width
+    return t.data_ptr(), ts, hs
+
+
+def paged_latent_append(c_new, r_new, q_rope, rope, rope_style, q_rope_out,
+                        c_pool, r_pool, num_blocks, block_tables, seq_lens,
+                        row_offsets, total, nb, max_blocks, Hq, workspace,
+                        stream=None, block_size=16):
+    """c_new [total][512], r_new [total][64]; q_rope, q_rope_out
+    [total][Hq][64], slices of wider rows or None."""
+    rp, rlen, rot = _rope_table(rope)
+    if rot != KV_LATENT_ROPE:
+        raise KVError(KV_ERR_INVALID_ARG, f"rope table for {rot} dimensions, "
+                                          f"not {KV_LATENT_ROPE}")
+    _check(_lib.paged_latent_append(
+        *_token_rows(c_new, KV_LATENT_RANK), *_token_rows(r_new, KV_LATENT_ROPE),
+        *_head_rows(q_rope, Hq, KV_LATENT_ROPE), rp, rlen, rope_style,
+        *_head_rows(q_rope_out, Hq, KV_LATENT_ROPE), _ptr(c_pool), _ptr(r_pool),
+        num_blocks, _ptr(block_tables), _ptr(seq_lens), _ptr(row_offsets),
+        total, nb, max_blocks, Hq, KV_LATENT_RANK, KV_LATENT_ROPE, block_size,
+        _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def paged_latent_decode_attn(q, c_pool, r_pool, num_blocks, block_tables,
+                             seq_lens, prefix_groups, n_groups, nb, max_blocks,
+                             Hq, scale, out, plan, info, workspace, ws_bytes,
+                             stream=None, block_size=16):
+    _check(_lib.paged_latent_decode_attn(
+        _ptr(q), _ptr(c_pool), _ptr(r_pool), num_blocks, _ptr(block_tables),
+        _ptr(seq_lens), _ptr(prefix_groups), n_groups, nb, max_blocks, Hq,
+        KV_LATENT_RANK, KV_LATENT_ROPE, block_size, scale, _ptr(out),
+        _ptr(plan), C.byref(info), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def paged_decode_attn_noalloc(q, k_pool, v_pool, num_blocks, block_tables,

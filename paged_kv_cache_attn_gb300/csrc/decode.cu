@@ -37,6 +37,7 @@
 #include <tuple>
 
 #include "device_common.cuh"
+#include "tensor_map.h"
 
 namespace pkv {
 
@@ -478,6 +479,26 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   return fn;
 }
 
+}  // namespace
+
+kv_status encode_bf16_map(CUtensorMap* tm, const void* base, int rank,
+                          const cuuint64_t* dims, const cuuint64_t* strides,
+                          const cuuint32_t* box) {
+  auto enc = get_encode();
+  if (!enc) return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r =
+      enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+          const_cast<void*>(base), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return KV_OK;
+}
+
+namespace {
+
 // 2-D view of one layer's pool: rows = block * Hkv * 16 + head * 16 + slot,
 // columns = head_dim; boxes of 16 rows x 64 columns, 128-byte swizzle.
 kv_status make_pool_map(CUtensorMap* tm, const void* pool, int64_t rows, int d) {
@@ -676,6 +697,8 @@ static kv_status decode_impl(
     return fail(KV_ERR_INVALID_ARG, e4m3 ? "an e4m3 step needs a plan made "
                                            "with KV_PLAN_KV_E4M3"
                                          : "plan was made for an e4m3 pool");
+  if (info->flags & KV_PLAN_LATENT)
+    return fail(KV_ERR_INVALID_ARG, "plan was made for a latent pool");
   if (info->n_tile_items != 0 && d != 128)
     return fail(KV_ERR_INVALID_ARG, "tensor-core tiles need head_dim 128");
   if (info->n_tile_wide_items < 0 ||

@@ -43,10 +43,18 @@ struct kv_pool {
 
   bool has_data() const { return k_pool != nullptr; }
   bool e4m3() const { return kv_dtype == KV_DTYPE_E4M3; }
-  // Bytes of one (layer, block) in each of the K and V pools, and in the
-  // scale pool (0 for bf16).
-  int64_t tile_bytes() const {
-    return (int64_t)num_kv_heads * 16 * head_dim * (e4m3() ? 1 : 2);
+  bool latent() const { return kv_dtype == KV_DTYPE_LATENT; }
+  // Values of one token and kv-head in the K and in the V pool (a latent
+  // pool's K is the latent vector, its V the rotated position key).
+  int32_t k_dim() const { return head_dim; }
+  int32_t v_dim() const { return latent() ? KV_LATENT_ROPE : head_dim; }
+  // Bytes of one (layer, block) in the K pool, the V pool and the scale pool
+  // (0 but for e4m3).
+  int64_t k_bytes() const {
+    return (int64_t)num_kv_heads * 16 * k_dim() * (e4m3() ? 1 : 2);
+  }
+  int64_t v_bytes() const {
+    return (int64_t)num_kv_heads * 16 * v_dim() * (e4m3() ? 1 : 2);
   }
   int64_t scale_bytes() const { return e4m3() ? (int64_t)num_kv_heads * 16 : 0; }
 };
@@ -65,6 +73,7 @@ void clear_error();
 // work items, and a CSR list telling the merge pass which partial rows belong
 // to each branch.
 constexpr int32_t kPlanMagic = 0x31564B50;  // "PKV1"
+constexpr int32_t kLatentPlanMagic = 0x314C4B50;  // "PKL1"
 constexpr int kPlanHeaderInts = 16;
 enum PlanHeader {
   H_MAGIC = 0, H_NB, H_HQ, H_HKV, H_D, H_N_ROW_ITEMS, H_N_TILE_ITEMS, H_N_CSR,
@@ -116,13 +125,22 @@ struct DeviceStatus {
   uint32_t pad;
 };
 
+// The plan of a latent step (plan_latent.cpp); segments validated by the
+// caller, nblk and shared_end per branch.
+kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
+                      const int32_t* nblk, const int32_t* groups,
+                      int32_t n_groups, const int32_t* shared_end,
+                      int32_t num_sms, int32_t flags, int32_t* plan,
+                      int64_t plan_cap, kv_decode_plan_info* info);
+
 // ---- kernel launchers (state_kernels.cu, decode kernels) -------------------
 // Copy appended K/V rows into their slots.  dst_blocks[i] = physical block of
 // logical block first_lblock + i; rows are tokens [tok0, tok0 + n) of the
-// branch (tok0 = its seq_len before the append).
+// branch (tok0 = its seq_len before the append).  dk, dv: values of a K row
+// and of a V row (multiples of 8, dv <= dk).
 int launch_append_scatter(void* k_pool, void* v_pool, const void* k_new,
                           const void* v_new, int64_t num_blocks, int L,
-                          int Hkv, int d, int B, int n, int tok0,
+                          int Hkv, int dk, int dv, int B, int n, int tok0,
                           const int32_t* dst_blocks, int n_dst,
                           void* stream);
 // One branch's run of a batched append: input rows [row, row + n) are the
@@ -132,11 +150,11 @@ struct ScatterRun {
   int32_t row, n, tok0, first_lblock;
   std::vector<int32_t> dst;
 };
-// Scatter a batch of runs (input [L][total][Hkv][d]) in as few launches as
-// the kernel parameter space allows.
+// Scatter a batch of runs (input [L][total][Hkv][dk] and [..][dv]) in as few
+// launches as the kernel parameter space allows.
 int launch_append_batch(void* k_pool, void* v_pool, const void* k_new,
                         const void* v_new, int64_t num_blocks, int L, int Hkv,
-                        int d, int32_t total, const std::vector<ScatterRun>& runs,
+                        int dk, int dv, int32_t total, const std::vector<ScatterRun>& runs,
                         void* stream);
 // One side of a block move: the K, V (and scale, or null) buffers of a pool
 // holding `blocks` blocks per layer.  May be pinned host memory reachable
@@ -148,11 +166,12 @@ struct PoolBufs {
   int64_t blocks;
 };
 // Copy whole blocks (every layer; K, V and scale records): block src[i] of
-// `from` -> block dst[i] of `to`.  kv_bytes / s_bytes: bytes of one (layer,
-// block) in each K/V buffer and in the scale buffer (multiples of 16).
+// `from` -> block dst[i] of `to`.  k_bytes / v_bytes / s_bytes: bytes of one
+// (layer, block) in the K, V and scale buffers (multiples of 16).
 int launch_block_move(const PoolBufs& from, const PoolBufs& to, int L,
-                      int64_t kv_bytes, int64_t s_bytes, const int32_t* src,
-                      const int32_t* dst, int n, void* stream);
+                      int64_t k_bytes, int64_t v_bytes, int64_t s_bytes,
+                      const int32_t* src, const int32_t* dst, int n,
+                      void* stream);
 // Quantising append into an e4m3 pool: the runs' rows (input bf16
 // [L][total][Hkv][d]) are written block by block under the pool's block
 // rule; writes to one block are applied in run order.

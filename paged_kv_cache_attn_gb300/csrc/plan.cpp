@@ -61,8 +61,16 @@ extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
   if (!info || !seq_lens) return fail(KV_ERR_INVALID_ARG, "null argument");
   if (nb < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
     return fail(KV_ERR_INVALID_ARG, "bad nb/Hq/Hkv (%d/%d/%d)", nb, Hq, Hkv);
-  if (d != 64 && d != 128)
+  const bool latent = (flags & KV_PLAN_LATENT) != 0;
+  if (latent) {
+    if (flags & ~(KV_PLAN_LATENT | KV_PLAN_IGNORE_GROUPS))
+      return fail(KV_ERR_INVALID_ARG, "KV_PLAN_LATENT goes with "
+                                      "KV_PLAN_IGNORE_GROUPS alone");
+    if (Hkv != 1 || d != KV_LATENT_RANK)
+      return fail(KV_ERR_INVALID_ARG, "a latent step has Hkv 1 and head_dim 512");
+  } else if (d != 64 && d != 128) {
     return fail(KV_ERR_INVALID_ARG, "head_dim must be 64 or 128");
+  }
   if (B != 16) return fail(KV_ERR_INVALID_ARG, "block_size must be 16");
   if (max_blocks < 1) return fail(KV_ERR_INVALID_ARG, "max_blocks must be >= 1");
   if (n_groups < 0 || (n_groups > 0 && !groups))
@@ -83,7 +91,7 @@ extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
   std::vector<Unit> units;
   const bool use_groups = !(flags & KV_PLAN_IGNORE_GROUPS);
   if (flags & ~(KV_PLAN_NO_TENSOR_CORES | KV_PLAN_IGNORE_GROUPS |
-                KV_PLAN_KV_E4M3 | KV_PLAN_NARROW_TILES))
+                KV_PLAN_KV_E4M3 | KV_PLAN_NARROW_TILES | KV_PLAN_LATENT))
     return fail(KV_ERR_INVALID_ARG, "unknown plan flags 0x%x", flags);
   // The tcgen05 tile kernels are built for head_dim 128 (bf16 and e4m3).
   const bool allow_tc = pkv::kTensorCoreKernel && d == 128 &&
@@ -140,6 +148,10 @@ extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
       shared_end[b] = end;
     }
   }
+  if (latent)
+    return pkv::latent_plan(nb, Hq, max_blocks, nblk.data(), groups,
+                            use_groups ? n_groups : 0, shared_end.data(),
+                            num_sms, flags, plan, plan_cap, info);
   for (int32_t b = 0; b < nb; ++b) {
     if (shared_end[b] < nblk[b])
       units.push_back({b, G, shared_end[b], nblk[b], 1, false, false});

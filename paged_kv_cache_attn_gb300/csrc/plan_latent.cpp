@@ -1,0 +1,216 @@
+// Host half of a latent decode step (paged_decode_plan with KV_PLAN_LATENT).
+//
+// Work is cut for pairs of CTAs (decode_latent.cu): an item is up to 128 query
+// rows (branches x heads of a shared segment, or one branch's heads) over a
+// range of logical blocks.  Every pair gets a list of items of about the same
+// cost: the units' blocks are dealt out in order, and a unit that does not fit
+// the rest of a pair's share goes on in the next pair's, cut on a 128-token
+// tile.  The cost of an item is its tiles plus a fixed part (the query load,
+// the first tile's latency, the epilogue), so that a step of many short items
+// is balanced too, and no piece is cut shorter than two tiles.
+//
+// A branch whose rows lie in one item each is finished by that item, which
+// writes its output; the other rows' partial results are merged.
+
+#include <algorithm>
+#include <cstring>
+
+#include "internal.h"
+
+namespace pkv {
+namespace {
+
+struct LatentUnit {
+  int32_t branch0, row0, nrows, blk_begin, blk_end, masked;
+};
+
+constexpr int kTileBlocks = 8;  // blocks of a 128-token tile
+// The fixed part of an item in tiles, and the shortest piece of a unit.
+constexpr int kItemTiles = 3;
+constexpr int kMinTiles = 2;
+
+struct Piece {
+  int32_t unit, lo, hi;  // blocks
+};
+
+int32_t tiles(int32_t blocks) { return (blocks + kTileBlocks - 1) / kTileBlocks; }
+
+// Deal the units out to pairs of at most `share` tiles each; returns whether
+// they fit `pairs` pairs.
+bool deal(const std::vector<LatentUnit>& units, int64_t share, int32_t pairs,
+          std::vector<Piece>* out, std::vector<int32_t>* ptr) {
+  out->clear();
+  ptr->assign(1, 0);
+  int64_t used = 0;  // tiles of the pair being filled
+  for (int32_t u = 0; u < (int32_t)units.size(); ++u) {
+    int32_t lo = units[u].blk_begin;
+    while (lo < units[u].blk_end) {
+      const int32_t left = tiles(units[u].blk_end - lo);
+      int64_t room = share - used - kItemTiles;
+      if (used > 0 && room < std::min(left, kMinTiles)) {
+        ptr->push_back((int32_t)out->size());
+        if ((int32_t)ptr->size() > pairs) return false;
+        used = 0;
+        room = share - kItemTiles;
+      }
+      room = std::max<int64_t>(room, kMinTiles);
+      // The rest of the unit is not left shorter than the shortest piece.
+      int32_t take = left;
+      if (left > room) {
+        take = (int32_t)room;
+        if (left - take < kMinTiles) take = left - kMinTiles;
+        if (take < kMinTiles) take = left;
+      }
+      const int32_t hi =
+          std::min(units[u].blk_end, lo + take * kTileBlocks);
+      out->push_back({u, lo, hi});
+      used += take + kItemTiles;
+      lo = hi;
+    }
+  }
+  ptr->push_back((int32_t)out->size());
+  return (int32_t)ptr->size() - 1 <= pairs;
+}
+
+}  // namespace
+
+kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
+                      const int32_t* nblk, const int32_t* groups,
+                      int32_t n_groups, const int32_t* shared_end,
+                      int32_t num_sms, int32_t flags, int32_t* plan,
+                      int64_t plan_cap, kv_decode_plan_info* info) {
+  (void)max_blocks;
+  if ((int64_t)nb * Hq > INT32_MAX / 2)
+    return fail(KV_ERR_INVALID_ARG, "nb x Hq too large");
+  std::vector<LatentUnit> units;
+  auto add = [&](int32_t b0, int64_t rows, int32_t lo, int32_t hi, int32_t masked) {
+    for (int64_t r = 0; r < rows; r += kTileRows)
+      units.push_back({b0, (int32_t)r,
+                       (int32_t)std::min<int64_t>(kTileRows, rows - r), lo, hi,
+                       masked});
+  };
+  std::vector<int32_t> n_units(nb, 0);
+  for (int32_t i = 0; i < n_groups; ++i) {
+    const int32_t* s = groups + 4 * (int64_t)i;
+    add(s[0], (int64_t)s[1] * Hq, s[2], s[2] + s[3], 0);
+    for (int32_t b = s[0]; b < s[0] + s[1]; ++b) ++n_units[b];
+  }
+  for (int32_t b = 0; b < nb; ++b)
+    if (shared_end[b] < nblk[b]) {
+      add(b, Hq, shared_end[b], nblk[b], 1);
+      ++n_units[b];
+    }
+  // Longest first: the short ones fill the shares' ends.
+  std::stable_sort(units.begin(), units.end(),
+                   [](const LatentUnit& x, const LatentUnit& y) {
+                     return x.blk_end - x.blk_begin > y.blk_end - y.blk_begin;
+                   });
+  const int32_t pairs_max = std::max(1, num_sms / 2);
+  int64_t cost = 0;
+  for (const LatentUnit& u : units)
+    cost += tiles(u.blk_end - u.blk_begin) + kItemTiles;
+  int64_t share = std::max<int64_t>((cost + pairs_max - 1) / pairs_max,
+                                    kItemTiles + kMinTiles);
+  std::vector<Piece> pieces;
+  std::vector<int32_t> ptr;
+  while (!deal(units, share, pairs_max, &pieces, &ptr))
+    share += std::max<int64_t>(1, share / 50);
+  const int32_t n_pairs = (int32_t)ptr.size() - 1;
+
+  // Pieces of each unit; a branch is finished in one item when it lies in one
+  // unit (per row tile) of one piece.
+  std::vector<int32_t> n_pieces(units.size(), 0);
+  for (const Piece& p : pieces) ++n_pieces[p.unit];
+  std::vector<char> single(nb, 1);
+  for (size_t u = 0; u < units.size(); ++u) {
+    const LatentUnit& x = units[u];
+    const int32_t b1 = x.branch0 + (x.row0 + x.nrows - 1) / Hq;
+    for (int32_t b = x.branch0 + x.row0 / Hq; b <= b1; ++b)
+      if (n_units[b] != 1 || n_pieces[u] != 1) single[b] = 0;
+  }
+  struct Tagged { int32_t branch; MergeEntry e; };
+  std::vector<Tagged> merge;
+  std::vector<WorkItem> items;
+  items.reserve(pieces.size());
+  int64_t prow = 0;
+  for (const Piece& p : pieces) {
+    const LatentUnit& u = units[p.unit];
+    const int32_t row1 = u.row0 + u.nrows;
+    bool direct = true;
+    for (int32_t b = u.row0 / Hq; b * (int64_t)Hq < row1; ++b)
+      direct &= single[u.branch0 + b] != 0;
+    // `g` (there is one kv-head) says whether the item writes the output.
+    items.push_back({u.branch0, direct ? 1 : 0, u.row0, u.nrows, p.lo, p.hi,
+                     direct ? 0 : (int32_t)prow, u.masked});
+    if (direct) continue;
+    for (int32_t b = u.row0 / Hq; b * (int64_t)Hq < row1; ++b) {
+      const int32_t a = std::max(u.row0, b * Hq);
+      const int32_t e = std::min<int64_t>(row1, (int64_t)b * Hq + Hq);
+      merge.push_back({u.branch0 + b,
+                       {(int32_t)(prow + (a - u.row0)), u.nrows, a - b * Hq,
+                        e - b * Hq}});
+    }
+    prow += u.nrows;
+    if (prow > INT32_MAX / 2)
+      return fail(KV_ERR_INVALID_ARG, "step too large for one plan");
+  }
+  // Branches with anything to merge.
+  std::vector<int32_t> merged;
+  {
+    std::vector<char> any(nb, 0);
+    for (const Tagged& t : merge) any[t.branch] = 1;
+    for (int32_t b = 0; b < nb; ++b)
+      if (any[b]) merged.push_back(b);
+  }
+  const int64_t n_csr = (int64_t)merge.size();
+  const int64_t off_item = kPlanHeaderInts;
+  const int64_t off_pair = off_item + 8 * (int64_t)items.size();
+  const int64_t off_merge = off_pair + n_pairs + 1;
+  const int64_t off_ptr = off_merge + (int64_t)merged.size();
+  const int64_t off_ent = off_ptr + nb + 1;
+  const int64_t total = off_ent + 4 * n_csr;
+  if (total > INT32_MAX) return fail(KV_ERR_INVALID_ARG, "plan too large");
+  std::memset(info, 0, sizeof *info);
+  info->plan_ints = total;
+  info->workspace_bytes = (int64_t)ws_total(prow, KV_LATENT_RANK);
+  info->partial_rows = prow;
+  info->n_tile_items = (int32_t)items.size();
+  info->n_tile_wide_items = n_pairs;
+  info->n_merge_rows = (int32_t)merged.size();
+  info->chunk_blocks = (int32_t)std::min<int64_t>(INT32_MAX, share * kTileBlocks);
+  info->flags = flags;
+  if (!plan) return KV_OK;
+  if (plan_cap < total)
+    return fail(KV_ERR_INVALID_ARG, "plan_cap %lld < %lld", (long long)plan_cap,
+                (long long)total);
+  int32_t* h = plan;
+  std::fill(h, h + kPlanHeaderInts, 0);
+  h[H_MAGIC] = kLatentPlanMagic;
+  h[H_NB] = nb;
+  h[H_HQ] = Hq;
+  h[H_HKV] = 1;
+  h[H_D] = KV_LATENT_RANK;
+  h[H_N_TILE_ITEMS] = (int32_t)items.size();
+  h[H_N_CSR] = (int32_t)n_csr;
+  h[H_OFF_TILE_ITEMS] = (int32_t)off_item;
+  h[H_OFF_CSR_PTR] = (int32_t)off_ptr;
+  h[H_OFF_CSR_ENT] = (int32_t)off_ent;
+  h[H_PARTIAL_ROWS] = (int32_t)prow;
+  h[H_CHUNK] = info->chunk_blocks;
+  h[H_FLAGS] = flags;
+  h[H_TOTAL] = (int32_t)total;
+  std::memcpy(h + off_item, items.data(), items.size() * sizeof(WorkItem));
+  std::copy(ptr.begin(), ptr.end(), h + off_pair);
+  std::copy(merged.begin(), merged.end(), h + off_merge);
+  int32_t* cp = h + off_ptr;
+  int32_t* ent = h + off_ent;
+  std::fill(cp, cp + nb + 1, 0);
+  for (const Tagged& t : merge) ++cp[t.branch + 1];
+  for (int32_t b = 0; b < nb; ++b) cp[b + 1] += cp[b];
+  std::vector<int32_t> at(cp, cp + nb);
+  for (const Tagged& t : merge)
+    std::memcpy(ent + 4 * (int64_t)at[t.branch]++, &t.e, sizeof(MergeEntry));
+  return KV_OK;
+}
+
+}  // namespace pkv

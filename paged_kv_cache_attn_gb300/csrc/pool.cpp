@@ -73,17 +73,25 @@ extern "C" kv_status kv_pool_create(const kv_pool_desc* d, kv_pool** out) {
                 d->block_size);
   if (d->num_layers < 1 || d->num_kv_heads < 1)
     return fail(KV_ERR_INVALID_ARG, "num_layers and num_kv_heads must be >= 1");
-  if (d->head_dim != 64 && d->head_dim != 128)
+  if (d->kv_dtype == KV_DTYPE_LATENT) {
+    if (d->num_kv_heads != 1 || d->head_dim != KV_LATENT_RANK)
+      return fail(KV_ERR_INVALID_ARG, "a latent pool has num_kv_heads 1 and "
+                                      "head_dim 512, got %d and %d",
+                  d->num_kv_heads, d->head_dim);
+  } else if (d->head_dim != 64 && d->head_dim != 128) {
     return fail(KV_ERR_INVALID_ARG, "head_dim must be 64 or 128, got %d",
                 d->head_dim);
+  }
   if ((d->k_pool == nullptr) != (d->v_pool == nullptr))
     return fail(KV_ERR_INVALID_ARG, "k_pool and v_pool must both be set or "
                                     "both be NULL");
   if (((uintptr_t)d->k_pool | (uintptr_t)d->v_pool) & 15)
     return fail(KV_ERR_INVALID_ARG, "pools must be 16-byte aligned");
-  if (d->kv_dtype != KV_DTYPE_BF16 && d->kv_dtype != KV_DTYPE_E4M3)
-    return fail(KV_ERR_INVALID_ARG, "kv_dtype must be KV_DTYPE_BF16 or "
-                                    "KV_DTYPE_E4M3, got %d", d->kv_dtype);
+  if (d->kv_dtype != KV_DTYPE_BF16 && d->kv_dtype != KV_DTYPE_E4M3 &&
+      d->kv_dtype != KV_DTYPE_LATENT)
+    return fail(KV_ERR_INVALID_ARG, "kv_dtype must be KV_DTYPE_BF16, "
+                                    "KV_DTYPE_E4M3 or KV_DTYPE_LATENT, got %d",
+                d->kv_dtype);
   if (d->kv_dtype == KV_DTYPE_E4M3 && d->k_pool != nullptr) {
     if (d->kv_scales == nullptr)
       return fail(KV_ERR_INVALID_ARG, "an e4m3 data pool needs kv_scales");
@@ -196,7 +204,7 @@ extern "C" kv_status kv_append(kv_pool* p, int32_t id, int32_t n,
     } else {
       err = pkv::launch_append_scatter(
           p->k_pool, p->v_pool, k_new, v_new, p->num_blocks, p->num_layers,
-          p->num_kv_heads, p->head_dim, B, n, nd->seq_len, dst.data(),
+          p->num_kv_heads, p->k_dim(), p->v_dim(), B, n, nd->seq_len, dst.data(),
           (int)dst.size(), stream);
     }
     if (err) return fail(KV_ERR_CUDA, "append copy launch failed (cuda %d)", err);
@@ -347,7 +355,7 @@ extern "C" kv_status kv_append_batch(kv_pool* p, int32_t n, const int32_t* ids,
                                       v_new, (int32_t)total, runs, stream)
             : pkv::launch_append_batch(p->k_pool, p->v_pool, k_new, v_new,
                                        p->num_blocks, p->num_layers,
-                                       p->num_kv_heads, p->head_dim,
+                                       p->num_kv_heads, p->k_dim(), p->v_dim(),
                                        (int32_t)total, runs, stream);
     if (err) return fail(KV_ERR_CUDA, "batch append launch failed (cuda %d)", err);
   } else if (!p->has_data() && (k_new || v_new)) {
@@ -385,8 +393,8 @@ extern "C" kv_status kv_fork_branches(kv_pool* p, int32_t parent, int32_t n,
       const pkv::PoolBufs dev{p->k_pool, p->v_pool, p->kv_scales,
                               p->num_blocks};
       int err = pkv::launch_block_move(dev, dev, p->num_layers,
-                                       p->tile_bytes(), p->scale_bytes(),
-                                       src.data(), dst.data(), n, stream);
+                                       p->k_bytes(), p->v_bytes(),
+                                       p->scale_bytes(), src.data(), dst.data(), n, stream);
       if (err)
         return fail(KV_ERR_CUDA, "copy-on-write launch failed (cuda %d)", err);
     }
@@ -784,8 +792,8 @@ extern "C" kv_status kv_spill(kv_pool* p, int32_t n, const int32_t* ids,
     const pkv::PoolBufs dev{p->k_pool, p->v_pool, p->kv_scales, p->num_blocks};
     const pkv::PoolBufs host{p->host_k, p->host_v, p->host_scales,
                              p->host_slots};
-    int err = pkv::launch_block_move(dev, host, p->num_layers, p->tile_bytes(),
-                                     p->scale_bytes(), src.data(), dst.data(),
+    int err = pkv::launch_block_move(dev, host, p->num_layers, p->k_bytes(),
+                                     p->v_bytes(), p->scale_bytes(), src.data(), dst.data(),
                                      (int)src.size(), stream);
     if (err) return fail(KV_ERR_CUDA, "spill copy launch failed (cuda %d)", err);
   }
@@ -831,8 +839,8 @@ extern "C" kv_status kv_restore(kv_pool* p, int32_t n, const int32_t* ids,
     const pkv::PoolBufs dev{p->k_pool, p->v_pool, p->kv_scales, p->num_blocks};
     const pkv::PoolBufs host{p->host_k, p->host_v, p->host_scales,
                              p->host_slots};
-    int err = pkv::launch_block_move(host, dev, p->num_layers, p->tile_bytes(),
-                                     p->scale_bytes(), src.data(), dst.data(),
+    int err = pkv::launch_block_move(host, dev, p->num_layers, p->k_bytes(),
+                                     p->v_bytes(), p->scale_bytes(), src.data(), dst.data(),
                                      (int)src.size(), stream);
     if (err)
       return fail(KV_ERR_CUDA, "restore copy launch failed (cuda %d)", err);

@@ -1,7 +1,8 @@
 // Data movement behind kv_append, kv_append_batch, kv_fork_branches,
 // kv_spill and kv_restore.
 //
-// bf16 pool layout: [layer][block][kv_head][16 slots][head_dim], so one
+// bf16 pool layout: [layer][block][kv_head][16 slots][head_dim] (a latent
+// pool's K rows have 512 values and its V rows 64), so one
 // (block, kv_head) is a contiguous 16 x d tile (4 KB at d = 128) and one
 // token's row of one head is d contiguous values.  e4m3 pools keep the same
 // tile order with 1-byte codes in the tile layouts of pagedkv.h and a 16-byte
@@ -30,7 +31,7 @@ struct ScatterArgs {
   const uint4* k_new;
   const uint4* v_new;
   int64_t num_blocks;
-  int L, Hkv, vec_per_row;  // vec_per_row = d / 8
+  int L, Hkv, vec_k, vec_v;  // 16-byte vectors of a K row, of a V row
   int n;                    // tokens in the whole append
   int tok_begin, tok_end;   // tokens [tok_begin, tok_end) of this launch
   int tok0;                 // branch length before the append
@@ -41,26 +42,25 @@ struct ScatterArgs {
 // One 16-byte vector per thread-iteration: (layer, token, head, vec).
 __global__ void append_scatter_kernel(const __grid_constant__ ScatterArgs a) {
   const int64_t toks = a.tok_end - a.tok_begin;
-  const int64_t per_layer = toks * a.Hkv * a.vec_per_row;
+  const int64_t per_layer = toks * a.Hkv * a.vec_k;
   const int64_t total = per_layer * a.L;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t layer = i / per_layer;
     int64_t r = i - layer * per_layer;
-    const int vec = (int)(r % a.vec_per_row);
-    r /= a.vec_per_row;
+    const int vec = (int)(r % a.vec_k);
+    r /= a.vec_k;
     const int h = (int)(r % a.Hkv);
     const int tok = a.tok_begin + (int)(r / a.Hkv);  // token within the append
     const int t = a.tok0 + tok;                      // token within the branch
     const int blk = a.dst[t / 16 - a.first_lblock];
     const int slot = t % 16;
-    const int64_t src =
-        ((layer * a.n + tok) * a.Hkv + h) * (int64_t)a.vec_per_row + vec;
+    const int64_t src = (layer * a.n + tok) * a.Hkv + h;  // row
     const int64_t dst =
-        (((layer * a.num_blocks + blk) * a.Hkv + h) * 16 + slot) *
-            (int64_t)a.vec_per_row + vec;
-    a.k_pool[dst] = a.k_new[src];
-    a.v_pool[dst] = a.v_new[src];
+        ((layer * a.num_blocks + blk) * a.Hkv + h) * 16 + slot;
+    a.k_pool[dst * a.vec_k + vec] = a.k_new[src * a.vec_k + vec];
+    if (vec < a.vec_v)
+      a.v_pool[dst * a.vec_v + vec] = a.v_new[src * a.vec_v + vec];
   }
 }
 
@@ -76,8 +76,8 @@ struct MoveArgs {
   uint4* to_s;
   int64_t from_blocks, to_blocks;
   int L;
-  int kv_vecs;  // 16-byte vectors of one (layer, block) in K (and in V)
-  int s_vecs;   // ... in the scale records (0 for bf16 pools)
+  int k_vecs, v_vecs;  // 16-byte vectors of one (layer, block) in K and in V
+  int s_vecs;          // ... in the scale records (0 but for e4m3 pools)
   int n;
   int src[kMaxDst / 2];
   int dst[kMaxDst / 2];
@@ -87,7 +87,7 @@ struct MoveArgs {
 // stored), so that U copies per thread are in flight over the CPU-GPU link.
 template <int U>
 __global__ void block_move_kernel(const __grid_constant__ MoveArgs a) {
-  const int per_layer = 2 * a.kv_vecs + a.s_vecs;
+  const int per_layer = a.k_vecs + a.v_vecs + a.s_vecs;
   const int64_t per_pair = (int64_t)a.L * per_layer;
   const int64_t total = per_pair * a.n;
   const int64_t step = (int64_t)gridDim.x * blockDim.x;
@@ -106,14 +106,14 @@ __global__ void block_move_kernel(const __grid_constant__ MoveArgs a) {
         int vec = (int)(r - layer * per_layer);
         const int64_t fb = layer * a.from_blocks + a.src[pair];
         const int64_t tb = layer * a.to_blocks + a.dst[pair];
-        if (vec < a.kv_vecs) {
-          v[u] = a.from_k[fb * a.kv_vecs + vec];
-          d[u] = a.to_k + tb * a.kv_vecs + vec;
-        } else if ((vec -= a.kv_vecs) < a.kv_vecs) {
-          v[u] = a.from_v[fb * a.kv_vecs + vec];
-          d[u] = a.to_v + tb * a.kv_vecs + vec;
+        if (vec < a.k_vecs) {
+          v[u] = a.from_k[fb * a.k_vecs + vec];
+          d[u] = a.to_k + tb * a.k_vecs + vec;
+        } else if ((vec -= a.k_vecs) < a.v_vecs) {
+          v[u] = a.from_v[fb * a.v_vecs + vec];
+          d[u] = a.to_v + tb * a.v_vecs + vec;
         } else {
-          vec -= a.kv_vecs;
+          vec -= a.v_vecs;
           v[u] = a.from_s[fb * a.s_vecs + vec];
           d[u] = a.to_s + tb * a.s_vecs + vec;
         }
@@ -138,7 +138,7 @@ struct BatchArgs {
   const uint4* k_new;
   const uint4* v_new;
   int64_t num_blocks;
-  int L, Hkv, vec_per_row, total;
+  int L, Hkv, vec_k, vec_v, total;
   int n_runs;
   RunDesc runs[kMaxRuns];
   int dst[kMaxRunDst];
@@ -147,25 +147,24 @@ struct BatchArgs {
 // blockIdx.y = run; grid-stride over (layer, token, head, vec) of that run.
 __global__ void append_batch_kernel(const __grid_constant__ BatchArgs a) {
   const RunDesc r = a.runs[blockIdx.y];
-  const int64_t per_layer = (int64_t)r.n * a.Hkv * a.vec_per_row;
+  const int64_t per_layer = (int64_t)r.n * a.Hkv * a.vec_k;
   const int64_t work = per_layer * a.L;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < work;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t layer = i / per_layer;
     int64_t rem = i - layer * per_layer;
-    const int vec = (int)(rem % a.vec_per_row);
-    rem /= a.vec_per_row;
+    const int vec = (int)(rem % a.vec_k);
+    rem /= a.vec_k;
     const int h = (int)(rem % a.Hkv);
     const int tok = (int)(rem / a.Hkv);
     const int t = r.tok0 + tok;
     const int blk = a.dst[r.dst_off + t / 16 - r.first_lb];
-    const int64_t src =
-        ((layer * a.total + r.row + tok) * a.Hkv + h) * (int64_t)a.vec_per_row + vec;
+    const int64_t src = (layer * a.total + r.row + tok) * a.Hkv + h;  // row
     const int64_t dst =
-        (((layer * a.num_blocks + blk) * a.Hkv + h) * 16 + t % 16) *
-            (int64_t)a.vec_per_row + vec;
-    a.k_pool[dst] = a.k_new[src];
-    a.v_pool[dst] = a.v_new[src];
+        ((layer * a.num_blocks + blk) * a.Hkv + h) * 16 + t % 16;
+    a.k_pool[dst * a.vec_k + vec] = a.k_new[src * a.vec_k + vec];
+    if (vec < a.vec_v)
+      a.v_pool[dst * a.vec_v + vec] = a.v_new[src * a.vec_v + vec];
   }
 }
 
@@ -181,7 +180,7 @@ int grid_for(int64_t work) {
 
 int launch_append_scatter(void* k_pool, void* v_pool, const void* k_new,
                           const void* v_new, int64_t num_blocks, int L,
-                          int Hkv, int d, int B, int n, int tok0,
+                          int Hkv, int dk, int dv, int B, int n, int tok0,
                           const int32_t* dst_blocks, int n_dst,
                           void* stream) {
   (void)B;
@@ -193,7 +192,8 @@ int launch_append_scatter(void* k_pool, void* v_pool, const void* k_new,
   a.num_blocks = num_blocks;
   a.L = L;
   a.Hkv = Hkv;
-  a.vec_per_row = d / 8;
+  a.vec_k = dk / 8;
+  a.vec_v = dv / 8;
   a.n = n;
   a.tok0 = tok0;
   const int first_lb = tok0 / 16;
@@ -209,7 +209,7 @@ int launch_append_scatter(void* k_pool, void* v_pool, const void* k_new,
     const int lb_end = (tok0 + tok_end - 1) / 16;
     for (int lb = lb_begin; lb <= lb_end; ++lb)
       a.dst[lb - lb_begin] = dst_blocks[lb - first_lb];
-    const int64_t work = (int64_t)(tok_end - tok) * Hkv * (d / 8) * L;
+    const int64_t work = (int64_t)(tok_end - tok) * Hkv * (dk / 8) * L;
     append_scatter_kernel<<<grid_for(work), 256, 0, (cudaStream_t)stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return (int)e;
@@ -221,8 +221,8 @@ int launch_append_scatter(void* k_pool, void* v_pool, const void* k_new,
 
 int launch_append_batch(void* k_pool, void* v_pool, const void* k_new,
                         const void* v_new, int64_t num_blocks, int L, int Hkv,
-                        int d, int32_t total, const std::vector<ScatterRun>& runs,
-                        void* stream) {
+                        int dk, int dv, int32_t total,
+                        const std::vector<ScatterRun>& runs, void* stream) {
   BatchArgs a;
   a.k_pool = static_cast<uint4*>(k_pool);
   a.v_pool = static_cast<uint4*>(v_pool);
@@ -231,7 +231,8 @@ int launch_append_batch(void* k_pool, void* v_pool, const void* k_new,
   a.num_blocks = num_blocks;
   a.L = L;
   a.Hkv = Hkv;
-  a.vec_per_row = d / 8;
+  a.vec_k = dk / 8;
+  a.vec_v = dv / 8;
   a.total = total;
   a.n_runs = 0;
   int n_dst = 0;
@@ -267,7 +268,7 @@ int launch_append_batch(void* k_pool, void* v_pool, const void* k_new,
       r.dst_off = n_dst;
       for (int lb = lb0; lb <= lb1; ++lb)
         a.dst[n_dst++] = run.dst[lb - run.first_lblock];
-      max_work = std::max<int64_t>(max_work, (int64_t)r.n * Hkv * (d / 8) * L);
+      max_work = std::max<int64_t>(max_work, (int64_t)r.n * Hkv * (dk / 8) * L);
       tok = tok_end;
     }
   }
@@ -275,8 +276,9 @@ int launch_append_batch(void* k_pool, void* v_pool, const void* k_new,
 }
 
 int launch_block_move(const PoolBufs& from, const PoolBufs& to, int L,
-                      int64_t kv_bytes, int64_t s_bytes, const int32_t* src,
-                      const int32_t* dst, int n, void* stream) {
+                      int64_t k_bytes, int64_t v_bytes, int64_t s_bytes,
+                      const int32_t* src, const int32_t* dst, int n,
+                      void* stream) {
   MoveArgs a;
   a.from_k = static_cast<const uint4*>(from.k);
   a.from_v = static_cast<const uint4*>(from.v);
@@ -287,7 +289,8 @@ int launch_block_move(const PoolBufs& from, const PoolBufs& to, int L,
   a.from_blocks = from.blocks;
   a.to_blocks = to.blocks;
   a.L = L;
-  a.kv_vecs = (int)(kv_bytes / 16);
+  a.k_vecs = (int)(k_bytes / 16);
+  a.v_vecs = (int)(v_bytes / 16);
   a.s_vecs = (int)(s_bytes / 16);
   // A light grid: one CTA for every four SMs, four 16-byte vectors in
   // flight per thread.  The moves that cross the CPU-GPU link (spill,
@@ -305,7 +308,7 @@ int launch_block_move(const PoolBufs& from, const PoolBufs& to, int L,
       a.src[i] = src[i0 + i];
       a.dst[i] = dst[i0 + i];
     }
-    const int64_t work = (int64_t)a.n * L * (2 * a.kv_vecs + a.s_vecs);
+    const int64_t work = (int64_t)a.n * L * (a.k_vecs + a.v_vecs + a.s_vecs);
     const int grid = (int)std::min<int64_t>(std::max(sms / 4, 1),
                                             std::max<int64_t>(1, (work + 255) / 256));
     block_move_kernel<4><<<grid, 256, 0, (cudaStream_t)stream>>>(a);
