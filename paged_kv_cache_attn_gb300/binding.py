@@ -244,11 +244,18 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_torch = None          # torch, once a call has found a GPU
+
+
 def _stream(s):
+    global _torch
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if \
-            torch.cuda.is_available() else None
+        if _torch is None:
+            import torch
+            if not torch.cuda.is_available():
+                return None
+            _torch = torch
+        return _torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -517,22 +524,28 @@ def _token_rows(t, width):
     tokens (dimension 0) are rows of `width` contiguous values."""
     if t is None:
         return None, 0
-    if t.element_size() != 2 or t.numel() != t.shape[0] * width or \
-            (t.shape[0] > 0 and not t[0].is_contiguous()):
+    sh, st = t.shape, t.stride()
+    if len(sh) == 3:
+        ok = sh[1] * sh[2] == width and st[2] == 1 and \
+            (st[1] == sh[2] or sh[1] == 1)
+    else:
+        ok = len(sh) == 2 and sh[1] == width and st[1] == 1
+    if not ok or t.element_size() != 2:
         raise KVError(KV_ERR_INVALID_ARG,
                       f"a token is {width} contiguous bf16 values, got "
-                      f"{tuple(t.shape)} of {t.dtype}, strides {t.stride()}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+                      f"{tuple(sh)} of {t.dtype}, strides {st}")
+    return t.data_ptr(), st[0] if sh[0] > 1 else width
 
 
 def _rope_table(rope):
     """(pointer, rope_len, rot_dim) of an fp32 table [rope_len][rot/2][2]."""
-    if rope.dim() != 3 or rope.shape[2] != 2 or rope.element_size() != 4 or \
+    sh = rope.shape
+    if len(sh) != 3 or sh[2] != 2 or rope.element_size() != 4 or \
             not rope.is_contiguous():
         raise KVError(KV_ERR_INVALID_ARG,
                       "rope is a contiguous fp32 [rope_len][rot_dim / 2][2], "
-                      f"got {tuple(rope.shape)} of {rope.dtype}")
-    return rope.data_ptr(), rope.shape[0], 2 * rope.shape[1]
+                      f"got {tuple(sh)} of {rope.dtype}")
+    return rope.data_ptr(), sh[0], 2 * sh[1]
 
 
 def paged_rope_append(q, k_new, v_new, rope, rope_style, q_out, k_pool, v_pool,
@@ -573,13 +586,14 @@ def _head_rows(t, heads, width):
     [total][heads][width] with contiguous values in a head."""
     if t is None:
         return None, 0, 0
-    if t.element_size() != 2 or t.dim() != 3 or \
-            tuple(t.shape[1:]) != (heads, width) or t.stride(2) != 1:
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[1] != heads or sh[2] != width or st[2] != 1 or \
+            t.element_size() != 2:
         raise KVError(KV_ERR_INVALID_ARG,
                       f"expected bf16 [total][{heads}][{width}], got "
-                      f"{tuple(t.shape)} of {t.dtype}, strides {t.stride()}")
-    hs = t.stride(1) if heads > 1 else width
-    ts = t.stride(0) if t.shape[0] > 1 else (heads - 1) * hs + width
+                      f"{tuple(sh)} of {t.dtype}, strides {st}")
+    hs = st[1] if heads > 1 else width
+    ts = st[0] if sh[0] > 1 else (heads - 1) * hs + width
     return t.data_ptr(), ts, hs
 
 

@@ -38,14 +38,27 @@ __device__ __forceinline__ void remote_arrive(uint32_t cluster_bar) {
                : "memory");
 }
 
-// Bulk copy of this CTA's shared memory into another CTA's, completing on a
-// barrier there (16-byte aligned addresses, size a multiple of 16).
-__device__ __forceinline__ void copy_to_cta(uint32_t dst, uint32_t src,
-                                            uint32_t bytes, uint32_t bar) {
+// Store into another CTA's shared memory, counted (16 or 4 bytes) on a barrier
+// there.  The stores of a warp run at the full rate of the SM-to-SM network
+// (21 bytes a cycle, measured) when they cover whole 128-byte lines, at half of
+// it as scattered 16-byte pieces.  They are ordinary (generic proxy) writes: the
+// side that feeds them to an MMA puts a proxy fence between its wait and the MMA.
+__device__ __forceinline__ void remote_store16(uint32_t dst, uint32_t a,
+                                               uint32_t b, uint32_t c,
+                                               uint32_t d, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes "
-      "[%0], [%1], %2, [%3];" ::"r"(dst),
-      "r"(src), "r"(bytes), "r"(bar)
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 "
+      "[%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+      "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void remote_store4(uint32_t dst, uint32_t a,
+                                              uint32_t bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 "
+      "[%0], %1, [%2];" ::"r"(dst),
+      "r"(a), "r"(bar)
       : "memory");
 }
 
@@ -73,6 +86,55 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar,
   return true;
 }
 
+// One lane of a converged warp, the same every time.  A warp that issues MMAs
+// keeps its control flow uniform and lets this lane issue: descriptors and
+// addresses then stay in uniform registers (an MMA of 65 cycles took 92 to issue
+// from a one-lane branch, 70 this way).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+__device__ __forceinline__ int uniform(int v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
+// Warp-wide waits polled by every lane, for a warp with nothing else to do.
+__device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ bool all_wait_cluster(uint32_t bar,
+                                                 uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity));
+}
+
+// Warp-wide waits polled by one lane: 32 lanes polling one barrier each cost
+// a shared-memory access, and eight waiting warps of them take that bandwidth
+// from the tensor pipe's operands.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
+                                          int lane) {
+  bool ok = true;
+  if (lane == 0) ok = mbar_wait(bar, parity);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok;
+}
+
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
+                                                  int lane) {
+  bool ok = true;
+  if (lane == 0) ok = mbar_wait_cluster(bar, parity);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok;
+}
+
 // Report all of this thread's earlier MMAs on the barrier at the same place
 // in the CTAs of `mask`.
 __device__ __forceinline__ void umma_commit_to(uint32_t bar, uint16_t mask) {
@@ -92,6 +154,29 @@ __device__ __forceinline__ void tma_load_5d_at(uint32_t dst,
       "bytes [%0], [%1, {%2, %2, %3, %2, %4}], [%5];" ::"r"(dst),
       "l"(tm), "r"(0), "r"(x2), "r"(x4), "r"(bar)
       : "memory");
+}
+
+// 128 rows x 32 bytes from shared memory (the layout of a K-major operand,
+// descriptor as for an MMA) to 8 columns of tensor memory; runs in order with
+// the thread's later MMAs.
+__device__ __forceinline__ void umma_copy(uint32_t tmem_d, uint64_t src) {
+  asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(tmem_d), "l"(src)
+               : "memory");
+}
+
+// K-major operand descriptor without swizzle: 8 rows x 16 bytes are 128
+// contiguous bytes, `k` bytes apart along K and `m` bytes along the rows.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t addr, uint32_t k,
+                                                uint32_t m) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) |
+         ((uint64_t)((k >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((m >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+}
+
+// Ask for `bytes` (a multiple of 16, 16-byte aligned) in L2.
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes)
+               : "memory");
 }
 
 // Named barriers over `n` threads (whole warps), combining a predicate.

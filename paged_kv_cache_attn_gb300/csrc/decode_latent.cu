@@ -14,9 +14,12 @@
 // SMs share an item as producer and consumer, a cluster of two CTAs:
 //
 //   score CTA (rank 0):  S = Q K^T.  TMEM: Q's latent part as the A operand
-//     (256 columns, bf16 pairs) and two S buffers (2 x 128 fp32 columns); the
+//     (256 columns, bf16 pairs; an item's Q comes through the K ring and is
+//     copied by the tensor pipe itself, so that the next item's scores follow
+//     the last ones) and two S buffers (2 x 128 fp32 columns); the
 //     position part of Q in shared memory.  K streams through a ring of
-//     128-token x 128-dimension stages.  256 softmax threads (two per row, 64
+//     128-token x 128-dimension stages, filled from L2 (one warp asks for the
+//     tokens some tiles ahead).  256 softmax threads (two per row, 64
 //     columns each, maxima exchanged through shared memory) turn S into P
 //     (bf16, base 2, lazy maximum) in two staging tiles of 64 tokens, which
 //     bulk copies carry into the other CTA's shared memory.
@@ -51,18 +54,22 @@
 namespace pkv {
 namespace lat {
 
+using tc::all_wait;
+using tc::all_wait_cluster;
 using tc::bar_and;
-using tc::bar_or;
 using tc::cluster_rank;
 using tc::cluster_sync;
-using tc::copy_to_cta;
+using tc::elect_one;
 using tc::fence_after_sync;
 using tc::fence_before_sync;
 using tc::idesc;
 using tc::map_rank;
 using tc::mbar_wait_cluster;
 using tc::remote_arrive;
+using tc::remote_store16;
+using tc::remote_store4;
 using tc::sdesc;
+using tc::sdesc_plain;
 using tc::tma_load_5d_at;
 using tc::tmem_ld32;
 using tc::tmem_st32;
@@ -70,12 +77,14 @@ using tc::tmem_wait_ld;
 using tc::tmem_wait_st;
 using tc::umma_commit;
 using tc::umma_commit_to;
+using tc::umma_copy;
 using tc::umma_ss;
 using tc::umma_ts;
+using tc::uniform;
+using tc::warp_wait;
+using tc::warp_wait_cluster;
 
 constexpr int kRank = KV_LATENT_RANK;
-constexpr int kRope = KV_LATENT_ROPE;
-constexpr int kQDim = kRank + kRope;
 constexpr int kT = 128;            // tokens of a score tile
 constexpr int kTB = kT / 16;       // its blocks
 constexpr int kG = 64;             // tokens of a P tile
@@ -83,29 +92,36 @@ constexpr int kGB = kG / 16;
 
 // Score CTA's shared memory.
 constexpr int kQr = 128 * 128;               // position part of Q
-constexpr int kKStage = kT * 256;            // 128 tokens x 128 dimensions
-constexpr int kNK = 4;
-constexpr int kRStage = kT * 128;            // position keys of a tile
-constexpr int kNR = 2;
-constexpr int kP = 128 * 128;                // 128 rows x 64 tokens of P
-// What goes with a P tile: 128 rescale factors and a flag word.
-constexpr int kHdr = 528, kHdrStride = 640;
+constexpr int kKDim = 128;                   // dimensions of a K stage
+constexpr int kKParts = kRank / kKDim;       // stages of a tile
+constexpr int kKBox = 16 * kKDim * 2;        // one block's part: a box
+constexpr int kKStage = kTB * kKBox;
+// Stages are refilled one by one, but waited for in pairs: a wait costs the
+// issuing warp as much as one or two MMAs.
+constexpr int kNK = 6;
+static_assert(kKParts % 2 == 0 && kNK % 2 == 0, "stages come in pairs");
+constexpr int kRTile = kT * 128;             // position keys of a tile
 constexpr int kOffK = kQr;
 constexpr int kOffR = kOffK + kNK * kKStage;
-constexpr int kOffStage = kOffR + kNR * kRStage;
-constexpr int kOffStageHdr = kOffStage + 2 * kP;
-constexpr int kOffStageFin = kOffStageHdr + 2 * kHdrStride;
-constexpr int kScoreSmem = kOffStageFin + 2 * 512;
+constexpr int kScoreSmem = kOffR + kRTile;
 // Output CTA's shared memory.
 constexpr int kVBlk = 16 * kRank * 2;        // one block
-constexpr int kNV = 9;
+constexpr int kVB = 2;                       // blocks of a V stage
+constexpr int kVStage = kVB * kVBlk;
+constexpr int kNV = 4;
+// A P tile: [8 chunks of 8 tokens][128 rows][16 bytes], the K-major layout
+// without swizzle; a warp's store of a chunk is 512 contiguous bytes.
+constexpr int kP = 128 * 128;
+constexpr int kPChunk = 128 * 16;
 constexpr int kNP = 4;
-constexpr int kOffP = kNV * kVBlk;
+// With it 128 rescale factors and a flag word for each row warp.
+constexpr int kHdr = 512 + 16;
+constexpr int kOffP = kNV * kVStage;
 constexpr int kOffHdr = kOffP + kNP * kP;
-constexpr int kOffFin = kOffHdr + kNP * kHdrStride;
-constexpr int kOutSmem = kOffFin + 2 * 512;
-constexpr int kSmem =
-    (kScoreSmem > kOutSmem ? kScoreSmem : kOutSmem) + 1024;
+constexpr int kOffFin = kOffHdr + kNP * kHdr;
+constexpr int kOffTurn = (kOffFin + 2 * 512 + 127) & ~127;  // 2 KB a row warp
+constexpr int kOutSmem = kOffTurn + 8 * 2048;
+constexpr int kTiles = kScoreSmem > kOutSmem ? kScoreSmem : kOutSmem;
 
 constexpr int kThreads = 12 * 32;
 constexpr int kRowThreads = 256;             // warps 0-7
@@ -115,7 +131,8 @@ constexpr uint32_t kColS = 256;              // score CTA: Q 0..255, S 256..511
 constexpr float kRescale = 8.f;              // lazy-max threshold (log2 units)
 
 struct Params {
-  const __nv_bfloat16* q;
+  const uint8_t* c_pool;
+  const uint8_t* r_pool;
   const int32_t* tables;
   const int32_t* seq_lens;
   const WorkItem* items;
@@ -129,19 +146,27 @@ struct Params {
   float scale_log2;
 };
 
-// At the same place in both CTAs.
-struct Bars {
+// Barriers and small arrays, behind the tiles; at the same place in both CTAs.
+struct Small {
   // score CTA
-  uint64_t k_full[kNK], k_empty[kNK], r_full[kNR], r_empty[kNR];
-  uint64_t q_full, s_full[2], s_empty[2];
-  uint64_t p_ack[2];       // a staged P tile has landed on the other side
+  uint64_t k_full[kNK / 2], k_empty[kNK], r_full, r_empty;
+  uint64_t qr_full, qr_empty, q_free, s_full[2], s_empty[2];
   uint64_t p_empty[kNP];   // the other side has consumed P slot i
   uint64_t fin_empty[2];
   // output CTA
   uint64_t v_full[kNV], v_empty[kNV], v_fix[kNV], p_full[kNP], fin_full[2];
   uint64_t event, o_ok;
-  uint64_t drain;
+  uint64_t drain[2];
+  uint32_t tmem_base;
+  int aborted;
+  int event_what;          // slot of a rescale, or -1: item done
+  float max_of[2][2][128]; // [tile parity][half][row]
+  float sum_of[128];
 };
+// The tiles need 1024-byte alignment and nearly all of the shared memory, so
+// there is no static shared memory in front of them.
+constexpr int kSmem = kTiles + (int)sizeof(Small);
+static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 
 __device__ __forceinline__ bool item_fits(const WorkItem& it, const Params& p) {
   const int64_t last = (int64_t)it.row0 + it.nrows - 1;
@@ -152,24 +177,38 @@ __device__ __forceinline__ bool item_fits(const WorkItem& it, const Params& p) {
                         (int64_t)it.prow_base + it.nrows <= p.partial_rows));
 }
 
-// The items of this pair, the same for every role of both CTAs.  A malformed
-// item or list is recorded by one thread and skipped by all.
+// The items of this pair, the same for every role of both CTAs, read one
+// ahead.  Malformed ones are skipped by all (and recorded by one warp, see
+// report_bad).
 struct ItemLoop {
   const Params& p;
   int i, end;
+  WorkItem ahead;
   __device__ ItemLoop(const Params& pp, int pair) : p(pp) {
     i = p.pair_ptr[pair];
     end = p.pair_ptr[pair + 1];
     if (i < 0 || end > p.n_items || i > end) i = end = 0;
+    if (i < end) ahead = p.items[i];
   }
   __device__ bool next(WorkItem& it) {
     while (i < end) {
-      it = p.items[i++];
+      it = ahead;
+      if (++i < end) ahead = p.items[i];
       if (item_fits(it, p)) return true;
     }
     return false;
   }
 };
+
+__device__ __forceinline__ void report_bad(const Params& p, int pair) {
+  const int a = p.pair_ptr[pair], b = p.pair_ptr[pair + 1];
+  if (a < 0 || b > p.n_items || a > b) {
+    record_status(p.status, KV_ERR_DEVICE, -1 - pair);
+    return;
+  }
+  for (int i = a; i < b; ++i)
+    if (!item_fits(p.items[i], p)) record_status(p.status, KV_ERR_DEVICE, -1 - i);
+}
 
 // The physical block of `blk` of the item, or -1 (past the range, or not a
 // block of the pool).
@@ -191,89 +230,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ CUtensorMap tmR,
+                         const __grid_constant__ CUtensorMap tmQ,
                          const Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) Bars bars;
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_sh;
-  __shared__ int event_sh;                // slot of a rescale, or -1: item done
-  __shared__ float max_sh[2][2][128];     // [tile parity][half][row]
-  __shared__ float sum_sh[128];
-
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Small& bars = *reinterpret_cast<Small*>(smem + kTiles);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool scores = rank == 0;
   const int pair = blockIdx.x >> 1;
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
-  volatile int* aborted = &abort_sh;
+  const uint32_t base = smem_u32(smem);
+  volatile int* aborted = &bars.aborted;
+  if (base & 1023) {  // never, with no static shared memory; both CTAs agree
+    if (threadIdx.x == 0) record_status(p.status, KV_ERR_INTERNAL, (int)base);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kNK; ++s) {
-      mbar_init(smem_u32(&bars.k_full[s]), 2);   // two producer warps
+      mbar_init(smem_u32(&bars.k_full[s / 2]), 2);  // both producer warps
       mbar_init(smem_u32(&bars.k_empty[s]), 1);
     }
-    for (int s = 0; s < kNR; ++s) {
-      mbar_init(smem_u32(&bars.r_full[s]), 1);
-      mbar_init(smem_u32(&bars.r_empty[s]), 1);
-    }
-    mbar_init(smem_u32(&bars.q_full), 8);        // the row warps
+    mbar_init(smem_u32(&bars.r_full), 1);
+    mbar_init(smem_u32(&bars.r_empty), 1);
+    mbar_init(smem_u32(&bars.qr_full), 1);
+    mbar_init(smem_u32(&bars.qr_empty), 1);
+    mbar_init(smem_u32(&bars.q_free), 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&bars.s_full[b]), 1);
       mbar_init(smem_u32(&bars.s_empty[b]), 8);
-      mbar_init(smem_u32(&bars.p_ack[b]), 1);
       mbar_init(smem_u32(&bars.fin_empty[b]), 8);  // the other side's row warps
       mbar_init(smem_u32(&bars.fin_full[b]), 1);
     }
     for (int s = 0; s < kNP; ++s) {
-      mbar_init(smem_u32(&bars.p_empty[s]), 1);
+      mbar_init(smem_u32(&bars.p_empty[s]), 2);    // both product warps
       mbar_init(smem_u32(&bars.p_full[s]), 1);
     }
     for (int s = 0; s < kNV; ++s) {
       mbar_init(smem_u32(&bars.v_full[s]), 1);
-      mbar_init(smem_u32(&bars.v_empty[s]), 1);
+      mbar_init(smem_u32(&bars.v_empty[s]), 2);
       mbar_init(smem_u32(&bars.v_fix[s]), 1);    // masked rows zeroed
     }
-    mbar_init(smem_u32(&bars.event), 2);         // the MMA thread and its commit
+    mbar_init(smem_u32(&bars.event), 4);         // two product warps, each
+                                                 // itself and its commit
     mbar_init(smem_u32(&bars.o_ok), 8);
-    mbar_init(smem_u32(&bars.drain), 1);
-    abort_sh = 0;
+    mbar_init(smem_u32(&bars.drain[0]), 1);
+    mbar_init(smem_u32(&bars.drain[1]), 1);
+    bars.aborted = 0;
     fence_mbar_init();
+    // What will arrive here from the other CTA, armed a phase ahead.
+    if (!scores) {
+      for (int s = 0; s < kNP; ++s)
+        mbar_expect_tx(smem_u32(&bars.p_full[s]), kP + kHdr);
+      for (int f = 0; f < 2; ++f) mbar_expect_tx(smem_u32(&bars.fin_full[f]), 512);
+    }
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmR);
-    if (rank == 0) {
-      // Malformed entries of this pair's list.
-      const int a = p.pair_ptr[pair], b = p.pair_ptr[pair + 1];
-      if (a < 0 || b > p.n_items || a > b) {
-        record_status(p.status, KV_ERR_DEVICE, -1 - pair);
-      } else {
-        for (int i = a; i < b; ++i)
-          if (!item_fits(p.items[i], p))
-            record_status(p.status, KV_ERR_DEVICE, -1 - i);
-      }
-    }
+    tma_prefetch_desc(&tmQ);
   }
   if (warp == kMmaWarp) {
     asm volatile(
         "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::
-            "r"(smem_u32(&tmem_base_sh)),
+            "r"(smem_u32(&bars.tmem_base)),
         "r"(kTmemCols)
         : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::
                      : "memory");
   }
+  ItemLoop loop(p, pair);  // its loads overlap the set-up
   fence_before_sync();
   __syncthreads();
   cluster_sync();  // the other CTA's barriers are ready too
   fence_after_sync();
-  const uint32_t tmem = tmem_base_sh;
-  ItemLoop loop(p, pair);
+  const uint32_t tmem = bars.tmem_base;
   WorkItem it;
   auto timed_out = [&](int site) {
     if (!*aborted) record_status(p.status, KV_ERR_TIMEOUT, site);
-    atomicExch(&abort_sh, 1);
+    atomicExch(&bars.aborted, 1);
   };
 
   if (scores && warp < 8) {
@@ -281,54 +315,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int wg = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t stage = base + kOffStage + wg * kP;
-    const uint32_t prow = stage + (r >> 3) * 1024 + (r & 7) * 128;
-    float* hdr = reinterpret_cast<float*>(base_ptr + kOffStageHdr + wg * kHdrStride);
-    const uint32_t peer_p = map_rank(base + kOffP, 1);
+    const uint32_t peer_p = map_rank(base + kOffP, 1) + r * 16;
     const uint32_t peer_hdr = map_rank(base + kOffHdr, 1);
-    const uint32_t peer_fin = map_rank(base + kOffFin, 1);
+    const uint32_t peer_fin = map_rank(base + kOffFin, 1) + r * 4;
+    const uint32_t peer_full = map_rank(smem_u32(&bars.p_full[0]), 1);
     uint32_t tc_n = 0;   // tiles so far
     uint32_t g_n = 0;    // P tiles sent so far, by both halves
-    uint32_t mine = 0;   // ... by this half
     uint32_t fin_n = 0;  // items whose sums were sent
     bool ok = true;
     while (ok && loop.next(it)) {
-      // Q of this row: latent part to TMEM (half of the columns each), the
-      // position part to shared memory.  The previous item's products are
-      // done (its last S has been read).
-      {
-        const uint4* src = r < it.nrows
-            ? reinterpret_cast<const uint4*>(
-                  p.q + ((int64_t)it.branch0 * p.Hq + it.row0 + r) * kQDim)
-            : nullptr;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t v[32];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 x = src ? __ldg(src + wg * 32 + h * 8 + c)
-                                : make_uint4(0, 0, 0, 0);
-            v[4 * c] = x.x;
-            v[4 * c + 1] = x.y;
-            v[4 * c + 2] = x.z;
-            v[4 * c + 3] = x.w;
-          }
-          tmem_st32(lane_base + wg * 128 + h * 32, v);
-        }
-        if (wg == 0) {
-          const uint32_t qrow = base + (r >> 3) * 1024 + (r & 7) * 128;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 x = src ? __ldg(src + 64 + c) : make_uint4(0, 0, 0, 0);
-            tc::st_shared_v4(qrow + ((c ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
-          }
-          fence_proxy_async_smem();
-        }
-        tmem_wait_st();
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
-      }
       const int seq_len = it.masked ? p.seq_lens[it.branch0] : 0x7fffffff;
       const int nt = n_tiles(it);
       float m_used = -INFINITY, l = 0.f;
@@ -339,8 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int valid = min(min(kT, left), max(seq_len - blk0 * 16, 0)) - wg * kG;
         valid = min(valid, kG);
         float s[kG];
-        bool w = mbar_wait(smem_u32(&bars.s_full[b]), (tc_n >> 1) & 1);
-        w = __all_sync(0xffffffffu, w);
+        const bool w = warp_wait(smem_u32(&bars.s_full[b]), (tc_n >> 1) & 1, lane);
         float mx = -INFINITY;
         if (w) {
           fence_after_sync();
@@ -370,22 +364,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {
           timed_out(30);
         }
-        max_sh[b][wg][r] = mx;
+        bars.max_of[b][wg][r] = mx;
         // Every row thread agrees whether to go on.
         ok = bar_and(1, kRowThreads, w && !*aborted);
         if (!ok) break;
-        const float m_tile = fmaxf(mx, max_sh[b][wg ^ 1][r]) * p.scale_log2;
-        const bool need = m_tile > m_used + kRescale;
+        const float m_tile = fmaxf(mx, bars.max_of[b][wg ^ 1][r]) * p.scale_log2;
+        // Rows past the item's hold whatever was there: they never ask.
+        const bool need = m_tile > m_used + kRescale && r < it.nrows;
         const float m_new = need ? m_tile : m_used;
         const float alpha = need ? ex2(m_used - m_new) : 1.f;
         m_used = m_new;
         l *= alpha;
         const bool two = left > kG;  // the tile has a second P tile
         if (wg == 0 || two) {
-          const uint32_t g = g_n + wg;
-          if (mine > 0 &&
-              !mbar_wait_cluster(smem_u32(&bars.p_ack[wg]), (mine - 1) & 1))
-            timed_out(31);
+          const uint32_t g = g_n + wg, slot = g % kNP;
+          if (g >= kNP && !warp_wait_cluster(smem_u32(&bars.p_empty[slot]),
+                                             (g / kNP - 1) & 1, lane))
+            timed_out(32);
+          const uint32_t bar = peer_full + slot * 8;
+          const uint32_t dst = peer_p + slot * kP;
           const float neg_m = m_new == -INFINITY ? 0.f : -m_new;
           float sum4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -399,153 +396,193 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               sum4[i] += p0 + p1;
               pk[i] = pack_bf16(p0, p1);
             }
-            tc::st_shared_v4(prow + ((c ^ (r & 7)) << 4), pk[0], pk[1], pk[2],
-                             pk[3]);
+            remote_store16(dst + c * kPChunk, pk[0], pk[1], pk[2], pk[3], bar);
           }
           l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
-          hdr[r] = alpha;
-          fence_proxy_async_smem();
-          const bool moved = bar_or(2 + wg, 128, need && j > 0);
-          if (r == 0) {
-            // Only the tile's first P tile carries the factors: O is rescaled
-            // once, before any of the tile's products.
-            reinterpret_cast<uint32_t*>(hdr)[128] = moved && wg == 0 ? 1u : 0u;
-            fence_proxy_async_smem();
-            const uint32_t slot = g % kNP;
-            if (g >= kNP &&
-                !mbar_wait_cluster(smem_u32(&bars.p_empty[slot]),
-                                   (g / kNP - 1) & 1))
-              timed_out(32);
-            if (!*aborted) {
-              const uint32_t bar = map_rank(smem_u32(&bars.p_full[slot]), 1);
-              copy_to_cta(peer_p + slot * kP, stage, kP, bar);
-              copy_to_cta(peer_hdr + slot * kHdrStride, smem_u32(hdr), kHdr, bar);
-            }
-          }
-          ++mine;
+          // O is rescaled once a tile, before any of its products: the first P
+          // tile's flags say so, the second's are 0.
+          const uint32_t hdr = peer_hdr + slot * kHdr;
+          const bool moved = __any_sync(0xffffffffu, need && j > 0) && wg == 0;
+          remote_store4(hdr + r * 4, __float_as_uint(alpha), bar);
+          if (lane == 0) remote_store4(hdr + 512 + (warp & 3) * 4, moved, bar);
         }
         g_n += two ? 2 : 1;
       }
       if (!ok) break;
       // The row's sum over both halves.
-      if (wg == 1) sum_sh[r] = l;
+      if (wg == 1) bars.sum_of[r] = l;
       ok = bar_and(1, kRowThreads, !*aborted);
       if (!ok) break;
       if (wg == 0) {
-        l += sum_sh[r];
+        l += bars.sum_of[r];
         if (it.g == 0) {
           if (r < it.nrows) p.ml[it.prow_base + r] = make_float2(m_used, l);
         } else {
           const int f = fin_n & 1;
           if (fin_n >= 2 &&
-              !mbar_wait_cluster(smem_u32(&bars.fin_empty[f]), (fin_n / 2 - 1) & 1))
+              !warp_wait_cluster(smem_u32(&bars.fin_empty[f]), (fin_n / 2 - 1) & 1,
+                                 lane))
             timed_out(33);
-          reinterpret_cast<float*>(base_ptr + kOffStageFin + f * 512)[r] = 1.f / l;
-          fence_proxy_async_smem();
-          bar_or(2, 128, false);
-          if (r == 0 && !*aborted)
-            copy_to_cta(peer_fin + f * 512, base + kOffStageFin + f * 512, 512,
+          remote_store4(peer_fin + f * 512, __float_as_uint(1.f / l),
                         map_rank(smem_u32(&bars.fin_full[f]), 1));
         }
       }
       if (it.g != 0) ++fin_n;
-      // sum_sh is read before the next item's sums are written: the tiles of
+      // bars.sum_of is read before the next item's sums are written: the tiles of
       // that item pass barrier 1 in between.
     }
-    // Copies out of this CTA have landed, and every arrival from the other
+    // What this CTA stored has been consumed, and every arrival from the other
     // side is in, before this CTA may leave.
-    if (r == 0) {
-      if (mine > 0) mbar_wait_cluster(smem_u32(&bars.p_ack[wg]), (mine - 1) & 1);
-      if (wg == 0) {
-        for (uint32_t g = g_n > kNP ? g_n - kNP : 0; g < g_n; ++g)
-          if (!mbar_wait_cluster(smem_u32(&bars.p_empty[g % kNP]), (g / kNP) & 1))
-            break;
-        for (uint32_t f = fin_n > 2 ? fin_n - 2 : 0; f < fin_n; ++f)
-          if (!mbar_wait_cluster(smem_u32(&bars.fin_empty[f & 1]), (f / 2) & 1))
-            break;
-      }
+    if (threadIdx.x == 0) {
+      for (uint32_t g = g_n > kNP ? g_n - kNP : 0; g < g_n; ++g)
+        if (!mbar_wait_cluster(smem_u32(&bars.p_empty[g % kNP]), (g / kNP) & 1))
+          break;
+      for (uint32_t f = fin_n > 2 ? fin_n - 2 : 0; f < fin_n; ++f)
+        if (!mbar_wait_cluster(smem_u32(&bars.fin_empty[f & 1]), (f / 2) & 1))
+          break;
     }
   } else if (scores && warp == kMmaWarp) {
-    // ---- score CTA, products -------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t id = idesc(128, kT, false);
-      uint32_t tn = 0, kn = 0, in = 0;
-      bool ok = true;
-      while (ok && loop.next(it)) {
-        ok = mbar_wait(smem_u32(&bars.q_full), in & 1);
-        ++in;
-        const int nt = n_tiles(it);
-        for (int j = 0; j < nt && ok; ++j, ++tn) {
-          const int b = tn & 1;
-          if (tn >= 2) ok = mbar_wait(smem_u32(&bars.s_empty[b]), ((tn >> 1) - 1) & 1);
-          const uint32_t d = tmem + kColS + b * kT;
-          for (int c = 0; c < 4 && ok; ++c, ++kn) {
-            const uint32_t s = kn % kNK;
-            ok = mbar_wait(smem_u32(&bars.k_full[s]), (kn / kNK) & 1);
-            if (!ok) break;
-            fence_after_sync();
-            const uint32_t kst = base + kOffK + s * kKStage;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_ts(d, tmem + c * 64 + kk * 8,
-                      sdesc(kst + (kk >> 2) * 1024 + (kk & 3) * 32, 16, 2048),
-                      id, (c > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(smem_u32(&bars.k_empty[s]));
-          }
-          if (!ok) break;
-          const uint32_t s = tn % kNR;
-          ok = mbar_wait(smem_u32(&bars.r_full[s]), (tn / kNR) & 1);
-          if (!ok) break;
-          fence_after_sync();
-          const uint32_t rst = base + kOffR + s * kRStage;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ss(d, sdesc(base + kk * 32, 16, 1024),
-                    sdesc(rst + kk * 32, 16, 1024), id, 1u);
-          umma_commit(smem_u32(&bars.r_empty[s]));
-          umma_commit(smem_u32(&bars.s_full[b]));
-        }
-        ok = ok && !*aborted;
-      }
-      if (!ok) timed_out(34);
-      umma_commit(smem_u32(&bars.drain));
-      mbar_wait(smem_u32(&bars.drain), 0);
-    }
-  } else if (scores && warp < 11) {
-    // ---- score CTA, K: warp 9 the first four blocks of a tile, warp 10 the
-    // other four; one box is a block x 128 dimensions.
-    const int half = warp - 9;
-    uint32_t kn = 0;
+    // ---- score CTA, products (the warp runs uniformly, one lane issues) ------
+    constexpr uint32_t id = idesc(128, kT, false);
+    const bool lead = elect_one();
+    uint32_t tn = 0, kn = 0, in = 0;
     bool ok = true;
     while (ok && loop.next(it)) {
-      const int nt = n_tiles(it);
-      for (int j = 0; j < nt && ok; ++j) {
-        bool bad = false;
-        int phys = -1;
-        if (lane < kTB / 2)
-          phys = block_of(p, it, it.blk_begin + j * kTB + half * (kTB / 2) + lane, bad);
-        if (bad) record_status(p.status, KV_ERR_DEVICE,
-                               p.tables[(int64_t)it.branch0 * p.max_blocks +
-                                        it.blk_begin + j * kTB + half * (kTB / 2) + lane]);
-        const int n = __popc(__ballot_sync(0xffffffffu, phys >= 0));
-        for (int c = 0; c < 4; ++c, ++kn) {
-          const uint32_t s = kn % kNK;
-          if (lane == 0) {
-            ok = !*aborted && (kn < kNK || mbar_wait(smem_u32(&bars.k_empty[s]),
-                                                     (kn / kNK - 1) & 1));
-            if (ok) {
-              if (n > 0)
-                mbar_expect_tx(smem_u32(&bars.k_full[s]), n * 4096);
-              else
-                mbar_arrive(smem_u32(&bars.k_full[s]));
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+      const int nt = uniform(n_tiles(it));
+      // Q: its latent part comes through the K ring and is copied to TMEM
+      // once the previous item's products have read theirs.
+      if (in > 0) ok = all_wait(smem_u32(&bars.q_free), (in - 1) & 1);
+      for (int c = 0; c < kKParts && ok; ++c, ++kn) {
+        const uint32_t s = kn % kNK;
+        if (c % 2 == 0) {
+          ok = all_wait(smem_u32(&bars.k_full[s / 2]), (kn / kNK) & 1);
           if (!ok) break;
+          fence_after_sync();
+        }
+        const uint64_t src = sdesc(base + kOffK + s * kKStage, 16, 1024);
+        if (lead) {
+#pragma unroll
+          for (int kk = 0; kk < kKDim / 16; ++kk)
+            umma_copy(tmem + c * (kKDim / 2) + kk * 8,
+                      src + (((kk >> 2) * kQr + (kk & 3) * 32) >> 4));
+          umma_commit(smem_u32(&bars.k_empty[s]));
+        }
+        __syncwarp();
+      }
+      if (ok) ok = all_wait(smem_u32(&bars.qr_full), in & 1);
+      ++in;
+      for (int j = 0; j < nt && ok; ++j, ++tn) {
+        const int b = tn & 1;
+        if (tn >= 2) ok = all_wait(smem_u32(&bars.s_empty[b]), ((tn >> 1) - 1) & 1);
+        const uint32_t d = tmem + kColS + b * kT;
+        // The position part first: after the last tile's, the next item's
+        // may be loaded.
+        ok = ok && all_wait(smem_u32(&bars.r_full), tn & 1);
+        if (!ok) break;
+        fence_after_sync();
+        const uint64_t qd = sdesc(base, 16, 1024);
+        const uint64_t rd = sdesc(base + kOffR, 16, 1024);
+        if (lead) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ss(d, qd + kk * 2, rd + kk * 2, id, kk > 0 ? 1u : 0u);
+          umma_commit(smem_u32(&bars.r_empty));
+          if (j == nt - 1) umma_commit(smem_u32(&bars.qr_empty));
+        }
+        __syncwarp();
+        for (int c = 0; c < kKParts; ++c, ++kn) {
+          const uint32_t s = kn % kNK;
+          if (c % 2 == 0) {
+            ok = all_wait(smem_u32(&bars.k_full[s / 2]), (kn / kNK) & 1);
+            if (!ok) break;
+            fence_after_sync();
+          }
+          const uint64_t kd = sdesc(base + kOffK + s * kKStage, 16, kKBox / 2);
+          const uint32_t qa = tmem + c * (kKDim / 2);
+          if (lead) {
+#pragma unroll
+            for (int kk = 0; kk < kKDim / 16; ++kk)
+              umma_ts(d, qa + kk * 8,
+                      kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id, 1u);
+            umma_commit(smem_u32(&bars.k_empty[s]));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lead) {
+          umma_commit(smem_u32(&bars.s_full[b]));
+          if (j == nt - 1) umma_commit(smem_u32(&bars.q_free));
+        }
+        __syncwarp();
+      }
+      ok = ok && !*aborted;
+    }
+    if (lead) {
+      if (!ok) timed_out(34);
+      umma_commit(smem_u32(&bars.drain[0]));
+      mbar_wait(smem_u32(&bars.drain[0]), 0);
+    }
+  } else if (scores && warp < 11) {
+    // ---- score CTA, K: warps 9 and 10 take every other stage; one box is a
+    // block x 128 dimensions, the eight of a stage issued by eight lanes at
+    // once (an issue costs a warp about 220 ns and 30 ns a box).
+    const uint32_t me = warp - 9;
+    uint32_t kn = 0;
+    bool ok = true;
+    // Stage kn is free; arm it.
+    auto arm = [&](uint32_t bytes) {
+      const uint32_t s = kn % kNK;
+      if (lane == 0) {
+        ok = !*aborted && (kn < kNK || mbar_wait(smem_u32(&bars.k_empty[s]),
+                                                 (kn / kNK - 1) & 1));
+        if (ok) {
+          if (bytes > 0)
+            mbar_expect_tx(smem_u32(&bars.k_full[s / 2]), bytes);
+          else
+            mbar_arrive(smem_u32(&bars.k_full[s / 2]));
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      return ok;
+    };
+    while (ok && loop.next(it)) {
+      const int nt = n_tiles(it);
+      const int blk = it.blk_begin + lane;
+      // A tile's block ids are read while the one before waits for its stages.
+      bool bad = false, next_bad = false;
+      int next = lane < kTB ? block_of(p, it, blk, next_bad) : -1;
+      // Q comes first, as stages of 128 rows x 128 dimensions in boxes of 16
+      // rows x 64.
+      const int qb = (it.nrows + 15) / 16;
+      for (int c = 0; c < kKParts; ++c, ++kn) {
+        if ((kn & 1) != me) continue;
+        if (!arm(qb * (kKDim / 64) * 2048)) break;
+        const uint32_t s = kn % kNK;
+        const int part = lane / 8, row = lane % 8;
+        if (lane < 8 * (kKDim / 64) && row < qb)
+          tma_load_2d(base + kOffK + s * kKStage + part * kQr + row * 2048, &tmQ,
+                      c * kKDim + part * 64,
+                      it.branch0 * p.Hq + it.row0 + row * 16,
+                      smem_u32(&bars.k_full[s / 2]));
+        __syncwarp();
+      }
+      for (int j = 0; j < nt && ok; ++j) {
+        const int phys = next;
+        bad = next_bad;
+        next = -1;
+        if (lane < kTB && j + 1 < nt)
+          next = block_of(p, it, blk + (j + 1) * kTB, next_bad);
+        if (bad && me == 0)
+          record_status(p.status, KV_ERR_DEVICE,
+                        p.tables[(int64_t)it.branch0 * p.max_blocks + blk + j * kTB]);
+        const int n = __popc(__ballot_sync(0xffffffffu, phys >= 0));
+        for (int c = 0; c < kKParts; ++c, ++kn) {
+          if ((kn & 1) != me) continue;
+          if (!arm(n * kKBox)) break;
+          const uint32_t s = kn % kNK;
           if (phys >= 0)
-            tma_load_5d_at(base + kOffK + s * kKStage +
-                               (half * (kTB / 2) + lane) * 4096,
-                           &tmK, 2 * c, phys, smem_u32(&bars.k_full[s]));
+            tma_load_5d_at(base + kOffK + s * kKStage + lane * kKBox, &tmK,
+                           c * (kKDim / 64), phys, smem_u32(&bars.k_full[s / 2]));
           __syncwarp();
         }
       }
@@ -553,42 +590,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       if (!ok) timed_out(35);
       for (uint32_t k = kn > kNK ? kn - kNK : 0; k < kn; ++k)
-        if (!mbar_wait(smem_u32(&bars.k_full[k % kNK]), (k / kNK) & 1)) break;
+        if ((k & 1) == me &&
+            !mbar_wait(smem_u32(&bars.k_full[k % kNK / 2]), (k / kNK) & 1))
+          break;
     }
   } else if (scores) {
-    // ---- score CTA, position keys (warp 11) --------------------------------
-    uint32_t tn = 0;
+    // ---- score CTA, position parts of Q and K (warp 11) ---------------------
+    uint32_t tn = 0, in = 0;
     bool ok = true;
     while (ok && loop.next(it)) {
       const int nt = n_tiles(it);
+      const int qb = (it.nrows + 15) / 16;
+      bool bad;
+      int next = lane < kTB ? block_of(p, it, it.blk_begin + lane, bad) : -1;
+      if (lane == 0) {
+        ok = !*aborted && (in == 0 || mbar_wait(smem_u32(&bars.qr_empty), (in - 1) & 1));
+        if (ok) mbar_expect_tx(smem_u32(&bars.qr_full), qb * 2048);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      ++in;
+      if (lane < qb)
+        tma_load_2d(base + lane * 2048, &tmQ, kRank,
+                    it.branch0 * p.Hq + it.row0 + lane * 16,
+                    smem_u32(&bars.qr_full));
+      __syncwarp();
       for (int j = 0; j < nt; ++j, ++tn) {
-        bool bad;
-        int phys = -1;
-        if (lane < kTB) phys = block_of(p, it, it.blk_begin + j * kTB + lane, bad);
+        const int phys = next;
+        next = -1;
+        if (lane < kTB && j + 1 < nt)
+          next = block_of(p, it, it.blk_begin + (j + 1) * kTB + lane, bad);
         const int n = __popc(__ballot_sync(0xffffffffu, phys >= 0));
-        const uint32_t s = tn % kNR;
         if (lane == 0) {
-          ok = !*aborted && (tn < kNR || mbar_wait(smem_u32(&bars.r_empty[s]),
-                                                   (tn / kNR - 1) & 1));
+          ok = !*aborted && (tn == 0 || mbar_wait(smem_u32(&bars.r_empty), (tn - 1) & 1));
           if (ok) {
             if (n > 0)
-              mbar_expect_tx(smem_u32(&bars.r_full[s]), n * 2048);
+              mbar_expect_tx(smem_u32(&bars.r_full), n * 2048);
             else
-              mbar_arrive(smem_u32(&bars.r_full[s]));
+              mbar_arrive(smem_u32(&bars.r_full));
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         if (phys >= 0)
-          tma_load_2d(base + kOffR + s * kRStage + lane * 2048, &tmR, 0, phys * 16,
-                      smem_u32(&bars.r_full[s]));
+          tma_load_2d(base + kOffR + lane * 2048, &tmR, 0, phys * 16,
+                      smem_u32(&bars.r_full));
         __syncwarp();
       }
     }
     if (lane == 0) {
       if (!ok) timed_out(36);
-      for (uint32_t k = tn > kNR ? tn - kNR : 0; k < tn; ++k)
-        if (!mbar_wait(smem_u32(&bars.r_full[k % kNR]), (k / kNR) & 1)) break;
+      report_bad(p, pair);
+      if (tn > 0) mbar_wait(smem_u32(&bars.r_full), (tn - 1) & 1);
+      if (in > 0) mbar_wait(smem_u32(&bars.qr_full), (in - 1) & 1);
     }
   } else if (warp < 8) {
     // ---- output CTA, rows: thread = (row r, half of the 512 columns) ---------
@@ -598,21 +652,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem + ((uint32_t)((warp & 3) * 32) << 16) + wg * (kRank / 2);
     uint32_t ev = 0, fin_n = 0;
     bool ok = true;
-    if (threadIdx.x == 0) {
-      mbar_expect_tx(smem_u32(&bars.fin_full[0]), 512);
-      mbar_expect_tx(smem_u32(&bars.fin_full[1]), 512);
-    }
     while (ok && loop.next(it)) {
       for (;;) {
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.event), ev & 1));
+        ok = warp_wait(smem_u32(&bars.event), ev & 1, lane);
         if (!ok) break;
         ++ev;
         fence_after_sync();
-        const int slot = *(volatile int*)&event_sh;
+        const int slot = *(volatile int*)&bars.event_what;
         if (slot < 0) break;
         // A maximum moved: this row of O times its factor.
         const float alpha =
-            reinterpret_cast<const float*>(base_ptr + kOffHdr + slot * kHdrStride)[r];
+            reinterpret_cast<const float*>(smem + kOffHdr + slot * kHdr)[r];
 #pragma unroll 1
         for (int c = 0; c < kRank / 2; c += 32) {
           uint32_t v[32];
@@ -634,10 +684,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float inv = 1.f;
       if (direct) {
         const int f = fin_n & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&bars.fin_full[f]),
-                                                       (fin_n >> 1) & 1));
+        ok = warp_wait_cluster(smem_u32(&bars.fin_full[f]), (fin_n >> 1) & 1, lane);
         if (!ok) break;
-        inv = reinterpret_cast<const float*>(base_ptr + kOffFin + f * 512)[r];
+        inv = reinterpret_cast<const float*>(smem + kOffFin + f * 512)[r];
         ++fin_n;
         // The factors are in registers: once every row warp says so, the slot
         // (armed again by the first) may be filled for the item after next.
@@ -647,35 +696,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           remote_arrive(map_rank(smem_u32(&bars.fin_empty[f]), 0));
         }
       }
-      const int64_t row = (int64_t)it.branch0 * p.Hq + it.row0 + r;
-#pragma unroll 1
-      for (int c = 0; c < kRank / 2; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(orow + c, v);
-        tmem_wait_ld();
-        const int col = wg * (kRank / 2) + c;
-        if (r >= it.nrows) {
-          // A row past the item's: its MMA row is padding.
-        } else if (direct) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * kRank + col);
+      // A warp turns 32 rows x 64 bytes at a time in its 2 KB of shared memory
+      // (16-byte pieces swizzled by the row), so that a store covers whole
+      // sectors of eight rows instead of 16-byte pieces of 32 (128 rows of
+      // partial results took 10 us that way).
+      const int wrow = (warp & 3) * 32;          // the warp's first row
+      if (wrow < it.nrows) {
+        uint8_t* turn = smem + kOffTurn + warp * 2048;
+        const int n = min(32, it.nrows - wrow);
+        uint8_t* dst = direct
+            ? reinterpret_cast<uint8_t*>(
+                  p.out + ((int64_t)it.branch0 * p.Hq + it.row0 + wrow) * kRank +
+                  wg * (kRank / 2))
+            : reinterpret_cast<uint8_t*>(
+                  p.o + ((int64_t)it.prow_base + wrow) * kRank + wg * (kRank / 2));
+        const int pitch = direct ? kRank * 2 : kRank * 4;  // bytes of a row
+        auto put = [&](const uint32_t (&w)[16]) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(
+                turn + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf16(__uint_as_float(v[8 * i + 2 * k]) * inv,
-                               __uint_as_float(v[8 * i + 2 * k + 1]) * inv);
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 4; ++k) {
+            const int rr = k * 8 + (lane >> 2), c = lane & 3;
+            const uint4 x = *reinterpret_cast<const uint4*>(
+                turn + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+            if (rr < n)
+              *reinterpret_cast<uint4*>(dst + (int64_t)rr * pitch + c * 16) = x;
           }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(
-              p.o + (int64_t)(it.prow_base + r) * kRank + col);
+          dst += 64;
+          __syncwarp();
+        };
+#pragma unroll 1
+        for (int c = 0; c < kRank / 2; c += 32) {
+          uint32_t v[32], w[16];
+          tmem_ld32(orow + c, v);
+          tmem_wait_ld();
+          if (direct) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(v[4 * i]),
-                                 __uint_as_float(v[4 * i + 1]),
-                                 __uint_as_float(v[4 * i + 2]),
-                                 __uint_as_float(v[4 * i + 3]));
+            for (int i = 0; i < 16; ++i)
+              w[i] = pack_bf16(__uint_as_float(v[2 * i]) * inv,
+                               __uint_as_float(v[2 * i + 1]) * inv);
+            put(w);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = v[h * 16 + i];
+              put(w);
+            }
+          }
         }
       }
       fence_before_sync();
@@ -683,101 +755,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&bars.o_ok));
     }
     if (!ok && lane == 0) timed_out(40);
-  } else if (warp == kMmaWarp) {
-    // ---- output CTA, products ------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t id = idesc(128, 256, true);
-      uint32_t g = 0, vn = 0, ev = 0, fixes = 0;
-      bool ok = true;
-      auto event = [&](int what) {
-        *(volatile int*)&event_sh = what;
+  } else if (warp == kMmaWarp || warp == 11) {
+    // ---- output CTA, products (uniform warps, one lane issues): warp 8 the
+    // first 256 columns of O, warp 11 the others.  A warp waits about half of
+    // the time that its products take; two keep the tensor pipe busy.
+    const int oh = warp == kMmaWarp ? 0 : 1;
+    constexpr uint32_t id = idesc(128, 256, true);
+    const bool lead = elect_one();
+    uint32_t g = 0, vn = 0, ev = 0, fixes = 0;
+    bool ok = true;
+    // Once every product so far is done, the rows act: rescale O with the
+    // factors in P slot `what`, or (-1) write the item's result.
+    auto event = [&](int what) {
+      if (lead) {
+        if (oh == 0) *(volatile int*)&bars.event_what = what;
         mbar_arrive(smem_u32(&bars.event));
         umma_commit(smem_u32(&bars.event));
-        const bool done = mbar_wait(smem_u32(&bars.o_ok), ev & 1);
-        ++ev;
-        fence_after_sync();
-        return done;
-      };
-      while (ok && loop.next(it)) {
-        const int nblk = it.blk_end - it.blk_begin;
-        const int tail = it.masked ? p.seq_lens[it.branch0] - (it.blk_end - 1) * 16 : 16;
-        for (int k0 = 0; k0 < nblk && ok; k0 += kGB, ++g) {
-          const uint32_t slot = g % kNP;
-          ok = mbar_wait_cluster(smem_u32(&bars.p_full[slot]), (g / kNP) & 1);
-          if (!ok) break;
-          if (k0 > 0 && k0 % kTB == 0 &&
-              *reinterpret_cast<volatile uint32_t*>(base_ptr + kOffHdr +
-                                                    slot * kHdrStride + 512)) {
+      }
+      __syncwarp();
+      const bool done = all_wait(smem_u32(&bars.o_ok), ev & 1);
+      ++ev;
+      fence_after_sync();
+      return done;
+    };
+    while (ok && loop.next(it)) {
+      const int nblk = uniform(it.blk_end - it.blk_begin);
+      const int tail =
+          uniform(it.masked ? p.seq_lens[it.branch0] - (it.blk_end - 1) * 16 : 16);
+      for (int k0 = 0; k0 < nblk && ok; k0 += kGB, ++g) {
+        const uint32_t slot = g % kNP;
+        ok = all_wait_cluster(smem_u32(&bars.p_full[slot]), (g / kNP) & 1);
+        if (!ok) break;
+        // Arm the slot's next phase; P came as ordinary stores.
+        if (lead && oh == 0)
+          mbar_expect_tx(smem_u32(&bars.p_full[slot]), kP + kHdr);
+        fence_proxy_async_smem();
+        if (k0 > 0 && k0 % kTB == 0) {
+          const int f = lane < 4 ? *reinterpret_cast<volatile int*>(
+                                       smem + kOffHdr + slot * kHdr + 512 + lane * 4)
+                                 : 0;
+          if (__any_sync(0xffffffffu, f != 0)) {
             ok = event((int)slot);
             if (!ok) break;
           }
-          const uint32_t pst = base + kOffP + slot * kP;
-          const int nk = min(kGB, nblk - k0);
-          for (int k = 0; k < nk && ok; ++k, ++vn) {
-            const uint32_t s = vn % kNV;
-            ok = mbar_wait(smem_u32(&bars.v_full[s]), (vn / kNV) & 1);
-            if (ok && k0 + k == nblk - 1 && tail < 16) {
-              ok = mbar_wait(smem_u32(&bars.v_fix[s]), (fixes >> s) & 1);
-              fixes ^= 1u << s;  // the stage's next fix has the other parity
-            }
-            if (!ok) break;
-            fence_after_sync();
-            const uint32_t vst = base + s * kVBlk;
-            const uint64_t a = sdesc(pst + k * 32, 16, 1024);
+        }
+        const uint64_t pd = sdesc_plain(base + kOffP + slot * kP, kPChunk, 128);
+        const int nk = min(kGB, nblk - k0);
+        const int ns = (nk + kVB - 1) / kVB;
+        // All of the P tile's V first, so that its products are issued
+        // without a pause (a wait costs the warp as much as an MMA or two).
+        for (int k = 0; k < ns && ok; ++k)
+          ok = all_wait(smem_u32(&bars.v_full[(vn + k) % kNV]),
+                        ((vn + k) / kNV) & 1);
+        if (ok && k0 + nk == nblk && tail < 16) {
+          const uint32_t s = (vn + ns - 1) % kNV;
+          ok = all_wait(smem_u32(&bars.v_fix[s]), (fixes >> s) & 1);
+          fixes ^= 1u << s;  // the stage's next fix has the other parity
+        }
+        if (!ok) break;
+        fence_after_sync();
+        if (lead) {
+#pragma unroll
+          for (int k = 0; k < kGB; ++k) {
+            if (k >= nk) break;
+            const uint32_t s = (vn + k / kVB) % kNV;
+            const uint64_t vd =
+                sdesc(base + s * kVStage + (k % kVB) * kVBlk + oh * 4096, 1024,
+                      8192);
             const uint32_t acc = (k0 > 0 || k > 0) ? 1u : 0u;
-            umma_ss(tmem, a, sdesc(vst, 1024, 8192), id, acc);
-            umma_ss(tmem + 256, a, sdesc(vst + 4096, 1024, 8192), id, acc);
-            umma_commit(smem_u32(&bars.v_empty[s]));
+            umma_ss(tmem + oh * 256, pd + k * (2 * kPChunk >> 4), vd, id, acc);
+            if (k % kVB == kVB - 1 || k == nk - 1)
+              umma_commit(smem_u32(&bars.v_empty[s]));
           }
           // The other CTA may refill the slot.
           umma_commit_to(smem_u32(&bars.p_empty[slot]), 1);
         }
-        if (ok) ok = event(-1);
-        ok = ok && !*aborted;
+        __syncwarp();
+        vn += ns;
       }
+      if (ok) ok = event(-1);
+      ok = ok && !*aborted;
+    }
+    if (lead) {
       if (!ok) timed_out(41);
-      umma_commit(smem_u32(&bars.drain));
-      mbar_wait(smem_u32(&bars.drain), 0);
+      umma_commit(smem_u32(&bars.drain[oh]));
+      mbar_wait(smem_u32(&bars.drain[oh]), 0);
     }
   } else if (warp < 11) {
-    // ---- output CTA, V: blocks alternate between warps 9 and 10 -------------
+    // ---- output CTA, V: stages of two blocks alternate between warps 9 and 10
     const uint32_t me = warp - 9;
     uint32_t vn = 0;
     bool ok = true;
     while (ok && loop.next(it)) {
       const int nblk = it.blk_end - it.blk_begin;
-      const int tail = it.masked ? p.seq_lens[it.branch0] - (it.blk_end - 1) * 16 : 16;
+      const int tail = max(
+          it.masked ? p.seq_lens[it.branch0] - (it.blk_end - 1) * 16 : 16, 0);
       for (int k0 = 0; k0 < nblk && ok; k0 += 32) {
         bool bad;
-        const int mineb = block_of(p, it, it.blk_begin + k0 + lane, bad);
+        const int ids = block_of(p, it, it.blk_begin + k0 + lane, bad);
         const int n = min(32, nblk - k0);
-        for (int k = 0; k < n; ++k, ++vn) {
-          const int phys = __shfl_sync(0xffffffffu, mineb, k);
+        for (int k = 0; k < n; k += kVB, ++vn) {
+          const int phys = __shfl_sync(0xffffffffu, ids, (k + lane) & 31);
           if ((vn & 1) != me) continue;
           const uint32_t s = vn % kNV;
           const uint32_t bar = smem_u32(&bars.v_full[s]);
+          const bool load = lane < kVB && k + lane < n && phys >= 0;
+          const int n_load = __popc(__ballot_sync(0xffffffffu, load));
           if (lane == 0) {
             ok = !*aborted && (vn < kNV || mbar_wait(smem_u32(&bars.v_empty[s]),
                                                      (vn / kNV - 1) & 1));
             if (ok) {
-              if (phys >= 0) {
-                mbar_expect_tx(bar, kVBlk);
-                tma_load_5d_at(base + s * kVBlk, &tmV, 0, phys, bar);
-              } else {
+              if (n_load > 0)
+                mbar_expect_tx(bar, n_load * kVBlk);
+              else
                 mbar_arrive(bar);
-              }
             }
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          if (k0 + k == nblk - 1 && tail < 16) {
-            // Rows past the branch's length: zero.
-            ok = __all_sync(0xffffffffu, mbar_wait(bar, (vn / kNV) & 1));
+          if (load)
+            tma_load_5d_at(base + s * kVStage + lane * kVBlk, &tmV, 0, phys, bar);
+          __syncwarp();
+          if (k0 + k + kVB >= nblk && tail < 16) {
+            // Rows of the last block past the branch's length: zero.
+            ok = warp_wait(bar, (vn / kNV) & 1, lane);
             if (!ok) break;
-            for (int i = lane; i < (16 - max(tail, 0)) * 64; i += 32) {
-              const int row = max(tail, 0) + (i >> 6), c = i & 63;
-              st_shared_zero16(base + s * kVBlk + (row >> 3) * 8192 +
-                               (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16);
+            const uint32_t blk = base + s * kVStage + ((nblk - 1 - k0 - k)) * kVBlk;
+            for (int i = lane; i < (16 - tail) * 64; i += 32) {
+              const int row = tail + (i >> 6), c = i & 63;
+              st_shared_zero16(blk + (row >> 3) * 8192 + (c >> 3) * 1024 +
+                               (row & 7) * 128 + (c & 7) * 16);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -793,27 +900,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if ((k & 1) == me &&
             !mbar_wait(smem_u32(&bars.v_full[k % kNV]), (k / kNV) & 1))
           break;
-    }
-  } else {
-    // ---- output CTA, arrivals of P (warp 11): arm each slot ahead of its
-    // copies, and tell the score CTA that its staging tile is free again.
-    if (lane == 0) {
-      const uint32_t ack = map_rank(smem_u32(&bars.p_ack[0]), 0);
-      for (int s = 0; s < kNP; ++s)
-        mbar_expect_tx(smem_u32(&bars.p_full[s]), kP + kHdr);
-      uint32_t g = 0;
-      bool ok = true;
-      while (ok && loop.next(it)) {
-        const int nblk = it.blk_end - it.blk_begin;
-        for (int k0 = 0; k0 < nblk; k0 += kGB, ++g) {
-          const uint32_t slot = g % kNP;
-          ok = mbar_wait_cluster(smem_u32(&bars.p_full[slot]), (g / kNP) & 1);
-          if (!ok) break;
-          mbar_expect_tx(smem_u32(&bars.p_full[slot]), kP + kHdr);
-          remote_arrive(ack + ((k0 / kGB) & 1) * 8);
-        }
-      }
-      if (!ok) timed_out(43);
     }
   }
   __syncwarp();
@@ -848,6 +934,9 @@ struct MergeArgs {
 __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  // Launched while the attention kernel runs; its results are complete and
+  // visible from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (w >= (int64_t)a.n * a.Hq) return;
   const int b = a.branches[w / a.Hq], r = (int)(w % a.Hq);
   if (b < 0 || b >= a.nb) return;
@@ -900,12 +989,13 @@ kv_status make_latent_map(CUtensorMap* tm, const void* pool, int64_t blocks,
   return encode_bf16_map(tm, pool, 5, dims, strides, box);
 }
 
-// The position keys: rows of 64, boxes of a block (16 rows).
-kv_status make_rope_map(CUtensorMap* tm, const void* pool, int64_t blocks) {
-  const cuuint64_t dims[2] = {64, (cuuint64_t)blocks * 16};
-  const cuuint64_t strides[1] = {128};
+// Rows of `width` values in boxes of 16 rows x 64 values (a block's position
+// keys, or 16 query rows).
+kv_status make_rows_map(CUtensorMap* tm, const void* base, int64_t rows, int width) {
+  const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)width * 2};
   const cuuint32_t box[2] = {64, 16};
-  return encode_bf16_map(tm, pool, 2, dims, strides, box);
+  return encode_bf16_map(tm, base, 2, dims, strides, box);
 }
 
 }  // namespace lat
@@ -953,10 +1043,13 @@ extern "C" kv_status paged_latent_decode_attn(
   if (ws_bytes < need || (size_t)info->workspace_bytes != need)
     return fail(KV_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", ws_bytes,
                 need);
-  CUtensorMap tk, tv, tr;
-  if (kv_status s = lat::make_latent_map(&tk, c_pool, num_blocks, 2)) return s;
+  CUtensorMap tk, tv, tr, tq;
+  if (kv_status s = lat::make_latent_map(&tk, c_pool, num_blocks, lat::kKDim / 64)) return s;
   if (kv_status s = lat::make_latent_map(&tv, c_pool, num_blocks, 8)) return s;
-  if (kv_status s = lat::make_rope_map(&tr, r_pool, num_blocks)) return s;
+  if (kv_status s = lat::make_rows_map(&tr, r_pool, num_blocks * 16, rope_dim))
+    return s;
+  if (kv_status s = lat::make_rows_map(&tq, q, (int64_t)nb * Hq, rank + rope_dim))
+    return s;
   const int64_t off_item = pkv::kPlanHeaderInts;
   const int64_t off_pair = off_item + 8 * (int64_t)info->n_tile_items;
   const int64_t off_merge = off_pair + info->n_tile_wide_items + 1;
@@ -965,7 +1058,8 @@ extern "C" kv_status paged_latent_decode_attn(
   auto* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = (cudaStream_t)stream;
   lat::Params p;
-  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.c_pool = static_cast<const uint8_t*>(c_pool);
+  p.r_pool = static_cast<const uint8_t*>(r_pool);
   p.tables = block_tables;
   p.seq_lens = seq_lens;
   p.items = reinterpret_cast<const pkv::WorkItem*>(plan + off_item);
@@ -988,7 +1082,7 @@ extern "C" kv_status paged_latent_decode_attn(
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "latent step: %s", cudaGetErrorString(e));
   lat::latent_decode_kernel<<<2 * p.n_pairs, lat::kThreads, lat::kSmem, st>>>(
-      tk, tv, tr, p);
+      tk, tv, tr, tq, p);
   e = cudaGetLastError();
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "latent kernel: %s", cudaGetErrorString(e));
@@ -1005,8 +1099,16 @@ extern "C" kv_status paged_latent_decode_attn(
     m.Hq = Hq;
     m.partial_rows = p.partial_rows;
     const int64_t warps = (int64_t)m.n * Hq;
-    lat::latent_merge_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(m);
-    e = cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, lat::latent_merge_kernel, m);
     if (e != cudaSuccess)
       return fail(KV_ERR_CUDA, "latent merge: %s", cudaGetErrorString(e));
   }
