@@ -123,9 +123,9 @@ constexpr int kOffTurn = (kOffFin + 2 * 512 + 127) & ~127;  // 2 KB a row warp
 constexpr int kOutSmem = kOffTurn + 8 * 2048;
 constexpr int kTiles = kScoreSmem > kOutSmem ? kScoreSmem : kOutSmem;
 
-constexpr int kThreads = 12 * 32;
+constexpr int kThreads = 13 * 32;
 constexpr int kRowThreads = 256;             // warps 0-7
-constexpr int kMmaWarp = 8;                  // warps 9-11 load (11: see below)
+constexpr int kMmaWarp = 8;                  // with 12 (score) or 11 (output CTA)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 256;              // score CTA: Q 0..255, S 256..511
 constexpr float kRescale = 8.f;              // lazy-max threshold (log2 units)
@@ -149,12 +149,12 @@ struct Params {
 // Barriers and small arrays, behind the tiles; at the same place in both CTAs.
 struct Small {
   // score CTA
-  uint64_t k_full[kNK / 2], k_empty[kNK], r_full, r_empty;
-  uint64_t qr_full, qr_empty, q_free, s_full[2], s_empty[2];
+  uint64_t k_full[kNK / 2], k_empty[kNK], r_full[2], r_empty;
+  uint64_t qr_full, qr_empty, q_ready, q_free, turn[2], s_full[2], s_empty[2];
   uint64_t p_empty[kNP];   // the other side has consumed P slot i
   uint64_t fin_empty[2];
   // output CTA
-  uint64_t v_full[kNV], v_empty[kNV], v_fix[kNV], p_full[kNP], fin_full[2];
+  uint64_t v_full[kNV / 2], v_empty[kNV], v_fix[kNV], p_full[kNP], fin_full[2];
   uint64_t event, o_ok;
   uint64_t drain[2];
   uint32_t tmem_base;
@@ -231,6 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ CUtensorMap tmR,
                          const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmQall,
                          const Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Small& bars = *reinterpret_cast<Small*>(smem + kTiles);
@@ -251,12 +252,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars.k_full[s / 2]), 2);  // both producer warps
       mbar_init(smem_u32(&bars.k_empty[s]), 1);
     }
-    mbar_init(smem_u32(&bars.r_full), 1);
     mbar_init(smem_u32(&bars.r_empty), 1);
     mbar_init(smem_u32(&bars.qr_full), 1);
-    mbar_init(smem_u32(&bars.qr_empty), 1);
-    mbar_init(smem_u32(&bars.q_free), 1);
+    mbar_init(smem_u32(&bars.qr_empty), 2);      // both product warps
+    mbar_init(smem_u32(&bars.q_ready), 1);
+    mbar_init(smem_u32(&bars.q_free), 2);
     for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&bars.r_full[b]), 1);
+      mbar_init(smem_u32(&bars.turn[b]), 1);
       mbar_init(smem_u32(&bars.s_full[b]), 1);
       mbar_init(smem_u32(&bars.s_empty[b]), 8);
       mbar_init(smem_u32(&bars.fin_empty[b]), 8);  // the other side's row warps
@@ -267,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars.p_full[s]), 1);
     }
     for (int s = 0; s < kNV; ++s) {
-      mbar_init(smem_u32(&bars.v_full[s]), 1);
+      mbar_init(smem_u32(&bars.v_full[s / 2]), 2);  // both producer warps
       mbar_init(smem_u32(&bars.v_empty[s]), 2);
       mbar_init(smem_u32(&bars.v_fix[s]), 1);    // masked rows zeroed
     }
@@ -288,6 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmR);
     tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmQall);
   }
   if (warp == kMmaWarp) {
     asm volatile(
@@ -298,7 +302,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::
                      : "memory");
   }
-  ItemLoop loop(p, pair);  // its loads overlap the set-up
+  // Launched early (the status word is being cleared): no global memory before
+  // this point.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  ItemLoop loop(p, pair);
   fence_before_sync();
   __syncthreads();
   cluster_sync();  // the other CTA's barriers are ready too
@@ -441,43 +448,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!mbar_wait_cluster(smem_u32(&bars.fin_empty[f & 1]), (f / 2) & 1))
           break;
     }
-  } else if (scores && warp == kMmaWarp) {
-    // ---- score CTA, products (the warp runs uniformly, one lane issues) ------
+  } else if (scores && (warp == kMmaWarp || warp == 12)) {
+    // ---- score CTA, products (uniform warps, one lane issues): warp 8 the even
+    // tiles (S buffer 0), warp 12 the odd ones, so that one warp's waits lie
+    // behind the other's products.  A warp waits for K only in its turn (the
+    // other has seen all of the stages before), which also keeps each
+    // barrier's phases unambiguous.
     constexpr uint32_t id = idesc(128, kT, false);
     const bool lead = elect_one();
-    uint32_t tn = 0, kn = 0, in = 0;
+    const uint32_t w = warp == kMmaWarp ? 0 : 1;
+    const uint32_t d = tmem + kColS + w * kT;
+    uint32_t tn = 0, kp = 0, in = 0, turns = 0;  // tiles, pairs of stages, items
     bool ok = true;
+    auto wait_pair = [&](uint32_t q) {
+      const bool got = all_wait(smem_u32(&bars.k_full[q % (kNK / 2)]),
+                                (q / (kNK / 2)) & 1);
+      fence_after_sync();
+      return got;
+    };
     while (ok && loop.next(it)) {
       const int nt = uniform(n_tiles(it));
-      // Q: its latent part comes through the K ring and is copied to TMEM
-      // once the previous item's products have read theirs.
+      const bool first = (tn & 1) == w;
+      // The previous item's products have read their Q.
       if (in > 0) ok = all_wait(smem_u32(&bars.q_free), (in - 1) & 1);
-      for (int c = 0; c < kKParts && ok; ++c, ++kn) {
-        const uint32_t s = kn % kNK;
-        if (c % 2 == 0) {
-          ok = all_wait(smem_u32(&bars.k_full[s / 2]), (kn / kNK) & 1);
-          if (!ok) break;
-          fence_after_sync();
-        }
-        const uint64_t src = sdesc(base + kOffK + s * kKStage, 16, 1024);
-        if (lead) {
+      if (first) {
+        // The warp of the item's first tile brings Q: its latent part comes
+        // through the K ring and is copied to TMEM.
+        for (int c = 0; c < kKParts / 2 && ok; ++c) {
+          ok = wait_pair(kp + c);
+          const uint32_t s = 2 * ((kp + c) % (kNK / 2));
+          if (ok && lead) {
 #pragma unroll
-          for (int kk = 0; kk < kKDim / 16; ++kk)
-            umma_copy(tmem + c * (kKDim / 2) + kk * 8,
-                      src + (((kk >> 2) * kQr + (kk & 3) * 32) >> 4));
-          umma_commit(smem_u32(&bars.k_empty[s]));
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t src = sdesc(base + kOffK + (s + h) * kKStage, 16, 1024);
+#pragma unroll
+              for (int kk = 0; kk < kKDim / 16; ++kk)
+                umma_copy(tmem + (c * 2 + h) * (kKDim / 2) + kk * 8,
+                          src + (((kk >> 2) * kQr + (kk & 3) * 32) >> 4));
+              umma_commit(smem_u32(&bars.k_empty[s + h]));
+            }
+          }
+          __syncwarp();
         }
+        if (lead) umma_commit(smem_u32(&bars.q_ready));
         __syncwarp();
+      } else if (ok) {
+        ok = all_wait(smem_u32(&bars.q_ready), in & 1);
       }
       if (ok) ok = all_wait(smem_u32(&bars.qr_full), in & 1);
-      ++in;
-      for (int j = 0; j < nt && ok; ++j, ++tn) {
-        const int b = tn & 1;
-        if (tn >= 2) ok = all_wait(smem_u32(&bars.s_empty[b]), ((tn >> 1) - 1) & 1);
-        const uint32_t d = tmem + kColS + b * kT;
-        // The position part first: after the last tile's, the next item's
-        // may be loaded.
-        ok = ok && all_wait(smem_u32(&bars.r_full), tn & 1);
+      fence_after_sync();
+      for (int j = first ? 0 : 1; j < nt && ok; j += 2) {
+        const uint32_t t = (tn + j) >> 1;  // this warp's tiles so far
+        if (t > 0) ok = all_wait(smem_u32(&bars.s_empty[w]), (t - 1) & 1);
+        // The position part first; after the item's last, the next item's may
+        // be loaded.
+        ok = ok && all_wait(smem_u32(&bars.r_full[w]), t & 1);
         if (!ok) break;
         fence_after_sync();
         const uint64_t qd = sdesc(base, 16, 1024);
@@ -487,40 +512,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             umma_ss(d, qd + kk * 2, rd + kk * 2, id, kk > 0 ? 1u : 0u);
           umma_commit(smem_u32(&bars.r_empty));
-          if (j == nt - 1) umma_commit(smem_u32(&bars.qr_empty));
+          if (j + 2 >= nt) umma_commit(smem_u32(&bars.qr_empty));
         }
         __syncwarp();
-        for (int c = 0; c < kKParts; ++c, ++kn) {
-          const uint32_t s = kn % kNK;
-          if (c % 2 == 0) {
-            ok = all_wait(smem_u32(&bars.k_full[s / 2]), (kn / kNK) & 1);
-            if (!ok) break;
-            fence_after_sync();
-          }
-          const uint64_t kd = sdesc(base + kOffK + s * kKStage, 16, kKBox / 2);
-          const uint32_t qa = tmem + c * (kKDim / 2);
+        if (j > 0) {
+          ok = all_wait(smem_u32(&bars.turn[w]), turns & 1);
+          ++turns;
+        }
+        for (int c = 0; c < kKParts / 2 && ok; ++c) {
+          const uint32_t q = kp + (1 + j) * (kKParts / 2) + c;
+          ok = wait_pair(q);
+          if (!ok) break;
+          const uint32_t s = 2 * (q % (kNK / 2));
           if (lead) {
+            if (c == kKParts / 2 - 1 && j + 1 < nt)
+              mbar_arrive(smem_u32(&bars.turn[w ^ 1]));
 #pragma unroll
-            for (int kk = 0; kk < kKDim / 16; ++kk)
-              umma_ts(d, qa + kk * 8,
-                      kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id, 1u);
-            umma_commit(smem_u32(&bars.k_empty[s]));
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t kd =
+                  sdesc(base + kOffK + (s + h) * kKStage, 16, kKBox / 2);
+              const uint32_t qa = tmem + (c * 2 + h) * (kKDim / 2);
+#pragma unroll
+              for (int kk = 0; kk < kKDim / 16; ++kk)
+                umma_ts(d, qa + kk * 8,
+                        kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id, 1u);
+              umma_commit(smem_u32(&bars.k_empty[s + h]));
+            }
           }
           __syncwarp();
         }
         if (!ok) break;
-        if (lead) {
-          umma_commit(smem_u32(&bars.s_full[b]));
-          if (j == nt - 1) umma_commit(smem_u32(&bars.q_free));
-        }
+        if (lead) umma_commit(smem_u32(&bars.s_full[w]));
         __syncwarp();
       }
-      ok = ok && !*aborted;
+      if (!ok) break;
+      if (lead) {
+        if (first || nt > 1) {
+          umma_commit(smem_u32(&bars.q_free));
+        } else {  // no tile of this item was this warp's
+          mbar_arrive(smem_u32(&bars.qr_empty));
+          mbar_arrive(smem_u32(&bars.q_free));
+        }
+      }
+      __syncwarp();
+      ++in;
+      tn += nt;
+      kp += (1 + nt) * (kKParts / 2);
+      ok = !*aborted;
     }
     if (lead) {
       if (!ok) timed_out(34);
-      umma_commit(smem_u32(&bars.drain[0]));
-      mbar_wait(smem_u32(&bars.drain[0]), 0);
+      umma_commit(smem_u32(&bars.drain[w]));
+      mbar_wait(smem_u32(&bars.drain[w]), 0);
     }
   } else if (scores && warp < 11) {
     // ---- score CTA, K: warps 9 and 10 take every other stage; one box is a
@@ -551,16 +594,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // A tile's block ids are read while the one before waits for its stages.
       bool bad = false, next_bad = false;
       int next = lane < kTB ? block_of(p, it, blk, next_bad) : -1;
-      // Q comes first, as stages of 128 rows x 128 dimensions in boxes of 16
-      // rows x 64.
-      const int qb = (it.nrows + 15) / 16;
+      // Q comes first, as stages of 128 rows x 128 dimensions in boxes of 64
+      // dimensions and 16 rows, or of 128 rows for an item with more than 64
+      // (the rows behind the item's are computed on and not stored).
+      const bool tall = it.nrows > 64;
+      const int qb = tall ? 8 : (it.nrows + 15) / 16;
       for (int c = 0; c < kKParts; ++c, ++kn) {
         if ((kn & 1) != me) continue;
         if (!arm(qb * (kKDim / 64) * 2048)) break;
         const uint32_t s = kn % kNK;
         const int part = lane / 8, row = lane % 8;
-        if (lane < 8 * (kKDim / 64) && row < qb)
-          tma_load_2d(base + kOffK + s * kKStage + part * kQr + row * 2048, &tmQ,
+        if (lane < 8 * (kKDim / 64) && row < (tall ? 1 : qb))
+          tma_load_2d(base + kOffK + s * kKStage + part * kQr + row * 2048,
+                      tall ? &tmQall : &tmQ,
                       c * kKDim + part * 64,
                       it.branch0 * p.Hq + it.row0 + row * 16,
                       smem_u32(&bars.k_full[s / 2]));
@@ -625,23 +671,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = !*aborted && (tn == 0 || mbar_wait(smem_u32(&bars.r_empty), (tn - 1) & 1));
           if (ok) {
             if (n > 0)
-              mbar_expect_tx(smem_u32(&bars.r_full), n * 2048);
+              mbar_expect_tx(smem_u32(&bars.r_full[tn & 1]), n * 2048);
             else
-              mbar_arrive(smem_u32(&bars.r_full));
+              mbar_arrive(smem_u32(&bars.r_full[tn & 1]));
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         if (phys >= 0)
           tma_load_2d(base + kOffR + lane * 2048, &tmR, 0, phys * 16,
-                      smem_u32(&bars.r_full));
+                      smem_u32(&bars.r_full[tn & 1]));
         __syncwarp();
       }
     }
     if (lane == 0) {
       if (!ok) timed_out(36);
       report_bad(p, pair);
-      if (tn > 0) mbar_wait(smem_u32(&bars.r_full), (tn - 1) & 1);
+      if (tn > 0)
+        mbar_wait(smem_u32(&bars.r_full[(tn - 1) & 1]), ((tn - 1) >> 1) & 1);
       if (in > 0) mbar_wait(smem_u32(&bars.qr_full), (in - 1) & 1);
     }
   } else if (warp < 8) {
@@ -762,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int oh = warp == kMmaWarp ? 0 : 1;
     constexpr uint32_t id = idesc(128, 256, true);
     const bool lead = elect_one();
-    uint32_t g = 0, vn = 0, ev = 0, fixes = 0;
+    uint32_t g = 0, ev = 0, fixes = 0;
     bool ok = true;
     // Once every product so far is done, the rows act: rescale O with the
     // factors in P slot `what`, or (-1) write the item's result.
@@ -801,14 +848,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const uint64_t pd = sdesc_plain(base + kOffP + slot * kP, kPChunk, 128);
         const int nk = min(kGB, nblk - k0);
-        const int ns = (nk + kVB - 1) / kVB;
-        // All of the P tile's V first, so that its products are issued
-        // without a pause (a wait costs the warp as much as an MMA or two).
-        for (int k = 0; k < ns && ok; ++k)
-          ok = all_wait(smem_u32(&bars.v_full[(vn + k) % kNV]),
-                        ((vn + k) / kNV) & 1);
+        // All of the P tile's V (a pair of stages) first, so that its products
+        // are issued without a pause.
+        ok = all_wait(smem_u32(&bars.v_full[g % (kNV / 2)]), (g / (kNV / 2)) & 1);
+        const uint32_t v0 = 2 * (g % (kNV / 2));  // its first stage
         if (ok && k0 + nk == nblk && tail < 16) {
-          const uint32_t s = (vn + ns - 1) % kNV;
+          const uint32_t s = v0 + (nk - 1) / kVB;
           ok = all_wait(smem_u32(&bars.v_fix[s]), (fixes >> s) & 1);
           fixes ^= 1u << s;  // the stage's next fix has the other parity
         }
@@ -817,21 +862,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lead) {
 #pragma unroll
           for (int k = 0; k < kGB; ++k) {
-            if (k >= nk) break;
-            const uint32_t s = (vn + k / kVB) % kNV;
-            const uint64_t vd =
-                sdesc(base + s * kVStage + (k % kVB) * kVBlk + oh * 4096, 1024,
-                      8192);
-            const uint32_t acc = (k0 > 0 || k > 0) ? 1u : 0u;
-            umma_ss(tmem + oh * 256, pd + k * (2 * kPChunk >> 4), vd, id, acc);
-            if (k % kVB == kVB - 1 || k == nk - 1)
-              umma_commit(smem_u32(&bars.v_empty[s]));
+            if (k < nk) {
+              const uint64_t vd = sdesc(base + (v0 + k / kVB) * kVStage +
+                                            (k % kVB) * kVBlk + oh * 4096,
+                                        1024, 8192);
+              umma_ss(tmem + oh * 256, pd + k * (2 * kPChunk >> 4), vd, id,
+                      (k0 > 0 || k > 0) ? 1u : 0u);
+            }
+            if (k % kVB == kVB - 1) umma_commit(smem_u32(&bars.v_empty[v0 + k / kVB]));
           }
           // The other CTA may refill the slot.
           umma_commit_to(smem_u32(&bars.p_empty[slot]), 1);
         }
         __syncwarp();
-        vn += ns;
       }
       if (ok) ok = event(-1);
       ok = ok && !*aborted;
@@ -842,63 +885,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_wait(smem_u32(&bars.drain[oh]), 0);
     }
   } else if (warp < 11) {
-    // ---- output CTA, V: stages of two blocks alternate between warps 9 and 10
+    // ---- output CTA, V: the two stages (of two blocks) of a P tile, warp 9 the
+    // first and warp 10 the second, empty or not.
     const uint32_t me = warp - 9;
-    uint32_t vn = 0;
+    uint32_t vn = 0;  // P tiles so far
     bool ok = true;
     while (ok && loop.next(it)) {
       const int nblk = it.blk_end - it.blk_begin;
       const int tail = max(
           it.masked ? p.seq_lens[it.branch0] - (it.blk_end - 1) * 16 : 16, 0);
-      for (int k0 = 0; k0 < nblk && ok; k0 += 32) {
-        bool bad;
-        const int ids = block_of(p, it, it.blk_begin + k0 + lane, bad);
-        const int n = min(32, nblk - k0);
-        for (int k = 0; k < n; k += kVB, ++vn) {
-          const int phys = __shfl_sync(0xffffffffu, ids, (k + lane) & 31);
-          if ((vn & 1) != me) continue;
-          const uint32_t s = vn % kNV;
-          const uint32_t bar = smem_u32(&bars.v_full[s]);
-          const bool load = lane < kVB && k + lane < n && phys >= 0;
-          const int n_load = __popc(__ballot_sync(0xffffffffu, load));
-          if (lane == 0) {
-            ok = !*aborted && (vn < kNV || mbar_wait(smem_u32(&bars.v_empty[s]),
-                                                     (vn / kNV - 1) & 1));
-            if (ok) {
-              if (n_load > 0)
-                mbar_expect_tx(bar, n_load * kVBlk);
-              else
-                mbar_arrive(bar);
-            }
+      const int blk = it.blk_begin + me * kVB + lane;
+      bool bad;
+      int next = lane < kVB ? block_of(p, it, blk, bad) : -1;
+      for (int k0 = 0; k0 < nblk && ok; k0 += kGB, ++vn) {
+        const int phys = next;
+        next = lane < kVB && k0 + kGB < nblk ? block_of(p, it, blk + k0 + kGB, bad)
+                                             : -1;
+        const uint32_t s = 2 * (vn % (kNV / 2)) + me;
+        const uint32_t use = vn / (kNV / 2);  // earlier uses of the stage
+        const uint32_t bar = smem_u32(&bars.v_full[s / 2]);
+        const int n_load = __popc(__ballot_sync(0xffffffffu, phys >= 0));
+        if (lane == 0) {
+          ok = !*aborted &&
+               (use == 0 || mbar_wait(smem_u32(&bars.v_empty[s]), (use - 1) & 1));
+          if (ok) {
+            if (n_load > 0)
+              mbar_expect_tx(bar, n_load * kVBlk);
+            else
+              mbar_arrive(bar);
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (phys >= 0)
+          tma_load_5d_at(base + s * kVStage + lane * kVBlk, &tmV, 0, phys, bar);
+        __syncwarp();
+        const int last = nblk - 1 - k0 - me * kVB;  // the last block's place here
+        if (tail < 16 && last >= 0 && last < kVB) {
+          // Rows of the last block past the branch's length: zero.
+          ok = warp_wait(bar, use & 1, lane);
           if (!ok) break;
-          if (load)
-            tma_load_5d_at(base + s * kVStage + lane * kVBlk, &tmV, 0, phys, bar);
-          __syncwarp();
-          if (k0 + k + kVB >= nblk && tail < 16) {
-            // Rows of the last block past the branch's length: zero.
-            ok = warp_wait(bar, (vn / kNV) & 1, lane);
-            if (!ok) break;
-            const uint32_t blk = base + s * kVStage + ((nblk - 1 - k0 - k)) * kVBlk;
-            for (int i = lane; i < (16 - tail) * 64; i += 32) {
-              const int row = tail + (i >> 6), c = i & 63;
-              st_shared_zero16(blk + (row >> 3) * 8192 + (c >> 3) * 1024 +
-                               (row & 7) * 128 + (c & 7) * 16);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.v_fix[s]));
+          const uint32_t dst = base + s * kVStage + last * kVBlk;
+          for (int i = lane; i < (16 - tail) * 64; i += 32) {
+            const int row = tail + (i >> 6), c = i & 63;
+            st_shared_zero16(dst + (row >> 3) * 8192 + (c >> 3) * 1024 +
+                             (row & 7) * 128 + (c & 7) * 16);
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.v_fix[s]));
         }
       }
     }
     if (lane == 0) {
       if (!ok) timed_out(42);
       // The stages this warp may still have loads in flight for.
-      for (uint32_t k = vn > kNV ? vn - kNV : 0; k < vn; ++k)
-        if ((k & 1) == me &&
-            !mbar_wait(smem_u32(&bars.v_full[k % kNV]), (k / kNV) & 1))
+      for (uint32_t k = vn > kNV / 2 ? vn - kNV / 2 : 0; k < vn; ++k)
+        if (!mbar_wait(smem_u32(&bars.v_full[k % (kNV / 2)]), (k / (kNV / 2)) & 1))
           break;
     }
   }
@@ -913,6 +956,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         "r"(kTmemCols)
         : "memory");
   }
+}
+
+// Clears the status word; a kernel, so that the attention kernel's launch and
+// set-up overlap it.
+__global__ void latent_clear_kernel(DeviceStatus* status) {
+  if (threadIdx.x == 0) *status = DeviceStatus{};
 }
 
 // ---- merge -------------------------------------------------------------------
@@ -976,6 +1025,24 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
 
 // ---- host side -----------------------------------------------------------------
 
+// Launch a kernel that may start before the one ahead of it in the stream has
+// ended (it waits for that by griddepcontrol.wait).
+template <typename... Formal, typename... Args>
+cudaError_t launch_early(void (*kernel)(Formal...), int grid, int block, int smem,
+                         cudaStream_t st, const Args&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // One layer's latent pool as 5-D boxes: 64 columns, 8 rows (1024 bytes apart),
 // `chunks` 64-column chunks (128), 2 groups of 8 rows (8192), a block (16384).
 // A box lands as [group][chunk][8 rows][128 bytes]: 8-row groups a fixed
@@ -989,12 +1056,13 @@ kv_status make_latent_map(CUtensorMap* tm, const void* pool, int64_t blocks,
   return encode_bf16_map(tm, pool, 5, dims, strides, box);
 }
 
-// Rows of `width` values in boxes of 16 rows x 64 values (a block's position
-// keys, or 16 query rows).
-kv_status make_rows_map(CUtensorMap* tm, const void* base, int64_t rows, int width) {
+// Rows of `width` values in boxes of 64 values (a block's position keys, or
+// query rows).
+kv_status make_rows_map(CUtensorMap* tm, const void* base, int64_t rows, int width,
+                        int box_rows) {
   const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)width * 2};
-  const cuuint32_t box[2] = {64, 16};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   return encode_bf16_map(tm, base, 2, dims, strides, box);
 }
 
@@ -1043,12 +1111,14 @@ extern "C" kv_status paged_latent_decode_attn(
   if (ws_bytes < need || (size_t)info->workspace_bytes != need)
     return fail(KV_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", ws_bytes,
                 need);
-  CUtensorMap tk, tv, tr, tq;
+  CUtensorMap tk, tv, tr, tq, tq_all;
   if (kv_status s = lat::make_latent_map(&tk, c_pool, num_blocks, lat::kKDim / 64)) return s;
   if (kv_status s = lat::make_latent_map(&tv, c_pool, num_blocks, 8)) return s;
-  if (kv_status s = lat::make_rows_map(&tr, r_pool, num_blocks * 16, rope_dim))
+  if (kv_status s = lat::make_rows_map(&tr, r_pool, num_blocks * 16, rope_dim, 16))
     return s;
-  if (kv_status s = lat::make_rows_map(&tq, q, (int64_t)nb * Hq, rank + rope_dim))
+  const int64_t q_rows = (int64_t)nb * Hq;
+  if (kv_status s = lat::make_rows_map(&tq, q, q_rows, rank + rope_dim, 16)) return s;
+  if (kv_status s = lat::make_rows_map(&tq_all, q, q_rows, rank + rope_dim, 128))
     return s;
   const int64_t off_item = pkv::kPlanHeaderInts;
   const int64_t off_pair = off_item + 8 * (int64_t)info->n_tile_items;
@@ -1078,12 +1148,13 @@ extern "C" kv_status paged_latent_decode_attn(
   p.scale_log2 = scale * 1.4426950408889634f;
   static std::atomic<uint64_t> opted{0};
   cudaError_t e = pkv::opt_in_smem(lat::latent_decode_kernel, lat::kSmem, opted);
-  if (e == cudaSuccess) e = cudaMemsetAsync(ws, 0, sizeof(pkv::DeviceStatus), st);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "latent step: %s", cudaGetErrorString(e));
-  lat::latent_decode_kernel<<<2 * p.n_pairs, lat::kThreads, lat::kSmem, st>>>(
-      tk, tv, tr, tq, p);
+  lat::latent_clear_kernel<<<1, 32, 0, st>>>(p.status);
   e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = lat::launch_early(lat::latent_decode_kernel, 2 * p.n_pairs, lat::kThreads,
+                          lat::kSmem, st, tk, tv, tr, tq, tq_all, p);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "latent kernel: %s", cudaGetErrorString(e));
   if (info->n_merge_rows > 0) {
@@ -1099,16 +1170,8 @@ extern "C" kv_status paged_latent_decode_attn(
     m.Hq = Hq;
     m.partial_rows = p.partial_rows;
     const int64_t warps = (int64_t)m.n * Hq;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, lat::latent_merge_kernel, m);
+    e = lat::launch_early(lat::latent_merge_kernel, (int)((warps + 7) / 8), 256, 0,
+                          st, m);
     if (e != cudaSuccess)
       return fail(KV_ERR_CUDA, "latent merge: %s", cudaGetErrorString(e));
   }

@@ -25,9 +25,12 @@ struct LatentUnit {
 };
 
 constexpr int kTileBlocks = 8;  // blocks of a 128-token tile
-// The fixed part of an item in tiles, and the shortest piece of a unit.
-constexpr int kItemTiles = 3;
-constexpr int kMinTiles = 2;
+constexpr int kMinTiles = 2;    // the shortest piece of a unit
+// Costs in half tiles (1 us): a tile, and an item's fixed part -- measured on
+// steps of long and of short items: about 3.5 us, and 3 to 5 us more for 128 rows
+// of partial results.
+constexpr int kTileCost = 2;
+int32_t item_cost(int32_t nrows) { return 4 + nrows / 32; }
 
 struct Piece {
   int32_t unit, lo, hi;  // blocks
@@ -35,23 +38,24 @@ struct Piece {
 
 int32_t tiles(int32_t blocks) { return (blocks + kTileBlocks - 1) / kTileBlocks; }
 
-// Deal the units out to pairs of at most `share` tiles each; returns whether
+// Deal the units out to pairs of at most `share` cost each; returns whether
 // they fit `pairs` pairs.
 bool deal(const std::vector<LatentUnit>& units, int64_t share, int32_t pairs,
           std::vector<Piece>* out, std::vector<int32_t>* ptr) {
   out->clear();
   ptr->assign(1, 0);
-  int64_t used = 0;  // tiles of the pair being filled
+  int64_t used = 0;  // cost of the pair being filled
   for (int32_t u = 0; u < (int32_t)units.size(); ++u) {
     int32_t lo = units[u].blk_begin;
     while (lo < units[u].blk_end) {
       const int32_t left = tiles(units[u].blk_end - lo);
-      int64_t room = share - used - kItemTiles;
+      const int32_t fixed = item_cost(units[u].nrows);
+      int64_t room = (share - used - fixed) / kTileCost;  // tiles
       if (used > 0 && room < std::min(left, kMinTiles)) {
         ptr->push_back((int32_t)out->size());
         if ((int32_t)ptr->size() > pairs) return false;
         used = 0;
-        room = share - kItemTiles;
+        room = (share - fixed) / kTileCost;
       }
       room = std::max<int64_t>(room, kMinTiles);
       // The rest of the unit is not left shorter than the shortest piece.
@@ -64,7 +68,7 @@ bool deal(const std::vector<LatentUnit>& units, int64_t share, int32_t pairs,
       const int32_t hi =
           std::min(units[u].blk_end, lo + take * kTileBlocks);
       out->push_back({u, lo, hi});
-      used += take + kItemTiles;
+      used += (int64_t)take * kTileCost + fixed;
       lo = hi;
     }
   }
@@ -108,9 +112,10 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   const int32_t pairs_max = std::max(1, num_sms / 2);
   int64_t cost = 0;
   for (const LatentUnit& u : units)
-    cost += tiles(u.blk_end - u.blk_begin) + kItemTiles;
+    cost += (int64_t)tiles(u.blk_end - u.blk_begin) * kTileCost +
+            item_cost(u.nrows);
   int64_t share = std::max<int64_t>((cost + pairs_max - 1) / pairs_max,
-                                    kItemTiles + kMinTiles);
+                                    kTileCost * kMinTiles);
   std::vector<Piece> pieces;
   std::vector<int32_t> ptr;
   while (!deal(units, share, pairs_max, &pieces, &ptr))
@@ -177,7 +182,7 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   info->n_tile_items = (int32_t)items.size();
   info->n_tile_wide_items = n_pairs;
   info->n_merge_rows = (int32_t)merged.size();
-  info->chunk_blocks = (int32_t)std::min<int64_t>(INT32_MAX, share * kTileBlocks);
+  info->chunk_blocks = (int32_t)std::min<int64_t>(INT32_MAX, share / kTileCost * kTileBlocks);
   info->flags = flags;
   if (!plan) return KV_OK;
   if (plan_cap < total)
