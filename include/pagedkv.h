@@ -621,6 +621,45 @@ kv_status paged_latent_decode_attn(
     const kv_decode_plan_info* info, void* workspace, size_t ws_bytes,
     void* stream);
 
+/* Host half of a latent prefill: new tokens of each branch (a prompt, a chunk)
+ * attend to the branch's cached tokens.  tables (host, [nb][max_blocks]),
+ * seq_lens, q_lens (host, nb): branch b's q_lens[b] newest tokens (0: not in
+ * the step) are the queries, seq_lens[b] its cached tokens with them included,
+ * written to the pool beforehand (paged_latent_append).  Writes the plan to
+ * host `plan` (plan = NULL: the size in info->plan_ints) and fills info:
+ * workspace_bytes, n_row_items = distinct blocks of the step (each expanded
+ * once, 8 KB of workspace a head), n_tile_items = query tiles a head,
+ * n_merge_rows = query rows.  num_sms: as for paged_decode_plan.  Errors:
+ * INVALID_ARG (lengths, a block id outside the pool). */
+kv_status paged_latent_prefill_plan(int32_t nb, int32_t Hq, int64_t num_blocks,
+                                    int32_t max_blocks, const int32_t* tables,
+                                    const int32_t* seq_lens,
+                                    const int32_t* q_lens, int32_t num_sms,
+                                    int32_t* plan, int64_t plan_cap,
+                                    kv_decode_plan_info* info);
+
+/* Latent attention of new tokens, expanded form: with keys and values expanded
+ * from the latents per head,
+ *   k[t][h] = [w_kv[h][0..128) c_t ; r_t],  v[t][h] = w_kv[h][128..256) c_t,
+ *   out[i][h] = sum_{t <= p(i)} softmax_t(scale * q[i][h] . k[t][h]) v[t][h],
+ * p(i) = seq_lens[b] - q_lens[b] + i the position of the branch's i-th query
+ * (it sees itself and everything before).  q [total][Hq][192] bf16: 128
+ * dimensions without position, then the 64 rotated ones; branches in order,
+ * total = sum of q_lens (0: nothing to do).  w_kv [Hq][256][512] bf16.  out
+ * [total][Hq][128] bf16.  c_pool, r_pool: this layer's latent pools.  rank must
+ * be 512, rope_dim 64, head_dim 128.  Keys and values are rounded to bf16 once,
+ * as cached ones are.  plan: a device copy of paged_latent_prefill_plan's,
+ * *info its host info; workspace: device, >= info->workspace_bytes, 256-byte
+ * aligned, no initial contents needed.  Rows behind the last query are left as
+ * they were.  All launches are on `stream` (capturable); status as for
+ * paged_decode_attn.  Errors: INVALID_ARG, CUDA. */
+kv_status paged_latent_prefill_attn(
+    const void* q, const void* c_pool, const void* r_pool, int64_t num_blocks,
+    const void* w_kv, int32_t total, int32_t nb, int32_t Hq, int32_t rank,
+    int32_t rope_dim, int32_t head_dim, int32_t block_size, float scale,
+    void* out, const int32_t* plan, const kv_decode_plan_info* info,
+    void* workspace, size_t ws_bytes, void* stream);
+
 /* paged_decode_attn without a caller workspace.  The pages have no
  * counterpart: this exists for callers that cannot allocate device memory
  * (a plug-in whose host engine owns every device buffer and offers it no

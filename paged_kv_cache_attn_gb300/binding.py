@@ -183,6 +183,15 @@ _SIGS = {
                                  [C.c_float, _vp, _vp,
                                   C.POINTER(kv_decode_plan_info), _vp,
                                   C.c_size_t, _vp]),
+    "paged_latent_prefill_plan": (C.c_int32, [C.c_int32, C.c_int32, C.c_int64,
+                                              C.c_int32, _i32p, _i32p, _i32p,
+                                              C.c_int32, _i32p, C.c_int64,
+                                              C.POINTER(kv_decode_plan_info)]),
+    "paged_latent_prefill_attn": (C.c_int32, [_vp, _vp, _vp, C.c_int64, _vp] +
+                                  [C.c_int32] * 7 +
+                                  [C.c_float, _vp, _vp,
+                                   C.POINTER(kv_decode_plan_info), _vp,
+                                   C.c_size_t, _vp]),
     "kv_check_device_status": (C.c_int32, [_vp, _vp, _i32p, _i32p]),
     "kv_selftest_timeout": (C.c_int32, [_vp, C.c_int64, _vp]),
     "kv_offload_attach": (C.c_int32, [_vp, _vp, _vp, _vp, C.c_int64]),
@@ -625,6 +634,36 @@ def paged_latent_decode_attn(q, c_pool, r_pool, num_blocks, block_tables,
         _ptr(seq_lens), _ptr(prefix_groups), n_groups, nb, max_blocks, Hq,
         KV_LATENT_RANK, KV_LATENT_ROPE, block_size, scale, _ptr(out),
         _ptr(plan), C.byref(info), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def paged_latent_prefill_plan(nb, Hq, num_blocks, tables, seq_lens, q_lens,
+                              num_sms=0):
+    """Host plan (int32 array) and its info; tables [nb][max_blocks]."""
+    t = _i32(tables).reshape(nb, -1)
+    lens, qn = _i32(seq_lens), _i32(q_lens)
+    if len(lens) < nb or len(qn) < nb:
+        raise KVError(KV_ERR_INVALID_ARG, "seq_lens and q_lens: nb entries")
+    info = kv_decode_plan_info()
+
+    def call(plan, cap):
+        _check(_lib.paged_latent_prefill_plan(
+            nb, Hq, num_blocks, t.shape[1], _as_i32p(t), _as_i32p(lens),
+            _as_i32p(qn), num_sms, plan, cap, C.byref(info)))
+
+    call(None, 0)
+    plan = np.zeros(info.plan_ints, dtype=np.int32)
+    call(_as_i32p(plan), len(plan))
+    return plan, info
+
+
+def paged_latent_prefill_attn(q, c_pool, r_pool, num_blocks, w_kv, total, nb,
+                              Hq, scale, out, plan, info, workspace, ws_bytes,
+                              stream=None, block_size=16):
+    _check(_lib.paged_latent_prefill_attn(
+        _ptr(q), _ptr(c_pool), _ptr(r_pool), num_blocks, _ptr(w_kv), total, nb,
+        Hq, KV_LATENT_RANK, KV_LATENT_ROPE, KV_LATENT_HEAD, block_size, scale,
+        _ptr(out), _ptr(plan), C.byref(info), _ptr(workspace), ws_bytes,
+        _stream(stream)))
 
 
 def paged_decode_attn_noalloc(q, k_pool, v_pool, num_blocks, block_tables,

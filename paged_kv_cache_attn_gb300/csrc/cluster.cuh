@@ -156,6 +156,16 @@ __device__ __forceinline__ void tma_load_5d_at(uint32_t dst,
       : "memory");
 }
 
+// One box of a 3-D map.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
+                                            int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
 // 128 rows x 32 bytes from shared memory (the layout of a K-major operand,
 // descriptor as for an MMA) to 8 columns of tensor memory; runs in order with
 // the thread's later MMAs.

@@ -697,7 +697,7 @@ static kv_status decode_impl(
     return fail(KV_ERR_INVALID_ARG, e4m3 ? "an e4m3 step needs a plan made "
                                            "with KV_PLAN_KV_E4M3"
                                          : "plan was made for an e4m3 pool");
-  if (info->flags & KV_PLAN_LATENT)
+  if (info->flags & (KV_PLAN_LATENT | pkv::kPrefillPlan))
     return fail(KV_ERR_INVALID_ARG, "plan was made for a latent pool");
   if (info->n_tile_items != 0 && d != 128)
     return fail(KV_ERR_INVALID_ARG, "tensor-core tiles need head_dim 128");

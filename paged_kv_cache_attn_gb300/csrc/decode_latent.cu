@@ -1025,24 +1025,6 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
 
 // ---- host side -----------------------------------------------------------------
 
-// Launch a kernel that may start before the one ahead of it in the stream has
-// ended (it waits for that by griddepcontrol.wait).
-template <typename... Formal, typename... Args>
-cudaError_t launch_early(void (*kernel)(Formal...), int grid, int block, int smem,
-                         cudaStream_t st, const Args&... args) {
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)block);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // One layer's latent pool as 5-D boxes: 64 columns, 8 rows (1024 bytes apart),
 // `chunks` 64-column chunks (128), 2 groups of 8 rows (8192), a block (16384).
 // A box lands as [group][chunk][8 rows][128 bytes]: 8-row groups a fixed
@@ -1153,7 +1135,7 @@ extern "C" kv_status paged_latent_decode_attn(
   lat::latent_clear_kernel<<<1, 32, 0, st>>>(p.status);
   e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = lat::launch_early(lat::latent_decode_kernel, 2 * p.n_pairs, lat::kThreads,
+    e = pkv::launch_early(lat::latent_decode_kernel, 2 * p.n_pairs, lat::kThreads,
                           lat::kSmem, st, tk, tv, tr, tq, tq_all, p);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "latent kernel: %s", cudaGetErrorString(e));
@@ -1170,7 +1152,7 @@ extern "C" kv_status paged_latent_decode_attn(
     m.Hq = Hq;
     m.partial_rows = p.partial_rows;
     const int64_t warps = (int64_t)m.n * Hq;
-    e = lat::launch_early(lat::latent_merge_kernel, (int)((warps + 7) / 8), 256, 0,
+    e = pkv::launch_early(lat::latent_merge_kernel, (int)((warps + 7) / 8), 256, 0,
                           st, m);
     if (e != cudaSuccess)
       return fail(KV_ERR_CUDA, "latent merge: %s", cudaGetErrorString(e));

@@ -117,6 +117,23 @@ inline size_t ws_total(int64_t rows, int d) {
   return align_up(ws_o_offset(rows) + (size_t)rows * d * 4, 256);
 }
 
+// A tile of a latent prefill: query rows [row0, row0 + nrows) of the batch,
+// the first at position pos0 of its branch, whose table is slots[table ..).
+struct PrefillTile {
+  int32_t row0, nrows, pos0, table;
+};
+constexpr int32_t kPrefillPlanMagic = 0x31504B50;  // "PKP1"
+constexpr int32_t kPrefillPlan = 32;  // info.flags of a prefill plan
+constexpr int kPrefillRows = 256;     // query rows of a tile
+// Workspace: the status block, then the expanded keys and values of the
+// distinct blocks, each [slot][Hq][16][128] bf16.
+inline size_t prefill_half(int64_t slots, int Hq) {
+  return (size_t)slots * Hq * 16 * KV_LATENT_HEAD * 2;
+}
+inline size_t prefill_workspace(int64_t slots, int Hq) {
+  return kStatusBytes + 2 * prefill_half(slots, Hq);
+}
+
 // Device status word (first 16 bytes of the workspace).
 struct DeviceStatus {
   uint32_t code;    // 0, KV_ERR_DEVICE or KV_ERR_TIMEOUT (first recorded)
