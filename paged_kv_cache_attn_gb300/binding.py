@@ -253,18 +253,30 @@ def _ptr(x):
     return x.data_ptr()
 
 
-_torch = None          # torch, once a call has found a GPU
+_current_stream = None     # once a call has found a GPU
+
+
+def _find_current_stream():
+    """The quickest way to torch's current stream handle (a decode step makes
+    a few calls per layer of some microseconds each)."""
+    import torch
+    if not torch.cuda.is_available():
+        return None
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    device = torch.cuda.current_device
+    return lambda: raw(device())
 
 
 def _stream(s):
-    global _torch
+    global _current_stream
     if s is None:
-        if _torch is None:
-            import torch
-            if not torch.cuda.is_available():
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+            if _current_stream is None:
                 return None
-            _torch = torch
-        return _torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -310,7 +310,7 @@ constexpr float kRescale = 8.f;    // lazy-max threshold (log2 units)
 
 struct Small {
   uint64_t q_full, k_full[2], k_empty[2], v_full, v_empty, s_full[2], p_full[2],
-      o_ready[2];
+      o_ready[2], turn[2];
   uint32_t tmem_base;
   int aborted;
 };
@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.s_full[s]), 1);
       mbar_init(smem_u32(&sh.p_full[s]), 4);
       mbar_init(smem_u32(&sh.o_ready[s]), 1);
+      mbar_init(smem_u32(&sh.turn[s]), 1);
     }
     mbar_init(smem_u32(&sh.v_full), 1);
     mbar_init(smem_u32(&sh.v_empty), n_m);
@@ -484,38 +485,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int blocks = uniform(nblk);
       const uint32_t ds = tmem + m * kT, dout = tmem + kColO + m * kHead;
       bool ok = all_wait(smem_u32(&sh.q_full), 0);
-      // O += P(j) V(j), or only the tile's release where the M-tile is past
-      // its last key tile.
-      auto pv = [&](int j) {
-        const bool use = j < mine;
-        if (use && !all_wait(smem_u32(&sh.p_full[m]), j & 1)) return false;
-        if (!all_wait(smem_u32(&sh.v_full), j & 1)) return false;
-        fence_after_sync();
-        const int nb = min(kTB, blocks - j * kTB);
-        if (lead) {
-          if (use) {
+      // PV(j) needs P and V; where the M-tile is past its last key tile, the
+      // tile is only released.
+      auto pv_ready = [&](int j) {
+        if (j < mine && !all_wait(smem_u32(&sh.p_full[m]), j & 1)) return false;
+        return all_wait(smem_u32(&sh.v_full), j & 1);
+      };
+      auto pv = [&](int j) {  // one lane: O += P(j) V(j)
+        if (j < mine) {
+          const int nb = min(kTB, blocks - j * kTB);
 #pragma unroll
-            for (int k = 0; k < kTB; ++k)
-              if (k < nb)
-                umma_ts(dout, ds + k * 8,
-                        sdesc(base + kOffV + k * kBlk, 1024, 2048), id_pv,
-                        j > 0 || k > 0 ? 1u : 0u);
-            umma_commit(smem_u32(&sh.v_empty));
-            if (j == mine - 1) umma_commit(smem_u32(&sh.o_ready[m]));
-          } else {
-            mbar_arrive(smem_u32(&sh.v_empty));
-          }
+          for (int k = 0; k < kTB; ++k)
+            if (k < nb)
+              umma_ts(dout, ds + k * 8, sdesc(base + kOffV + k * kBlk, 1024, 2048),
+                      id_pv, j > 0 || k > 0 ? 1u : 0u);
+          umma_commit(smem_u32(&sh.v_empty));
+          if (j == mine - 1) umma_commit(smem_u32(&sh.o_ready[m]));
+        } else {
+          mbar_arrive(smem_u32(&sh.v_empty));
         }
-        __syncwarp();
-        return true;
       };
       for (int j = 0; j < all && ok; ++j) {
-        if (j > 0) ok = pv(j - 1);
+        if (j > 0) ok = pv_ready(j - 1);
         ok = ok && all_wait(smem_u32(&sh.k_full[j & 1]), (j >> 1) & 1);
+        // The M-tiles' products alternate in whole blocks: issued side by side
+        // they would interleave, both softmaxes would start when both were done,
+        // and the tensor pipe would idle meanwhile (2.6 us a key tile instead of
+        // 1.9).
+        if (n_m == 2 && (m == 1 || j > 0))
+          ok = ok && all_wait(smem_u32(&sh.turn[m]), (m == 1 ? j : j - 1) & 1);
         if (!ok) break;
         fence_after_sync();
         const uint32_t kst = base + kOffK + (j & 1) * kK;
         if (lead) {
+          if (j > 0) pv(j - 1);
           if (j < mine) {
             const uint64_t qd = sdesc(base + m * kQ, 16, 1024);
             const uint64_t kd = sdesc(kst, 16, 2048);
@@ -533,11 +536,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             mbar_arrive(smem_u32(&sh.k_empty[j & 1]));
           }
+          if (n_m == 2) mbar_arrive(smem_u32(&sh.turn[m ^ 1]));
         }
         __syncwarp();
         ok = !*aborted;
       }
-      if (ok) ok = pv(all - 1);
+      if (ok) ok = pv_ready(all - 1);
+      if (ok) {
+        fence_after_sync();
+        if (lead) pv(all - 1);
+      }
       if (lead) {
         if (!ok) {
           timed_out(61);

@@ -40,31 +40,31 @@ struct Token {
   bool ok;
 };
 
-// Warp-wide: branch, position and block of token t.  A token whose branch,
-// position or block is out of range is recorded and not ok.
-__device__ __forceinline__ Token locate(const TokenMap& m, int t, int lane) {
-  int b = t, first = t, n = 1;
-  if (m.off) {
-    // The last branch whose first token is <= t, 32 candidates at a time.
-    int lo = 0, hi = m.nb;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int idx = lo + lane * step;
-      const bool le = idx < hi && m.off[idx] <= t;
-      const int cnt = __popc(__ballot_sync(0xffffffffu, le));
-      lo += max(cnt - 1, 0) * step;
-      hi = min(lo + step, hi);
-    }
-    b = lo;
-    first = m.off[b];
-    n = m.off[b + 1] - first;
+// Warp-wide: the last branch whose first token is <= t, 32 candidates at a time.
+__device__ __forceinline__ int find_branch(const TokenMap& m, int t, int lane) {
+  int lo = 0, hi = m.nb;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int idx = lo + lane * step;
+    const bool le = idx < hi && m.off[idx] <= t;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, le));
+    lo += max(cnt - 1, 0) * step;
+    hi = min(lo + step, hi);
   }
+  return lo;
+}
+
+// Position and block of token t of branch b.  A token whose branch, position
+// or block is out of range is recorded (by the calling threads with `tell`) and
+// not ok.
+__device__ __forceinline__ Token place(const TokenMap& m, int t, int b,
+                                       bool tell) {
   Token k;
-  k.first = first;
-  k.n = n;
-  k.pos = m.seq_lens[b] - n + (t - first);
+  k.first = m.off ? m.off[b] : t;
+  k.n = m.off ? m.off[b + 1] - k.first : 1;
+  k.pos = m.seq_lens[b] - k.n + (t - k.first);
   k.phys = -1;
-  k.ok = t >= first && t - first < n && k.pos >= 0 && k.pos < m.rope_len &&
+  k.ok = t >= k.first && t - k.first < k.n && k.pos >= 0 && k.pos < m.rope_len &&
          (k.pos >> 4) < m.max_blocks;
   int bad = k.pos;
   if (k.ok) {
@@ -72,8 +72,13 @@ __device__ __forceinline__ Token locate(const TokenMap& m, int t, int lane) {
     bad = k.phys;
     k.ok = k.phys >= 0 && (int64_t)k.phys < m.num_blocks;
   }
-  if (!k.ok && lane == 0) record_status(m.status, KV_ERR_DEVICE, bad);
+  if (!k.ok && tell) record_status(m.status, KV_ERR_DEVICE, bad);
   return k;
+}
+
+// Warp-wide, the same token for all lanes.
+__device__ __forceinline__ Token locate(const TokenMap& m, int t, int lane) {
+  return place(m, t, m.off ? find_branch(m, t, lane) : t, lane == 0);
 }
 
 // Rows of D values handled alike ("heads" of a token).  Destination of head
@@ -203,6 +208,8 @@ __global__ void __launch_bounds__(256)
 
 // ---- e4m3 pools ---------------------------------------------------------------
 
+constexpr int kQuantWarps = 4;
+
 struct QuantArgs {
   RotateArgs rot;  // queries only (rows[0])
   int q_ctas;      // CTAs of the rotation part
@@ -216,148 +223,270 @@ struct QuantArgs {
   int Hkv;
 };
 
-// One warp: slots [s0, s1) of one (block, head) tile of K or V from the rows
-// of tokens t0 .., under the block rule of kv_pool_desc.  The values stay in
-// registers between the maximum and the codes, so a row is read once and
-// rounded once (fp32 to e4m3).  Lane l holds dimensions l * V .. of every slot.
-template <int D, bool PAIRS>
-__device__ __forceinline__ void quant_tile(const QuantArgs& a, bool is_v, int h,
-                                           int t0, int pos0, int phys, int m,
-                                           int lane) {
-  constexpr int V = D / 32;  // values per lane
-  const int s0 = pos0 & 15, s1 = s0 + m;
-  const int half = a.rot.half;
-  const int64_t tile = (int64_t)phys * a.Hkv + h;
-  uint8_t* codes = (is_v ? a.v8 : a.k8) + tile * 16 * D;
-  float* scale = reinterpret_cast<float*>(a.scales + tile) + (is_v ? 1 : 0);
-  const int64_t stride = is_v ? a.v_token : a.k_token;
-  const __nv_bfloat16* src = (is_v ? a.v_new : a.k_new) + (int64_t)t0 * stride +
-                             (int64_t)h * D + lane * V;
-  const int c0 = lane * V;
-  const bool rot = !is_v && c0 < 2 * half;
-  const bool low = c0 < half;
-  float x[16][V];
+// Two codes, `lo` in the lower byte: nearest, ties to even, saturating (the
+// conversion of e4m3_encode, two values at a time).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t join16(uint32_t lo, uint32_t hi) {
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+// Where one warp's write goes and comes from.
+struct QuantTile {
+  uint8_t* codes;
+  float* scale;
+  const __nv_bfloat16* src;  // this lane's values of the first row
+  int64_t stride;
+  const float2* table;       // the first row's (cos, sin)
+  int c0;                    // this lane's first dimension
+  bool is_v, rot, low;
+};
+
+// This lane's V values of R rows (row min(r, m - 1) as the r-th), rotated for
+// keys.  All the rows are asked for before the first is used, and all of their
+// (cos, sin) next: taken row by row, a tile waited for memory sixteen times.
+template <int D, bool PAIRS, int R>
+__device__ __forceinline__ void quant_rows(const QuantTile& q, int m, int half,
+                                           int lane, float (&x)[R][D / 32]) {
+  constexpr int V = D / 32;
+  uint32_t raw[R][V / 2];
 #pragma unroll
-  for (int t = 0; t < 16; ++t) {
-    uint32_t w[V / 2];
-    const bool in = t >= s0 && t < s1;
+  for (int r = 0; r < R; ++r) {
+    const __nv_bfloat16* at = q.src + min(r, m - 1) * q.stride;
     if constexpr (V == 4) {
-      const uint2 u = in ? *reinterpret_cast<const uint2*>(src + (t - s0) * stride)
-                         : make_uint2(0, 0);
-      w[0] = u.x;
-      w[1] = u.y;
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(at));
+      raw[r][0] = u.x;
+      raw[r][1] = u.y;
     } else {
-      w[0] = in ? *reinterpret_cast<const uint32_t*>(src + (t - s0) * stride) : 0u;
+      raw[r][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      x[t][i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
-  if (!is_v) {
+  auto value = [&](int r, int i) {
+    return __uint_as_float(i & 1 ? raw[r][i / 2] & 0xffff0000u : raw[r][i / 2] << 16);
+  };
+  if (q.is_v) {
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      const bool in = t >= s0 && t < s1;
-      const float2* row = a.rot.table + (int64_t)(pos0 + t - s0) * half;
-      if constexpr (PAIRS) {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          const float2 f = in && rot ? __ldg(row + (c0 + i) / 2) : make_float2(1.f, 0.f);
-          const float p = x[t][i], q = x[t][i + 1];
-          x[t][i] = fmaf(p, f.x, -(q * f.y));
-          x[t][i + 1] = fmaf(q, f.x, p * f.y);
-        }
-      } else {
-        const int mate = low ? lane + half / V : lane - half / V;
-        float o[V];
+      for (int i = 0; i < V; ++i) x[r][i] = value(r, i);
+    return;
+  }
+  const int j0 = PAIRS ? q.c0 / 2 : q.low ? q.c0 : q.c0 - half;
+  const float2* row = q.table + (q.rot ? j0 : 0);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          o[i] = __shfl_sync(0xffffffffu, x[t][i], mate & 31);
+  for (int r = 0; r < R; ++r) {
+    const float2* at = row + (int64_t)min(r, m - 1) * half;
+    if constexpr (PAIRS) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 f = in && rot ? __ldg(row + (low ? c0 : c0 - half) + i)
-                                     : make_float2(1.f, 0.f);
-          x[t][i] = fmaf(x[t][i], f.x, o[i] * (low ? -f.y : f.y));
-        }
+      for (int i = 0; i < V; i += 2) {
+        const float2 f = __ldg(at + i / 2);
+        const float a = value(r, i), b = value(r, i + 1);
+        x[r][i] = q.rot ? fmaf(a, f.x, -(b * f.y)) : a;
+        x[r][i + 1] = q.rot ? fmaf(b, f.x, a * f.y) : b;
+      }
+    } else {
+      const int mate = (q.low ? lane + half / V : lane - half / V) & 31;
+      uint32_t o[V / 2];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) o[i] = __shfl_sync(0xffffffffu, raw[r][i], mate);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 f = __ldg(at + i);
+        const float a = value(r, i);
+        const float b = __uint_as_float(i & 1 ? o[i / 2] & 0xffff0000u : o[i / 2] << 16);
+        x[r][i] = q.rot ? fmaf(a, f.x, b * (q.low ? -f.y : f.y)) : a;
       }
     }
   }
-  float amax = 0.f;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// A whole block (16 rows from slot 0), nearly every write of a prompt: the
+// rows stay in registers between the maximum and the codes.
+template <int D, bool PAIRS>
+__device__ __forceinline__ void quant_block(const QuantTile& q, int half,
+                                            int lane) {
+  constexpr int V = D / 32;  // values per lane and row
+  float x[16][V];
+  quant_rows<D, PAIRS, 16>(q, 16, half, lane, x);
+  float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int t = 0; t < 16; ++t)
 #pragma unroll
-    for (int i = 0; i < V; ++i) amax = fmaxf(amax, fabsf(x[t][i]));
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const int e_req = e4m3_exponent_for(amax);
-  int e = e_req, sh = 0;
-  if (s0 > 0) {
-    const int e_old = scale_exponent(*scale);
-    e = max(e_old, e_req);
-    sh = e_old - e;  // the rows already stored move by this exponent
-  }
+    for (int i = 0; i < V; ++i) m4[t & 3] = fmaxf(m4[t & 3], fabsf(x[t][i]));
+  const int e = e4m3_exponent_for(
+      warp_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]))));
   const float inv = pow2f(-e);
-  auto shifted = [&](uint32_t c) {
-    return (uint32_t)e4m3_encode(ldexpf(e4m3_decode((uint8_t)c), sh));
-  };
-  if (!is_v) {
+  if (!q.is_v) {
 #pragma unroll
     for (int t = 0; t < 16; ++t) {
-      uint8_t* at = codes + k_tile_offset(t, c0, D);
-      uint32_t w = 0;
-      if (t >= s0 && t < s1) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          w |= (uint32_t)e4m3_encode(x[t][i] * inv) << (8 * i);
-      } else if (t < s0 && sh != 0) {
-        const uint32_t old = V == 4 ? *reinterpret_cast<const uint32_t*>(at)
-                                    : *reinterpret_cast<const uint16_t*>(at);
-#pragma unroll
-        for (int i = 0; i < V; ++i) w |= shifted((old >> (8 * i)) & 0xff) << (8 * i);
-      } else {
-        continue;
-      }
+      uint8_t* at = q.codes + k_tile_offset(t, q.c0, D);
+      const uint32_t lo = e4m3x2(x[t][0] * inv, x[t][1] * inv);
       if constexpr (V == 4)
-        *reinterpret_cast<uint32_t*>(at) = w;
+        *reinterpret_cast<uint32_t*>(at) =
+            join16(lo, e4m3x2(x[t][2] * inv, x[t][3] * inv));
       else
-        *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+        *reinterpret_cast<uint16_t*>(at) = (uint16_t)lo;
     }
   } else {
     // Transposed tile: the 16 slots of a dimension are 16 contiguous bytes.
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      uint4* at = reinterpret_cast<uint4*>(codes + v_tile_offset(0, c0 + i));
-      uint32_t w[4] = {0, 0, 0, 0};
-      if (m < 16) {
-        const uint4 old = *at;
-        w[0] = old.x; w[1] = old.y; w[2] = old.z; w[3] = old.w;
-      }
+      uint32_t w[4];
 #pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        const uint32_t mask = 0xffu << (8 * (t & 3));
-        uint32_t c = (w[t >> 2] >> (8 * (t & 3))) & 0xff;
-        if (t >= s0 && t < s1)
-          c = e4m3_encode(x[t][i] * inv);
-        else if (t < s0 && sh != 0)
-          c = shifted(c);
-        w[t >> 2] = (w[t >> 2] & ~mask) | (c << (8 * (t & 3)));
-      }
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int k = 0; k < 4; ++k)
+        w[k] = join16(e4m3x2(x[4 * k][i] * inv, x[4 * k + 1][i] * inv),
+                      e4m3x2(x[4 * k + 2][i] * inv, x[4 * k + 3][i] * inv));
+      *reinterpret_cast<uint4*>(q.codes + v_tile_offset(0, q.c0 + i)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  if (lane == 0) *q.scale = pow2f(e);
+}
+
+// The rows already stored, slots [0, s0), move by an exponent (a pure shift of
+// their stored values).  All of a lane's codes are loaded before the first is
+// written back.
+template <int D>
+__device__ __forceinline__ void shift_rows(const QuantTile& q, int s0, int sh) {
+  constexpr int V = D / 32;
+  auto moved = [&](uint32_t w, int n) {  // the n lowest codes of a word
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= n) break;
+      const float v = ldexpf(e4m3_decode((uint8_t)(w >> (8 * i))), sh);
+      w = (w & ~(0xffu << (8 * i))) | ((uint32_t)e4m3_encode(v) << (8 * i));
+    }
+    return w;
+  };
+  if (!q.is_v) {
+    uint32_t w[15];
+#pragma unroll
+    for (int t = 0; t < 15; ++t) {
+      const uint8_t* at = q.codes + k_tile_offset(t, q.c0, D);
+      if (t < s0)
+        w[t] = V == 4 ? *reinterpret_cast<const uint32_t*>(at)
+                      : *reinterpret_cast<const uint16_t*>(at);
+    }
+#pragma unroll
+    for (int t = 0; t < 15; ++t) {
+      uint8_t* at = q.codes + k_tile_offset(t, q.c0, D);
+      if (t >= s0) break;
+      if constexpr (V == 4)
+        *reinterpret_cast<uint32_t*>(at) = moved(w[t], 4);
+      else
+        *reinterpret_cast<uint16_t*>(at) = (uint16_t)moved(w[t], 2);
+    }
+  } else {
+    uint4 v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      v[i] = *reinterpret_cast<const uint4*>(q.codes + v_tile_offset(0, q.c0 + i));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = moved(w[k], min(max(s0 - 4 * k, 0), 4));
+      *reinterpret_cast<uint4*>(q.codes + v_tile_offset(0, q.c0 + i)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// Slots [s0, s0 + m) of a block, m <= R (a decode step's token: R = 1; the ends
+// of a chunk: 16).
+template <int D, bool PAIRS, int R>
+__device__ __forceinline__ void quant_part(const QuantTile& q, int s0, int m,
+                                           int half, int lane) {
+  constexpr int V = D / 32;
+  float x[R][V];
+  float amax = 0.f;
+  quant_rows<D, PAIRS, R>(q, m, half, lane, x);  // rows past m: the last again
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < V; ++i) amax = fmaxf(amax, fabsf(x[r][i]));
+  int e = e4m3_exponent_for(warp_max(amax));
+  if (s0 > 0) {
+    const int e_old = scale_exponent(*q.scale);
+    if (e_old >= e)
+      e = e_old;
+    else
+      shift_rows<D>(q, s0, e_old - e);
+  }
+  const float inv = pow2f(-e);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (r >= m) break;
+    const uint32_t lo = e4m3x2(x[r][0] * inv, x[r][1] * inv);
+    const uint32_t w =
+        V == 4 ? join16(lo, e4m3x2(x[r][V - 2] * inv, x[r][V - 1] * inv)) : lo;
+    if (!q.is_v) {
+      uint8_t* at = q.codes + k_tile_offset(s0 + r, q.c0, D);
+      if constexpr (V == 4)
+        *reinterpret_cast<uint32_t*>(at) = w;
+      else
+        *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        q.codes[v_tile_offset(s0 + r, q.c0 + i)] = (uint8_t)(w >> (8 * i));
     }
   }
   __syncwarp();  // every lane has read the old scale
-  if (lane == 0) *scale = pow2f(e);
+  if (lane == 0) *q.scale = pow2f(e);
+}
+
+// One warp: slots from pos0's of one (block, head) tile of K or V, from the
+// rows of tokens t0 .., under the block rule of kv_pool_desc; values are
+// rounded once, from fp32 to e4m3.  Lane l holds dimensions l * D / 32 ..
+template <int D, bool PAIRS>
+__device__ __forceinline__ void quant_tile(const QuantArgs& a, bool is_v, int h,
+                                           int t0, int pos0, int phys, int m,
+                                           int lane) {
+  constexpr int V = D / 32;
+  const int half = a.rot.half;
+  const int64_t tile = (int64_t)phys * a.Hkv + h;
+  QuantTile q;
+  q.is_v = is_v;
+  q.c0 = lane * V;
+  q.rot = !is_v && q.c0 < 2 * half;
+  q.low = q.c0 < half;
+  q.codes = (is_v ? a.v8 : a.k8) + tile * 16 * D;
+  q.scale = reinterpret_cast<float*>(a.scales + tile) + (is_v ? 1 : 0);
+  q.stride = is_v ? a.v_token : a.k_token;
+  q.src = (is_v ? a.v_new : a.k_new) + (int64_t)t0 * q.stride + (int64_t)h * D +
+          q.c0;
+  q.table = a.rot.table + (int64_t)pos0 * half;
+  if (m == 16)
+    quant_block<D, PAIRS>(q, half, lane);
+  else if (m == 1)
+    quant_part<D, PAIRS, 1>(q, pos0 & 15, m, half, lane);
+  else
+    quant_part<D, PAIRS, 16>(q, pos0 & 15, m, half, lane);
 }
 
 // CTAs [0, q_ctas) rotate queries; each later CTA takes a window of tokens,
 // finds those that begin a write (a branch's first new token, or slot 0) and
-// runs one warp per (write, kv-head, K or V).
+// runs one warp per (write, kv-head, K or V); the CTAs of grid.y share a
+// window's units.  128 threads and four CTAs an SM: a tile's 64 values and its
+// table entries stay in registers.
 template <int D, bool PAIRS>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kQuantWarps * 32, 4)
     quant_append_kernel(const __grid_constant__ QuantArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((int)blockIdx.x < a.q_ctas) {
-    const int64_t w = (int64_t)blockIdx.x * 8 + warp;
+    if (blockIdx.y > 0) return;
+    const int64_t w = (int64_t)blockIdx.x * kQuantWarps + warp;
     const int64_t t = w / a.rot.split;
     if (t < a.rot.map.total)
       rotate_share<D, PAIRS>(a.rot, (int)t, (int)(w - t * a.rot.split), lane);
@@ -368,20 +497,26 @@ __global__ void __launch_bounds__(256)
   if (threadIdx.x == 0) n_write = 0;
   __syncthreads();
   const int64_t w0 = (int64_t)((int)blockIdx.x - a.q_ctas) * a.window;
-  for (int i = warp; i < a.window; i += 8) {
-    const int64_t t = w0 + i;
-    if (t >= a.rot.map.total) break;
-    const Token k = locate(a.rot.map, (int)t, lane);
-    if (!k.ok || lane != 0) continue;
-    if (t != k.first && (k.pos & 15) != 0) continue;
-    int m = min(16 - (k.pos & 15), k.n - ((int)t - k.first));
-    m = min(m, a.rot.map.rope_len - k.pos);
-    m = min(m, a.rot.map.total - (int)t);
-    write[atomicAdd(&n_write, 1)] = make_int4((int)t, k.pos, k.phys, m);
+  if (warp == 0 && w0 < a.rot.map.total) {
+    // A lane a token: the first one's branch, and on from there.
+    const TokenMap& map = a.rot.map;
+    int br = map.off ? find_branch(map, (int)w0, lane) : (int)w0;
+    const int64_t t = w0 + lane;
+    if (lane < a.window && t < map.total) {
+      while (map.off && br + 1 < map.nb && map.off[br + 1] <= t) ++br;
+      const Token k = place(map, (int)t, br, blockIdx.y == 0);
+      if (k.ok && (t == k.first || (k.pos & 15) == 0)) {
+        int m = min(16 - (k.pos & 15), k.n - ((int)t - k.first));
+        m = min(m, map.rope_len - k.pos);
+        m = min(m, map.total - (int)t);
+        write[atomicAdd(&n_write, 1)] = make_int4((int)t, k.pos, k.phys, m);
+      }
+    }
   }
   __syncthreads();
   const int units = n_write * a.Hkv * 2;
-  for (int u = warp; u < units; u += 8) {
+  for (int u = blockIdx.y * kQuantWarps + warp; u < units;
+       u += kQuantWarps * gridDim.y) {
     const int4 w = write[u / (2 * a.Hkv)];
     const int r = u % (2 * a.Hkv);
     quant_tile<D, PAIRS>(a, r >= a.Hkv, r % a.Hkv, w.x, w.y, w.z, w.w, lane);
@@ -410,10 +545,14 @@ template <int D>
 cudaError_t launch_quant(const QuantArgs& a, bool pairs, cudaStream_t st) {
   const int64_t ctas =
       a.q_ctas + ((int64_t)a.rot.map.total + a.window - 1) / a.window;
+  // A decode step has one write a window, and CTAs to spare.
+  const int share = std::max(1, std::min(a.window > 1 ? 2 : 8,
+                                         2 * a.Hkv / kQuantWarps));
+  const dim3 grid((unsigned)ctas, (unsigned)share);
   if (pairs)
-    quant_append_kernel<D, true><<<(unsigned)ctas, 256, 0, st>>>(a);
+    quant_append_kernel<D, true><<<grid, kQuantWarps * 32, 0, st>>>(a);
   else
-    quant_append_kernel<D, false><<<(unsigned)ctas, 256, 0, st>>>(a);
+    quant_append_kernel<D, false><<<grid, kQuantWarps * 32, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -524,10 +663,23 @@ kv_status rope_append_impl(
                  : rope::launch_rotate<64>(r, pairs, st);
   } else {
     r.split = rope::split_for(total, std::max(its, 1));
-    a.q_ctas = q ? (int)(((int64_t)total * r.split + 7) / 8) : 0;
-    // A decode step's tokens each begin a write: one CTA a token.  In a
-    // chunk about every sixteenth does.
+    // A decode step's tokens each begin a write: one CTA a token, and the
+    // queries in the same launch.  In a chunk about every sixteenth does; the
+    // queries are most of the bytes then and take a launch of their own, which
+    // keeps twice the warps on an SM (24 chunks of 37 to 701 tokens: 73 us in
+    // one launch).
     a.window = off ? 16 : 1;
+    const bool own_launch = off != nullptr && q != nullptr;
+    a.q_ctas = q && !own_launch
+                   ? (int)(((int64_t)total * r.split + rope::kQuantWarps - 1) /
+                           rope::kQuantWarps)
+                   : 0;
+    if (own_launch) {
+      e = d == 128 ? rope::launch_rotate<128>(r, pairs, st)
+                   : rope::launch_rotate<64>(r, pairs, st);
+      if (e != cudaSuccess)
+        return fail(KV_ERR_CUDA, "rope append launch: %s", cudaGetErrorString(e));
+    }
     a.k_new = static_cast<const __nv_bfloat16*>(k_new);
     a.v_new = static_cast<const __nv_bfloat16*>(v_new);
     a.k_token = k_stride;
