@@ -104,7 +104,8 @@ __device__ __forceinline__ int uniform(int v) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// Warp-wide waits polled by every lane, for a warp with nothing else to do.
+// Warp-wide waits polled by every lane.  Polled by one lane with the others
+// waiting for it, a completed barrier was seen some 700 cycles late.
 __device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
@@ -112,27 +113,6 @@ __device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool all_wait_cluster(uint32_t bar,
                                                  uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity));
-}
-
-// Warp-wide waits polled by one lane: 32 lanes polling one barrier each cost
-// a shared-memory access, and eight waiting warps of them take that bandwidth
-// from the tensor pipe's operands.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
-                                          int lane) {
-  bool ok = true;
-  if (lane == 0) ok = mbar_wait(bar, parity);
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  __syncwarp();
-  return ok;
-}
-
-__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
-                                                  int lane) {
-  bool ok = true;
-  if (lane == 0) ok = mbar_wait_cluster(bar, parity);
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  __syncwarp();
-  return ok;
 }
 
 // Report all of this thread's earlier MMAs on the barrier at the same place
@@ -145,6 +125,105 @@ __device__ __forceinline__ void umma_commit_to(uint32_t bar, uint16_t mask) {
       : "memory");
 }
 
+// ---- a pair of CTAs as one unit of the tensor cores (cta_group::2) ---------------
+// D of 256 rows: the even CTA's tensor memory holds rows 0-127, the odd one's rows
+// 128-255, each from its own A; each CTA holds half of B's N.  One thread of the
+// even CTA issues for both; addresses and descriptors hold in both CTAs.
+
+__device__ __forceinline__ void tmem_alloc2(uint32_t where, uint32_t cols) {
+  asm volatile(
+      "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+          where),
+      "r"(cols)
+      : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" :::
+                   "memory");
+}
+
+__device__ __forceinline__ void tmem_free2(uint32_t tmem, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+               "r"(cols)
+               : "memory");
+}
+
+__device__ __forceinline__ void umma2_ts(uint32_t tmem_d, uint32_t tmem_a,
+                                         uint64_t b, uint32_t id,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+          tmem_d),
+      "r"(tmem_a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma2_ss(uint32_t tmem_d, uint64_t a, uint64_t b,
+                                         uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+          tmem_d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+
+// Report all of this thread's earlier pair MMAs on the barrier at the same
+// place in both CTAs.
+__device__ __forceinline__ void umma2_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+      ".multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// Loads of a CTA of the pair that complete on a barrier (cluster address) of
+// either CTA.
+__device__ __forceinline__ void tma2_load_2d(uint32_t dst, const CUtensorMap* tm,
+                                             int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::"
+      "bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(tm), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* tm,
+                                             int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::"
+      "bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma2_load_5d_at(uint32_t dst,
+                                                const CUtensorMap* tm, int x2,
+                                                int x4, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::"
+      "bytes.cta_group::2 [%0], [%1, {%2, %2, %3, %2, %4}], [%5];" ::"r"(dst),
+      "l"(tm), "r"(0), "r"(x2), "r"(x4), "r"(bar)
+      : "memory");
+}
+
+// Arrive on a barrier of a CTA of the cluster with bytes to expect there;
+// relaxed like remote_arrive (a release at cluster scope took 1400 cycles).
+__device__ __forceinline__ void remote_expect_tx(uint32_t cluster_bar,
+                                                 uint32_t bytes) {
+  asm volatile(
+      "mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], "
+      "%1;" ::"r"(cluster_bar),
+      "r"(bytes)
+      : "memory");
+}
+
+__device__ __forceinline__ void cluster_store4(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // One box of a 5-D map whose x0, x1 and x3 start at 0.
 __device__ __forceinline__ void tma_load_5d_at(uint32_t dst,
                                                const CUtensorMap* tm, int x2,
@@ -153,16 +232,6 @@ __device__ __forceinline__ void tma_load_5d_at(uint32_t dst,
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::"
       "bytes [%0], [%1, {%2, %2, %3, %2, %4}], [%5];" ::"r"(dst),
       "l"(tm), "r"(0), "r"(x2), "r"(x4), "r"(bar)
-      : "memory");
-}
-
-// One box of a 3-D map.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
-                                            int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 
@@ -183,12 +252,6 @@ __device__ __forceinline__ uint64_t sdesc_plain(uint32_t addr, uint32_t k,
          ((uint64_t)((m >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
 
-// Ask for `bytes` (a multiple of 16, 16-byte aligned) in L2.
-__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes)
-               : "memory");
-}
-
 // Named barriers over `n` threads (whole warps), combining a predicate.
 __device__ __forceinline__ bool bar_and(int id, int n, bool v) {
   uint32_t r;
@@ -196,19 +259,6 @@ __device__ __forceinline__ bool bar_and(int id, int n, bool v) {
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %3, 0;\n\t"
       "barrier.cta.red.and.pred.aligned q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(n), "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
-}
-
-__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.or.pred.aligned q, %1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(id), "r"(n), "r"((uint32_t)v)

@@ -81,8 +81,6 @@ using tc::umma_copy;
 using tc::umma_ss;
 using tc::umma_ts;
 using tc::uniform;
-using tc::warp_wait;
-using tc::warp_wait_cluster;
 
 constexpr int kRank = KV_LATENT_RANK;
 constexpr int kT = 128;            // tokens of a score tile
@@ -341,7 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int valid = min(min(kT, left), max(seq_len - blk0 * 16, 0)) - wg * kG;
         valid = min(valid, kG);
         float s[kG];
-        const bool w = warp_wait(smem_u32(&bars.s_full[b]), (tc_n >> 1) & 1, lane);
+        const bool w = all_wait(smem_u32(&bars.s_full[b]), (tc_n >> 1) & 1);
         float mx = -INFINITY;
         if (w) {
           fence_after_sync();
@@ -385,8 +383,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool two = left > kG;  // the tile has a second P tile
         if (wg == 0 || two) {
           const uint32_t g = g_n + wg, slot = g % kNP;
-          if (g >= kNP && !warp_wait_cluster(smem_u32(&bars.p_empty[slot]),
-                                             (g / kNP - 1) & 1, lane))
+          if (g >= kNP && !all_wait_cluster(smem_u32(&bars.p_empty[slot]),
+                                             (g / kNP - 1) & 1))
             timed_out(32);
           const uint32_t bar = peer_full + slot * 8;
           const uint32_t dst = peer_p + slot * kP;
@@ -427,8 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {
           const int f = fin_n & 1;
           if (fin_n >= 2 &&
-              !warp_wait_cluster(smem_u32(&bars.fin_empty[f]), (fin_n / 2 - 1) & 1,
-                                 lane))
+              !all_wait_cluster(smem_u32(&bars.fin_empty[f]), (fin_n / 2 - 1) & 1))
             timed_out(33);
           remote_store4(peer_fin + f * 512, __float_as_uint(1.f / l),
                         map_rank(smem_u32(&bars.fin_full[f]), 1));
@@ -575,17 +572,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Stage kn is free; arm it.
     auto arm = [&](uint32_t bytes) {
       const uint32_t s = kn % kNK;
-      if (lane == 0) {
-        ok = !*aborted && (kn < kNK || mbar_wait(smem_u32(&bars.k_empty[s]),
-                                                 (kn / kNK - 1) & 1));
-        if (ok) {
-          if (bytes > 0)
-            mbar_expect_tx(smem_u32(&bars.k_full[s / 2]), bytes);
-          else
-            mbar_arrive(smem_u32(&bars.k_full[s / 2]));
-        }
+      ok = kn < kNK || all_wait(smem_u32(&bars.k_empty[s]), (kn / kNK - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok && !*aborted);
+      if (ok && lane == 0) {
+        if (bytes > 0)
+          mbar_expect_tx(smem_u32(&bars.k_full[s / 2]), bytes);
+        else
+          mbar_arrive(smem_u32(&bars.k_full[s / 2]));
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      __syncwarp();
       return ok;
     };
     while (ok && loop.next(it)) {
@@ -649,12 +644,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int qb = (it.nrows + 15) / 16;
       bool bad;
       int next = lane < kTB ? block_of(p, it, it.blk_begin + lane, bad) : -1;
-      if (lane == 0) {
-        ok = !*aborted && (in == 0 || mbar_wait(smem_u32(&bars.qr_empty), (in - 1) & 1));
-        if (ok) mbar_expect_tx(smem_u32(&bars.qr_full), qb * 2048);
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = in == 0 || all_wait(smem_u32(&bars.qr_empty), (in - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok && !*aborted);
       if (!ok) break;
+      if (lane == 0) mbar_expect_tx(smem_u32(&bars.qr_full), qb * 2048);
+      __syncwarp();
       ++in;
       if (lane < qb)
         tma_load_2d(base + lane * 2048, &tmQ, kRank,
@@ -667,17 +661,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane < kTB && j + 1 < nt)
           next = block_of(p, it, it.blk_begin + (j + 1) * kTB + lane, bad);
         const int n = __popc(__ballot_sync(0xffffffffu, phys >= 0));
-        if (lane == 0) {
-          ok = !*aborted && (tn == 0 || mbar_wait(smem_u32(&bars.r_empty), (tn - 1) & 1));
-          if (ok) {
-            if (n > 0)
-              mbar_expect_tx(smem_u32(&bars.r_full[tn & 1]), n * 2048);
-            else
-              mbar_arrive(smem_u32(&bars.r_full[tn & 1]));
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = tn == 0 || all_wait(smem_u32(&bars.r_empty), (tn - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && !*aborted);
         if (!ok) break;
+        if (lane == 0) {
+          if (n > 0)
+            mbar_expect_tx(smem_u32(&bars.r_full[tn & 1]), n * 2048);
+          else
+            mbar_arrive(smem_u32(&bars.r_full[tn & 1]));
+        }
+        __syncwarp();
         if (phys >= 0)
           tma_load_2d(base + kOffR + lane * 2048, &tmR, 0, phys * 16,
                       smem_u32(&bars.r_full[tn & 1]));
@@ -701,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && loop.next(it)) {
       for (;;) {
-        ok = warp_wait(smem_u32(&bars.event), ev & 1, lane);
+        ok = all_wait(smem_u32(&bars.event), ev & 1);
         if (!ok) break;
         ++ev;
         fence_after_sync();
@@ -731,7 +724,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float inv = 1.f;
       if (direct) {
         const int f = fin_n & 1;
-        ok = warp_wait_cluster(smem_u32(&bars.fin_full[f]), (fin_n >> 1) & 1, lane);
+        ok = all_wait_cluster(smem_u32(&bars.fin_full[f]), (fin_n >> 1) & 1);
         if (!ok) break;
         inv = reinterpret_cast<const float*>(smem + kOffFin + f * 512)[r];
         ++fin_n;
@@ -905,25 +898,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t use = vn / (kNV / 2);  // earlier uses of the stage
         const uint32_t bar = smem_u32(&bars.v_full[s / 2]);
         const int n_load = __popc(__ballot_sync(0xffffffffu, phys >= 0));
-        if (lane == 0) {
-          ok = !*aborted &&
-               (use == 0 || mbar_wait(smem_u32(&bars.v_empty[s]), (use - 1) & 1));
-          if (ok) {
-            if (n_load > 0)
-              mbar_expect_tx(bar, n_load * kVBlk);
-            else
-              mbar_arrive(bar);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = use == 0 || all_wait(smem_u32(&bars.v_empty[s]), (use - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && !*aborted);
         if (!ok) break;
+        if (lane == 0) {
+          if (n_load > 0)
+            mbar_expect_tx(bar, n_load * kVBlk);
+          else
+            mbar_arrive(bar);
+        }
+        __syncwarp();
         if (phys >= 0)
           tma_load_5d_at(base + s * kVStage + lane * kVBlk, &tmV, 0, phys, bar);
         __syncwarp();
         const int last = nblk - 1 - k0 - me * kVB;  // the last block's place here
         if (tail < 16 && last >= 0 && last < kVB) {
           // Rows of the last block past the branch's length: zero.
-          ok = warp_wait(bar, use & 1, lane);
+          ok = all_wait(bar, use & 1);
           if (!ok) break;
           const uint32_t dst = base + s * kVStage + last * kVBlk;
           for (int i = lane; i < (16 - tail) * 64; i += 32) {

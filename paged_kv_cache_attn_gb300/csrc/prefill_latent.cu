@@ -15,15 +15,17 @@
 // products.  Bound by what L2 delivers to an SM (48 KB per four MMAs of 128
 // cycles).
 //
-// Attention kernel: one CTA per tile of 256 query rows (two M-tiles of 128)
-// and head.  TMEM: S of the two M-tiles (2 x 128 columns; P overwrites its S as
-// bf16 pairs) and O (2 x 128).  Q in shared memory (96 KB), K in two stages of
-// 128 tokens (128 expanded dimensions and the 64 shared position dimensions),
-// V in one.  One product warp per M-tile runs PV(j - 1) and then QK(j); when
-// S(j) is complete so is everything before it, so the rows may overwrite P and
-// rescale O without another wait.  The softmax of one M-tile (a thread a row,
-// base 2, lazy maximum) lies behind the other M-tile's products.  Bound by the
-// chain of an M-tile, QK -> softmax -> PV.
+// Attention kernel: a pair of CTAs (cta_group::2) per tile of 256 query rows and
+// head; each CTA has 128 rows and loads half of every key tile of 128 tokens (64
+// tokens of K, 64 columns of V), which leaves room for four stages of each: with
+// whole tiles in one CTA, V had one stage and its load (1.3 us) lay on every
+// tile's path (2.4 us a tile of 256 rows and 128 keys on an SM; 1.3 us here, 0.7
+// of them products).  The rows' two warpgroups take the key tiles in turn, each
+// with its own maximum, sum and O, joined at the end.  TMEM: S (128 columns), P
+// of the two warpgroups (2 x 64, bf16 pairs), O of the two (2 x 128).  QK(j) may
+// overwrite S once it has been read, which the rows do while PV(j - 2) runs; the
+// softmax of a tile (a thread a row, base 2, lazy maximum) thus lies behind the
+// products of two others.
 //
 // Tokens past a row's position are replaced by -inf before the maximum; values
 // of slots past a branch's length are written as zeros by the expansion, and
@@ -44,7 +46,6 @@ using tc::fence_after_sync;
 using tc::fence_before_sync;
 using tc::idesc;
 using tc::sdesc;
-using tc::tma_load_5d_at;
 using tc::tmem_ld32;
 using tc::tmem_st32;
 using tc::tmem_wait_ld;
@@ -53,7 +54,6 @@ using tc::umma_commit;
 using tc::umma_ss;
 using tc::umma_ts;
 using tc::uniform;
-using tc::warp_wait;
 
 constexpr int kRank = KV_LATENT_RANK, kRope = KV_LATENT_ROPE, kHead = KV_LATENT_HEAD;
 constexpr uint32_t kTmemCols = 512;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = blockIdx.x; i < n_work; i += gridDim.x, ++n) {
       const int slot0 = i / p.Hq * 8, h = i % p.Hq;
       const uint32_t b = n & 1;
-      ok = warp_wait(smem_u32(&sh.d_full[b]), (n >> 1) & 1, lane) && !*aborted;
+      ok = all_wait(smem_u32(&sh.d_full[b]), (n >> 1) & 1) && !*aborted;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       fence_after_sync();
@@ -261,13 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < kChunks; ++c, ++k) {
         if ((k & 1) != me) continue;
         const uint32_t s = k % kNS, bar = smem_u32(&sh.full[s]);
-        if (lane == 0) {
-          ok = !*aborted && (k < kNS || mbar_wait(smem_u32(&sh.empty[s]),
-                                                  (k / kNS - 1) & 1));
-          if (ok) mbar_expect_tx(bar, nb * 2048 + kB);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = k < kNS || all_wait(smem_u32(&sh.empty[s]), (k / kNS - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && !*aborted);
         if (!ok) break;
+        if (lane == 0) mbar_expect_tx(bar, nb * 2048 + kB);
+        __syncwarp();
         if (phys >= 0)
           tma_load_2d(base + s * kStage + lane * 2048, &tmX, c * 64, phys * 16, bar);
         else if (lane == 8)
@@ -296,28 +294,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 namespace at {
 
 constexpr int kT = 128, kTB = 8;             // tokens and blocks of a key tile
-constexpr int kQ = 3 * 128 * 128;            // Q of an M-tile: three 64-wide parts
+constexpr int kM = 128;                      // query rows of a CTA
+constexpr int kQ = 3 * kM * 128;             // Q: three 64-wide parts
 constexpr int kBlk = 16 * kHead * 2;         // a block's expanded keys of a head
-constexpr int kKn = kTB * kBlk;              // a K stage: expanded part,
-constexpr int kK = kKn + kT * 128;           // and position part
-constexpr int kV = kTB * kBlk;
-constexpr int kOffK = 2 * kQ;
-constexpr int kOffV = kOffK + 2 * kK;
-constexpr int kTiles = kOffV + kV;
-constexpr int kThreads = 12 * 32;  // warps 0-7 rows, 8 and 11 products, 9-10 loads
-constexpr uint32_t kColO = 256;
+constexpr int kKn = kTB / 2 * kBlk;          // a K stage (64 tokens): expanded part,
+constexpr int kK = kKn + kT / 2 * 128;       // and position part
+constexpr int kV = kT * 128;                 // a V stage: 128 tokens x 64 columns
+constexpr int kNS = 4;                       // stages of K and of V
+constexpr int kOffK = kQ;
+constexpr int kOffV = kOffK + kNS * kK;
+constexpr int kTiles = kOffV + kNS * kV;
+constexpr int kLoads = 3;                    // load warps
+constexpr int kThreads = (9 + kLoads) * 32;  // warps 0-7 rows, 8 products, 9- loads
+constexpr uint32_t kColP = 128, kColO = 256;  // TMEM: S, P (2), O (2)
 constexpr float kRescale = 8.f;    // lazy-max threshold (log2 units)
 
 struct Small {
-  uint64_t q_full, k_full[2], k_empty[2], v_full, v_empty, s_full[2], p_full[2],
-      o_ready[2], turn[2];
+  // q_full, k_full, v_full, s_empty and p_full are used in the even CTA alone.
+  uint64_t q_full, k_full[kNS], k_empty[kNS], v_full[kNS], v_empty[kNS],
+      s_full[2], s_empty, p_full[2], p_empty[2], o_ready;
+  float stat[2][2][kM];  // maximum and sum of the two halves' rows
   uint32_t tmem_base;
   int aborted;
 };
 constexpr int kSmem = kTiles + (int)sizeof(Small);
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ,
                    const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV,
@@ -333,35 +336,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // Launched while the expansion runs: nothing of global memory before this.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int h = blockIdx.x / p.n_tiles;
-  PrefillTile t = p.tiles[blockIdx.x % p.n_tiles];
+  const int rank = (int)tc::cluster_rank();
+  const int item = blockIdx.x >> 1;
+  const int h = item / p.n_tiles;
+  const PrefillTile t = p.tiles[item % p.n_tiles];
   const int len = t.pos0 + t.nrows;  // tokens the tile's last row sees
   const int nblk = (len + 15) / 16;
   if (t.nrows < 1 || t.nrows > kPrefillRows || t.pos0 < 0 || t.row0 < 0 ||
       t.row0 + t.nrows > p.total || t.table < 0 || t.table + nblk > p.n_slots) {
     if (threadIdx.x == 0)
       record_status(p.status, KV_ERR_DEVICE, -1 - (int)blockIdx.x);
-    return;  // the whole CTA, before any barrier
+    return;  // both CTAs, before any barrier
   }
-  const int n_m = t.nrows > 128 ? 2 : 1;
-  // Key tiles of M-tile m: up to its last row's position.
-  auto tiles_of = [&](int m) {
-    return (t.pos0 + min(t.nrows, 128 * (m + 1)) - 1) / kT + 1;
-  };
-  const int nt = tiles_of(n_m - 1);
+  const int nt = (len - 1) / kT + 1;  // key tiles
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&sh.q_full), 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&sh.k_full[s]), 1);
-      mbar_init(smem_u32(&sh.k_empty[s]), n_m);
-      mbar_init(smem_u32(&sh.s_full[s]), 1);
-      mbar_init(smem_u32(&sh.p_full[s]), 4);
-      mbar_init(smem_u32(&sh.o_ready[s]), 1);
-      mbar_init(smem_u32(&sh.turn[s]), 1);
+    mbar_init(smem_u32(&sh.q_full), 2);
+    for (int s = 0; s < kNS; ++s) {
+      mbar_init(smem_u32(&sh.k_full[s]), 2);
+      mbar_init(smem_u32(&sh.k_empty[s]), 1);
+      mbar_init(smem_u32(&sh.v_full[s]), 2);
+      mbar_init(smem_u32(&sh.v_empty[s]), 1);
     }
-    mbar_init(smem_u32(&sh.v_full), 1);
-    mbar_init(smem_u32(&sh.v_empty), n_m);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(smem_u32(&sh.s_full[g]), 1);
+      mbar_init(smem_u32(&sh.p_full[g]), 8);
+      mbar_init(smem_u32(&sh.p_empty[g]), 1);
+    }
+    mbar_init(smem_u32(&sh.s_empty), 8);
+    mbar_init(smem_u32(&sh.o_ready), 1);
     sh.aborted = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
@@ -369,287 +372,300 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmR);
   }
-  if (warp == 8) tmem_alloc(smem_u32(&sh.tmem_base));
+  __syncwarp();
+  if (warp == 8) tc::tmem_alloc2(smem_u32(&sh.tmem_base), kTmemCols);
   fence_before_sync();
-  __syncthreads();
+  tc::cluster_sync();
   fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
   auto timed_out = [&](int site) {
     if (!*aborted) record_status(p.status, KV_ERR_TIMEOUT, site);
     atomicExch(&sh.aborted, 1);
+    tc::cluster_store4(tc::map_rank(smem_u32(&sh.aborted), rank ^ 1), 1u);
   };
 
   if (warp < 8) {
-    // ---- rows: thread = row r of M-tile m ------------------------------------
-    const int m = warp >> 2;
+    // ---- rows: thread = row r, key tiles j = g (mod 2) --------------------------
+    const int g = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
-    if (m < n_m) {
-      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint32_t srow = lane_base + m * kT;
-      const uint32_t orow = lane_base + kColO + m * kHead;
-      const int pos = t.pos0 + m * 128 + r;     // this row's position
-      const int pos_lo = t.pos0 + m * 128 + (warp & 3) * 32;  // the warp's first
-      const int my_nt = tiles_of(m);
-      float m_used = -INFINITY, l = 0.f;
-      bool ok = true;
-      for (int j = 0; j < my_nt; ++j) {
-        ok = warp_wait(smem_u32(&sh.s_full[m]), j & 1, lane);
-        if (!ok) break;
-        fence_after_sync();
-        uint32_t u[4][32];
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t prow = lane_base + kColP + g * 64;
+    const uint32_t orow = lane_base + kColO + g * kHead;
+    const uint32_t s_empty = tc::map_rank(smem_u32(&sh.s_empty), 0);
+    const uint32_t p_full = tc::map_rank(smem_u32(&sh.p_full[g]), 0);
+    const int pos = t.pos0 + rank * kM + r;  // this row's position
+    const int pos_lo = pos - lane;           // the warp's first
+    float m_used = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = g; j < nt; j += 2) {
+      ok = all_wait(smem_u32(&sh.s_full[g]), (j >> 1) & 1);
+      if (!ok) break;
+      fence_after_sync();
+      uint32_t u[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(srow + c * 32, u[c]);
-        tmem_wait_ld();
-        const int seen = pos - j * kT + 1;      // tokens of the tile this row sees
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (pos_lo - j * kT + 1 >= kT) {        // every row of the warp: all
+      for (int c = 0; c < 4; ++c) tmem_ld32(lane_base + c * 32, u[c]);
+      tmem_wait_ld();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::remote_arrive(s_empty);  // S may be overwritten
+      const int seen = pos - j * kT + 1;      // tokens of the tile this row sees
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (pos_lo - j * kT + 1 >= kT) {        // every row of the warp: all
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(u[c][i]));
-        } else {
+          for (int i = 0; i < 32; ++i)
+            m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(u[c][i]));
+      } else {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (c * 32 + i >= seen) u[c][i] = 0xff800000u;  // -inf
-              m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(u[c][i]));
-            }
-        }
-        const float m_tile =
-            fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
-        const bool need = m_tile > m_used + kRescale;
-        const float alpha = need ? ex2(m_used - m_tile) : 1.f;
-        if (need) m_used = m_tile;
-        l *= alpha;
-        const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t pk[32];
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int c = g * 2 + (i >> 4), k = (2 * i) & 31;
-            const float a = ex2(fmaf(__uint_as_float(u[c][k]), p.scale_log2, neg_m));
-            const float b =
-                ex2(fmaf(__uint_as_float(u[c][k + 1]), p.scale_log2, neg_m));
-            s4[i & 3] += a + b;
-            pk[i] = pack_bf16(a, b);
+            if (c * 32 + i >= seen) u[c][i] = 0xff800000u;  // -inf
+            m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(u[c][i]));
           }
-          tmem_st32(srow + g * 32, pk);
-        }
-        l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-        // O holds the products up to tile j - 1, all of them done.
-        if (__any_sync(0xffffffffu, need) && j > 0) tc::rescale_o_row(orow, alpha);
-        tmem_wait_st();
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[m]));
       }
-      if (!ok && lane == 0) timed_out(60);
-      ok = warp_wait(smem_u32(&sh.o_ready[m]), 0, lane) && ok && !*aborted;
-      ok = __all_sync(0xffffffffu, ok);
-      fence_after_sync();
-      if (ok) {
-        const float inv = 1.f / l;
-        // The M-tile's Q has been read: its place turns the rows.
-        uint8_t* turn = smem + m * kQ + (warp & 3) * 2048;
-        const int n = t.nrows - m * 128 - (warp & 3) * 32;  // rows of the warp
-        const int64_t row0 = t.row0 + m * 128 + (warp & 3) * 32;
-#pragma unroll 1
-        for (int c = 0; c < kHead; c += 32) {
-          uint32_t v[32], w[16];
-          tmem_ld32(orow + c, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            w[k] = pack_bf16(__uint_as_float(v[2 * k]) * inv,
-                             __uint_as_float(v[2 * k + 1]) * inv);
-          put_rows(turn, w, lane, [&](int rr) -> uint8_t* {
-            if (rr >= n) return nullptr;
-            return reinterpret_cast<uint8_t*>(
-                p.out + ((row0 + rr) * p.Hq + h) * kHead + c);
-          });
-        }
-      }
-    }
-  } else if (warp == 8 || warp == 11) {
-    // ---- products of one M-tile (uniform warp, one lane issues) ---------------
-    const int m = warp == 8 ? 0 : 1;
-    if (m < n_m) {
-      constexpr uint32_t id_qk = idesc(128, kT, false);
-      constexpr uint32_t id_pv = idesc(128, kHead, true);
-      const bool lead = elect_one();
-      const int all = uniform(nt), mine = uniform(tiles_of(m));
-      const int blocks = uniform(nblk);
-      const uint32_t ds = tmem + m * kT, dout = tmem + kColO + m * kHead;
-      bool ok = all_wait(smem_u32(&sh.q_full), 0);
-      // PV(j) needs P and V; where the M-tile is past its last key tile, the
-      // tile is only released.
-      auto pv_ready = [&](int j) {
-        if (j < mine && !all_wait(smem_u32(&sh.p_full[m]), j & 1)) return false;
-        return all_wait(smem_u32(&sh.v_full), j & 1);
-      };
-      auto pv = [&](int j) {  // one lane: O += P(j) V(j)
-        if (j < mine) {
-          const int nb = min(kTB, blocks - j * kTB);
-#pragma unroll
-          for (int k = 0; k < kTB; ++k)
-            if (k < nb)
-              umma_ts(dout, ds + k * 8, sdesc(base + kOffV + k * kBlk, 1024, 2048),
-                      id_pv, j > 0 || k > 0 ? 1u : 0u);
-          umma_commit(smem_u32(&sh.v_empty));
-          if (j == mine - 1) umma_commit(smem_u32(&sh.o_ready[m]));
-        } else {
-          mbar_arrive(smem_u32(&sh.v_empty));
-        }
-      };
-      for (int j = 0; j < all && ok; ++j) {
-        if (j > 0) ok = pv_ready(j - 1);
-        ok = ok && all_wait(smem_u32(&sh.k_full[j & 1]), (j >> 1) & 1);
-        // The M-tiles' products alternate in whole blocks: issued side by side
-        // they would interleave, both softmaxes would start when both were done,
-        // and the tensor pipe would idle meanwhile (2.6 us a key tile instead of
-        // 1.9).
-        if (n_m == 2 && (m == 1 || j > 0))
-          ok = ok && all_wait(smem_u32(&sh.turn[m]), (m == 1 ? j : j - 1) & 1);
+      const float m_tile =
+          fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+      const bool need = m_tile > m_used + kRescale;
+      const float alpha = need ? ex2(m_used - m_tile) : 1.f;
+      if (need) m_used = m_tile;
+      l *= alpha;
+      const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+      float s4[4] = {0.f, 0.f, 0.f, 0.f};
+      // PV(j - 2) done: P may be overwritten, and O rescaled.
+      if (j > 1) {
+        ok = all_wait(smem_u32(&sh.p_empty[g]), ((j - 2) >> 1) & 1);
         if (!ok) break;
         fence_after_sync();
-        const uint32_t kst = base + kOffK + (j & 1) * kK;
-        if (lead) {
-          if (j > 0) pv(j - 1);
-          if (j < mine) {
-            const uint64_t qd = sdesc(base + m * kQ, 16, 1024);
+      }
+#pragma unroll
+      for (int c2 = 0; c2 < 2; ++c2) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int c = c2 * 2 + (i >> 4), k = (2 * i) & 31;
+          const float a = ex2(fmaf(__uint_as_float(u[c][k]), p.scale_log2, neg_m));
+          const float b =
+              ex2(fmaf(__uint_as_float(u[c][k + 1]), p.scale_log2, neg_m));
+          s4[i & 3] += a + b;
+          pk[i] = pack_bf16(a, b);
+        }
+        tmem_st32(prow + c2 * 32, pk);
+      }
+      l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      if (__any_sync(0xffffffffu, need) && j > 1) tc::rescale_o_row(orow, alpha);
+      tmem_wait_st();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::remote_arrive(p_full);
+    }
+    if (!ok && lane == 0) timed_out(60);
+    ok = all_wait(smem_u32(&sh.o_ready), 0) && ok && !*aborted;
+    sh.stat[g][0][r] = m_used;
+    sh.stat[g][1][r] = l;
+    ok = tc::bar_and(1, 256, ok);
+    fence_after_sync();
+    if (ok) {
+      // The two halves of the key tiles joined; each warp 64 columns.
+      const float m0 = sh.stat[0][0][r], m1 = sh.stat[1][0][r];
+      const float top = fmaxf(m0, m1);  // finite: every row sees token 0
+      const float e0 = ex2(m0 - top), e1 = ex2(m1 - top);
+      const float inv = 1.f / (e0 * sh.stat[0][1][r] + e1 * sh.stat[1][1][r]);
+      const float w0 = e0 * inv, w1 = e1 * inv;
+      const bool second = nt > 1;  // else the second O has not been written
+      // Q has been read: its place turns the rows.
+      uint8_t* turn = smem + warp * 2048;
+      const int n = t.nrows - rank * kM - (warp & 3) * 32;  // rows of the warp
+      const int64_t row0 = t.row0 + rank * kM + (warp & 3) * 32;
+#pragma unroll 1
+      for (int c = g * 64; c < g * 64 + 64; c += 32) {
+        uint32_t v[32], v1[32], w[16];
+        tmem_ld32(lane_base + kColO + c, v);
+        tmem_ld32(lane_base + kColO + kHead + c, v1);
+        tmem_wait_ld();
+        float o[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          o[k] = __uint_as_float(v[k]) * w0 +
+                 (second ? __uint_as_float(v1[k]) * w1 : 0.f);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[k] = pack_bf16(o[2 * k], o[2 * k + 1]);
+        put_rows(turn, w, lane, [&](int rr) -> uint8_t* {
+          if (rr >= n) return nullptr;
+          return reinterpret_cast<uint8_t*>(
+              p.out + ((row0 + rr) * p.Hq + h) * kHead + c);
+        });
+      }
+    }
+  } else if (warp == 8) {
+    // ---- products of both CTAs (uniform warp, one lane issues) -------------------
+    if (rank == 0) {
+      constexpr uint32_t id_qk = idesc(256, kT, false);
+      constexpr uint32_t id_pv = idesc(256, kHead, true);
+      const bool lead = elect_one();
+      const int n = uniform(nt), blocks = uniform(nblk);
+      bool ok = all_wait(smem_u32(&sh.q_full), 0);
+      // QK(j) and PV(j - 2) in turn: the rows read S(j) while PV(j - 2) runs.
+      for (int j = 0; j < n + 2 && ok; ++j) {
+        if (j < n) {
+          ok = all_wait(smem_u32(&sh.k_full[j % kNS]), (j / kNS) & 1) &&
+               (j == 0 || all_wait(smem_u32(&sh.s_empty), (j - 1) & 1));
+          if (!ok) break;
+          fence_after_sync();
+          if (lead) {
+            const uint32_t kst = base + kOffK + (j % kNS) * kK;
+            const uint64_t qd = sdesc(base, 16, 1024);
             const uint64_t kd = sdesc(kst, 16, 2048);
             const uint64_t rd = sdesc(kst + kKn, 16, 1024);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              umma_ss(ds, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
-                      kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), id_qk,
-                      k > 0 ? 1u : 0u);
+              tc::umma2_ss(tmem, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                           kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), id_qk,
+                           k > 0 ? 1u : 0u);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_ss(ds, qd + ((2 * 16384 + k * 32) >> 4), rd + k * 2, id_qk, 1u);
-            umma_commit(smem_u32(&sh.k_empty[j & 1]));
-            umma_commit(smem_u32(&sh.s_full[m]));
-          } else {
-            mbar_arrive(smem_u32(&sh.k_empty[j & 1]));
+              tc::umma2_ss(tmem, qd + ((2 * 16384 + k * 32) >> 4), rd + k * 2,
+                           id_qk, 1u);
+            tc::umma2_commit(smem_u32(&sh.s_full[j & 1]));
+            tc::umma2_commit(smem_u32(&sh.k_empty[j % kNS]));
           }
-          if (n_m == 2) mbar_arrive(smem_u32(&sh.turn[m ^ 1]));
+          __syncwarp();
         }
-        __syncwarp();
+        const int i = j - 2;
+        if (i >= 0) {
+          ok = all_wait(smem_u32(&sh.v_full[i % kNS]), (i / kNS) & 1) &&
+               all_wait(smem_u32(&sh.p_full[i & 1]), (i >> 1) & 1);
+          if (!ok) break;
+          fence_after_sync();
+          if (lead) {
+            const uint32_t pcol = tmem + kColP + (i & 1) * 64;
+            const uint32_t dout = tmem + kColO + (i & 1) * kHead;
+            const int nb = min(kTB, blocks - i * kTB);
+            const uint64_t vd = sdesc(base + kOffV + (i % kNS) * kV, 1024, 1024);
+#pragma unroll
+            for (int k = 0; k < kTB; ++k)
+              if (k < nb)
+                tc::umma2_ts(dout, pcol + k * 8, vd + k * (2048 >> 4), id_pv,
+                             i > 1 || k > 0 ? 1u : 0u);
+            tc::umma2_commit(smem_u32(&sh.p_empty[i & 1]));
+            tc::umma2_commit(smem_u32(&sh.v_empty[i % kNS]));
+          }
+          __syncwarp();
+        }
         ok = !*aborted;
       }
-      if (ok) ok = pv_ready(all - 1);
-      if (ok) {
-        fence_after_sync();
-        if (lead) pv(all - 1);
-      }
       if (lead) {
-        if (!ok) {
-          timed_out(61);
-          umma_commit(smem_u32(&sh.o_ready[m]));  // let the rows end
-        }
-        // Every product this warp issued has finished once this lands.
-        if (!ok) mbar_wait(smem_u32(&sh.o_ready[m]), 0);
+        if (!ok) timed_out(61);
+        // Every product has finished once this lands: the rows may end, and the
+        // pair's shared memory is no longer read.
+        tc::umma2_commit(smem_u32(&sh.o_ready));
+        if (!mbar_wait(smem_u32(&sh.o_ready), 0)) timed_out(64);
       }
     }
   } else {
-    // ---- loads: warp 9 Q and K, warp 10 V ---------------------------------------
-    const bool is_v = warp == 10;
+    // ---- loads of this CTA's halves: its rows of Q, half of a key tile's keys,
+    // half of the values' columns; a warp takes every third key tile --------------
+    const int me = warp - 9;
     bool ok = true;
     // The expansion's stores, read by bulk copies from here on.
     asm volatile("fence.proxy.async;" ::: "memory");
-    if (!is_v) {
-      if (lane == 0) mbar_expect_tx(smem_u32(&sh.q_full), n_m * kQ);
+    if (me == 0) {
+      const uint32_t bar = tc::map_rank(smem_u32(&sh.q_full), 0);
+      if (lane == 0) tc::remote_expect_tx(bar, kQ);
       __syncwarp();
-      if (lane < 3 * n_m)
-        tc::tma_load_3d(base + (lane / 3) * kQ + (lane % 3) * 16384, &tmQ,
-                        (lane % 3) * 64, h, t.row0 + (lane / 3) * 128,
-                        smem_u32(&sh.q_full));
+      if (lane < 3)
+        tc::tma2_load_3d(base + lane * 16384, &tmQ, lane * 64, h,
+                         t.row0 + rank * kM, bar);
       __syncwarp();
     }
-    auto slot_of = [&](int blk) {
-      if (blk >= nblk) return -1;
+    // Lanes 0-3 the half's expanded keys, 4-7 its position keys, 8-15 values.
+    const int kb = rank * 4 + (lane & 3);  // K block of the tile
+    const int bi = lane < 8 ? kb : lane & 7;
+    int j = me;
+    auto slot_of = [&](int tile) {
+      const int blk = tile * kTB + bi;
+      if (lane >= 16 || tile >= nt || blk >= nblk) return -1;
       const int s = p.slots[t.table + blk];
       if (s >= 0 && s < p.n_uniq) return s;
-      if (!is_v && lane < 8) record_status(p.status, KV_ERR_DEVICE, s);
+      record_status(p.status, KV_ERR_DEVICE, s);
       return -1;
     };
-    // K: lanes 0-7 the blocks' expanded keys, lanes 8-15 their position keys.
-    const int bi = lane & 7;
-    const bool part = lane < (is_v ? 8 : 16);
-    int next = part ? slot_of(bi) : -1;
-    int next_phys = !is_v && lane >= 8 && next >= 0 ? p.uniq[next] : -1;
-    int j = 0;
-    for (; j < nt; ++j) {
+    auto phys_of = [&](int slot) {
+      if (lane < 4 || lane >= 8 || slot < 0) return -1;
+      const int b = p.uniq[slot];
+      return b >= 0 && b < p.num_blocks ? b : -1;
+    };
+    int next = slot_of(j), next_phys = phys_of(next);
+    for (; j < nt; j += kLoads) {
       const int slot = next, phys = next_phys;
-      next = part && j + 1 < nt ? slot_of((j + 1) * kTB + bi) : -1;
-      next_phys = !is_v && lane >= 8 && next >= 0 ? p.uniq[next] : -1;
-      const bool pos_ok = phys >= 0 && phys < p.num_blocks;
-      const bool load = slot >= 0 && (is_v || lane < 8 || pos_ok);
+      next = slot_of(j + kLoads);
+      next_phys = phys_of(next);
+      const bool load = slot >= 0 && (lane < 4 || lane >= 8 || phys >= 0);
       const uint32_t act = __ballot_sync(0xffffffffu, load);
-      const uint32_t bar =
-          is_v ? smem_u32(&sh.v_full) : smem_u32(&sh.k_full[j & 1]);
-      if (lane == 0) {
-        if (is_v)
-          ok = j == 0 || mbar_wait(smem_u32(&sh.v_empty), (j - 1) & 1);
-        else
-          ok = j < 2 || mbar_wait(smem_u32(&sh.k_empty[j & 1]), ((j >> 1) - 1) & 1);
-        ok = ok && !*aborted;
-        const uint32_t bytes = __popc(act & 0xff) * kBlk + __popc(act >> 8) * 2048;
-        if (ok) {
-          if (bytes > 0)
-            mbar_expect_tx(bar, bytes);
-          else
-            mbar_arrive(bar);
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      if (load) {
-        if (is_v)
-          tc::tma_load_5d(base + kOffV + bi * kBlk, &tmV, slot * p.Hq + h, bar);
-        else if (lane < 8)
-          tc::tma_load_5d(base + kOffK + (j & 1) * kK + bi * kBlk, &tmK,
-                          slot * p.Hq + h, bar);
-        else
-          tma_load_2d(base + kOffK + (j & 1) * kK + kKn + bi * 2048, &tmR, 0,
-                      phys * 16, bar);
-      }
+      const int s = j % kNS;
+      const uint32_t kbar = tc::map_rank(smem_u32(&sh.k_full[s]), 0);
+      const uint32_t vbar = tc::map_rank(smem_u32(&sh.v_full[s]), 0);
+      if (j >= kNS)
+        ok = all_wait(smem_u32(&sh.k_empty[s]), (j / kNS - 1) & 1);
+      ok = ok && !*aborted;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0)
+        tc::remote_expect_tx(kbar, __popc(act & 0xf) * kBlk +
+                                        __popc(act & 0xf0) * 2048);
+      __syncwarp();
+      const uint32_t kst = base + kOffK + s * kK;
+      if (load && lane < 4)
+        tc::tma2_load_5d_at(kst + lane * kBlk, &tmK, 0, slot * p.Hq + h, kbar);
+      else if (load && lane < 8)
+        tc::tma2_load_2d(kst + kKn + (lane - 4) * 2048, &tmR, 0, phys * 16, kbar);
+      __syncwarp();
+      if (j >= kNS)
+        ok = all_wait(smem_u32(&sh.v_empty[s]), (j / kNS - 1) & 1);
+      ok = ok && !*aborted;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) tc::remote_expect_tx(vbar, __popc(act >> 8) * 2048);
+      __syncwarp();
+      if (load && lane >= 8)
+        tc::tma2_load_5d_at(base + kOffV + s * kV + bi * 2048, &tmV, rank,
+                            slot * p.Hq + h, vbar);
       __syncwarp();
     }
-    if (lane == 0) {
-      if (!ok) timed_out(is_v ? 63 : 62);
-      // Loads in flight land before the CTA can leave.
-      if (is_v) {
-        if (j > 0) mbar_wait(smem_u32(&sh.v_full), (j - 1) & 1);
-      } else {
-        mbar_wait(smem_u32(&sh.q_full), 0);
-        for (int k = j > 2 ? j - 2 : 0; k < j; ++k)
-          mbar_wait(smem_u32(&sh.k_full[k & 1]), (k >> 1) & 1);
-      }
-    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok && lane == 0) timed_out(62);
   }
   __syncwarp();
   fence_before_sync();
   __syncthreads();
+  // After a time-out loads may be in flight (else every one has been waited for
+  // by a product): both CTAs' report here.
+  if (*aborted && rank == 0 && threadIdx.x == 0) {
+    mbar_wait(smem_u32(&sh.q_full), 0);
+    for (int j = nt > kNS ? nt - kNS : 0; j < nt; ++j)
+      if (!mbar_wait(smem_u32(&sh.k_full[j % kNS]), (j / kNS) & 1) ||
+          !mbar_wait(smem_u32(&sh.v_full[j % kNS]), (j / kNS) & 1))
+        break;
+  }
+  __syncwarp();
+  tc::cluster_sync();
   fence_after_sync();
-  if (warp == 8) tmem_free(tmem);
+  if (warp == 8) tc::tmem_free2(tmem, kTmemCols);
+  tc::cluster_sync();  // neither CTA leaves before both have given it back
 }
 
 }  // namespace at
 
 // ---- host side ------------------------------------------------------------------
 
-// Expanded keys or values, [slot][Hq][16][128] bf16: a box is a (slot, head)
-// tile of 4 KB, landing as four 1 KB atoms of 8 rows x 64 columns ordered (rows
-// 0-7, half 0), (0-7, 1), (8-15, 0), (8-15, 1).
-kv_status make_expanded_map(CUtensorMap* tm, const void* base, int64_t tiles) {
+// Expanded keys or values, [slot][Hq][16][128] bf16.  Keys: a box is a (slot,
+// head) tile of 4 KB, landing as four 1 KB atoms of 8 rows x 64 columns ordered
+// (rows 0-7, half 0), (0-7, 1), (8-15, 0), (8-15, 1).  Values: one half of the
+// columns, (rows 0-7), (8-15).
+kv_status make_expanded_map(CUtensorMap* tm, const void* base, int64_t tiles,
+                            int halves) {
   const cuuint64_t dims[5] = {64, 8, 2, 2, (cuuint64_t)tiles};
   const cuuint64_t strides[4] = {256, 128, 2048, 4096};
-  const cuuint32_t box[5] = {64, 8, 2, 2, 1};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)halves, 2, 1};
   return encode_bf16_map(tm, base, 5, dims, strides, box);
 }
 
@@ -712,7 +728,7 @@ extern "C" kv_status paged_latent_prefill_attn(
       info->n_tile_items < 0 || info->partial_rows < 0 ||
       info->partial_rows > INT32_MAX || (total > 0) != (info->n_tile_items > 0) ||
       (total > 0) != (info->n_row_items > 0) ||
-      (int64_t)info->n_tile_items * Hq > INT32_MAX ||
+      (int64_t)info->n_tile_items * Hq > INT32_MAX / 2 ||
       (int64_t)info->n_row_items * Hq > INT32_MAX / 2)
     return fail(KV_ERR_INVALID_ARG, "plan info does not match the step");
   const size_t need = pkv::prefill_workspace(info->n_row_items, Hq);
@@ -751,8 +767,8 @@ extern "C" kv_status paged_latent_prefill_attn(
                                          rank, 2 * head_dim))
     return s;
   if (kv_status s = pre::make_query_map(&tq, q, total, Hq)) return s;
-  if (kv_status s = pre::make_expanded_map(&tk, p.k_exp, tiles)) return s;
-  if (kv_status s = pre::make_expanded_map(&tv, p.v_exp, tiles)) return s;
+  if (kv_status s = pre::make_expanded_map(&tk, p.k_exp, tiles, 2)) return s;
+  if (kv_status s = pre::make_expanded_map(&tv, p.v_exp, tiles, 1)) return s;
   if (kv_status s = pre::make_matrix_map(&tr, r_pool, num_blocks * 16, rope_dim, 16))
     return s;
   static std::atomic<uint64_t> opted_ex{0}, opted_at{0};
@@ -772,7 +788,7 @@ extern "C" kv_status paged_latent_prefill_attn(
   e = cudaGetLastError();
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "expansion kernel: %s", cudaGetErrorString(e));
-  e = pkv::launch_early(pre::at::prefill_kernel, p.n_tiles * Hq,
+  e = pkv::launch_early(pre::at::prefill_kernel, 2 * p.n_tiles * Hq,
                         pre::at::kThreads, pre::at::kSmem, st, tq, tk, tv, tr, p);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "prefill kernel: %s", cudaGetErrorString(e));
