@@ -15,22 +15,25 @@
 // products.  Bound by what L2 delivers to an SM (48 KB per four MMAs of 128
 // cycles).
 //
-// Attention kernel: a pair of CTAs (cta_group::2) per tile of 256 query rows and
-// head; each CTA has 128 rows and loads half of every key tile of 128 tokens (64
-// tokens of K, 64 columns of V), which leaves room for four stages of each: with
-// whole tiles in one CTA, V had one stage and its load (1.3 us) lay on every
-// tile's path (2.4 us a tile of 256 rows and 128 keys on an SM; 1.3 us here, 0.7
-// of them products).  The rows' two warpgroups take the key tiles in turn, each
-// with its own maximum, sum and O, joined at the end.  TMEM: S (128 columns), P
-// of the two warpgroups (2 x 64, bf16 pairs), O of the two (2 x 128).  QK(j) may
-// overwrite S once it has been read, which the rows do while PV(j - 2) runs; the
-// softmax of a tile (a thread a row, base 2, lazy maximum) thus lies behind the
-// products of two others.
+// Attention kernel: pairs of CTAs (cta_group::2), one on every two SMs, that take
+// work items (a tile of 256 query rows and a head) as they come.  Each CTA has 128
+// of the rows and loads half of every key tile of 128 tokens (64 tokens of K, 64
+// columns of V), which leaves room for four stages of each: with whole tiles in
+// one CTA, V had one stage and its load (1.3 us) lay on every tile's path (2.4 us
+// a tile of 256 rows and 128 keys on an SM; 1.4 us here, 1.25 of them products).
+// The rows' two warpgroups take the key tiles in turn, each with its own maximum,
+// sum and O, joined at the item's end.  TMEM: S (128 columns), P of the two
+// warpgroups (2 x 64, bf16 pairs), O of the two (2 x 128).  QK(j) may overwrite S
+// once it has been read, which the rows do while PV(j - 2) runs; the softmax of a
+// tile (a thread a row, base 2, lazy maximum, two columns to an instruction) lies
+// behind the products of two others.  Bound by power: 1 x 8192 tokens with 32
+// heads run at 1.6 PFLOP/s, 1.5 when repeated without a pause.
 //
 // Tokens past a row's position are replaced by -inf before the maximum; values
 // of slots past a branch's length are written as zeros by the expansion, and
 // blocks past the tile's range take no part in PV.
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -67,7 +70,8 @@ struct Params {
   __nv_bfloat16* v_exp;
   __nv_bfloat16* out;     // [total][Hq][128]
   DeviceStatus* status;
-  int n_uniq, n_slots, n_tiles, Hq, total;
+  int* next;              // work items handed out past the first of each pair
+  int n_uniq, n_slots, n_tiles, Hq, total, heads;  // heads of a group
   int64_t num_blocks;
   float scale_log2;
 };
@@ -86,6 +90,29 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                "r"(kTmemCols)
                : "memory");
+}
+
+// Two fp32 in one operation.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // 32 rows x 64 bytes of a warp (lane = row, w = its 16 words) out to dst(row)
@@ -303,22 +330,33 @@ constexpr int kV = kT * 128;                 // a V stage: 128 tokens x 64 colum
 constexpr int kNS = 4;                       // stages of K and of V
 constexpr int kOffK = kQ;
 constexpr int kOffV = kOffK + kNS * kK;
-constexpr int kTiles = kOffV + kNS * kV;
+constexpr int kOffTurn = kOffV + kNS * kV;
+constexpr int kTiles = kOffTurn + 8 * 2048;
 constexpr int kLoads = 3;                    // load warps
 constexpr int kThreads = (9 + kLoads) * 32;  // warps 0-7 rows, 8 products, 9- loads
 constexpr uint32_t kColP = 128, kColO = 256;  // TMEM: S, P (2), O (2)
 constexpr float kRescale = 8.f;    // lazy-max threshold (log2 units)
 
 struct Small {
-  // q_full, k_full, v_full, s_empty and p_full are used in the even CTA alone.
+  // q_full, k_full, v_full, s_empty, p_full and o_empty are used in the even CTA
+  // alone, item_empty in the odd one.
   uint64_t q_full, k_full[kNS], k_empty[kNS], v_full[kNS], v_empty[kNS],
-      s_full[2], s_empty, p_full[2], p_empty[2], o_ready;
+      s_full[2], s_empty, p_full[2], p_empty[2], o_ready, o_empty, q_empty,
+      item_full[2], item_empty[2];
+  int4 item[2];          // PrefillTile,
+  int item_head[2];      // and head, -1: no more
   float stat[2][2][kM];  // maximum and sum of the two halves' rows
   uint32_t tmem_base;
   int aborted;
 };
 constexpr int kSmem = kTiles + (int)sizeof(Small);
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+
+__device__ __forceinline__ int next_index(const Params& p, int pairs, int lane) {
+  int i = 0;
+  if (lane == 0) i = pairs + atomicAdd(p.next, 1);
+  return __shfl_sync(0xffffffffu, i, 0);
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -337,18 +375,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // Launched while the expansion runs: nothing of global memory before this.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rank = (int)tc::cluster_rank();
-  const int item = blockIdx.x >> 1;
-  const int h = item / p.n_tiles;
-  const PrefillTile t = p.tiles[item % p.n_tiles];
-  const int len = t.pos0 + t.nrows;  // tokens the tile's last row sees
-  const int nblk = (len + 15) / 16;
-  if (t.nrows < 1 || t.nrows > kPrefillRows || t.pos0 < 0 || t.row0 < 0 ||
-      t.row0 + t.nrows > p.total || t.table < 0 || t.table + nblk > p.n_slots) {
-    if (threadIdx.x == 0)
-      record_status(p.status, KV_ERR_DEVICE, -1 - (int)blockIdx.x);
-    return;  // both CTAs, before any barrier
-  }
-  const int nt = (len - 1) / kT + 1;  // key tiles
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&sh.q_full), 2);
@@ -365,6 +391,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&sh.s_empty), 8);
     mbar_init(smem_u32(&sh.o_ready), 1);
+    mbar_init(smem_u32(&sh.o_empty), 16);
+    mbar_init(smem_u32(&sh.q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.item_full[i]), 1);
+      mbar_init(smem_u32(&sh.item_empty[i]), 2 * (8 + kLoads) + 1);
+    }
     sh.aborted = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
@@ -384,8 +416,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::cluster_store4(tc::map_rank(smem_u32(&sh.aborted), rank ^ 1), 1u);
   };
 
+  // The pair's items in turn; `tiles0` key tiles came before the item, and its
+  // tile j is tile tiles0 + j of the pair's stream, which the stages, barriers and
+  // the warpgroups' turns go by.
+  struct Items {
+    PrefillTile t;
+    int h, nt = 0, nblk;
+    uint32_t n = 0, tiles0 = 0;  // n: items taken
+  } it;
+  auto next_item = [&](bool& ok) {
+    it.tiles0 += it.nt;
+    const uint32_t slot = it.n & 1;
+    ok = ok && tc::all_wait_cluster(smem_u32(&sh.item_full[slot]), (it.n >> 1) & 1);
+    if (!ok) return false;
+    const int4 v = sh.item[slot];
+    it.t = {v.x, v.y, v.z, v.w};
+    it.h = sh.item_head[slot];
+    __syncwarp();
+    if (lane == 0)
+      tc::remote_arrive(tc::map_rank(smem_u32(&sh.item_empty[slot]), 1));
+    ++it.n;
+    const int len = it.t.pos0 + it.t.nrows;  // tokens the tile's last row sees
+    it.nblk = (len + 15) / 16;
+    it.nt = (len - 1) / kT + 1;
+    return it.h >= 0;
+  };
+
   if (warp < 8) {
-    // ---- rows: thread = row r, key tiles j = g (mod 2) --------------------------
+    // ---- rows: thread = row r, every second key tile ----------------------------
     const int g = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -393,89 +451,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t orow = lane_base + kColO + g * kHead;
     const uint32_t s_empty = tc::map_rank(smem_u32(&sh.s_empty), 0);
     const uint32_t p_full = tc::map_rank(smem_u32(&sh.p_full[g]), 0);
-    const int pos = t.pos0 + rank * kM + r;  // this row's position
-    const int pos_lo = pos - lane;           // the warp's first
-    float m_used = -INFINITY, l = 0.f;
+    const uint32_t o_empty = tc::map_rank(smem_u32(&sh.o_empty), 0);
     bool ok = true;
-    for (int j = g; j < nt; j += 2) {
-      ok = all_wait(smem_u32(&sh.s_full[g]), (j >> 1) & 1);
-      if (!ok) break;
-      fence_after_sync();
-      uint32_t u[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(lane_base + c * 32, u[c]);
-      tmem_wait_ld();
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::remote_arrive(s_empty);  // S may be overwritten
-      const int seen = pos - j * kT + 1;      // tokens of the tile this row sees
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (pos_lo - j * kT + 1 >= kT) {        // every row of the warp: all
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(u[c][i]));
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (c * 32 + i >= seen) u[c][i] = 0xff800000u;  // -inf
-            m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(u[c][i]));
-          }
-      }
-      const float m_tile =
-          fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
-      const bool need = m_tile > m_used + kRescale;
-      const float alpha = need ? ex2(m_used - m_tile) : 1.f;
-      if (need) m_used = m_tile;
-      l *= alpha;
-      const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-      float s4[4] = {0.f, 0.f, 0.f, 0.f};
-      // PV(j - 2) done: P may be overwritten, and O rescaled.
-      if (j > 1) {
-        ok = all_wait(smem_u32(&sh.p_empty[g]), ((j - 2) >> 1) & 1);
+    // All or none go on: they meet at the item's end.
+    while (tc::bar_and(1, 256, next_item(ok))) {
+      const PrefillTile t = it.t;
+      const int nt = it.nt, h = it.h;
+      const int pos = t.pos0 + rank * kM + r;  // this row's position
+      const int pos_lo = pos - lane;           // the warp's first
+      float m_used = -INFINITY, l = 0.f;
+      for (int j = (it.tiles0 ^ g) & 1; j < nt; j += 2) {
+        const uint32_t q = it.tiles0 + j;
+        ok = all_wait(smem_u32(&sh.s_full[g]), (q >> 1) & 1);
         if (!ok) break;
         fence_after_sync();
-      }
+        uint32_t u[4][32];
 #pragma unroll
-      for (int c2 = 0; c2 < 2; ++c2) {
-        uint32_t pk[32];
+        for (int c = 0; c < 4; ++c) tmem_ld32(lane_base + c * 32, u[c]);
+        tmem_wait_ld();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::remote_arrive(s_empty);  // S may be overwritten
+        const int seen = pos - j * kT + 1;      // tokens of the tile this row sees
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (pos_lo - j * kT + 1 >= kT) {        // every row of the warp: all
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int c = c2 * 2 + (i >> 4), k = (2 * i) & 31;
-          const float a = ex2(fmaf(__uint_as_float(u[c][k]), p.scale_log2, neg_m));
-          const float b =
-              ex2(fmaf(__uint_as_float(u[c][k + 1]), p.scale_log2, neg_m));
-          s4[i & 3] += a + b;
-          pk[i] = pack_bf16(a, b);
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(u[c][i]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (c * 32 + i >= seen) u[c][i] = 0xff800000u;  // -inf
+              m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(u[c][i]));
+            }
         }
-        tmem_st32(prow + c2 * 32, pk);
+        const float m_tile =
+            fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+        const bool need = m_tile > m_used + kRescale;
+        const float alpha = need ? ex2(m_used - m_tile) : 1.f;
+        if (need) m_used = m_tile;
+        l *= alpha;
+        const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+        const uint64_t neg2 = pack2(neg_m, neg_m);
+        uint64_t s2[2] = {0, 0};  // sums of the even and the odd columns, twice
+#pragma unroll
+        for (int c2 = 0; c2 < 2; ++c2) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int c = c2 * 2 + (i >> 4), k = (2 * i) & 31;
+            float a, b;
+            unpack2(fma2((uint64_t)u[c][k + 1] << 32 | u[c][k], scale2, neg2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            s2[i & 1] = add2(s2[i & 1], pack2(a, b));
+            pk[i] = pack_bf16(a, b);
+          }
+          if (c2 == 0 && j > 1) {
+            // PV(j - 2) done: P may be overwritten, and O rescaled.
+            ok = all_wait(smem_u32(&sh.p_empty[g]), ((q - 2) >> 1) & 1);
+            if (!ok) break;
+            fence_after_sync();
+          }
+          tmem_st32(prow + c2 * 32, pk);
+        }
+        if (!ok) break;
+        float s_even, s_odd;
+        unpack2(add2(s2[0], s2[1]), s_even, s_odd);
+        l += s_even + s_odd;
+        if (__any_sync(0xffffffffu, need) && j > 1) tc::rescale_o_row(orow, alpha);
+        tmem_wait_st();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::remote_arrive(p_full);
       }
-      l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-      if (__any_sync(0xffffffffu, need) && j > 1) tc::rescale_o_row(orow, alpha);
-      tmem_wait_st();
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::remote_arrive(p_full);
-    }
-    if (!ok && lane == 0) timed_out(60);
-    ok = all_wait(smem_u32(&sh.o_ready), 0) && ok && !*aborted;
-    sh.stat[g][0][r] = m_used;
-    sh.stat[g][1][r] = l;
-    ok = tc::bar_and(1, 256, ok);
-    fence_after_sync();
-    if (ok) {
+      ok = ok && all_wait(smem_u32(&sh.o_ready), (it.n - 1) & 1);
+      sh.stat[g][0][r] = m_used;
+      sh.stat[g][1][r] = l;
+      ok = tc::bar_and(1, 256, ok && !*aborted);
+      if (!ok) break;
+      fence_after_sync();
       // The two halves of the key tiles joined; each warp 64 columns.
       const float m0 = sh.stat[0][0][r], m1 = sh.stat[1][0][r];
       const float top = fmaxf(m0, m1);  // finite: every row sees token 0
       const float e0 = ex2(m0 - top), e1 = ex2(m1 - top);
       const float inv = 1.f / (e0 * sh.stat[0][1][r] + e1 * sh.stat[1][1][r]);
       const float w0 = e0 * inv, w1 = e1 * inv;
-      const bool second = nt > 1;  // else the second O has not been written
-      // Q has been read: its place turns the rows.
-      uint8_t* turn = smem + warp * 2048;
+      // An item of one tile has written one O.
+      const bool has0 = nt > 1 || !(it.tiles0 & 1), has1 = nt > 1 || (it.tiles0 & 1);
+      uint8_t* turn = smem + kOffTurn + warp * 2048;
       const int n = t.nrows - rank * kM - (warp & 3) * 32;  // rows of the warp
       const int64_t row0 = t.row0 + rank * kM + (warp & 3) * 32;
 #pragma unroll 1
@@ -484,13 +553,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_ld32(lane_base + kColO + c, v);
         tmem_ld32(lane_base + kColO + kHead + c, v1);
         tmem_wait_ld();
-        float o[32];
+        if (c & 32) {  // O has been read
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::remote_arrive(o_empty);
+        }
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          o[k] = __uint_as_float(v[k]) * w0 +
-                 (second ? __uint_as_float(v1[k]) * w1 : 0.f);
+        for (int k = 0; k < 16; ++k) {
+          float o[2];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) w[k] = pack_bf16(o[2 * k], o[2 * k + 1]);
+          for (int x = 0; x < 2; ++x)
+            o[x] = (has0 ? __uint_as_float(v[2 * k + x]) * w0 : 0.f) +
+                   (has1 ? __uint_as_float(v1[2 * k + x]) * w1 : 0.f);
+          w[k] = pack_bf16(o[0], o[1]);
+        }
         put_rows(turn, w, lane, [&](int rr) -> uint8_t* {
           if (rr >= n) return nullptr;
           return reinterpret_cast<uint8_t*>(
@@ -498,70 +574,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         });
       }
     }
+    if (!ok && lane == 0) timed_out(60);
   } else if (warp == 8) {
-    // ---- products of both CTAs (uniform warp, one lane issues) -------------------
+    bool ok = true;
     if (rank == 0) {
+      // ---- products of both CTAs (uniform warp, one lane issues) -----------------
       constexpr uint32_t id_qk = idesc(256, kT, false);
       constexpr uint32_t id_pv = idesc(256, kHead, true);
       const bool lead = elect_one();
-      const int n = uniform(nt), blocks = uniform(nblk);
-      bool ok = all_wait(smem_u32(&sh.q_full), 0);
-      // QK(j) and PV(j - 2) in turn: the rows read S(j) while PV(j - 2) runs.
-      for (int j = 0; j < n + 2 && ok; ++j) {
-        if (j < n) {
-          ok = all_wait(smem_u32(&sh.k_full[j % kNS]), (j / kNS) & 1) &&
-               (j == 0 || all_wait(smem_u32(&sh.s_empty), (j - 1) & 1));
-          if (!ok) break;
-          fence_after_sync();
-          if (lead) {
-            const uint32_t kst = base + kOffK + (j % kNS) * kK;
+      while (next_item(ok)) {
+        const int n = uniform(it.nt), blocks = uniform(it.nblk);
+        const uint32_t t0 = uniform(it.tiles0), item = it.n - 1;
+        ok = all_wait(smem_u32(&sh.q_full), item & 1);
+        // QK(j) and PV(j - 2) in turn: the rows read S(j) while PV(j - 2) runs.
+        for (int j = 0; j < n + 2 && ok; ++j) {
+          if (j < n) {
+            const uint32_t q = t0 + j, st = q % kNS;
+            const uint32_t kst = base + kOffK + st * kK;
             const uint64_t qd = sdesc(base, 16, 1024);
             const uint64_t kd = sdesc(kst, 16, 2048);
             const uint64_t rd = sdesc(kst + kKn, 16, 1024);
+            ok = all_wait(smem_u32(&sh.k_full[st]), (q / kNS) & 1) &&
+                 (q == 0 || all_wait(smem_u32(&sh.s_empty), (q - 1) & 1));
+            if (!ok) break;
+            fence_after_sync();
+            if (lead) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc::umma2_ss(tmem, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
-                           kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), id_qk,
-                           k > 0 ? 1u : 0u);
+              for (int k = 0; k < 8; ++k)
+                tc::umma2_ss(tmem, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                             kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), id_qk,
+                             k > 0 ? 1u : 0u);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::umma2_ss(tmem, qd + ((2 * 16384 + k * 32) >> 4), rd + k * 2,
-                           id_qk, 1u);
-            tc::umma2_commit(smem_u32(&sh.s_full[j & 1]));
-            tc::umma2_commit(smem_u32(&sh.k_empty[j % kNS]));
+              for (int k = 0; k < 4; ++k)
+                tc::umma2_ss(tmem, qd + ((2 * 16384 + k * 32) >> 4), rd + k * 2,
+                             id_qk, 1u);
+              tc::umma2_commit(smem_u32(&sh.s_full[q & 1]));
+              tc::umma2_commit(smem_u32(&sh.k_empty[st]));
+              if (j == n - 1) tc::umma2_commit(smem_u32(&sh.q_empty));
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        }
-        const int i = j - 2;
-        if (i >= 0) {
-          ok = all_wait(smem_u32(&sh.v_full[i % kNS]), (i / kNS) & 1) &&
-               all_wait(smem_u32(&sh.p_full[i & 1]), (i >> 1) & 1);
-          if (!ok) break;
-          fence_after_sync();
-          if (lead) {
-            const uint32_t pcol = tmem + kColP + (i & 1) * 64;
-            const uint32_t dout = tmem + kColO + (i & 1) * kHead;
-            const int nb = min(kTB, blocks - i * kTB);
-            const uint64_t vd = sdesc(base + kOffV + (i % kNS) * kV, 1024, 1024);
+          const int i = j - 2;
+          if (i >= 0) {
+            const uint32_t q = t0 + i, st = q % kNS;
+            ok = all_wait(smem_u32(&sh.v_full[st]), (q / kNS) & 1) &&
+                 all_wait(smem_u32(&sh.p_full[q & 1]), (q >> 1) & 1) &&
+                 (i > 0 || item == 0 ||
+                  all_wait(smem_u32(&sh.o_empty), (item - 1) & 1));
+            if (!ok) break;
+            fence_after_sync();
+            if (lead) {
+              const uint32_t pcol = tmem + kColP + (q & 1) * 64;
+              const uint32_t dout = tmem + kColO + (q & 1) * kHead;
+              const int nb = min(kTB, blocks - i * kTB);
+              const uint64_t vd = sdesc(base + kOffV + st * kV, 1024, 1024);
 #pragma unroll
-            for (int k = 0; k < kTB; ++k)
-              if (k < nb)
-                tc::umma2_ts(dout, pcol + k * 8, vd + k * (2048 >> 4), id_pv,
-                             i > 1 || k > 0 ? 1u : 0u);
-            tc::umma2_commit(smem_u32(&sh.p_empty[i & 1]));
-            tc::umma2_commit(smem_u32(&sh.v_empty[i % kNS]));
+              for (int k = 0; k < kTB; ++k)
+                if (k < nb)
+                  tc::umma2_ts(dout, pcol + k * 8, vd + k * (2048 >> 4), id_pv,
+                               i > 1 || k > 0 ? 1u : 0u);
+              tc::umma2_commit(smem_u32(&sh.p_empty[q & 1]));
+              tc::umma2_commit(smem_u32(&sh.v_empty[st]));
+              if (i == n - 1) tc::umma2_commit(smem_u32(&sh.o_ready));
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          ok = __all_sync(0xffffffffu, !*aborted);
         }
-        ok = !*aborted;
       }
-      if (lead) {
-        if (!ok) timed_out(61);
-        // Every product has finished once this lands: the rows may end, and the
-        // pair's shared memory is no longer read.
+      if (!ok && lead) {
+        timed_out(61);
+        // Every product issued has finished once this lands, or a time has passed.
         tc::umma2_commit(smem_u32(&sh.o_ready));
-        if (!mbar_wait(smem_u32(&sh.o_ready), 0)) timed_out(64);
+        mbar_wait(smem_u32(&sh.o_ready), (it.n - 1) & 1);
       }
+    } else {
+      // ---- the pair's work items (odd CTA): the first by its place in the grid,
+      // then as they come.  Head groups in turn (what the pairs read at a time
+      // stays in L2), in a group the longest tiles first.
+      const int n_items = p.n_tiles * p.Hq, pairs = gridDim.x >> 1;
+      int i = blockIdx.x >> 1;
+      for (uint32_t n = 0;; ++n) {
+        const uint32_t slot = n & 1;
+        if (n >= 2) ok = all_wait(smem_u32(&sh.item_empty[slot]), ((n >> 1) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && !*aborted);
+        if (!ok) break;
+        PrefillTile t{0, 1, 0, 0};
+        int h = -1;
+        for (; i < n_items; i = next_index(p, pairs, lane)) {
+          const int group = i / (p.n_tiles * p.heads);
+          const int heads = min(p.heads, p.Hq - group * p.heads);
+          const int rest = i - group * p.n_tiles * p.heads;
+          t = p.tiles[rest / heads];
+          h = group * p.heads + rest % heads;
+          if (t.nrows >= 1 && t.nrows <= kPrefillRows && t.pos0 >= 0 &&
+              t.row0 >= 0 && t.row0 + t.nrows <= p.total && t.table >= 0 &&
+              t.table + (t.pos0 + t.nrows + 15) / 16 <= p.n_slots)
+            break;
+          if (lane == 0) record_status(p.status, KV_ERR_DEVICE, -1 - i);
+          h = -1;
+        }
+        if (lane < 2) {
+          const uint32_t bar = tc::map_rank(smem_u32(&sh.item_full[slot]), lane);
+          tc::remote_expect_tx(bar, 20);
+          tc::remote_store16(tc::map_rank(smem_u32(&sh.item[slot]), lane), t.row0,
+                             t.nrows, t.pos0, t.table, bar);
+          tc::remote_store4(tc::map_rank(smem_u32(&sh.item_head[slot]), lane), h, bar);
+        }
+        __syncwarp();
+        if (h < 0) break;
+        i = next_index(p, pairs, lane);
+      }
+      if (!ok && lane == 0) timed_out(65);
     }
   } else {
     // ---- loads of this CTA's halves: its rows of Q, half of a key tile's keys,
@@ -570,81 +694,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     // The expansion's stores, read by bulk copies from here on.
     asm volatile("fence.proxy.async;" ::: "memory");
-    if (me == 0) {
-      const uint32_t bar = tc::map_rank(smem_u32(&sh.q_full), 0);
-      if (lane == 0) tc::remote_expect_tx(bar, kQ);
-      __syncwarp();
-      if (lane < 3)
-        tc::tma2_load_3d(base + lane * 16384, &tmQ, lane * 64, h,
-                         t.row0 + rank * kM, bar);
-      __syncwarp();
-    }
     // Lanes 0-3 the half's expanded keys, 4-7 its position keys, 8-15 values.
-    const int kb = rank * 4 + (lane & 3);  // K block of the tile
-    const int bi = lane < 8 ? kb : lane & 7;
-    int j = me;
-    auto slot_of = [&](int tile) {
-      const int blk = tile * kTB + bi;
-      if (lane >= 16 || tile >= nt || blk >= nblk) return -1;
-      const int s = p.slots[t.table + blk];
-      if (s >= 0 && s < p.n_uniq) return s;
-      record_status(p.status, KV_ERR_DEVICE, s);
-      return -1;
-    };
-    auto phys_of = [&](int slot) {
-      if (lane < 4 || lane >= 8 || slot < 0) return -1;
-      const int b = p.uniq[slot];
-      return b >= 0 && b < p.num_blocks ? b : -1;
-    };
-    int next = slot_of(j), next_phys = phys_of(next);
-    for (; j < nt; j += kLoads) {
-      const int slot = next, phys = next_phys;
-      next = slot_of(j + kLoads);
-      next_phys = phys_of(next);
-      const bool load = slot >= 0 && (lane < 4 || lane >= 8 || phys >= 0);
-      const uint32_t act = __ballot_sync(0xffffffffu, load);
-      const int s = j % kNS;
-      const uint32_t kbar = tc::map_rank(smem_u32(&sh.k_full[s]), 0);
-      const uint32_t vbar = tc::map_rank(smem_u32(&sh.v_full[s]), 0);
-      if (j >= kNS)
-        ok = all_wait(smem_u32(&sh.k_empty[s]), (j / kNS - 1) & 1);
-      ok = ok && !*aborted;
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0)
-        tc::remote_expect_tx(kbar, __popc(act & 0xf) * kBlk +
-                                        __popc(act & 0xf0) * 2048);
-      __syncwarp();
-      const uint32_t kst = base + kOffK + s * kK;
-      if (load && lane < 4)
-        tc::tma2_load_5d_at(kst + lane * kBlk, &tmK, 0, slot * p.Hq + h, kbar);
-      else if (load && lane < 8)
-        tc::tma2_load_2d(kst + kKn + (lane - 4) * 2048, &tmR, 0, phys * 16, kbar);
-      __syncwarp();
-      if (j >= kNS)
-        ok = all_wait(smem_u32(&sh.v_empty[s]), (j / kNS - 1) & 1);
-      ok = ok && !*aborted;
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0) tc::remote_expect_tx(vbar, __popc(act >> 8) * 2048);
-      __syncwarp();
-      if (load && lane >= 8)
-        tc::tma2_load_5d_at(base + kOffV + s * kV + bi * 2048, &tmV, rank,
-                            slot * p.Hq + h, vbar);
-      __syncwarp();
+    const int bi = lane < 8 ? rank * 4 + (lane & 3) : lane & 7;
+    while (next_item(ok)) {
+      const int nt = it.nt, h = it.h;
+      const uint32_t item = it.n - 1;
+      if (me == 0) {
+        if (item > 0) ok = all_wait(smem_u32(&sh.q_empty), (item - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && !*aborted);
+        if (!ok) break;
+        const uint32_t bar = tc::map_rank(smem_u32(&sh.q_full), 0);
+        if (lane == 0) tc::remote_expect_tx(bar, kQ);
+        __syncwarp();
+        if (lane < 3)
+          tc::tma2_load_3d(base + lane * 16384, &tmQ, lane * 64, h,
+                           it.t.row0 + rank * kM, bar);
+        __syncwarp();
+      }
+      auto slot_of = [&](int tile) {
+        const int blk = tile * kTB + bi;
+        if (lane >= 16 || tile >= nt || blk >= it.nblk) return -1;
+        const int s = p.slots[it.t.table + blk];
+        if (s >= 0 && s < p.n_uniq) return s;
+        record_status(p.status, KV_ERR_DEVICE, s);
+        return -1;
+      };
+      auto phys_of = [&](int slot) {
+        if (lane < 4 || lane >= 8 || slot < 0) return -1;
+        const int b = p.uniq[slot];
+        return b >= 0 && b < p.num_blocks ? b : -1;
+      };
+      int j = (me + kLoads - (int)(it.tiles0 % kLoads)) % kLoads;
+      int next = slot_of(j), next_phys = phys_of(next);
+      for (; j < nt; j += kLoads) {
+        const int slot = next, phys = next_phys;
+        next = slot_of(j + kLoads);
+        next_phys = phys_of(next);
+        const bool load = slot >= 0 && (lane < 4 || lane >= 8 || phys >= 0);
+        const uint32_t act = __ballot_sync(0xffffffffu, load);
+        const uint32_t q = it.tiles0 + j, s = q % kNS;
+        const uint32_t kbar = tc::map_rank(smem_u32(&sh.k_full[s]), 0);
+        const uint32_t vbar = tc::map_rank(smem_u32(&sh.v_full[s]), 0);
+        if (q >= kNS) ok = all_wait(smem_u32(&sh.k_empty[s]), (q / kNS - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && !*aborted);
+        if (!ok) break;
+        if (lane == 0)
+          tc::remote_expect_tx(kbar, __popc(act & 0xf) * kBlk +
+                                         __popc(act & 0xf0) * 2048);
+        __syncwarp();
+        const uint32_t kst = base + kOffK + s * kK;
+        if (load && lane < 4)
+          tc::tma2_load_5d_at(kst + lane * kBlk, &tmK, 0, slot * p.Hq + h, kbar);
+        else if (load && lane < 8)
+          tc::tma2_load_2d(kst + kKn + (lane - 4) * 2048, &tmR, 0, phys * 16, kbar);
+        __syncwarp();
+        if (q >= kNS) ok = all_wait(smem_u32(&sh.v_empty[s]), (q / kNS - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && !*aborted);
+        if (!ok) break;
+        if (lane == 0) tc::remote_expect_tx(vbar, __popc(act >> 8) * 2048);
+        __syncwarp();
+        if (load && lane >= 8)
+          tc::tma2_load_5d_at(base + kOffV + s * kV + bi * 2048, &tmV, rank,
+                              slot * p.Hq + h, vbar);
+        __syncwarp();
+      }
     }
-    ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) timed_out(62);
   }
   __syncwarp();
   fence_before_sync();
   __syncthreads();
-  // After a time-out loads may be in flight (else every one has been waited for
-  // by a product): both CTAs' report here.
-  if (*aborted && rank == 0 && threadIdx.x == 0) {
-    mbar_wait(smem_u32(&sh.q_full), 0);
-    for (int j = nt > kNS ? nt - kNS : 0; j < nt; ++j)
-      if (!mbar_wait(smem_u32(&sh.k_full[j % kNS]), (j / kNS) & 1) ||
-          !mbar_wait(smem_u32(&sh.v_full[j % kNS]), (j / kNS) & 1))
-        break;
+  // After a time-out loads may be in flight (else a product has waited for every
+  // one): about two milliseconds for them to land.
+  if (*aborted) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1 << 22)) {
+    }
   }
   __syncwarp();
   tc::cluster_sync();
@@ -686,8 +811,10 @@ kv_status make_query_map(CUtensorMap* tm, const void* q, int64_t total, int Hq) 
   return encode_bf16_map(tm, q, 3, dims, strides, box);
 }
 
-__global__ void clear_kernel(DeviceStatus* status) {
-  if (threadIdx.x == 0) *status = DeviceStatus{};
+__global__ void clear_kernel(DeviceStatus* status, int* next) {
+  if (threadIdx.x != 0) return;
+  *status = DeviceStatus{};
+  *next = 0;
 }
 
 }  // namespace pre
@@ -737,13 +864,15 @@ extern "C" kv_status paged_latent_prefill_attn(
                 need);
   auto* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = (cudaStream_t)stream;
-  pre::clear_kernel<<<1, 32, 0, st>>>(reinterpret_cast<pkv::DeviceStatus*>(ws));
+  pre::Params p;
+  p.status = reinterpret_cast<pkv::DeviceStatus*>(ws);
+  p.next = reinterpret_cast<int*>(ws + sizeof(pkv::DeviceStatus));
+  pre::clear_kernel<<<1, 32, 0, st>>>(p.status, p.next);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "latent prefill: %s", cudaGetErrorString(e));
   if (total == 0) return KV_OK;
   const int64_t tiles = (int64_t)info->n_row_items * Hq;
-  pre::Params p;
   p.uniq = plan + pkv::kPlanHeaderInts;
   p.valid = p.uniq + info->n_row_items;
   p.slots = p.valid + info->n_row_items;
@@ -752,7 +881,6 @@ extern "C" kv_status paged_latent_prefill_attn(
   p.v_exp = reinterpret_cast<__nv_bfloat16*>(
       ws + pkv::kStatusBytes + pkv::prefill_half(info->n_row_items, Hq));
   p.out = static_cast<__nv_bfloat16*>(out);
-  p.status = reinterpret_cast<pkv::DeviceStatus*>(ws);
   p.n_uniq = info->n_row_items;
   p.n_slots = (int)info->partial_rows;
   p.n_tiles = info->n_tile_items;
@@ -782,14 +910,18 @@ extern "C" kv_status paged_latent_prefill_attn(
     e = pkv::opt_in_smem(pre::at::prefill_kernel, pre::at::kSmem, opted_at);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "latent prefill: %s", cudaGetErrorString(e));
+  // Heads whose expanded keys and values the pairs share L2 for.
+  p.heads = (int)std::clamp<int64_t>(
+      (48ll << 20) / ((int64_t)p.n_uniq * 16 * pre::kHead * 4), 1, Hq);
   const int64_t work = (int64_t)((p.n_uniq + 7) / 8) * Hq;
   pre::ex::expand_kernel<<<(unsigned)std::min<int64_t>(work, sms),
                            pre::ex::kThreads, pre::ex::kSmem, st>>>(tx, tw, p);
   e = cudaGetLastError();
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "expansion kernel: %s", cudaGetErrorString(e));
-  e = pkv::launch_early(pre::at::prefill_kernel, 2 * p.n_tiles * Hq,
-                        pre::at::kThreads, pre::at::kSmem, st, tq, tk, tv, tr, p);
+  const int pairs = std::min(p.n_tiles * Hq, std::max(sms / 2, 1));
+  e = pkv::launch_early(pre::at::prefill_kernel, 2 * pairs, pre::at::kThreads,
+                        pre::at::kSmem, st, tq, tk, tv, tr, p);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "prefill kernel: %s", cudaGetErrorString(e));
   return KV_OK;
