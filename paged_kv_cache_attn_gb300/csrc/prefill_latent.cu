@@ -6,14 +6,17 @@
 // Against the absorbed form this costs 2 x 320 flops a row and token instead of
 // 2 x 1088, for 2 x 512 x 256 flops a token and head once.
 //
-// Expansion kernel: [128 tokens x 512] x [512 x 256] per token tile and head
-// (the tokens are eight distinct blocks of the step, gathered through the
-// plan's list; a block shared by branches is expanded once), written as bf16 to
-// [slot][head][16][128] -- the rounding of a cached key or value.  Operands
-// stream through a ring of 64-dimension stages (16 + 32 KB), products in two
-// 256-column halves of TMEM so that a tile's epilogue overlaps the next one's
-// products.  Bound by what L2 delivers to an SM (48 KB per four MMAs of 128
-// cycles).
+// Expansion kernel: pairs of CTAs (cta_group::2), [256 tokens x 512] x [512 x 256]
+// per token tile and head (the tokens are sixteen distinct blocks of the step,
+// gathered through the plan's list; a block shared by branches is expanded once),
+// written as bf16 to [slot][head][16][128] -- the rounding of a cached key or
+// value.  A pair's work is a run of (tile, head), heads innermost: each CTA keeps
+// its 128 tokens' latents in shared memory (128 KB) while the heads pass, and half
+// of a head's weights stream through a ring of 64-dimension stages (16 KB each;
+// with both operands streamed to single CTAs, 48 KB per four products of 128
+// cycles, L2 bounded it: 63 us for 8192 tokens and 32 heads, 45 now).  Products
+// go to two 256-column halves of TMEM so that a tile's epilogue, which bounds it
+// now, overlaps the next one's products.
 //
 // Attention kernel: pairs of CTAs (cta_group::2), one on every two SMs, that take
 // work items (a tile of 256 query rows and a head) as they come.  Each CTA has 128
@@ -53,9 +56,6 @@ using tc::tmem_ld32;
 using tc::tmem_st32;
 using tc::tmem_wait_ld;
 using tc::tmem_wait_st;
-using tc::umma_commit;
-using tc::umma_ss;
-using tc::umma_ts;
 using tc::uniform;
 
 constexpr int kRank = KV_LATENT_RANK, kRope = KV_LATENT_ROPE, kHead = KV_LATENT_HEAD;
@@ -76,20 +76,12 @@ struct Params {
   float scale_log2;
 };
 
-__device__ __forceinline__ void tmem_alloc(uint32_t where) {
-  asm volatile(
-      "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-          where),
-      "r"(kTmemCols)
-      : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" :::
-                   "memory");
-}
-
-__device__ __forceinline__ void tmem_free(uint32_t tmem) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-               "r"(kTmemCols)
-               : "memory");
+// After a time-out loads may be in flight (else a product has waited for every
+// one): about two milliseconds for them to land.
+__device__ __forceinline__ void wait_for_copies() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < (1 << 22)) {
+  }
 }
 
 // Two fp32 in one operation.
@@ -140,39 +132,52 @@ __device__ __forceinline__ void put_rows(uint8_t* turn, const uint32_t (&w)[16],
 
 namespace ex {
 
-constexpr int kA = 128 * 128, kB = 256 * 128;   // a stage of X and of W
-constexpr int kStage = kA + kB;
-constexpr int kNS = 4;
+constexpr int kX = 128 * 128;                   // 64 dimensions of a CTA's latents
+constexpr int kW = 128 * 128;                   // and of half a head's weights
+constexpr int kNS = 5;                          // stages of W
 constexpr int kChunks = kRank / 64;
-constexpr int kOffTurn = kNS * kStage;
+constexpr int kSlots = 16;                      // slots of a pair's token tile
+constexpr int kOffW = kChunks * kX;
+constexpr int kOffTurn = kOffW + kNS * kW;
 constexpr int kTiles = kOffTurn + 8 * 2048;
-constexpr int kThreads = 11 * 32;  // warps 0-7 rows, 8 products, 9-10 loads
+constexpr int kThreads = 12 * 32;  // warps 0-7 rows, 8 products, 9-10 W, 11 X
 
 struct Small {
-  uint64_t full[kNS], empty[kNS], d_full[2], d_empty[2], drain;
+  // x_full, w_full and d_empty are used in the even CTA alone.
+  uint64_t x_full[kChunks], x_empty[kChunks], w_full[kNS], w_empty[kNS], d_full[2],
+      d_empty[2], drain;
   uint32_t tmem_base;
   int aborted;
 };
-constexpr int kSmem = kTiles + (int)sizeof(Small) + 1024;
+constexpr int kSmem = kTiles + (int)sizeof(Small);
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap tmX,
                   const __grid_constant__ CUtensorMap tmW, const Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
   Small& sh = *reinterpret_cast<Small*>(smem + kTiles);
   volatile int* aborted = &sh.aborted;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (base & 1023) {  // never, with no static shared memory
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0) record_status(p.status, KV_ERR_INTERNAL, (int)base);
+    return;
+  }
+  const int rank = (int)tc::cluster_rank();
   if (threadIdx.x == 0) {
+    for (int c = 0; c < kChunks; ++c) {
+      mbar_init(smem_u32(&sh.x_full[c]), 2);
+      mbar_init(smem_u32(&sh.x_empty[c]), 1);
+    }
     for (int s = 0; s < kNS; ++s) {
-      mbar_init(smem_u32(&sh.full[s]), 1);
-      mbar_init(smem_u32(&sh.empty[s]), 1);
+      mbar_init(smem_u32(&sh.w_full[s]), 2);
+      mbar_init(smem_u32(&sh.w_empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sh.d_full[b]), 1);
-      mbar_init(smem_u32(&sh.d_empty[b]), 8);
+      mbar_init(smem_u32(&sh.d_empty[b]), 16);
     }
     mbar_init(smem_u32(&sh.drain), 1);
     sh.aborted = 0;
@@ -180,45 +185,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
   }
-  if (warp == 8) tmem_alloc(smem_u32(&sh.tmem_base));
+  __syncwarp();
+  if (warp == 8) tc::tmem_alloc2(smem_u32(&sh.tmem_base), kTmemCols);
   fence_before_sync();
-  __syncthreads();
+  tc::cluster_sync();
   fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
-  // Tiles of eight slots, heads innermost: a tile's latents stay in L2 while
-  // its heads pass, and the weights of all heads do throughout.
-  const int n_work = (p.n_uniq + 7) / 8 * p.Hq;
+  // Launched while the status is cleared: nothing of it before this.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // A pair's work: consecutive (token tile, head), heads innermost; a tile's
+  // latents stay in shared memory while its heads pass.
+  const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+  const int64_t n_work = (int64_t)((p.n_uniq + kSlots - 1) / kSlots) * p.Hq;
+  const int begin = (int)(n_work * pair / pairs);
+  const int end = (int)(n_work * (pair + 1) / pairs);
   auto timed_out = [&](int site) {
     if (!*aborted) record_status(p.status, KV_ERR_TIMEOUT, site);
     atomicExch(&sh.aborted, 1);
+    tc::cluster_store4(tc::map_rank(smem_u32(&sh.aborted), rank ^ 1), 1u);
   };
 
   if (warp < 8) {
     const int wg = warp >> 2;  // 0: keys, 1: values
-    const int r = (warp & 3) * 32 + lane;
-    const uint32_t drow =
-        tmem + ((uint32_t)((warp & 3) * 32) << 16) + wg * kHead;
+    const int row0 = (warp & 3) * 32, r = row0 + lane;
+    const uint32_t drow = tmem + ((uint32_t)row0 << 16) + wg * kHead;
     uint8_t* turn = smem + kOffTurn + warp * 2048;
     __nv_bfloat16* exp = wg == 0 ? p.k_exp : p.v_exp;
     uint32_t n = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < n_work; i += gridDim.x, ++n) {
-      const int slot0 = i / p.Hq * 8, h = i % p.Hq;
+    for (int i = begin; i < end; ++i, ++n) {
+      const int slot0 = i / p.Hq * kSlots + rank * 8, h = i % p.Hq;
       const uint32_t b = n & 1;
-      ok = all_wait(smem_u32(&sh.d_full[b]), (n >> 1) & 1) && !*aborted;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      fence_after_sync();
       const int slot = slot0 + (r >> 4);
       // Values past the branch's length would meet weights of zero: zeros.
       const bool zero =
           wg == 1 && (slot >= p.n_uniq || (r & 15) >= p.valid[min(slot, p.n_uniq - 1)]);
-      const int row0 = (warp & 3) * 32;
+      ok = all_wait(smem_u32(&sh.d_full[b]), (n >> 1) & 1);
+      ok = __all_sync(0xffffffffu, ok && !*aborted);
+      if (!ok) break;
+      fence_after_sync();
 #pragma unroll 1
       for (int c = 0; c < kHead; c += 32) {
         uint32_t v[32], w[16];
         tmem_ld32(drow + b * 256 + c, v);
         tmem_wait_ld();
+        if (c == kHead - 32) {  // D has been read
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::remote_arrive(tc::map_rank(smem_u32(&sh.d_empty[b]), 0));
+        }
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           w[k] = zero ? 0u
@@ -231,87 +246,109 @@ __global__ void __launch_bounds__(kThreads, 1)
               exp + (((int64_t)s * p.Hq + h) * 16 + (row & 15)) * kHead + c);
         });
       }
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.d_empty[b]));
     }
     if (!ok && lane == 0) timed_out(50);
   } else if (warp == 8) {
-    constexpr uint32_t id = idesc(128, 256, false);
-    const bool lead = elect_one();
-    uint32_t n = 0, s = 0, ph = 0;
-    bool ok = true;
-    const int work = uniform(n_work);
-    for (int i = blockIdx.x; i < work && ok; i += gridDim.x, ++n) {
-      const uint32_t b = n & 1, d = tmem + b * 256;
-      if (n >= 2) ok = all_wait(smem_u32(&sh.d_empty[b]), ((n >> 1) - 1) & 1);
-      for (int c = 0; c < kChunks && ok; ++c) {
-        ok = all_wait(smem_u32(&sh.full[s]), ph);
-        if (!ok) break;
-        fence_after_sync();
-        const uint64_t ad = sdesc(base + s * kStage, 16, 1024);
-        const uint64_t bd = sdesc(base + s * kStage + kA, 16, 1024);
-        if (lead) {
+    if (rank == 0) {
+      constexpr uint32_t id = idesc(256, 256, false);
+      const bool lead = elect_one();
+      const int heads = uniform(p.Hq);
+      uint32_t n = 0, s = 0, ph = 0, tile = 0;  // tile: of the pair's
+      bool ok = true;
+      for (int i = uniform(begin); i < end && ok; ++i, ++n) {
+        const uint32_t b = n & 1, d = tmem + b * 256;
+        const bool first = n == 0 || i % heads == 0;
+        const bool last = i == end - 1 || (i + 1) % heads == 0;
+        if (n >= 2) ok = all_wait(smem_u32(&sh.d_empty[b]), ((n >> 1) - 1) & 1);
+        for (int c = 0; c < kChunks && ok; ++c) {
+          if (first) ok = all_wait(smem_u32(&sh.x_full[c]), tile & 1);
+          ok = ok && all_wait(smem_u32(&sh.w_full[s]), ph);
+          if (!ok) break;
+          fence_after_sync();
+          const uint64_t xd = sdesc(base + c * kX, 16, 1024);
+          const uint64_t wd = sdesc(base + kOffW + s * kW, 16, 1024);
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_ss(d, ad + k * 2, bd + k * 2, id, c > 0 || k > 0 ? 1u : 0u);
-          umma_commit(smem_u32(&sh.empty[s]));
-          if (c == kChunks - 1) umma_commit(smem_u32(&sh.d_full[b]));
+            for (int k = 0; k < 4; ++k)
+              tc::umma2_ss(d, xd + k * 2, wd + k * 2, id, c > 0 || k > 0 ? 1u : 0u);
+            tc::umma2_commit(smem_u32(&sh.w_empty[s]));
+            if (last) tc::umma2_commit(smem_u32(&sh.x_empty[c]));
+            if (c == kChunks - 1) tc::umma2_commit(smem_u32(&sh.d_full[b]));
+          }
+          __syncwarp();
+          if (++s == kNS) {
+            s = 0;
+            ph ^= 1;
+          }
         }
-        __syncwarp();
-        if (++s == kNS) {
-          s = 0;
-          ph ^= 1;
-        }
+        tile += last;
+        ok = __all_sync(0xffffffffu, ok && !*aborted);
       }
-      ok = ok && !*aborted;
+      if (lead) {
+        if (!ok) timed_out(51);
+        // Every product has finished once this lands.
+        tc::umma2_commit(smem_u32(&sh.drain));
+        mbar_wait(smem_u32(&sh.drain), 0);
+      }
     }
-    if (lead) {
-      if (!ok) timed_out(51);
-      umma_commit(smem_u32(&sh.drain));
-      mbar_wait(smem_u32(&sh.drain), 0);
-    }
-  } else {
-    // Stages alternate between the two warps: eight boxes of a block and one of
-    // the head's weights.
+  } else if (warp < 11) {
+    // Half of a head's weights: keys' rows in the even CTA, values' in the odd
+    // one; stages alternate between the two warps.
     const uint32_t me = warp - 9;
     uint32_t k = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < n_work && ok; i += gridDim.x) {
-      const int slot = i / p.Hq * 8 + lane, h = i % p.Hq;
+    for (int i = begin; i < end && ok; ++i) {
+      const int h = i % p.Hq;
+      for (int c = 0; c < kChunks; ++c, ++k) {
+        if ((k & 1) != me) continue;
+        const uint32_t s = k % kNS, bar = tc::map_rank(smem_u32(&sh.w_full[s]), 0);
+        if (k >= kNS) ok = all_wait(smem_u32(&sh.w_empty[s]), (k / kNS - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && !*aborted);
+        if (!ok) break;
+        if (lane == 0) tc::remote_expect_tx(bar, kW);
+        __syncwarp();
+        if (lane < 2)
+          tc::tma2_load_2d(base + kOffW + s * kW + lane * (kW / 2), &tmW, c * 64,
+                           h * 256 + rank * 128 + lane * 64, bar);
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) timed_out(52);
+  } else {
+    // Latents: eight slots of each token tile, a box a slot and 64 dimensions.
+    bool ok = true;
+    uint32_t tile = 0;
+    for (int i = begin; i < end && ok; i = (i / p.Hq + 1) * p.Hq, ++tile) {
+      const int slot = i / p.Hq * kSlots + rank * 8 + lane;
       int phys = lane < 8 && slot < p.n_uniq ? p.uniq[slot] : -1;
       if (lane < 8 && slot < p.n_uniq && (phys < 0 || phys >= p.num_blocks)) {
-        if (me == 0) record_status(p.status, KV_ERR_DEVICE, phys);
+        record_status(p.status, KV_ERR_DEVICE, phys);
         phys = -1;
       }
       const int nb = __popc(__ballot_sync(0xffffffffu, phys >= 0));
-      for (int c = 0; c < kChunks; ++c, ++k) {
-        if ((k & 1) != me) continue;
-        const uint32_t s = k % kNS, bar = smem_u32(&sh.full[s]);
-        ok = k < kNS || all_wait(smem_u32(&sh.empty[s]), (k / kNS - 1) & 1);
+      for (int c = 0; c < kChunks; ++c) {
+        const uint32_t bar = tc::map_rank(smem_u32(&sh.x_full[c]), 0);
+        if (tile > 0) ok = all_wait(smem_u32(&sh.x_empty[c]), (tile - 1) & 1);
         ok = __all_sync(0xffffffffu, ok && !*aborted);
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(bar, nb * 2048 + kB);
+        if (lane == 0) tc::remote_expect_tx(bar, nb * 2048);
         __syncwarp();
         if (phys >= 0)
-          tma_load_2d(base + s * kStage + lane * 2048, &tmX, c * 64, phys * 16, bar);
-        else if (lane == 8)
-          tma_load_2d(base + s * kStage + kA, &tmW, c * 64, h * 256, bar);
+          tc::tma2_load_2d(base + c * kX + lane * 2048, &tmX, c * 64, phys * 16, bar);
         __syncwarp();
       }
     }
-    if (lane == 0) {
-      if (!ok) timed_out(52);
-      for (uint32_t j = k > kNS ? k - kNS : 0; j < k; ++j)
-        if ((j & 1) == me && !mbar_wait(smem_u32(&sh.full[j % kNS]), (j / kNS) & 1))
-          break;
-    }
+    if (!ok && lane == 0) timed_out(53);
   }
   __syncwarp();
   fence_before_sync();
   __syncthreads();
+  if (*aborted) wait_for_copies();
+  __syncwarp();
+  tc::cluster_sync();
   fence_after_sync();
-  if (warp == 8) tmem_free(tmem);
+  if (warp == 8) tc::tmem_free2(tmem, kTmemCols);
+  tc::cluster_sync();  // neither CTA leaves before both have given it back
 }
 
 }  // namespace ex
@@ -369,11 +406,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* aborted = &sh.aborted;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (base & 1023) {  // never, with no static shared memory
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) record_status(p.status, KV_ERR_INTERNAL, (int)base);
     return;
   }
-  // Launched while the expansion runs: nothing of global memory before this.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rank = (int)tc::cluster_rank();
 
   if (threadIdx.x == 0) {
@@ -410,6 +446,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::cluster_sync();
   fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
+  // Launched while the expansion runs: nothing of global memory before this.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   auto timed_out = [&](int site) {
     if (!*aborted) record_status(p.status, KV_ERR_TIMEOUT, site);
     atomicExch(&sh.aborted, 1);
@@ -764,13 +802,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   fence_before_sync();
   __syncthreads();
-  // After a time-out loads may be in flight (else a product has waited for every
-  // one): about two milliseconds for them to land.
-  if (*aborted) {
-    const long long t0 = clock64();
-    while (clock64() - t0 < (1 << 22)) {
-    }
-  }
+  if (*aborted) wait_for_copies();
   __syncwarp();
   tc::cluster_sync();
   fence_after_sync();
@@ -892,7 +924,7 @@ extern "C" kv_status paged_latent_prefill_attn(
   if (kv_status s = pre::make_matrix_map(&tx, c_pool, num_blocks * 16, rank, 16))
     return s;
   if (kv_status s = pre::make_matrix_map(&tw, w_kv, (int64_t)Hq * 2 * head_dim,
-                                         rank, 2 * head_dim))
+                                         rank, 64))
     return s;
   if (kv_status s = pre::make_query_map(&tq, q, total, Hq)) return s;
   if (kv_status s = pre::make_expanded_map(&tk, p.k_exp, tiles, 2)) return s;
@@ -913,13 +945,15 @@ extern "C" kv_status paged_latent_prefill_attn(
   // Heads whose expanded keys and values the pairs share L2 for.
   p.heads = (int)std::clamp<int64_t>(
       (48ll << 20) / ((int64_t)p.n_uniq * 16 * pre::kHead * 4), 1, Hq);
-  const int64_t work = (int64_t)((p.n_uniq + 7) / 8) * Hq;
-  pre::ex::expand_kernel<<<(unsigned)std::min<int64_t>(work, sms),
-                           pre::ex::kThreads, pre::ex::kSmem, st>>>(tx, tw, p);
-  e = cudaGetLastError();
+  const int sm_pairs = std::max(sms / 2, 1);
+  const int64_t work =
+      (int64_t)((p.n_uniq + pre::ex::kSlots - 1) / pre::ex::kSlots) * Hq;
+  e = pkv::launch_early(pre::ex::expand_kernel,
+                        2 * (int)std::min<int64_t>(work, sm_pairs),
+                        pre::ex::kThreads, pre::ex::kSmem, st, tx, tw, p);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "expansion kernel: %s", cudaGetErrorString(e));
-  const int pairs = std::min(p.n_tiles * Hq, std::max(sms / 2, 1));
+  const int pairs = std::min(p.n_tiles * Hq, sm_pairs);
   e = pkv::launch_early(pre::at::prefill_kernel, 2 * pairs, pre::at::kThreads,
                         pre::at::kSmem, st, tq, tk, tv, tr, p);
   if (e != cudaSuccess)
