@@ -21,6 +21,7 @@
 
 #include "device_common.cuh"
 #include "e4m3.cuh"
+#include "tensor_map.h"
 
 namespace pkv {
 namespace rope {
@@ -202,8 +203,11 @@ __global__ void __launch_bounds__(256)
     rotate_kernel(const __grid_constant__ RotateArgs a) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t t = w / a.split;
-  if (t >= a.map.total) return;
-  rotate_share<D, PAIRS>(a, (int)t, (int)(w - t * a.split), threadIdx.x & 31);
+  if (t < a.map.total)
+    rotate_share<D, PAIRS>(a, (int)t, (int)(w - t * a.split), threadIdx.x & 31);
+  // Beside a quantising launch (below) it runs with that one, which has to be
+  // complete when this one is.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---- e4m3 pools ---------------------------------------------------------------
@@ -484,6 +488,8 @@ template <int D, bool PAIRS>
 __global__ void __launch_bounds__(kQuantWarps * 32, 4)
     quant_append_kernel(const __grid_constant__ QuantArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The queries' launch depends on nothing of this one.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if ((int)blockIdx.x < a.q_ctas) {
     if (blockIdx.y > 0) return;
     const int64_t w = (int64_t)blockIdx.x * kQuantWarps + warp;
@@ -532,8 +538,12 @@ int split_for(int total, int iterations) {
 }
 
 template <int D>
-cudaError_t launch_rotate(const RotateArgs& a, bool pairs, cudaStream_t st) {
+cudaError_t launch_rotate(const RotateArgs& a, bool pairs, cudaStream_t st,
+                          bool beside = false) {
   const int64_t ctas = ((int64_t)a.map.total * a.split + 7) / 8;
+  if (beside)  // the launch before
+    return pairs ? launch_early(rotate_kernel<D, true>, (int)ctas, 256, 0, st, a)
+                 : launch_early(rotate_kernel<D, false>, (int)ctas, 256, 0, st, a);
   if (pairs)
     rotate_kernel<D, true><<<(unsigned)ctas, 256, 0, st>>>(a);
   else
@@ -666,20 +676,14 @@ kv_status rope_append_impl(
     // A decode step's tokens each begin a write: one CTA a token, and the
     // queries in the same launch.  In a chunk about every sixteenth does; the
     // queries are most of the bytes then and take a launch of their own, which
-    // keeps twice the warps on an SM (24 chunks of 37 to 701 tokens: 73 us in
-    // one launch).
+    // keeps twice the warps on an SM and runs beside the other (24 chunks of 37
+    // to 701 tokens: 73 us in one launch, 58 us one after the other).
     a.window = off ? 16 : 1;
     const bool own_launch = off != nullptr && q != nullptr;
     a.q_ctas = q && !own_launch
                    ? (int)(((int64_t)total * r.split + rope::kQuantWarps - 1) /
                            rope::kQuantWarps)
                    : 0;
-    if (own_launch) {
-      e = d == 128 ? rope::launch_rotate<128>(r, pairs, st)
-                   : rope::launch_rotate<64>(r, pairs, st);
-      if (e != cudaSuccess)
-        return fail(KV_ERR_CUDA, "rope append launch: %s", cudaGetErrorString(e));
-    }
     a.k_new = static_cast<const __nv_bfloat16*>(k_new);
     a.v_new = static_cast<const __nv_bfloat16*>(v_new);
     a.k_token = k_stride;
@@ -690,6 +694,9 @@ kv_status rope_append_impl(
     a.Hkv = Hkv;
     e = d == 128 ? rope::launch_quant<128>(a, pairs, st)
                  : rope::launch_quant<64>(a, pairs, st);
+    if (e == cudaSuccess && own_launch)
+      e = d == 128 ? rope::launch_rotate<128>(r, pairs, st, true)
+                   : rope::launch_rotate<64>(r, pairs, st, true);
   }
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "rope append launch: %s", cudaGetErrorString(e));
