@@ -162,6 +162,69 @@ def test_graph_and_two_streams():
         b.check()
 
 
+def test_rising_scores_rescale_every_tile():
+    """Scores that rise by more than 8 powers of two a key tile move the maximum,
+    and O with it, at every one."""
+    s = Step([1500], [600], 2, seed=11)
+    t = torch.arange(1500, device="cuda")
+    blk = torch.from_numpy(s.tables[0][t.cpu().numpy() // 16].astype(np.int64)).cuda()
+    s.r[blk, t % 16] = 0
+    s.r[blk, t % 16, 0] = (t // 16).bfloat16()
+    s.q.zero_()
+    s.q[..., 128] = 14.0        # 14 x 192^-0.5 = 1.01 a block, 8.1 a tile
+    s.run()
+    s.check()
+
+
+def test_many_ragged_items():
+    """Items of one, two and three key tiles in turn on every pair of SMs."""
+    lens = [(37 * i) % 331 + 1 for i in range(48)]
+    q_lens = [n if i % 3 else (n + 1) // 2 for i, n in enumerate(lens)]
+    s = Step(lens, q_lens, 12, seed=12)
+    s.run()
+    s.check(heads=[0, 5, 11])
+    # 132 heads: groups of heads that do not divide them.
+    s = Step([900, 70], [900, 70], 132, seed=13)
+    s.run()
+    s.check(heads=[0, 63, 131])
+
+
+def test_bad_plan_entries_are_reported():
+    """A block, an index or a tile out of range is recorded, and what does not
+    depend on it is right."""
+    s = Step([100, 300, 40], [100, 60, 40], 2, seed=14)
+    s.run()
+    s.check()
+    good = s.out.clone()
+    U, slots = s.info.n_row_items, s.info.partial_rows
+    head = s.info.plan_ints - 4 * s.info.n_tile_items - slots - 2 * U
+    for at, value in ((head + U - 1, s.blocks),           # a block of branch 2
+                      (head + 2 * U + slots - 1, U),      # its index
+                      (head + 2 * U + slots - 1, -1)):
+        keep = int(s.plan[at])
+        s.plan[at] = value
+        s.run()
+        assert B.kv_check_device_status(s.ws) == (B.KV_ERR_DEVICE, value)
+        assert torch.equal(s.out[:160].view(torch.int16), good[:160].view(torch.int16))
+        s.plan[at] = keep
+    # Tiles are sorted by their keys: the first is branch 1's.
+    at = head + 2 * U + slots
+    for field, value in ((0, -1), (0, s.n), (1, 0), (1, 257), (2, -5), (3, -1),
+                         (3, slots)):
+        keep = int(s.plan[at + field])
+        s.plan[at + field] = value
+        s.out[:] = 3
+        s.run()
+        assert B.kv_check_device_status(s.ws)[0] == B.KV_ERR_DEVICE
+        for lo, hi, same in ((0, 100, True), (100, 160, False), (160, 200, True)):
+            x = s.out[lo:hi].view(torch.int16)
+            y = (good[lo:hi] if same else torch.full_like(good[lo:hi], 3.0))
+            assert torch.equal(x, y.view(torch.int16)), (field, value, lo)
+        s.plan[at + field] = keep
+    s.run()
+    s.check()
+
+
 def test_prompt_then_decode():
     """A prompt enters a latent pool, attends, is forked, and the branches
     decode: append, expanded and absorbed attention over one cache.  The absorbed
