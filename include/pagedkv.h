@@ -46,7 +46,8 @@ extern "C" {
 typedef int32_t kv_status;
 
 #define KV_OK 0
-#define KV_ERR_OOM 1          /* pool has too few free blocks ([TRM] §6 MemoryError) */
+#define KV_ERR_OOM 1          /* pool has too few free blocks ([TRM] §6 MemoryError),
+                                or no host memory for a latent plan */
 #define KV_ERR_INVALID_ARG 2  /* bad size, pointer, layout or plan */
 #define KV_ERR_NOT_FOUND 3    /* unknown or already-freed branch ([TRM] §6 KeyError) */
 #define KV_ERR_CUDA 4         /* a CUDA runtime call failed */

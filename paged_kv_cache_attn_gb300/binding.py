@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import sys
 
 import numpy as np
 
@@ -540,6 +541,17 @@ def paged_decode_append_attn_e4m3(q, k_step, v_step, k_pool, v_pool,
         _ptr(workspace), ws_bytes, _stream(stream)))
 
 
+_dtypes = None     # (bf16, fp32), once a call has brought a tensor
+
+
+def _types():
+    global _dtypes
+    if _dtypes is None:
+        torch = sys.modules["torch"]
+        _dtypes = torch.bfloat16, torch.float32
+    return _dtypes
+
+
 def _token_rows(t, width):
     """(pointer, distance between tokens in values) of a bf16 tensor whose
     tokens (dimension 0) are rows of `width` contiguous values."""
@@ -551,7 +563,7 @@ def _token_rows(t, width):
             (st[1] == sh[2] or sh[1] == 1)
     else:
         ok = len(sh) == 2 and sh[1] == width and st[1] == 1
-    if not ok or t.element_size() != 2:
+    if not ok or t.dtype is not _types()[0]:
         raise KVError(KV_ERR_INVALID_ARG,
                       f"a token is {width} contiguous bf16 values, got "
                       f"{tuple(sh)} of {t.dtype}, strides {st}")
@@ -561,7 +573,7 @@ def _token_rows(t, width):
 def _rope_table(rope):
     """(pointer, rope_len, rot_dim) of an fp32 table [rope_len][rot/2][2]."""
     sh = rope.shape
-    if len(sh) != 3 or sh[2] != 2 or rope.element_size() != 4 or \
+    if len(sh) != 3 or sh[2] != 2 or rope.dtype is not _types()[1] or \
             not rope.is_contiguous():
         raise KVError(KV_ERR_INVALID_ARG,
                       "rope is a contiguous fp32 [rope_len][rot_dim / 2][2], "
@@ -609,7 +621,7 @@ def _head_rows(t, heads, width):
         return None, 0, 0
     sh, st = t.shape, t.stride()
     if len(sh) != 3 or sh[1] != heads or sh[2] != width or st[2] != 1 or \
-            t.element_size() != 2:
+            t.dtype is not _types()[0]:
         raise KVError(KV_ERR_INVALID_ARG,
                       f"expected bf16 [total][{heads}][{width}], got "
                       f"{tuple(sh)} of {t.dtype}, strides {st}")

@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <new>
 #include <numeric>
 
 #include "internal.h"
@@ -148,10 +149,15 @@ extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
       shared_end[b] = end;
     }
   }
-  if (latent)
-    return pkv::latent_plan(nb, Hq, max_blocks, nblk.data(), groups,
-                            use_groups ? n_groups : 0, shared_end.data(),
-                            num_sms, flags, plan, plan_cap, info);
+  if (latent) {
+    try {
+      return pkv::latent_plan(nb, Hq, max_blocks, nblk.data(), groups,
+                              use_groups ? n_groups : 0, shared_end.data(),
+                              num_sms, flags, plan, plan_cap, info);
+    } catch (const std::bad_alloc&) {
+      return fail(KV_ERR_OOM, "no host memory for the plan");
+    }
+  }
   for (int32_t b = 0; b < nb; ++b) {
     if (shared_end[b] < nblk[b])
       units.push_back({b, G, shared_end[b], nblk[b], 1, false, false});

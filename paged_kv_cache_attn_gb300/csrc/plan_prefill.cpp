@@ -8,17 +8,19 @@
 
 #include <algorithm>
 #include <cstring>
+#include <new>
 
 #include "internal.h"
 
 using pkv::fail;
 
-extern "C" kv_status paged_latent_prefill_plan(
-    int32_t nb, int32_t Hq, int64_t num_blocks, int32_t max_blocks,
-    const int32_t* tables, const int32_t* seq_lens, const int32_t* q_lens,
-    int32_t num_sms, int32_t* plan, int64_t plan_cap,
-    kv_decode_plan_info* info) {
-  pkv::clear_error();
+namespace {
+
+kv_status prefill_plan(int32_t nb, int32_t Hq, int64_t num_blocks,
+                       int32_t max_blocks, const int32_t* tables,
+                       const int32_t* seq_lens, const int32_t* q_lens,
+                       int32_t* plan, int64_t plan_cap,
+                       kv_decode_plan_info* info) {
   if (!info || !tables || !seq_lens || !q_lens)
     return fail(KV_ERR_INVALID_ARG, "null argument");
   if (nb < 1 || Hq < 1 || Hq > 65535 || max_blocks < 1)
@@ -26,7 +28,6 @@ extern "C" kv_status paged_latent_prefill_plan(
                 max_blocks);
   if (num_blocks < 1 || num_blocks > (int64_t)INT32_MAX / 16)
     return fail(KV_ERR_INVALID_ARG, "num_blocks out of range");
-  (void)num_sms;
   std::vector<int32_t> uniq, valid, slots;
   std::vector<pkv::PrefillTile> tiles;
   std::vector<int32_t> slot_of(num_blocks, -1);
@@ -102,4 +103,21 @@ extern "C" kv_status paged_latent_prefill_plan(
   std::copy(slots.begin(), slots.end(), plan + off_slots);
   std::memcpy(plan + off_tiles, tiles.data(), tiles.size() * sizeof(pkv::PrefillTile));
   return KV_OK;
+}
+
+}  // namespace
+
+extern "C" kv_status paged_latent_prefill_plan(
+    int32_t nb, int32_t Hq, int64_t num_blocks, int32_t max_blocks,
+    const int32_t* tables, const int32_t* seq_lens, const int32_t* q_lens,
+    int32_t num_sms, int32_t* plan, int64_t plan_cap,
+    kv_decode_plan_info* info) {
+  pkv::clear_error();
+  (void)num_sms;
+  try {
+    return prefill_plan(nb, Hq, num_blocks, max_blocks, tables, seq_lens, q_lens,
+                        plan, plan_cap, info);
+  } catch (const std::bad_alloc&) {
+    return fail(KV_ERR_OOM, "no host memory for the plan");
+  }
 }

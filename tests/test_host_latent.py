@@ -349,3 +349,64 @@ def test_other_steps_refuse_latent_plans():
                                    0.1, P, P, i, P, 1 << 20, None)
     assert st == B.KV_ERR_INVALID_ARG
     assert b"latent" in B.lib().kv_last_error()
+
+
+def test_rows_and_tables_of_other_types_are_refused():
+    """A 16-bit float that is not bf16, or an integer table, has the right size
+    and would be read as something else."""
+    torch = pytest.importorskip("torch")
+    bf = dict(dtype=torch.bfloat16)
+    q, kv = torch.zeros(2, 4, 128, **bf), torch.zeros(2, 1, 128, **bf)
+    table = torch.zeros(8, 64, 2)
+    c, r, qr = (torch.zeros(2, 512, **bf), torch.zeros(2, 64, **bf),
+                torch.zeros(2, 4, 64, **bf))
+    t64 = torch.zeros(8, 32, 2)
+
+    def rope(**kw):
+        a = dict(q=q, k_new=kv, v_new=kv, rope=table, q_out=q, **{})
+        a.update(kw)
+        B.paged_rope_append(a["q"], a["k_new"], a["v_new"], a["rope"],
+                            B.KV_ROPE_HALVES, a["q_out"], P, P, 4, P, P, None, 2,
+                            2, 2, 4, 1, 128, torch.zeros(256, dtype=torch.uint8))
+
+    def latent(**kw):
+        a = dict(c=c, r=r, qr=qr, rope=t64)
+        a.update(kw)
+        B.paged_latent_append(a["c"], a["r"], a["qr"], a["rope"], B.KV_ROPE_PAIRS,
+                              a["qr"], P, P, 4, P, P, None, 2, 2, 2, 4,
+                              torch.zeros(256, dtype=torch.uint8))
+
+    for call, change in ((rope, dict(q=q.half())), (rope, dict(k_new=kv.half())),
+                         (rope, dict(v_new=kv.view(torch.int16))),
+                         (rope, dict(q_out=q.half())),
+                         (rope, dict(rope=table.int())),
+                         (latent, dict(c=c.half())), (latent, dict(r=r.half())),
+                         (latent, dict(qr=qr.half())),
+                         (latent, dict(rope=t64.int()))):
+        with pytest.raises(B.KVError) as e:
+            call(**change)
+        assert e.value.code == B.KV_ERR_INVALID_ARG
+
+
+NO_MEMORY = """
+import resource, numpy as np
+from paged_kv_cache_attn_gb300 import binding as B
+used = int(open("/proc/self/statm").read().split()[0]) * 4096
+resource.setrlimit(resource.RLIMIT_AS, (used + (64 << 20), used + (64 << 20)))
+try:
+    B.paged_latent_prefill_plan(1, 1, (2 ** 31 - 1) // 16, np.zeros((1, 1), np.int32),
+                                [5], [5])
+except B.KVError as e:
+    print("refused", e.code)
+"""
+
+
+def test_prefill_plan_without_host_memory():
+    """A plan that finds no memory is an error, not the end of the process."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(B.__file__)))
+    r = subprocess.run([sys.executable, "-c", NO_MEMORY], cwd=root,
+                       capture_output=True, text=True, timeout=120)
+    assert r.stdout.split() == ["refused", str(B.KV_ERR_OOM)], r.stderr[-2000:]
