@@ -26,7 +26,7 @@ struct LatentUnit {
 
 constexpr int kTileBlocks = 8;  // blocks of a 128-token tile
 constexpr int kMinTiles = 2;    // the shortest piece of a unit
-// Costs in half tiles (1 us): a tile, and an item's fixed part -- measured on
+// Costs in half tiles (0.85 us): a tile, and an item's fixed part -- measured on
 // steps of long and of short items: about 3.5 us, and 3 to 5 us more for 128 rows
 // of partial results.
 constexpr int kTileCost = 2;
