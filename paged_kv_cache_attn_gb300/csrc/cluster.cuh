@@ -252,6 +252,13 @@ __device__ __forceinline__ uint64_t sdesc_plain(uint32_t addr, uint32_t k,
          ((uint64_t)((m >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
 
+// Ask for one box of a 2-D map in L2.
+__device__ __forceinline__ void l2_prefetch_2d(const CUtensorMap* tm, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(tm),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 // Named barriers over `n` threads (whole warps), combining a predicate.
 __device__ __forceinline__ bool bar_and(int id, int n, bool v) {
   uint32_t r;

@@ -56,7 +56,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "cluster.cuh"
+#include "latent.cuh"
 #include "tensor_map.h"
 
 namespace pkv {
@@ -90,7 +90,6 @@ using tc::umma_ss;
 using tc::umma_ts;
 using tc::uniform;
 
-constexpr int kRank = KV_LATENT_RANK;
 constexpr int kT = 128;            // tokens of a score tile
 constexpr int kTB = kT / 16;       // its blocks
 constexpr int kG = 64;             // tokens of a P tile
@@ -136,22 +135,6 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 256;              // score CTA: Q 0..255, S 256..511
 constexpr float kRescale = 8.f;              // lazy-max threshold (log2 units)
 
-struct Params {
-  const uint8_t* c_pool;
-  const uint8_t* r_pool;
-  const int32_t* tables;
-  const int32_t* seq_lens;
-  const WorkItem* items;
-  const int32_t* pair_ptr;
-  float2* ml;
-  float* o;
-  __nv_bfloat16* out;
-  DeviceStatus* status;
-  int nb, Hq, max_blocks, n_items, n_pairs;
-  int64_t num_blocks, partial_rows;
-  float scale_log2;
-};
-
 // Barriers and small arrays, behind the tiles; at the same place in both CTAs.
 struct Small {
   // score CTA
@@ -173,60 +156,6 @@ struct Small {
 // there is no static shared memory in front of them.
 constexpr int kSmem = kTiles + (int)sizeof(Small);
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-
-__device__ __forceinline__ bool item_fits(const WorkItem& it, const Params& p) {
-  const int64_t last = (int64_t)it.row0 + it.nrows - 1;
-  return it.nrows >= 1 && it.nrows <= 128 && it.row0 >= 0 && it.branch0 >= 0 &&
-         it.branch0 + last / p.Hq < p.nb && it.blk_begin >= 0 &&
-         it.blk_begin < it.blk_end && it.blk_end <= p.max_blocks &&
-         (it.g != 0 || (it.prow_base >= 0 &&
-                        (int64_t)it.prow_base + it.nrows <= p.partial_rows));
-}
-
-// The items of this pair, the same for every role of both CTAs, read one
-// ahead.  Malformed ones are skipped by all (and recorded by one warp, see
-// report_bad).
-struct ItemLoop {
-  const Params& p;
-  int i, end;
-  WorkItem ahead;
-  __device__ ItemLoop(const Params& pp, int pair) : p(pp) {
-    i = p.pair_ptr[pair];
-    end = p.pair_ptr[pair + 1];
-    if (i < 0 || end > p.n_items || i > end) i = end = 0;
-    if (i < end) ahead = p.items[i];
-  }
-  __device__ bool next(WorkItem& it) {
-    while (i < end) {
-      it = ahead;
-      if (++i < end) ahead = p.items[i];
-      if (item_fits(it, p)) return true;
-    }
-    return false;
-  }
-};
-
-__device__ __forceinline__ void report_bad(const Params& p, int pair) {
-  const int a = p.pair_ptr[pair], b = p.pair_ptr[pair + 1];
-  if (a < 0 || b > p.n_items || a > b) {
-    record_status(p.status, KV_ERR_DEVICE, -1 - pair);
-    return;
-  }
-  for (int i = a; i < b; ++i)
-    if (!item_fits(p.items[i], p)) record_status(p.status, KV_ERR_DEVICE, -1 - i);
-}
-
-// The physical block of `blk` of the item, or -1 (past the range, or not a
-// block of the pool).
-__device__ __forceinline__ int block_of(const Params& p, const WorkItem& it,
-                                        int blk, bool& bad) {
-  bad = false;
-  if (blk >= it.blk_end) return -1;
-  const int phys = p.tables[(int64_t)it.branch0 * p.max_blocks + blk];
-  if (phys >= 0 && (int64_t)phys < p.num_blocks) return phys;
-  bad = true;
-  return -1;
-}
 
 __device__ __forceinline__ int n_tiles(const WorkItem& it) {
   return (it.blk_end - it.blk_begin + kTB - 1) / kTB;
@@ -311,7 +240,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // Launched early (the status word is being cleared): no global memory before
   // this point.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  ItemLoop loop(p, pair);
+  if (p.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  ItemLoop<false> loop(p, pair);
   fence_before_sync();
   __syncthreads();
   cluster_sync();  // the other CTA's barriers are ready too
@@ -687,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {
       if (!ok) timed_out(36);
-      report_bad(p, pair);
+      report_bad<false>(p, pair);
       if (tn > 0)
         mbar_wait(smem_u32(&bars.r_full[(tn - 1) & 1]), ((tn - 1) >> 1) & 1);
       if (in > 0) mbar_wait(smem_u32(&bars.qr_full), (in - 1) & 1);
@@ -988,31 +918,58 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
   if (w >= (int64_t)a.n * a.Hq) return;
   const int b = a.branches[w / a.Hq], r = (int)(w % a.Hq);
   if (b < 0 || b >= a.nb) return;
+  // A lane an entry for the weights, then every entry's row over the lanes: the
+  // rows' loads depend on nothing of one another.
   float m = -INFINITY, l = 0.f;
   float4 acc[4] = {};
   const int e1 = a.csr_ptr[b + 1];
-  for (int e = a.csr_ptr[b]; e < e1; ++e) {
-    const MergeEntry me = a.csr[e];
-    if (r < me.r_lo || r >= me.r_hi) continue;
-    const int64_t row = (int64_t)me.base + (r - me.r_lo);
-    if (row < 0 || row >= a.partial_rows) continue;
-    const float2 ml = a.ml[row];
-    const float4* src = reinterpret_cast<const float4*>(a.o + row * kRank) + lane;
-    float4 v[4];
+  for (int e0 = a.csr_ptr[b]; e0 < e1; e0 += 32) {
+    const int n = min(32, e1 - e0);
+    int row = -1;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) {
+      const MergeEntry me = a.csr[e0 + lane];
+      const int64_t at = (int64_t)me.base + (r - me.r_lo);
+      if (r >= me.r_lo && r < me.r_hi && at >= 0 && at < a.partial_rows) {
+        row = (int)at;
+        ml = a.ml[row];
+      }
+    }
+    float m_new = fmaxf(m, ml.x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = src[i * 32];
-    const float m_new = fmaxf(m, ml.x);
+    for (int k = 16; k > 0; k >>= 1)
+      m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, k));
+    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m_new);
+    float sum = ml.y * w;
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
     const float x = m == -INFINITY ? 0.f : ex2(m - m_new);
-    const float y = ml.x == -INFINITY ? 0.f : ex2(ml.x - m_new);
-    l = l * x + ml.y * y;
+    l = l * x + sum;
+    m = m_new;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      acc[i].x = acc[i].x * x + v[i].x * y;
-      acc[i].y = acc[i].y * x + v[i].y * y;
-      acc[i].z = acc[i].z * x + v[i].z * y;
-      acc[i].w = acc[i].w * x + v[i].w * y;
+      acc[i].x *= x;
+      acc[i].y *= x;
+      acc[i].z *= x;
+      acc[i].w *= x;
     }
-    m = m_new;
+#pragma unroll 2
+    for (int e = 0; e < n; ++e) {
+      const int at = __shfl_sync(0xffffffffu, row, e);
+      const float y = __shfl_sync(0xffffffffu, w, e);
+      if (at < 0 || y == 0.f) continue;
+      const float4* src = reinterpret_cast<const float4*>(a.o + (int64_t)at * kRank) + lane;
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = src[i * 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i].x += v[i].x * y;
+        acc[i].y += v[i].y * y;
+        acc[i].z += v[i].z * y;
+        acc[i].w += v[i].w * y;
+      }
+    }
   }
   const float inv = 1.f / l;
   uint2* dst = reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.Hq + r) * kRank) + lane;
@@ -1084,9 +1041,13 @@ extern "C" kv_status paged_latent_decode_attn(
   if (!(info->flags & KV_PLAN_LATENT))
     return fail(KV_ERR_INVALID_ARG, "a latent step needs a plan made with "
                                     "KV_PLAN_LATENT");
-  if (info->n_tile_items < 1 || info->n_tile_wide_items < 1 ||
-      info->n_tile_wide_items > 4096 || info->n_merge_rows < 0 ||
-      info->n_merge_rows > nb || info->partial_rows < 0)
+  if (info->n_tile_items < 1 || info->n_tile_wide_items < 0 ||
+      info->n_tile_wide_items > 4096 || info->n_row_warp_items < 0 ||
+      info->n_row_warp_items > 8192 || info->n_row_items < 0 ||
+      info->n_row_items > info->n_tile_items ||
+      (info->n_row_items > 0) != (info->n_row_warp_items > 0) ||
+      (info->n_row_items < info->n_tile_items) != (info->n_tile_wide_items > 0) ||
+      info->n_merge_rows < 0 || info->n_merge_rows > nb || info->partial_rows < 0)
     return fail(KV_ERR_INVALID_ARG, "plan info does not match the step");
   const size_t need = pkv::ws_total(info->partial_rows, rank);
   if (ws_bytes < need || (size_t)info->workspace_bytes != need)
@@ -1103,7 +1064,8 @@ extern "C" kv_status paged_latent_decode_attn(
     return s;
   const int64_t off_item = pkv::kPlanHeaderInts;
   const int64_t off_pair = off_item + 8 * (int64_t)info->n_tile_items;
-  const int64_t off_merge = off_pair + info->n_tile_wide_items + 1;
+  const int64_t off_few = off_pair + info->n_tile_wide_items + 1;
+  const int64_t off_merge = off_few + info->n_row_warp_items + 1;
   const int64_t off_ptr = off_merge + info->n_merge_rows;
   const int64_t off_ent = off_ptr + nb + 1;
   auto* ws = static_cast<uint8_t*>(workspace);
@@ -1115,6 +1077,7 @@ extern "C" kv_status paged_latent_decode_attn(
   p.seq_lens = seq_lens;
   p.items = reinterpret_cast<const pkv::WorkItem*>(plan + off_item);
   p.pair_ptr = plan + off_pair;
+  p.few_ptr = plan + off_few;
   p.ml = reinterpret_cast<float2*>(ws + pkv::ws_ml_offset());
   p.o = reinterpret_cast<float*>(ws + pkv::ws_o_offset(info->partial_rows));
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -1124,6 +1087,7 @@ extern "C" kv_status paged_latent_decode_attn(
   p.max_blocks = max_blocks;
   p.n_items = info->n_tile_items;
   p.n_pairs = info->n_tile_wide_items;
+  p.n_few_lists = info->n_row_warp_items;
   p.num_blocks = num_blocks;
   p.partial_rows = info->partial_rows;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -1133,9 +1097,14 @@ extern "C" kv_status paged_latent_decode_attn(
     return fail(KV_ERR_CUDA, "latent step: %s", cudaGetErrorString(e));
   lat::latent_clear_kernel<<<1, 32, 0, st>>>(p.status);
   e = cudaGetLastError();
-  if (e == cudaSuccess)
+  const bool few = info->n_row_items > 0;
+  const bool many = info->n_row_items < info->n_tile_items;
+  p.trigger = few && many;
+  if (e == cudaSuccess && many)
     e = pkv::launch_early(lat::latent_decode_kernel, 2 * p.n_pairs, lat::kThreads,
                           lat::kSmem, st, tk, tv, tr, tq, tq_all, p);
+  if (e == cudaSuccess && few)
+    e = pkv::launch_latent_few(tv, tr, tq, p, many, st);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "latent kernel: %s", cudaGetErrorString(e));
   if (info->n_merge_rows > 0) {

@@ -122,6 +122,8 @@ inline size_t ws_total(int64_t rows, int d) {
 struct PrefillTile {
   int32_t row0, nrows, pos0, table;
 };
+// Latent decode items of at most this many rows run on one SM each.
+constexpr int kLatentFewRows = 16;
 constexpr int32_t kPrefillPlanMagic = 0x31504B50;  // "PKP1"
 constexpr int32_t kPrefillPlan = 32;  // info.flags of a prefill plan
 constexpr int kPrefillRows = 256;     // query rows of a tile

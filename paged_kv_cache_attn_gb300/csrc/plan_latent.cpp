@@ -9,11 +9,17 @@
 // the first tile's latency, the epilogue), so that a step of many short items
 // is balanced too, and no piece is cut shorter than two tiles.
 //
+// Items of at most 16 rows run on one SM each (decode_latent_few.cu), in lists of
+// their own; the other items' lists come first in the plan.  The two kernels run
+// beside each other, each on the SMs that its share of the work is worth.
+//
 // A branch whose rows lie in one item each is finished by that item, which
 // writes its output; the other rows' partial results are merged.
 
 #include <algorithm>
 #include <cstring>
+#include <functional>
+#include <utility>
 
 #include "internal.h"
 
@@ -25,12 +31,16 @@ struct LatentUnit {
 };
 
 constexpr int kTileBlocks = 8;  // blocks of a 128-token tile
-constexpr int kMinTiles = 2;    // the shortest piece of a unit
+constexpr int kMinTiles = 2;    // the shortest piece of a unit (few rows: 1)
 // Costs in half tiles (0.85 us): a tile, and an item's fixed part -- measured on
 // steps of long and of short items: about 3.5 us, and 3 to 5 us more for 128 rows
 // of partial results.
 constexpr int kTileCost = 2;
-int32_t item_cost(int32_t nrows) { return 4 + nrows / 32; }
+// For few rows, in tiles' worth of an SM's time (3.3 us a 128-token tile, where
+// HBM brings every SM its share): about 3 us.
+int32_t item_cost(int32_t nrows) {
+  return nrows <= kLatentFewRows ? 2 : 4 + nrows / 32;
+}
 
 struct Piece {
   int32_t unit, lo, hi;  // blocks
@@ -38,32 +48,33 @@ struct Piece {
 
 int32_t tiles(int32_t blocks) { return (blocks + kTileBlocks - 1) / kTileBlocks; }
 
-// Deal the units out to pairs of at most `share` cost each; returns whether
-// they fit `pairs` pairs.
-bool deal(const std::vector<LatentUnit>& units, int64_t share, int32_t pairs,
-          std::vector<Piece>* out, std::vector<int32_t>* ptr) {
+// Deal the units `which` out to `bins` lists of at most `share` cost each, no
+// piece shorter than `least` tiles; returns whether they fit.
+bool deal(const std::vector<LatentUnit>& units, const std::vector<int32_t>& which,
+          int64_t share, int32_t bins, int32_t least, std::vector<Piece>* out,
+          std::vector<int32_t>* ptr) {
   out->clear();
   ptr->assign(1, 0);
   int64_t used = 0;  // cost of the pair being filled
-  for (int32_t u = 0; u < (int32_t)units.size(); ++u) {
+  for (int32_t u : which) {
     int32_t lo = units[u].blk_begin;
     while (lo < units[u].blk_end) {
       const int32_t left = tiles(units[u].blk_end - lo);
       const int32_t fixed = item_cost(units[u].nrows);
       int64_t room = (share - used - fixed) / kTileCost;  // tiles
-      if (used > 0 && room < std::min(left, kMinTiles)) {
+      if (used > 0 && room < std::min(left, least)) {
         ptr->push_back((int32_t)out->size());
-        if ((int32_t)ptr->size() > pairs) return false;
+        if ((int32_t)ptr->size() > bins) return false;
         used = 0;
         room = (share - fixed) / kTileCost;
       }
-      room = std::max<int64_t>(room, kMinTiles);
+      room = std::max<int64_t>(room, least);
       // The rest of the unit is not left shorter than the shortest piece.
       int32_t take = left;
       if (left > room) {
         take = (int32_t)room;
-        if (left - take < kMinTiles) take = left - kMinTiles;
-        if (take < kMinTiles) take = left;
+        if (left - take < least) take = left - least;
+        if (take < least) take = left;
       }
       const int32_t hi =
           std::min(units[u].blk_end, lo + take * kTileBlocks);
@@ -73,7 +84,60 @@ bool deal(const std::vector<LatentUnit>& units, int64_t share, int32_t pairs,
     }
   }
   ptr->push_back((int32_t)out->size());
-  return (int32_t)ptr->size() - 1 <= pairs;
+  return (int32_t)ptr->size() - 1 <= bins;
+}
+
+// Place the units `which` whole, the costliest first (they come so), each on the
+// list with the least so far; what a unit costs beyond a share is cut off in
+// shares.  Returns whether no list gets more than `share`.
+bool place(const std::vector<LatentUnit>& units, const std::vector<int32_t>& which,
+           int64_t share, int32_t bins, std::vector<Piece>* out,
+           std::vector<int32_t>* ptr) {
+  struct Part {
+    Piece p;
+    int64_t cost;
+  };
+  std::vector<Part> parts;
+  for (int32_t u : which) {
+    const LatentUnit& x = units[u];
+    const int64_t n = tiles(x.blk_end - x.blk_begin);
+    const int64_t fixed = item_cost(x.nrows);
+    int64_t room = n;
+    if (n * kTileCost + fixed > share) {
+      room = (share - fixed) / kTileCost;
+      if (room < 2 * kMinTiles) return false;
+    }
+    for (int64_t i = 0; i < n;) {
+      int64_t k = std::min(room, n - i);
+      if (n - i - k > 0 && n - i - k < kMinTiles) k -= kMinTiles;
+      parts.push_back({{u, x.blk_begin + (int32_t)i * kTileBlocks,
+                        (int32_t)std::min<int64_t>(
+                            x.blk_end, x.blk_begin + (i + k) * kTileBlocks)},
+                       k * kTileCost + fixed});
+      i += k;
+    }
+  }
+  std::stable_sort(parts.begin(), parts.end(),
+                   [](const Part& x, const Part& y) { return x.cost > y.cost; });
+  bins = (int32_t)std::min<size_t>(bins, parts.size());
+  std::vector<std::pair<int64_t, int32_t>> load(bins);  // min-heap
+  for (int32_t i = 0; i < bins; ++i) load[i] = {0, i};
+  std::vector<std::vector<int32_t>> of(bins);
+  for (int32_t i = 0; i < (int32_t)parts.size(); ++i) {
+    std::pop_heap(load.begin(), load.end(), std::greater<>());
+    auto& least = load.back();
+    least.first += parts[i].cost;
+    if (least.first > share) return false;
+    of[least.second].push_back(i);
+    std::push_heap(load.begin(), load.end(), std::greater<>());
+  }
+  out->clear();
+  ptr->assign(1, 0);
+  for (const auto& list : of) {
+    for (int32_t i : list) out->push_back(parts[i].p);
+    ptr->push_back((int32_t)out->size());
+  }
+  return true;
 }
 
 }  // namespace
@@ -110,17 +174,69 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
                      return x.blk_end - x.blk_begin > y.blk_end - y.blk_begin;
                    });
   const int32_t pairs_max = std::max(1, num_sms / 2);
-  int64_t cost = 0;
-  for (const LatentUnit& u : units)
-    cost += (int64_t)tiles(u.blk_end - u.blk_begin) * kTileCost +
-            item_cost(u.nrows);
-  int64_t share = std::max<int64_t>((cost + pairs_max - 1) / pairs_max,
-                                    kTileCost * kMinTiles);
-  std::vector<Piece> pieces;
-  std::vector<int32_t> ptr;
-  while (!deal(units, share, pairs_max, &pieces, &ptr))
-    share += std::max<int64_t>(1, share / 50);
-  const int32_t n_pairs = (int32_t)ptr.size() - 1;
+  std::vector<Piece> pieces, more;
+  std::vector<int32_t> ptr[2];  // the pairs' lists, the SMs' lists of few rows
+  int64_t chunk = 0;
+  int32_t n_few = 0;
+  std::vector<int32_t> kind[2];
+  int64_t total_cost[2] = {0, 0};
+  for (int32_t u = 0; u < (int32_t)units.size(); ++u) {
+    const int few = units[u].nrows <= kLatentFewRows;
+    kind[few].push_back(u);
+    total_cost[few] +=
+        (int64_t)tiles(units[u].blk_end - units[u].blk_begin) * kTileCost +
+        item_cost(units[u].nrows);
+  }
+  // Both kinds: SMs in proportion to their times there, 0.7 us a pair and 0.94 us
+  // an SM for a unit of cost.
+  int32_t lists_max[2] = {pairs_max, 2 * pairs_max};
+  if (!kind[0].empty() && !kind[1].empty()) {
+    const double many = 0.7 * total_cost[0], few = 0.47 * total_cost[1];
+    lists_max[0] = std::max(
+        1, std::min(pairs_max - 1, (int32_t)(pairs_max * many / (many + few) + 0.5)));
+    lists_max[1] = std::max(1, 2 * (pairs_max - lists_max[0]));
+  }
+  for (int few = 0; few < 2; ++few) {
+    const std::vector<int32_t>& which = kind[few];
+    const int64_t cost = total_cost[few];
+    ptr[few].assign(1, few ? (int32_t)pieces.size() : 0);
+    if (which.empty()) continue;
+    const int32_t bins = lists_max[few];
+    const int32_t least = few ? 1 : kMinTiles;
+    std::vector<Piece> dealt, whole;
+    std::vector<int32_t> cuts, whole_cuts;
+    const int64_t mean = (cost + bins - 1) / bins;
+    int64_t share = std::max<int64_t>(mean, kTileCost * least);
+    while (!deal(units, which, share, bins, least, &dealt, &cuts))
+      share += std::max<int64_t>(1, share / 50);
+    // Dealt out in order, every share's end cuts a unit, and a cut of 128 rows
+    // costs a second query load, 128 rows more of partial results and their
+    // merge.  Where the units fit whole into no larger shares they are placed so.
+    if (!few && place(units, which, share, bins, &whole, &whole_cuts)) {
+      int64_t lo = mean, hi = share;
+      dealt.swap(whole);
+      cuts.swap(whole_cuts);
+      while (hi - lo > hi / 64) {
+        const int64_t mid = (lo + hi) / 2;
+        if (place(units, which, mid, bins, &whole, &whole_cuts)) {
+          dealt.swap(whole);
+          cuts.swap(whole_cuts);
+          hi = mid;
+        } else {
+          lo = mid + 1;
+        }
+      }
+      share = hi;
+    }
+    chunk = std::max(chunk, share);
+    const int32_t at = (int32_t)pieces.size();
+    pieces.insert(pieces.end(), dealt.begin(), dealt.end());
+    ptr[few].clear();
+    for (int32_t c : cuts) ptr[few].push_back(at + c);
+    if (few) n_few = (int32_t)dealt.size();
+  }
+  const int32_t n_pairs = (int32_t)ptr[0].size() - 1;
+  const int32_t n_lists = (int32_t)ptr[1].size() - 1;
 
   // Pieces of each unit; a branch is finished in one item when it lies in one
   // unit (per row tile) of one piece.
@@ -170,7 +286,7 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   const int64_t n_csr = (int64_t)merge.size();
   const int64_t off_item = kPlanHeaderInts;
   const int64_t off_pair = off_item + 8 * (int64_t)items.size();
-  const int64_t off_merge = off_pair + n_pairs + 1;
+  const int64_t off_merge = off_pair + n_pairs + 1 + n_lists + 1;
   const int64_t off_ptr = off_merge + (int64_t)merged.size();
   const int64_t off_ent = off_ptr + nb + 1;
   const int64_t total = off_ent + 4 * n_csr;
@@ -181,8 +297,10 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   info->partial_rows = prow;
   info->n_tile_items = (int32_t)items.size();
   info->n_tile_wide_items = n_pairs;
+  info->n_row_items = n_few;
+  info->n_row_warp_items = n_lists;
   info->n_merge_rows = (int32_t)merged.size();
-  info->chunk_blocks = (int32_t)std::min<int64_t>(INT32_MAX, share / kTileCost * kTileBlocks);
+  info->chunk_blocks = (int32_t)std::min<int64_t>(INT32_MAX, chunk / kTileCost * kTileBlocks);
   info->flags = flags;
   if (!plan) return KV_OK;
   if (plan_cap < total)
@@ -205,7 +323,8 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   h[H_FLAGS] = flags;
   h[H_TOTAL] = (int32_t)total;
   std::memcpy(h + off_item, items.data(), items.size() * sizeof(WorkItem));
-  std::copy(ptr.begin(), ptr.end(), h + off_pair);
+  std::copy(ptr[1].begin(), ptr[1].end(),
+            std::copy(ptr[0].begin(), ptr[0].end(), h + off_pair));
   std::copy(merged.begin(), merged.end(), h + off_merge);
   int32_t* cp = h + off_ptr;
   int32_t* ent = h + off_ent;

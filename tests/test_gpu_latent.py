@@ -133,6 +133,64 @@ def test_rising_scores_rescale_every_tile():
     c.close()
 
 
+@pytest.mark.parametrize("lens,Hq", [([600] * 170, 16), ([2000, 700], 128),
+                                     ([333] * 90, 24), ([1500, 40], 1)])
+def test_rising_scores_of_whole_branches(lens, Hq):
+    """The same where an item has many tiles: long lists, 1 to 128 rows."""
+    w = lengths(lens, Hq)
+    c = H.Cache(w, kv_dtype="latent")
+    bt = c.batch().upload()
+    c.v[0, :, 0, :, :] = 0
+    for b, L in enumerate(lens):
+        t = torch.from_numpy(bt.tables[b][:-(-L // 16)].astype(np.int64)).cuda()
+        ramp = torch.arange(len(t) * 16, device="cuda") * 0.25
+        c.v[0, t, 0, :, 0] = ramp.view(-1, 16).bfloat16()
+    q = queries(len(lens), Hq, 7)
+    q[..., 512:] = 0
+    q[..., 512] = 8.0
+    out = torch.empty((len(lens), Hq, 512), dtype=torch.bfloat16, device="cuda")
+    bt.decode(q, out)
+    assert bt.device_status() == (0, 0)
+    check(c, bt, q, out, "ramp", rows=range(0, len(lens), 13))
+    c.close()
+
+
+@pytest.mark.parametrize("name", ["fanout", "many_short", "split_128", "long"])
+def test_repeated_steps(name):
+    """Hundreds of steps without a pause: no wait runs out, the bits stay."""
+    w = CASES[name]()
+    c = H.Cache(w, kv_dtype="latent", poison=True)
+    bt = c.batch().upload()
+    q = queries(bt.nb, w.Hq, 11)
+    first = torch.empty((bt.nb, w.Hq, 512), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(first)
+    bt.decode(q, first)
+    assert bt.device_status() == (0, 0)
+    for _ in range(40):
+        for _ in range(10):
+            bt.decode(q, out)
+        assert bt.device_status() == (0, 0)
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16))
+    c.close()
+
+
+def test_bad_block_ids_of_many_rows():
+    w = lengths([100, 300], 48)
+    c = H.Cache(w, kv_dtype="latent")
+    bt = c.batch().upload()
+    q = queries(2, 48, 2)
+    out = torch.empty((2, 48, 512), dtype=torch.bfloat16, device="cuda")
+    for bad in (w.num_blocks, -1, 1 << 30):
+        bt.dev["tables"][1, 4] = bad
+        bt.decode(q, out)
+        assert bt.device_status() == (B.KV_ERR_DEVICE, bad)
+    bt.dev["tables"][1, 4] = int(bt.tables[1, 4])
+    bt.decode(q, out)
+    assert bt.device_status() == (0, 0)
+    check(c, bt, q, out, "after")
+    c.close()
+
+
 @pytest.mark.parametrize("name,Hq", [("independent", 128), ("fanout", 16),
                                      ("deep_tree", 16)])
 def test_full_size(name, Hq):

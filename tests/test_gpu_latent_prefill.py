@@ -225,6 +225,19 @@ def test_bad_plan_entries_are_reported():
     s.check()
 
 
+def test_repeated_steps():
+    """Hundreds of steps without a pause: no wait runs out, the bits stay."""
+    s = Step([700, 333, 90], [300, 333, 1], 16, seed=15)
+    s.run()
+    s.check(heads=[3])
+    first = s.out.clone()
+    for _ in range(40):
+        for _ in range(10):
+            s.run()
+        assert B.kv_check_device_status(s.ws) == (0, 0)
+        assert torch.equal(s.out.view(torch.int16), first.view(torch.int16))
+
+
 def test_prompt_then_decode():
     """A prompt enters a latent pool, attends, is forked, and the branches
     decode: append, expanded and absorbed attention over one cache.  The absorbed

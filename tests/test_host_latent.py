@@ -42,19 +42,26 @@ def read_plan(plan, info, nb):
     o = 16 + 8 * n
     ptr = plan[o:o + pairs + 1]
     o += pairs + 1
+    few = plan[o:o + info.n_row_warp_items + 1]
+    o += info.n_row_warp_items + 1
     branches = plan[o:o + merged]
     o += merged
     cp = plan[o:o + nb + 1]
     ent = plan[o + nb + 1:].reshape(-1, 4)
     assert o + nb + 1 + 4 * cp[-1] == info.plan_ints == len(plan)
-    return items, ptr, branches, cp, ent
+    return items, ptr, few, branches, cp, ent
 
 
 def check_plan(Hq, lens, groups, plan, info, num_sms):
     nb = len(lens)
-    items, ptr, branches, cp, ent = read_plan(plan, info, nb)
-    assert ptr[0] == 0 and ptr[-1] == len(items) and (np.diff(ptr) > 0).all()
+    items, ptr, few, branches, cp, ent = read_plan(plan, info, nb)
+    # The pairs' lists, then the SMs' lists of items of at most 16 rows.
+    assert ptr[0] == 0 and ptr[-1] == few[0] and few[-1] == len(items)
+    assert (np.diff(ptr) > 0).all() and (np.diff(few) > 0).all()
     assert len(ptr) - 1 <= max(num_sms // 2, 1)
+    assert len(few) - 1 <= 2 * max(num_sms // 2, 1)
+    assert info.n_row_items == len(items) - few[0]
+    assert (items[:few[0], 3] > 16).all() and (items[few[0]:, 3] <= 16).all()
     # Every (row, block) once.
     seen = [np.zeros((Hq, -(-n // 16)), int) for n in lens]
     rows_of = {}                       # partial row -> (branch, head)
@@ -91,9 +98,9 @@ def check_plan(Hq, lens, groups, plan, info, num_sms):
     for b, h in done:
         assert cp[b + 1] == cp[b]
     assert len(rows_of) == info.partial_rows
-    cost = [sum(2 * -(-(i[5] - i[4]) // 8) + 4 + i[3] // 32
-                for i in items[ptr[p]:ptr[p + 1]]) for p in range(len(ptr) - 1)]
-    return cost
+    return [[sum(2 * -(-(i[5] - i[4]) // 8) + fixed(i[3])
+                 for i in items[x[p]:x[p + 1]]) for p in range(len(x) - 1)]
+            for x, fixed in ((ptr, lambda r: 4 + r // 32), (few, lambda r: 2))]
 
 
 @pytest.mark.parametrize("Hq", [1, 3, 16, 64, 128, 129, 300])
@@ -127,12 +134,15 @@ def test_latent_plan_trees(name, Hq):
 
 
 def test_latent_plan_balances_long_steps():
-    """No pair of a long step costs more than a few percent above the mean."""
+    """No pair (or SM) of a long step costs more than a few percent above the
+    mean."""
     lens = [32768] * 16
-    plan, info = B.paged_decode_plan(16, 16, 1, 512, 2048, lens, [], 152,
-                                     B.KV_PLAN_LATENT)
-    cost = check_plan(16, lens, [], plan, info, 152)
-    assert max(cost) <= 1.06 * sum(cost) / 76
+    for Hq, which, lists in ((16, 1, 152), (128, 0, 76)):
+        plan, info = B.paged_decode_plan(16, Hq, 1, 512, 2048, lens, [], 152,
+                                         B.KV_PLAN_LATENT)
+        cost = check_plan(Hq, lens, [], plan, info, 152)
+        assert not cost[1 - which]
+        assert max(cost[which]) <= 1.06 * sum(cost[which]) / lists
 
 
 def test_latent_plan_refusals():
