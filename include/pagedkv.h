@@ -474,7 +474,9 @@ typedef struct kv_decode_plan_info {
   int64_t plan_ints;       /* int32 entries of the plan */
   int64_t workspace_bytes; /* device workspace paged_decode_attn needs */
   int64_t partial_rows;    /* (o, m, l) partial rows in the workspace */
-  int32_t n_row_items;     /* work items of the split-KV (mma.sync) kernel */
+  int32_t n_row_items;     /* work items of the split-KV (mma.sync) kernel;
+                              latent steps: those of n_tile_items with at most
+                              16 query rows, which run on one SM each */
   int32_t n_tile_items;    /* work items of the tcgen05 kernels (the first
                               n_tile_wide_items of up to 256 rows, the rest
                               of up to 128) */
@@ -487,7 +489,9 @@ typedef struct kv_decode_plan_info {
   int32_t n_row_warp_items; /* the last n_row_warp_items of the split-KV
                                items are short (at most 16 blocks): the bf16
                                split-KV kernel runs them four to a CTA, one
-                               per warp; the others take a whole CTA */
+                               per warp; the others take a whole CTA.  Latent
+                               steps: the lists of items of few rows
+                               (n_tile_wide_items: the lists of the others) */
   int32_t reserved;        /* 0 */
 } kv_decode_plan_info;
 

@@ -1,4 +1,6 @@
-// Decode attention over a latent pool, absorbed form (paged_latent_decode_attn).
+// Decode attention over a latent pool, absorbed form (paged_latent_decode_attn):
+// the entry, the merge, and the kernel for items of more than 16 rows (the others
+// run on one SM each, decode_latent_few.cu, beside this one).
 //
 // For every query row (a branch and a head), with c_t the latent (512) and r_t
 // the position key (64) of token t:
@@ -39,8 +41,7 @@
 // Measured: 1.7 us a 128-token tile and pair of SMs, on steps of many rows (1.13
 // us of products) as on steps of few.  The latents pass from L2 twice, as K into
 // one SM and as V into the other: 272 KB a tile, 13 TB/s over all SMs, which is
-// what L2 gave a kernel that does nothing else (13.9); with 16 long contexts HBM
-// is at its limit too (6.6 TB/s).  An item's end costs 128 rows 4 us (256 KB of
+// what L2 gave a kernel that does nothing else (13.9).  An item's end costs 128 rows 4 us (256 KB of
 // partial results; an SM stores 29 bytes a cycle, by bulk copies too), a step's
 // start 5 to 7 us.  Prefetches of K or of the position keys into L2 changed
 // nothing or made it slower.

@@ -18,8 +18,6 @@
 
 #include <algorithm>
 #include <cstring>
-#include <functional>
-#include <utility>
 
 #include "internal.h"
 
@@ -87,59 +85,6 @@ bool deal(const std::vector<LatentUnit>& units, const std::vector<int32_t>& whic
   return (int32_t)ptr->size() - 1 <= bins;
 }
 
-// Place the units `which` whole, the costliest first (they come so), each on the
-// list with the least so far; what a unit costs beyond a share is cut off in
-// shares.  Returns whether no list gets more than `share`.
-bool place(const std::vector<LatentUnit>& units, const std::vector<int32_t>& which,
-           int64_t share, int32_t bins, std::vector<Piece>* out,
-           std::vector<int32_t>* ptr) {
-  struct Part {
-    Piece p;
-    int64_t cost;
-  };
-  std::vector<Part> parts;
-  for (int32_t u : which) {
-    const LatentUnit& x = units[u];
-    const int64_t n = tiles(x.blk_end - x.blk_begin);
-    const int64_t fixed = item_cost(x.nrows);
-    int64_t room = n;
-    if (n * kTileCost + fixed > share) {
-      room = (share - fixed) / kTileCost;
-      if (room < 2 * kMinTiles) return false;
-    }
-    for (int64_t i = 0; i < n;) {
-      int64_t k = std::min(room, n - i);
-      if (n - i - k > 0 && n - i - k < kMinTiles) k -= kMinTiles;
-      parts.push_back({{u, x.blk_begin + (int32_t)i * kTileBlocks,
-                        (int32_t)std::min<int64_t>(
-                            x.blk_end, x.blk_begin + (i + k) * kTileBlocks)},
-                       k * kTileCost + fixed});
-      i += k;
-    }
-  }
-  std::stable_sort(parts.begin(), parts.end(),
-                   [](const Part& x, const Part& y) { return x.cost > y.cost; });
-  bins = (int32_t)std::min<size_t>(bins, parts.size());
-  std::vector<std::pair<int64_t, int32_t>> load(bins);  // min-heap
-  for (int32_t i = 0; i < bins; ++i) load[i] = {0, i};
-  std::vector<std::vector<int32_t>> of(bins);
-  for (int32_t i = 0; i < (int32_t)parts.size(); ++i) {
-    std::pop_heap(load.begin(), load.end(), std::greater<>());
-    auto& least = load.back();
-    least.first += parts[i].cost;
-    if (least.first > share) return false;
-    of[least.second].push_back(i);
-    std::push_heap(load.begin(), load.end(), std::greater<>());
-  }
-  out->clear();
-  ptr->assign(1, 0);
-  for (const auto& list : of) {
-    for (int32_t i : list) out->push_back(parts[i].p);
-    ptr->push_back((int32_t)out->size());
-  }
-  return true;
-}
-
 }  // namespace
 
 kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
@@ -174,7 +119,7 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
                      return x.blk_end - x.blk_begin > y.blk_end - y.blk_begin;
                    });
   const int32_t pairs_max = std::max(1, num_sms / 2);
-  std::vector<Piece> pieces, more;
+  std::vector<Piece> pieces;
   std::vector<int32_t> ptr[2];  // the pairs' lists, the SMs' lists of few rows
   int64_t chunk = 0;
   int32_t n_few = 0;
@@ -188,7 +133,8 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
         item_cost(units[u].nrows);
   }
   // Both kinds: SMs in proportion to their times there, 0.7 us a pair and 0.94 us
-  // an SM for a unit of cost.
+  // an SM for a unit of cost (8 roots x 64 branches: 108 us; with 1.1 us 113, with
+  // 0.8 113; one kind after the other on all SMs 123).
   int32_t lists_max[2] = {pairs_max, 2 * pairs_max};
   if (!kind[0].empty() && !kind[1].empty()) {
     const double many = 0.7 * total_cost[0], few = 0.47 * total_cost[1];
@@ -203,31 +149,12 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
     if (which.empty()) continue;
     const int32_t bins = lists_max[few];
     const int32_t least = few ? 1 : kMinTiles;
-    std::vector<Piece> dealt, whole;
-    std::vector<int32_t> cuts, whole_cuts;
-    const int64_t mean = (cost + bins - 1) / bins;
-    int64_t share = std::max<int64_t>(mean, kTileCost * least);
+    std::vector<Piece> dealt;
+    std::vector<int32_t> cuts;
+    int64_t share =
+        std::max<int64_t>((cost + bins - 1) / bins, kTileCost * least);
     while (!deal(units, which, share, bins, least, &dealt, &cuts))
       share += std::max<int64_t>(1, share / 50);
-    // Dealt out in order, every share's end cuts a unit, and a cut of 128 rows
-    // costs a second query load, 128 rows more of partial results and their
-    // merge.  Where the units fit whole into no larger shares they are placed so.
-    if (!few && place(units, which, share, bins, &whole, &whole_cuts)) {
-      int64_t lo = mean, hi = share;
-      dealt.swap(whole);
-      cuts.swap(whole_cuts);
-      while (hi - lo > hi / 64) {
-        const int64_t mid = (lo + hi) / 2;
-        if (place(units, which, mid, bins, &whole, &whole_cuts)) {
-          dealt.swap(whole);
-          cuts.swap(whole_cuts);
-          hi = mid;
-        } else {
-          lo = mid + 1;
-        }
-      }
-      share = hi;
-    }
     chunk = std::max(chunk, share);
     const int32_t at = (int32_t)pieces.size();
     pieces.insert(pieces.end(), dealt.begin(), dealt.end());
