@@ -552,9 +552,9 @@ def _types():
     return _dtypes
 
 
-def _token_rows(t, width):
-    """(pointer, distance between tokens in values) of a bf16 tensor whose
-    tokens (dimension 0) are rows of `width` contiguous values."""
+def _token_rows(t, width, total):
+    """(pointer, distance between tokens in values) of a bf16 tensor of at least
+    `total` tokens (dimension 0), rows of `width` contiguous values."""
     if t is None:
         return None, 0
     sh, st = t.shape, t.stride()
@@ -563,10 +563,10 @@ def _token_rows(t, width):
             (st[1] == sh[2] or sh[1] == 1)
     else:
         ok = len(sh) == 2 and sh[1] == width and st[1] == 1
-    if not ok or t.dtype is not _types()[0]:
+    if not ok or t.dtype is not _types()[0] or sh[0] < total:
         raise KVError(KV_ERR_INVALID_ARG,
-                      f"a token is {width} contiguous bf16 values, got "
-                      f"{tuple(sh)} of {t.dtype}, strides {st}")
+                      f"expected {total} tokens of {width} contiguous bf16 "
+                      f"values, got {tuple(sh)} of {t.dtype}, strides {st}")
     return t.data_ptr(), st[0] if sh[0] > 1 else width
 
 
@@ -590,9 +590,10 @@ def paged_rope_append(q, k_new, v_new, rope, rope_style, q_out, k_pool, v_pool,
     workspace: a zeroed uint8 tensor of >= 256 bytes."""
     rp, rlen, rot = _rope_table(rope)
     _check(_lib.paged_rope_append(
-        *_token_rows(q, Hq * head_dim), *_token_rows(k_new, Hkv * head_dim),
-        *_token_rows(v_new, Hkv * head_dim), rp, rlen, rot, rope_style,
-        *_token_rows(q_out, Hq * head_dim), _ptr(k_pool), _ptr(v_pool),
+        *_token_rows(q, Hq * head_dim, total),
+        *_token_rows(k_new, Hkv * head_dim, total),
+        *_token_rows(v_new, Hkv * head_dim, total), rp, rlen, rot, rope_style,
+        *_token_rows(q_out, Hq * head_dim, total), _ptr(k_pool), _ptr(v_pool),
         num_blocks, _ptr(block_tables), _ptr(seq_lens), _ptr(row_offsets),
         total, nb, max_blocks, Hq, Hkv, head_dim, block_size, _ptr(workspace),
         workspace.numel(), _stream(stream)))
@@ -606,24 +607,25 @@ def paged_rope_append_e4m3(q, k_new, v_new, rope, rope_style, q_out, k_pool,
     """As paged_rope_append, into an e4m3 pool."""
     rp, rlen, rot = _rope_table(rope)
     _check(_lib.paged_rope_append_e4m3(
-        *_token_rows(q, Hq * head_dim), *_token_rows(k_new, Hkv * head_dim),
-        *_token_rows(v_new, Hkv * head_dim), rp, rlen, rot, rope_style,
-        *_token_rows(q_out, Hq * head_dim), _ptr(k_pool), _ptr(v_pool),
+        *_token_rows(q, Hq * head_dim, total),
+        *_token_rows(k_new, Hkv * head_dim, total),
+        *_token_rows(v_new, Hkv * head_dim, total), rp, rlen, rot, rope_style,
+        *_token_rows(q_out, Hq * head_dim, total), _ptr(k_pool), _ptr(v_pool),
         _ptr(kv_scales), num_blocks, _ptr(block_tables), _ptr(seq_lens),
         _ptr(row_offsets), total, nb, max_blocks, Hq, Hkv, head_dim,
         block_size, _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
-def _head_rows(t, heads, width):
-    """(pointer, distance between tokens, between heads) of a bf16 tensor
-    [total][heads][width] with contiguous values in a head."""
+def _head_rows(t, heads, width, total):
+    """(pointer, distance between tokens, between heads) of a bf16 tensor of at
+    least `total` tokens [total][heads][width], contiguous values in a head."""
     if t is None:
         return None, 0, 0
     sh, st = t.shape, t.stride()
     if len(sh) != 3 or sh[1] != heads or sh[2] != width or st[2] != 1 or \
-            t.dtype is not _types()[0]:
+            t.dtype is not _types()[0] or sh[0] < total:
         raise KVError(KV_ERR_INVALID_ARG,
-                      f"expected bf16 [total][{heads}][{width}], got "
+                      f"expected bf16 [{total}][{heads}][{width}], got "
                       f"{tuple(sh)} of {t.dtype}, strides {st}")
     hs = st[1] if heads > 1 else width
     ts = st[0] if sh[0] > 1 else (heads - 1) * hs + width
@@ -641,9 +643,10 @@ def paged_latent_append(c_new, r_new, q_rope, rope, rope_style, q_rope_out,
         raise KVError(KV_ERR_INVALID_ARG, f"rope table for {rot} dimensions, "
                                           f"not {KV_LATENT_ROPE}")
     _check(_lib.paged_latent_append(
-        *_token_rows(c_new, KV_LATENT_RANK), *_token_rows(r_new, KV_LATENT_ROPE),
-        *_head_rows(q_rope, Hq, KV_LATENT_ROPE), rp, rlen, rope_style,
-        *_head_rows(q_rope_out, Hq, KV_LATENT_ROPE), _ptr(c_pool), _ptr(r_pool),
+        *_token_rows(c_new, KV_LATENT_RANK, total),
+        *_token_rows(r_new, KV_LATENT_ROPE, total),
+        *_head_rows(q_rope, Hq, KV_LATENT_ROPE, total), rp, rlen, rope_style,
+        *_head_rows(q_rope_out, Hq, KV_LATENT_ROPE, total), _ptr(c_pool), _ptr(r_pool),
         num_blocks, _ptr(block_tables), _ptr(seq_lens), _ptr(row_offsets),
         total, nb, max_blocks, Hq, KV_LATENT_RANK, KV_LATENT_ROPE, block_size,
         _ptr(workspace), workspace.numel(), _stream(stream)))

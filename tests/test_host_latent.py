@@ -363,7 +363,7 @@ def test_other_steps_refuse_latent_plans():
 
 def test_rows_and_tables_of_other_types_are_refused():
     """A 16-bit float that is not bf16, or an integer table, has the right size
-    and would be read as something else."""
+    and would be read as something else; a tensor of fewer tokens past its end."""
     torch = pytest.importorskip("torch")
     bf = dict(dtype=torch.bfloat16)
     q, kv = torch.zeros(2, 4, 128, **bf), torch.zeros(2, 1, 128, **bf)
@@ -390,6 +390,9 @@ def test_rows_and_tables_of_other_types_are_refused():
                          (rope, dict(v_new=kv.view(torch.int16))),
                          (rope, dict(q_out=q.half())),
                          (rope, dict(rope=table.int())),
+                         (rope, dict(q=q[:1])), (rope, dict(k_new=kv[:1])),
+                         (rope, dict(q_out=q[:1])), (latent, dict(r=r[:1])),
+                         (latent, dict(qr=qr[:1])),
                          (latent, dict(c=c.half())), (latent, dict(r=r.half())),
                          (latent, dict(qr=qr.half())),
                          (latent, dict(rope=t64.int()))):
