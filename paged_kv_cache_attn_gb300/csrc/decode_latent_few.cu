@@ -224,20 +224,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (need) m_used = m_tile;
         const float neg = m_used == -INFINITY ? 0.f : -m_used;
         const bool moved = __any_sync(0xffffffffu, need);
-        const uint32_t prow = base + kOffP + b * kP;
+        if (moved) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i) l[i] *= __shfl_sync(0xffffffffu, alpha, i);
+        }
+        uint16_t h[kN];
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
           const float e =
               ex2(fmaf(s[i], p.scale_log2, __shfl_sync(0xffffffffu, neg, i)));
-          if (moved) l[i] *= __shfl_sync(0xffffffffu, alpha, i);
           l[i] += e;
-          // Row i of P^T: 64 tokens, 16-byte pieces swizzled by the row.
-          const uint16_t h = __bfloat16_as_ushort(__float2bfloat16(e));
-          if (lane < 16)
+          h[i] = __bfloat16_as_ushort(__float2bfloat16(e));
+        }
+        // Row i of P^T: 64 tokens, 16-byte pieces swizzled by the row.
+        if (lane < 16) {
+          const uint32_t prow = base + kOffP + b * kP + (tok & 7) * 2;
+#pragma unroll
+          for (int i = 0; i < kN; ++i)
             asm volatile("st.shared.u16 [%0], %1;" ::"r"(
                              prow + (i >> 3) * 1024 + (i & 7) * 128 +
-                             (((tok >> 3) ^ (i & 7)) << 4) + (tok & 7) * 2),
-                         "h"(h)
+                             (((tok >> 3) ^ (i & 7)) << 4)),
+                         "h"(h[i])
                          : "memory");
         }
         // O holds the products up to tile q - 1 once they are done.  Waited for at
