@@ -38,13 +38,13 @@
 // Measured alternatives of the tile shape (cycles per MMA with K = 16): N = 64
 // 56, N = 128 65 (A in TMEM) or 69 (A in shared memory), N = 256 128.
 //
-// Measured: 1.7 us a 128-token tile and pair of SMs, on steps of many rows (1.13
-// us of products) as on steps of few.  The latents pass from L2 twice, as K into
-// one SM and as V into the other: 272 KB a tile, 12 TB/s over all SMs, near to
-// what L2 gave a kernel that does nothing else (13.9).  An item's end costs 128 rows 4 us (256 KB of
-// partial results; an SM stores 29 bytes a cycle, by bulk copies too), a step's
-// start 5 to 7 us.  Prefetches of K or of the position keys into L2 changed
-// nothing or made it slower.
+// Measured: 1.7 us a 128-token tile and pair of SMs (1.13 us of products).  The
+// latents pass from L2 twice, as K into one SM and as V into the other: 272 KB a
+// tile, 12 TB/s over all SMs, near to what L2 gave a kernel that does nothing else
+// (13.9).  An item's end costs 128 rows 4 us (256 KB of partial results; an SM
+// stores 29 bytes a cycle, by bulk copies too), a step's start 5 to 7 us.
+// Prefetches of K or of the position keys into L2 changed nothing or made it
+// slower.
 //
 // Slots past a branch's length may hold anything: their scores are replaced
 // by -inf before the maximum, and their rows of V are zeroed in shared memory
