@@ -959,7 +959,8 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
       const int at = __shfl_sync(0xffffffffu, row, e);
       const float y = __shfl_sync(0xffffffffu, w, e);
       if (at < 0 || y == 0.f) continue;
-      const float4* src = reinterpret_cast<const float4*>(a.o + (int64_t)at * kRank) + lane;
+      const float4* src =
+          reinterpret_cast<const float4*>(a.o + (int64_t)at * kRank) + lane;
       float4 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = src[i * 32];
@@ -1055,7 +1056,8 @@ extern "C" kv_status paged_latent_decode_attn(
     return fail(KV_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", ws_bytes,
                 need);
   CUtensorMap tk, tv, tr, tq, tq_all;
-  if (kv_status s = lat::make_latent_map(&tk, c_pool, num_blocks, lat::kKDim / 64)) return s;
+  if (kv_status s = lat::make_latent_map(&tk, c_pool, num_blocks, lat::kKDim / 64))
+    return s;
   if (kv_status s = lat::make_latent_map(&tv, c_pool, num_blocks, 8)) return s;
   if (kv_status s = lat::make_rows_map(&tr, r_pool, num_blocks * 16, rope_dim, 16))
     return s;

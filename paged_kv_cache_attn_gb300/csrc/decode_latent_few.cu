@@ -19,10 +19,10 @@
 // with its 16 scores; maxima go across lanes by shuffles (each step halves the
 // columns a lane keeps) and across warps through shared memory; base 2, lazy
 // maximum.  P^T (bf16) goes to shared memory as the B operand.  Warps 4 and 7
-// products, S(j + 1) ahead of O += P(j) C(j).  Warp 5 loads latents, warp 6 Q and position
-// keys (one stage: they are the last part of S, and asked into L2 a tile ahead).
-// Slots of a last block past the branch's length are zeroed by warp 7 before O's
-// products (0 x NaN would not be 0).
+// products, S(j + 1) ahead of O += P(j) C(j).  Warp 5 loads latents, warp 6 Q and
+// position keys (one stage: they are the last part of S, and asked into L2 a tile
+// ahead).  Slots of a last block past the branch's length are zeroed by warp 7
+// before O's products (0 x NaN would not be 0).
 //
 // Scores of tokens past the length or the range are -inf before the maximum;
 // blocks past the range are not loaded and take no part in O.  Columns past the
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) timed_out(71);
   } else if (warp == 4) {
-    // ---- S (uniform warp, one lane issues) -------------------------------------------
+    // ---- S (uniform warp, one lane issues) -----------------------------------
     constexpr uint32_t id = idesc(64, kN, false);
     const bool lead = elect_one();
     bool ok = true;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lead) timed_out(72);
   } else if (warp == 7) {
-    // ---- O (another warp, so that the waits of one lie behind the other's products) ----
+    // ---- O (another warp: the waits of one lie behind the other's products) ---
     constexpr uint32_t id = idesc(128, kN, false) | (1u << 15);  // A MN-major
     const bool lead = elect_one();
     bool ok = true;
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lead) timed_out(77);
   } else if (warp == 5) {
-    // ---- latents --------------------------------------------------------------------
+    // ---- latents -----------------------------------------------------------------
     bool ok = true;
     while (ok && loop.next(it)) {
       const int nt = tiles_of(it);
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) timed_out(73);
   } else {
-    // ---- Q and position keys ----------------------------------------------------------
+    // ---- Q and position keys ---------------------------------------------------
     bool ok = true;
     while (ok && loop.next(it)) {
       const int nt = tiles_of(it);

@@ -227,7 +227,8 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   info->n_row_items = n_few;
   info->n_row_warp_items = n_lists;
   info->n_merge_rows = (int32_t)merged.size();
-  info->chunk_blocks = (int32_t)std::min<int64_t>(INT32_MAX, chunk / kTileCost * kTileBlocks);
+  info->chunk_blocks =
+      (int32_t)std::min<int64_t>(INT32_MAX, chunk / kTileCost * kTileBlocks);
   info->flags = flags;
   if (!plan) return KV_OK;
   if (plan_cap < total)
