@@ -11,13 +11,15 @@
 //
 // Items of at most 16 rows run on one SM each (decode_latent_few.cu), in lists of
 // their own; the other items' lists come first in the plan.  The two kernels run
-// beside each other, each on the SMs that its share of the work is worth.
+// beside each other, each on the SMs that its share of the work is worth.  In a
+// small step with both kinds all are the pairs'.
 //
 // A branch whose rows lie in one item each is finished by that item, which
 // writes its output; the other rows' partial results are merged.
 
 #include <algorithm>
 #include <cstring>
+#include <numeric>
 
 #include "internal.h"
 
@@ -36,9 +38,7 @@ constexpr int kMinTiles = 2;    // the shortest piece of a unit (few rows: 1)
 constexpr int kTileCost = 2;
 // For few rows, in tiles' worth of an SM's time (3.3 us a 128-token tile, where
 // HBM brings every SM its share): about 3 us.
-int32_t item_cost(int32_t nrows) {
-  return nrows <= kLatentFewRows ? 2 : 4 + nrows / 32;
-}
+int32_t item_cost(int32_t nrows, bool few) { return few ? 2 : 4 + nrows / 32; }
 
 struct Piece {
   int32_t unit, lo, hi;  // blocks
@@ -46,19 +46,20 @@ struct Piece {
 
 int32_t tiles(int32_t blocks) { return (blocks + kTileBlocks - 1) / kTileBlocks; }
 
-// Deal the units `which` out to `bins` lists of at most `share` cost each, no
-// piece shorter than `least` tiles; returns whether they fit.
+// Deal the units `which` out to `bins` lists (few: of items of few rows) of at most
+// `share` cost each; returns whether they fit.
 bool deal(const std::vector<LatentUnit>& units, const std::vector<int32_t>& which,
-          int64_t share, int32_t bins, int32_t least, std::vector<Piece>* out,
+          int64_t share, int32_t bins, bool few, std::vector<Piece>* out,
           std::vector<int32_t>* ptr) {
   out->clear();
   ptr->assign(1, 0);
-  int64_t used = 0;  // cost of the pair being filled
+  const int32_t least = few ? 1 : kMinTiles;
+  int64_t used = 0;  // cost of the list being filled
   for (int32_t u : which) {
     int32_t lo = units[u].blk_begin;
     while (lo < units[u].blk_end) {
       const int32_t left = tiles(units[u].blk_end - lo);
-      const int32_t fixed = item_cost(units[u].nrows);
+      const int32_t fixed = item_cost(units[u].nrows, few);
       int64_t room = (share - used - fixed) / kTileCost;  // tiles
       if (used > 0 && room < std::min(left, least)) {
         ptr->push_back((int32_t)out->size());
@@ -122,16 +123,23 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   std::vector<Piece> pieces;
   std::vector<int32_t> ptr[2];  // the pairs' lists, the SMs' lists of few rows
   int64_t chunk = 0;
-  int32_t n_few = 0;
   std::vector<int32_t> kind[2];
-  int64_t total_cost[2] = {0, 0};
-  for (int32_t u = 0; u < (int32_t)units.size(); ++u) {
-    const int few = units[u].nrows <= kLatentFewRows;
-    kind[few].push_back(u);
-    total_cost[few] +=
-        (int64_t)tiles(units[u].blk_end - units[u].blk_begin) * kTileCost +
-        item_cost(units[u].nrows);
+  for (int32_t u = 0; u < (int32_t)units.size(); ++u)
+    kind[units[u].nrows <= kLatentFewRows].push_back(u);
+  // The second kernel starts 2 us after the first: a small step of both kinds runs
+  // in the pairs' kernel alone (17 branches of 16 heads on a shared segment 26.6 us
+  // instead of 30.7, 72 branches of 4 heads on three 24.6 instead of 26.6).
+  if (!kind[0].empty() && (int64_t)units.size() <= 2 * pairs_max) {
+    kind[0].resize(units.size());
+    std::iota(kind[0].begin(), kind[0].end(), 0);
+    kind[1].clear();
   }
+  int64_t total_cost[2] = {0, 0};
+  for (int few = 0; few < 2; ++few)
+    for (int32_t u : kind[few])
+      total_cost[few] +=
+          (int64_t)tiles(units[u].blk_end - units[u].blk_begin) * kTileCost +
+          item_cost(units[u].nrows, few);
   // Both kinds: SMs in proportion to their times there, 0.7 us a pair and 0.94 us
   // an SM for a unit of cost (8 roots x 64 branches: 108 us; with 1.1 us 113, with
   // 0.8 113; one kind after the other on all SMs 123).
@@ -142,26 +150,24 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
         1, std::min(pairs_max - 1, (int32_t)(pairs_max * many / (many + few) + 0.5)));
     lists_max[1] = std::max(1, 2 * (pairs_max - lists_max[0]));
   }
-  for (int few = 0; few < 2; ++few) {
-    const std::vector<int32_t>& which = kind[few];
-    const int64_t cost = total_cost[few];
-    ptr[few].assign(1, few ? (int32_t)pieces.size() : 0);
-    if (which.empty()) continue;
+  std::vector<Piece> dealt[2];
+  std::vector<int32_t> cuts[2];
+  for (int few = 1; few >= 0; --few) {
+    cuts[few].assign(1, 0);
+    if (kind[few].empty()) continue;
     const int32_t bins = lists_max[few];
-    const int32_t least = few ? 1 : kMinTiles;
-    std::vector<Piece> dealt;
-    std::vector<int32_t> cuts;
-    int64_t share =
-        std::max<int64_t>((cost + bins - 1) / bins, kTileCost * least);
-    while (!deal(units, which, share, bins, least, &dealt, &cuts))
+    int64_t share = std::max<int64_t>((total_cost[few] + bins - 1) / bins,
+                                      kTileCost * (few ? 1 : kMinTiles));
+    while (!deal(units, kind[few], share, bins, few, &dealt[few], &cuts[few]))
       share += std::max<int64_t>(1, share / 50);
     chunk = std::max(chunk, share);
-    const int32_t at = (int32_t)pieces.size();
-    pieces.insert(pieces.end(), dealt.begin(), dealt.end());
-    ptr[few].clear();
-    for (int32_t c : cuts) ptr[few].push_back(at + c);
-    if (few) n_few = (int32_t)dealt.size();
   }
+  for (int few = 0; few < 2; ++few) {
+    const int32_t at = (int32_t)pieces.size();
+    pieces.insert(pieces.end(), dealt[few].begin(), dealt[few].end());
+    for (int32_t c : cuts[few]) ptr[few].push_back(at + c);
+  }
+  const int32_t n_few = (int32_t)dealt[1].size();
   const int32_t n_pairs = (int32_t)ptr[0].size() - 1;
   const int32_t n_lists = (int32_t)ptr[1].size() - 1;
 

@@ -42,6 +42,9 @@ CASES = {
     "tiny_tree": lambda: latent(W.tiny_tree()),
     "fanout": lambda: latent(W.fanout(n_roots=2, root_tokens=256, fan=8,
                                       min_suffix=1, max_suffix=100, Hq=16)),
+    # Enough of both kinds of items for the two kernels beside each other.
+    "fanout_both": lambda: latent(W.fanout(n_roots=4, root_tokens=300, fan=48,
+                                           min_suffix=1, max_suffix=260, Hq=16)),
     "fanout_3tiles": lambda: latent(W.fanout(n_roots=1, root_tokens=777,
                                              fan=40, min_suffix=1,
                                              max_suffix=50, Hq=9)),
@@ -155,12 +158,14 @@ def test_rising_scores_of_whole_branches(lens, Hq):
     c.close()
 
 
-@pytest.mark.parametrize("name", ["fanout", "many_short", "split_128", "long"])
+@pytest.mark.parametrize("name", ["fanout_both", "many_short", "split_128", "long"])
 def test_repeated_steps(name):
     """Hundreds of steps without a pause: no wait runs out, the bits stay."""
     w = CASES[name]()
     c = H.Cache(w, kv_dtype="latent", poison=True)
     bt = c.batch().upload()
+    both = bt.info.n_tile_wide_items > 0 and bt.info.n_row_warp_items > 0
+    assert both == (name == "fanout_both")
     q = queries(bt.nb, w.Hq, 11)
     first = torch.empty((bt.nb, w.Hq, 512), dtype=torch.bfloat16, device="cuda")
     out = torch.empty_like(first)

@@ -61,7 +61,13 @@ def check_plan(Hq, lens, groups, plan, info, num_sms):
     assert len(ptr) - 1 <= max(num_sms // 2, 1)
     assert len(few) - 1 <= 2 * max(num_sms // 2, 1)
     assert info.n_row_items == len(items) - few[0]
-    assert (items[:few[0], 3] > 16).all() and (items[few[0]:, 3] <= 16).all()
+    assert (items[few[0]:, 3] <= 16).all()
+    # A step of few rows alone is the SMs', a large one of both kinds both's.
+    small = items[:, 3] <= 16
+    if small.all():
+        assert few[0] == 0
+    if len(few) > 1:
+        assert not small[:few[0]].any()
     # Every (row, block) once.
     seen = [np.zeros((Hq, -(-n // 16)), int) for n in lens]
     rows_of = {}                       # partial row -> (branch, head)
@@ -116,18 +122,23 @@ def test_latent_plan_independent(Hq, lens, sms):
     assert info.workspace_bytes >= 256 + info.partial_rows * (512 * 4 + 8)
 
 
-@pytest.mark.parametrize("name", ["fanout", "deep_tree", "tiny_tree"])
+@pytest.mark.parametrize("name", ["fanout", "wide", "deep_tree", "tiny_tree"])
 @pytest.mark.parametrize("Hq", [2, 16, 128])
 def test_latent_plan_trees(name, Hq):
-    small = {"fanout": dict(n_roots=3, root_tokens=300, fan=20, min_suffix=1,
+    small = {"wide": dict(n_roots=7, root_tokens=700, fan=40, min_suffix=1,
+                          max_suffix=400),
+             "fanout": dict(n_roots=3, root_tokens=300, fan=20, min_suffix=1,
                             max_suffix=90),
              "deep_tree": dict(root_tokens=300, depth=3, min_seg=5, max_seg=40),
              "tiny_tree": {}}[name]
-    w = W.CONFIGS[name](Hq=Hq, Hkv=1, d=512, **small)
+    w = W.CONFIGS["fanout" if name == "wide" else name](Hq=Hq, Hkv=1, d=512,
+                                                         **small)
     c = H.Cache(w, with_data=False, kv_dtype="latent")
     bt = c.batch(num_sms=152)
     assert len(bt.groups) > 0
     check_plan(Hq, [int(x) for x in bt.seq_lens], bt.groups, bt.plan, bt.info, 152)
+    both = bt.info.n_tile_wide_items > 0 and bt.info.n_row_warp_items > 0
+    assert both == (name == "wide" and Hq < 128)
     alone = c.batch(num_sms=152, flags=B.KV_PLAN_IGNORE_GROUPS)
     check_plan(Hq, [int(x) for x in alone.seq_lens], [], alone.plan, alone.info, 152)
     c.close()
