@@ -903,13 +903,15 @@ struct MergeArgs {
   const float2* ml;
   const float* o;
   __nv_bfloat16* out;
+  DeviceStatus* status;
   int n, nb, Hq;
   int64_t partial_rows;
 };
 
 // One warp per (branch, head): m* = max m_i, out = sum o_i 2^(m_i - m*) /
 // sum l_i 2^(m_i - m*), in one pass with a running maximum.  Bound by the
-// partial rows it reads (2 KB each).
+// partial rows it reads (2 KB each).  A row without an entry (a malformed plan) is
+// recorded and left as it was.
 __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -923,6 +925,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
   // rows' loads depend on nothing of one another.
   float m = -INFINITY, l = 0.f;
   float4 acc[4] = {};
+  bool any = false;
   const int e1 = a.csr_ptr[b + 1];
   for (int e0 = a.csr_ptr[b]; e0 < e1; e0 += 32) {
     const int n = min(32, e1 - e0);
@@ -936,6 +939,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
         ml = a.ml[row];
       }
     }
+    any |= __any_sync(0xffffffffu, row >= 0);
     float m_new = fmaxf(m, ml.x);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1)
@@ -972,6 +976,10 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
         acc[i].w += v[i].w * y;
       }
     }
+  }
+  if (!any) {
+    if (lane == 0) record_status(a.status, KV_ERR_DEVICE, -1 - b);
+    return;
   }
   const float inv = 1.f / l;
   uint2* dst = reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.Hq + r) * kRank) + lane;
@@ -1118,6 +1126,7 @@ extern "C" kv_status paged_latent_decode_attn(
     m.ml = p.ml;
     m.o = p.o;
     m.out = p.out;
+    m.status = p.status;
     m.n = info->n_merge_rows;
     m.nb = nb;
     m.Hq = Hq;

@@ -14,12 +14,13 @@
 // beside each other, each on the SMs that its share of the work is worth.  In a
 // small step with both kinds all are the pairs'.
 //
-// A branch whose rows lie in one item each is finished by that item, which
-// writes its output; the other rows' partial results are merged.
+// An item whose branches' rows all lie in one item each writes their output; the
+// other branches' partial results are merged, all heads of a branch one way.
 
 #include <algorithm>
 #include <cstring>
 #include <numeric>
+#include <utility>
 
 #include "internal.h"
 
@@ -171,17 +172,33 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   const int32_t n_pairs = (int32_t)ptr[0].size() - 1;
   const int32_t n_lists = (int32_t)ptr[1].size() - 1;
 
-  // Pieces of each unit; a branch is finished in one item when it lies in one
-  // unit (per row tile) of one piece.
+  // Pieces of each unit; a branch is finished by its items when it lies in one
+  // unit (per row tile) of one piece, and so do the branches beside it there.
   std::vector<int32_t> n_pieces(units.size(), 0);
   for (const Piece& p : pieces) ++n_pieces[p.unit];
   std::vector<char> single(nb, 1);
+  auto branches_of = [&](const LatentUnit& x) {  // [first, second)
+    return std::pair<int32_t, int32_t>(
+        x.branch0 + x.row0 / Hq, x.branch0 + (x.row0 + x.nrows - 1) / Hq + 1);
+  };
   for (size_t u = 0; u < units.size(); ++u) {
-    const LatentUnit& x = units[u];
-    const int32_t b1 = x.branch0 + (x.row0 + x.nrows - 1) / Hq;
-    for (int32_t b = x.branch0 + x.row0 / Hq; b <= b1; ++b)
+    const auto [b0, b1] = branches_of(units[u]);
+    for (int32_t b = b0; b < b1; ++b)
       if (n_units[b] != 1 || n_pieces[u] != 1) single[b] = 0;
   }
+  // A unit finishes all of its rows or none, so a branch that shares a unit with a
+  // merged one is merged too; one whose heads lie in two units of a segment (Hq does
+  // not divide 128) hands that on to the next unit.  A segment's units are next to
+  // one another in row order: a pass up and a pass down reach the ends of a chain.
+  std::vector<char> direct(units.size(), 1);
+  auto settle = [&](size_t u) {
+    const auto [b0, b1] = branches_of(units[u]);
+    for (int32_t b = b0; b < b1; ++b)
+      if (!single[b]) direct[u] = 0;
+    if (!direct[u]) std::fill(single.begin() + b0, single.begin() + b1, 0);
+  };
+  for (size_t u = 0; u < units.size(); ++u) settle(u);
+  for (size_t u = units.size(); u-- > 0;) settle(u);
   struct Tagged { int32_t branch; MergeEntry e; };
   std::vector<Tagged> merge;
   std::vector<WorkItem> items;
@@ -190,13 +207,11 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   for (const Piece& p : pieces) {
     const LatentUnit& u = units[p.unit];
     const int32_t row1 = u.row0 + u.nrows;
-    bool direct = true;
-    for (int32_t b = u.row0 / Hq; b * (int64_t)Hq < row1; ++b)
-      direct &= single[u.branch0 + b] != 0;
+    const bool done = direct[p.unit] != 0;
     // `g` (there is one kv-head) says whether the item writes the output.
-    items.push_back({u.branch0, direct ? 1 : 0, u.row0, u.nrows, p.lo, p.hi,
-                     direct ? 0 : (int32_t)prow, u.masked});
-    if (direct) continue;
+    items.push_back({u.branch0, done ? 1 : 0, u.row0, u.nrows, p.lo, p.hi,
+                     done ? 0 : (int32_t)prow, u.masked});
+    if (done) continue;
     for (int32_t b = u.row0 / Hq; b * (int64_t)Hq < row1; ++b) {
       const int32_t a = std::max(u.row0, b * Hq);
       const int32_t e = std::min<int64_t>(row1, (int64_t)b * Hq + Hq);

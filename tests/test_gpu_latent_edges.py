@@ -1,0 +1,71 @@
+"""Latent steps at the edges of their plans on the GPU, against attention in 64
+bits."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+from paged_kv_cache_attn_gb300 import binding as B  # noqa: E402
+from paged_kv_cache_attn_gb300 import harness as H  # noqa: E402
+from paged_kv_cache_attn_gb300 import workloads as W  # noqa: E402
+from test_gpu_latent import check, queries  # noqa: E402
+
+
+def forked(root_tokens, tails, Hq):
+    """Branches forked from one root; a tail of 0 tokens ends with the root."""
+    w = W.Workload("forked", Hq, 1, 512, 37)
+    w.nodes.append(W.NodeSpec(-1, root_tokens))
+    w.ops += [("create",), ("append", 0), ("fork", 0, len(tails))]
+    for i, n in enumerate(tails):
+        w.nodes.append(W.NodeSpec(0, n))
+        if n:
+            w.ops.append(("append", i + 1))
+    w.num_blocks = -(-root_tokens // 16) + sum(-(-n // 16) for n in tails) + 3
+    return w
+
+
+@pytest.mark.parametrize("Hq,root,tails", [
+    (48, 32, [8, 8, 0]), (48, 32, [0, 0, 0, 1]), (20, 32, [0] * 6 + [18]),
+    (9, 64, [1] + [0] * 14), (9, 64, [0] * 30 + [40] + [0] * 30),
+    (96, 640, [0, 0, 6, 0]), (200, 160, [0, 5, 0])])
+def test_branches_that_end_with_their_segment(Hq, root, tails):
+    w = forked(root, tails, Hq)
+    c = H.Cache(w, kv_dtype="latent", poison=True)
+    bt = c.batch().upload()
+    assert [list(g) for g in bt.groups] == [[0, len(tails), 0, root // 16]]
+    q = queries(bt.nb, Hq, 3)
+    out = torch.full((bt.nb, Hq, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    bt.decode(q, out)
+    assert bt.device_status() == (0, 0)
+    assert torch.isfinite(out).all()
+    check(c, bt, q, out, "forked")
+    c.close()
+
+
+def test_merge_entries_out_of_place_are_reported():
+    """A head without a partial row is recorded and left as it was."""
+    w = forked(320, [50, 50, 70], 16)
+    c = H.Cache(w, kv_dtype="latent")
+    bt = c.batch().upload()
+    q = queries(3, 16, 4)
+    out = torch.empty((3, 16, 512), dtype=torch.bfloat16, device="cuda")
+    bt.decode(q, out)
+    assert bt.device_status() == (0, 0)
+    check(c, bt, q, out, "before")
+    i = bt.info
+    ptr = 16 + 8 * i.n_tile_items + i.n_tile_wide_items + i.n_row_warp_items + 2 + \
+        i.n_merge_rows
+    cp = bt.plan[ptr:ptr + 4]
+    assert cp[2] > cp[1]
+    good = out.clone()
+    for e in range(cp[1], cp[2]):                 # branch 1: heads 0 to 4 only
+        bt.dev["plan"][ptr + 4 + 4 * int(e) + 3] = 5
+    out[:] = 3
+    bt.decode(q, out)
+    assert bt.device_status() == (B.KV_ERR_DEVICE, -2)
+    assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+    assert torch.equal(out[1, :5], good[1, :5]) and (out[1, 5:] == 3).all()
+    c.close()

@@ -1,0 +1,64 @@
+"""Plans of latent steps where few units share branches, and the calls of steps
+without new tokens: host logic, no GPU."""
+
+import numpy as np
+import pytest
+
+from paged_kv_cache_attn_gb300 import binding as B
+from test_host_latent import check_plan
+
+
+# Branches that end with the shared segment (one unit each) beside branches with
+# tails (two), where 128 rows are no whole number of branches: a branch's heads lie
+# in two row tiles of the segment.  (Hq, lens, segments.)
+STRADDLING = [
+    (48, [40, 40, 32], [[0, 3, 0, 2]]),
+    (48, [32, 32, 32, 33], [[0, 4, 0, 2]]),
+    (20, [32] * 6 + [50], [[0, 7, 0, 2]]),
+    (20, [50] + [32] * 19, [[0, 20, 0, 2]]),
+    (9, [33] + [32] * 14, [[0, 15, 0, 2]]),
+    (9, [32] * 30 + [33] + [32] * 30, [[0, 61, 0, 2]]),
+    (96, [64, 64, 70, 64], [[0, 4, 0, 4]]),
+    # Two levels: the second segment's branches have two units each.
+    (48, [32, 32, 64, 64, 32], [[0, 5, 0, 2], [2, 2, 2, 2]]),
+    # Long segments, cut into pieces, one after another.
+    (48, [16000] * 5 + [16010] * 3 + [8000] * 4, [[0, 8, 0, 1000], [8, 4, 0, 500]]),
+    (200, [8000] * 3, [[0, 3, 0, 500]]),
+]
+
+
+@pytest.mark.parametrize("sms", [152, 4, 1])
+@pytest.mark.parametrize("case", range(len(STRADDLING)))
+def test_rows_are_finished_or_merged_and_not_both(case, sms):
+    """A branch whose heads lie in two items is finished by both or merged."""
+    Hq, lens, groups = STRADDLING[case]
+    plan, info = B.paged_decode_plan(len(lens), Hq, 1, 512,
+                                     max(-(-n // 16) for n in lens), lens, groups,
+                                     sms, B.KV_PLAN_LATENT)
+    check_plan(Hq, lens, groups, plan, info, sms)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_segments(seed):
+    """Segments one beside another and below one another, some branches ending
+    with theirs, in every head count."""
+    rng = np.random.default_rng(seed)
+    Hq = int(rng.choice([1, 5, 9, 16, 20, 48, 96, 127, 129, 200]))
+    lens, groups = [], []
+    while len(lens) < 40:
+        n, blocks = int(rng.integers(1, 16)), int(rng.integers(1, 200))
+        b0 = len(lens)
+        end = [blocks] * n
+        if n > 1:
+            groups.append([b0, n, 0, blocks])
+            k = int(rng.integers(0, n))            # the first k: one level more
+            if k > 1:
+                more = int(rng.integers(1, 30))
+                groups.append([b0, k, blocks, more])
+                end[:k] = [blocks + more] * k
+        lens += [16 * e + int(rng.integers(1, 60)) * int(rng.random() < 0.4)
+                 for e in end]
+    plan, info = B.paged_decode_plan(len(lens), Hq, 1, 512,
+                                     max(-(-n // 16) for n in lens), lens, groups,
+                                     152, B.KV_PLAN_LATENT)
+    check_plan(Hq, lens, groups, plan, info, 152)
