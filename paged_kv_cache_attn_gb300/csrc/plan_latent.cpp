@@ -11,8 +11,8 @@
 //
 // Items of at most 16 rows run on one SM each (decode_latent_few.cu), in lists of
 // their own; the other items' lists come first in the plan.  The two kernels run
-// beside each other, each on the SMs that its share of the work is worth.  In a
-// small step with both kinds all are the pairs'.
+// beside each other, each on the SMs that its share of the work is worth.  Where
+// there is little work of few rows all of it is the pairs'.
 //
 // An item whose branches' rows all lie in one item each writes their output; the
 // other branches' partial results are merged, all heads of a branch one way.
@@ -127,29 +127,40 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   std::vector<int32_t> kind[2];
   for (int32_t u = 0; u < (int32_t)units.size(); ++u)
     kind[units[u].nrows <= kLatentFewRows].push_back(u);
-  // The second kernel starts 2 us after the first: a small step of both kinds runs
-  // in the pairs' kernel alone (17 branches of 16 heads on a shared segment 26.6 us
-  // instead of 30.7, 72 branches of 4 heads on three 24.6 instead of 26.6).
-  if (!kind[0].empty() && (int64_t)units.size() <= 2 * pairs_max) {
-    kind[0].resize(units.size());
-    std::iota(kind[0].begin(), kind[0].end(), 0);
-    kind[1].clear();
-  }
-  int64_t total_cost[2] = {0, 0};
-  for (int few = 0; few < 2; ++few)
-    for (int32_t u : kind[few])
-      total_cost[few] +=
-          (int64_t)tiles(units[u].blk_end - units[u].blk_begin) * kTileCost +
-          item_cost(units[u].nrows, few);
-  // Both kinds: SMs in proportion to their times there, 0.7 us a pair and 0.94 us
-  // an SM for a unit of cost (8 roots x 64 branches: 108 us; with 1.1 us 113, with
-  // 0.8 113; one kind after the other on all SMs 123).
+  auto cost_of = [&](const std::vector<int32_t>& which, bool few) {
+    int64_t c = 0;
+    for (int32_t u : which)
+      c += (int64_t)tiles(units[u].blk_end - units[u].blk_begin) * kTileCost +
+           item_cost(units[u].nrows, few);
+    return c;
+  };
+  int64_t total_cost[2] = {cost_of(kind[0], false), cost_of(kind[1], true)};
   int32_t lists_max[2] = {pairs_max, 2 * pairs_max};
   if (!kind[0].empty() && !kind[1].empty()) {
-    const double many = 0.7 * total_cost[0], few = 0.47 * total_cost[1];
-    lists_max[0] = std::max(
-        1, std::min(pairs_max - 1, (int32_t)(pairs_max * many / (many + few) + 0.5)));
-    lists_max[1] = std::max(1, 2 * (pairs_max - lists_max[0]));
+    // Times, spread over all pairs: 0.7 us a pair and 0.94 us an SM for a unit of
+    // cost.  The second kernel starts some 2 us after the first, so that a step
+    // whose few rows the pairs would not take much longer for runs in the pairs'
+    // kernel alone (17 branches of 16 heads and 100 tokens on a segment of 256 24.6
+    // us instead of 26.6; 16 branches of 32752 tokens on a segment of 16 run in both,
+    // 108.7 us instead of 122.5).  Of 130 steps with 4 to 140
+    // branches measured in both ways a limit of 2.5 us picks one that is 0.6%
+    // slower than the faster on average; 1.5 and 4.5 us 1.2% and 0.8%, the pairs
+    // alone 5.8%, both always 3.9%.
+    const double us = 1.0 / pairs_max;
+    const double many = 0.7 * us * total_cost[0], few = 0.47 * us * total_cost[1];
+    const double alone = many + 0.7 * us * cost_of(kind[1], false);
+    if (alone - (many + few) <= 2.5) {
+      kind[0].resize(units.size());
+      std::iota(kind[0].begin(), kind[0].end(), 0);
+      kind[1].clear();
+      total_cost[0] = cost_of(kind[0], false);
+    } else {
+      // SMs in proportion (8 roots x 64 branches: 108 us; with 1.1 us an SM 113,
+      // with 0.8 113; one kind after the other on all SMs 123).
+      lists_max[0] = std::max(
+          1, std::min(pairs_max - 1, (int32_t)(pairs_max * many / (many + few) + 0.5)));
+      lists_max[1] = std::max(1, 2 * (pairs_max - lists_max[0]));
+    }
   }
   std::vector<Piece> dealt[2];
   std::vector<int32_t> cuts[2];

@@ -62,3 +62,30 @@ def test_random_segments(seed):
                                      max(-(-n // 16) for n in lens), lens, groups,
                                      152, B.KV_PLAN_LATENT)
     check_plan(Hq, lens, groups, plan, info, 152)
+
+
+def layout(Hq, lens, groups):
+    plan, info = B.paged_decode_plan(len(lens), Hq, 1, 512,
+                                     max(-(-n // 16) for n in lens), lens, groups,
+                                     152, B.KV_PLAN_LATENT)
+    check_plan(Hq, lens, groups, plan, info, 152)
+    return info.n_tile_wide_items > 0, info.n_row_warp_items > 0
+
+
+def test_a_short_prefix_does_not_move_long_tails():
+    """Long branches run as items of few rows, with a shared block or without."""
+    assert layout(16, [32768] * 16, []) == (False, True)
+    for blocks in (1, 2, 64):
+        assert layout(16, [32768] * 16, [[0, 16, 0, blocks]]) == (True, True)
+    assert layout(4, [16016] * 64, [[0, 64, 0, 1]]) == (True, True)
+    assert layout(2, [4000] * 40, [[0, 40, 0, 1]]) == (True, True)
+
+
+def test_small_steps_of_both_kinds_run_in_one_kernel():
+    """A second kernel is not started for little work."""
+    assert layout(16, [356] * 17, [[0, 17, 0, 16]]) == (True, False)
+    assert layout(4, [612] * 72, [[0, 24, 0, 32], [24, 24, 0, 32],
+                                  [48, 24, 0, 32]]) == (True, False)
+    assert layout(2, [56] * 40, [[0, 40, 0, 1]]) == (True, False)
+    # Many short tails are not little work.
+    assert layout(16, [112] * 600, [[0, 600, 0, 4]]) == (True, True)
