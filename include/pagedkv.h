@@ -424,8 +424,9 @@ kv_status kv_build_batch(kv_pool* pool, int32_t nb, const int32_t* ids,
  * kv_check_device_status reads and clears it.  A token whose position lies
  * outside [0, min(rope_len, 16 max_blocks)), or whose block lies outside the
  * pool, is recorded there and nothing is written for it.  Two branches must
- * not write the same slot.  total = 0 does nothing.  Launches only (no host
- * copy, capturable).  Errors: INVALID_ARG, CUDA. */
+ * not write the same slot.  total = 0 does nothing (q, k_new, v_new and q_out
+ * may be NULL then).  Launches only (no host copy, capturable).  Errors:
+ * INVALID_ARG, CUDA. */
 kv_status paged_rope_append(
     const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
     const void* v_new, int64_t v_stride, const float* rope, int32_t rope_len,
@@ -650,10 +651,10 @@ kv_status paged_latent_prefill_plan(int32_t nb, int32_t Hq, int64_t num_blocks,
  * p(i) = seq_lens[b] - q_lens[b] + i the position of the branch's i-th query
  * (it sees itself and everything before).  q [total][Hq][192] bf16: 128
  * dimensions without position, then the 64 rotated ones; branches in order,
- * total = sum of q_lens (0: nothing to do).  w_kv [Hq][256][512] bf16.  out
- * [total][Hq][128] bf16.  c_pool, r_pool: this layer's latent pools.  rank must
- * be 512, rope_dim 64, head_dim 128.  Keys and values are rounded to bf16 once,
- * as cached ones are.  plan: a device copy of paged_latent_prefill_plan's,
+ * total = sum of q_lens (0: nothing to do, q and out may be NULL).  w_kv
+ * [Hq][256][512] bf16.  out [total][Hq][128] bf16.  c_pool, r_pool: this layer's
+ * latent pools.  rank must be 512, rope_dim 64, head_dim 128.  Keys and values
+ * are rounded to bf16 once, as cached ones are.  plan: a device copy of paged_latent_prefill_plan's,
  * *info its host info; workspace: device, >= info->workspace_bytes, 256-byte
  * aligned, no initial contents needed.  Rows behind the last query are left as
  * they were.  All launches are on `stream` (capturable); status as for

@@ -862,7 +862,9 @@ extern "C" kv_status paged_latent_prefill_attn(
     void* workspace, size_t ws_bytes, void* stream) {
   namespace pre = pkv::pre;
   pkv::clear_error();
-  if (!info || !plan || !workspace || !c_pool || !r_pool || !w_kv || !q || !out)
+  // A step without queries may have empty tensors, which have no address.
+  if (!info || !plan || !workspace || !c_pool || !r_pool || !w_kv ||
+      (total != 0 && (!q || !out)))
     return fail(KV_ERR_INVALID_ARG, "null argument");
   if (rank != KV_LATENT_RANK || rope_dim != KV_LATENT_ROPE ||
       head_dim != KV_LATENT_HEAD)

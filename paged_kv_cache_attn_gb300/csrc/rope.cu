@@ -623,9 +623,10 @@ kv_status rope_append_impl(
     int32_t total, int32_t nb, int32_t max_blocks, int32_t Hq, int32_t Hkv,
     int32_t d, int32_t block_size, void* workspace, size_t ws_bytes,
     void* stream) {
-  if (!k_new || !v_new || !k_pool || !v_pool)
+  // A step without new tokens may have empty tensors, which have no address.
+  if (!k_pool || !v_pool || (total != 0 && (!k_new || !v_new)))
     return fail(KV_ERR_INVALID_ARG, "null argument");
-  if ((q == nullptr) != (q_out == nullptr))
+  if (total != 0 && (q == nullptr) != (q_out == nullptr))
     return fail(KV_ERR_INVALID_ARG, "q and q_out both set or both NULL");
   if (d != 64 && d != 128) return fail(KV_ERR_INVALID_ARG, "head_dim 64 or 128");
   if (Hkv < 1 || Hq < 0 || (q && Hq < 1) || Hq > 65536 || Hkv > 65536)
@@ -757,9 +758,10 @@ extern "C" kv_status paged_latent_append(
     int32_t block_size, void* workspace, size_t ws_bytes, void* stream) {
   pkv::clear_error();
   namespace rp = pkv::rope;
-  if (!c_new || !r_new || !c_pool || !r_pool)
+  // A step without new tokens may have empty tensors, which have no address.
+  if (!c_pool || !r_pool || (total != 0 && (!c_new || !r_new)))
     return fail(KV_ERR_INVALID_ARG, "null argument");
-  if ((q_rope == nullptr) != (q_rope_out == nullptr))
+  if (total != 0 && (q_rope == nullptr) != (q_rope_out == nullptr))
     return fail(KV_ERR_INVALID_ARG, "q_rope and q_rope_out both set or both NULL");
   if (rank != KV_LATENT_RANK || rope_dim != KV_LATENT_ROPE)
     return fail(KV_ERR_INVALID_ARG, "a latent cache has rank 512 and rope_dim "

@@ -69,3 +69,20 @@ def test_merge_entries_out_of_place_are_reported():
     assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
     assert torch.equal(out[1, :5], good[1, :5]) and (out[1, 5:] == 3).all()
     c.close()
+
+
+def test_prefill_of_no_tokens_does_nothing():
+    """Empty tensors have no address; the status is cleared all the same."""
+    blocks, Hq = 8, 4
+    pools = [torch.zeros(blocks, 16, n, dtype=torch.bfloat16, device="cuda")
+             for n in (512, 64)]
+    plan, info = B.paged_latent_prefill_plan(2, Hq, blocks, [[0, 1], [2, 3]],
+                                             [20, 30], [0, 0])
+    plan = torch.from_numpy(plan).cuda()
+    ws = torch.full((info.workspace_bytes,), 255, dtype=torch.uint8, device="cuda")
+    w = torch.zeros(Hq, 256, 512, dtype=torch.bfloat16, device="cuda")
+    e = dict(dtype=torch.bfloat16, device="cuda")
+    B.paged_latent_prefill_attn(torch.empty(0, Hq, 192, **e), *pools, blocks, w, 0,
+                                2, Hq, 0.1, torch.empty(0, Hq, 128, **e), plan,
+                                info, ws, ws.numel())
+    assert B.kv_check_device_status(ws) == (0, 0)

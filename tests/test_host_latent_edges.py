@@ -89,3 +89,37 @@ def test_small_steps_of_both_kinds_run_in_one_kernel():
     assert layout(2, [56] * 40, [[0, 40, 0, 1]]) == (True, False)
     # Many short tails are not little work.
     assert layout(16, [112] * 600, [[0, 600, 0, 4]]) == (True, True)
+
+
+P = 1 << 20          # a pointer that no call here follows
+
+
+@pytest.mark.parametrize("with_q", [True, False])
+def test_appends_of_no_tokens_do_nothing(with_q):
+    """A step in which no branch has new tokens: torch's empty tensors have no
+    address."""
+    torch = pytest.importorskip("torch")
+    bf = dict(dtype=torch.bfloat16)
+    ws = torch.zeros(512, dtype=torch.uint8)
+    ws = ws[-ws.data_ptr() % 256:][:256]
+    table, t64 = torch.zeros(8, 64, 2), torch.zeros(8, 32, 2)
+    qkv = torch.zeros(0, 6 * 128, **bf)
+    q = qkv[:, :512].unflatten(1, (4, 128)) if with_q else None
+    k, v = (qkv[:, a:a + 128].unflatten(1, (1, 128)) for a in (512, 640))
+    row = torch.zeros(0, 576, **bf)
+    qr = torch.zeros(0, 4, 192, **bf)[..., 128:] if with_q else None
+    tail = (P, P, P, 0, 2, 2, 4)      # tables, lengths, row_offsets, total, nb, ..
+    B.paged_rope_append(q, k, v, table, B.KV_ROPE_HALVES, q, P, P, 4, *tail, 1, 128,
+                        ws)
+    B.paged_rope_append_e4m3(q, k, v, table, B.KV_ROPE_PAIRS, q, P, P, P, 4, *tail,
+                             1, 128, ws)
+    B.paged_latent_append(row[:, :512], row[:, 512:], qr, t64, B.KV_ROPE_PAIRS, qr,
+                          P, P, 4, *tail, ws)
+    # What is wrong without tokens too is still refused.
+    for change in (dict(block_size=8), dict(nb=0), dict(pool=None), dict(off=None)):
+        a = dict(dict(pool=P, off=P, nb=2, block_size=16), **change)
+        with pytest.raises(B.KVError) as e:
+            B.paged_rope_append(q, k, v, table, B.KV_ROPE_HALVES, q, a["pool"], P,
+                                4, P, P, a["off"], 0, a["nb"], 2, 4, 1, 128, ws,
+                                block_size=a["block_size"])
+        assert e.value.code == B.KV_ERR_INVALID_ARG
