@@ -574,22 +574,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = tc::bar_and(1, 256, ok && !*aborted);
       if (!ok) break;
       fence_after_sync();
-      // The two halves of the key tiles joined; each warp 64 columns.
-      const float m0 = sh.stat[0][0][r], m1 = sh.stat[1][0][r];
+      // The two halves of the key tiles joined, that of tile 0 first: which
+      // warpgroup has it depends on the items before, and a fused multiply-add
+      // rounds its two products differently.  Each warp 64 columns.
+      const int a = it.tiles0 & 1;  // the warpgroup of tile 0
+      const float m0 = sh.stat[a][0][r], m1 = sh.stat[a ^ 1][0][r];
       const float top = fmaxf(m0, m1);  // finite: every row sees token 0
       const float e0 = ex2(m0 - top), e1 = ex2(m1 - top);
-      const float inv = 1.f / (e0 * sh.stat[0][1][r] + e1 * sh.stat[1][1][r]);
+      const float inv = 1.f / (e0 * sh.stat[a][1][r] + e1 * sh.stat[a ^ 1][1][r]);
       const float w0 = e0 * inv, w1 = e1 * inv;
-      // An item of one tile has written one O.
-      const bool has0 = nt > 1 || !(it.tiles0 & 1), has1 = nt > 1 || (it.tiles0 & 1);
+      const bool has1 = nt > 1;  // an item of one tile has written one O
+      const uint32_t o0 = lane_base + kColO + a * kHead;
+      const uint32_t o1 = lane_base + kColO + (a ^ 1) * kHead;
       uint8_t* turn = smem + kOffTurn + warp * 2048;
       const int n = t.nrows - rank * kM - (warp & 3) * 32;  // rows of the warp
       const int64_t row0 = t.row0 + rank * kM + (warp & 3) * 32;
 #pragma unroll 1
       for (int c = g * 64; c < g * 64 + 64; c += 32) {
         uint32_t v[32], v1[32], w[16];
-        tmem_ld32(lane_base + kColO + c, v);
-        tmem_ld32(lane_base + kColO + kHead + c, v1);
+        tmem_ld32(o0 + c, v);
+        tmem_ld32(o1 + c, v1);
         tmem_wait_ld();
         if (c & 32) {  // O has been read
           fence_before_sync();
@@ -601,7 +605,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float o[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            o[x] = (has0 ? __uint_as_float(v[2 * k + x]) * w0 : 0.f) +
+            o[x] = __uint_as_float(v[2 * k + x]) * w0 +
                    (has1 ? __uint_as_float(v1[2 * k + x]) * w1 : 0.f);
           w[k] = pack_bf16(o[0], o[1]);
         }
