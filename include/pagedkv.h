@@ -493,7 +493,7 @@ typedef struct kv_decode_plan_info {
                                per warp; the others take a whole CTA.  Latent
                                steps: the lists of items of few rows
                                (n_tile_wide_items: the lists of the others) */
-  int32_t reserved;        /* 0 */
+  int32_t latent_rows;     /* latent decode steps: nb x Hq; others 0 */
 } kv_decode_plan_info;
 
 /* Host half of a decode step: split the step into work items.

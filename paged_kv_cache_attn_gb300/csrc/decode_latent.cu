@@ -904,14 +904,14 @@ struct MergeArgs {
   const float* o;
   __nv_bfloat16* out;
   DeviceStatus* status;
-  int n, nb, Hq;
+  int n, nb, Hq, n_csr;
   int64_t partial_rows;
 };
 
 // One warp per (branch, head): m* = max m_i, out = sum o_i 2^(m_i - m*) /
 // sum l_i 2^(m_i - m*), in one pass with a running maximum.  Bound by the
-// partial rows it reads (2 KB each).  A row without an entry (a malformed plan) is
-// recorded and left as it was.
+// partial rows it reads (2 KB each).  In a malformed plan, a row without an entry or
+// with entries behind the list's end is recorded and left as it was.
 __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -926,8 +926,9 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
   float m = -INFINITY, l = 0.f;
   float4 acc[4] = {};
   bool any = false;
-  const int e1 = a.csr_ptr[b + 1];
-  for (int e0 = a.csr_ptr[b]; e0 < e1; e0 += 32) {
+  int e0 = a.csr_ptr[b], e1 = a.csr_ptr[b + 1];
+  if (e0 < 0 || e1 > a.n_csr) e0 = e1;
+  for (; e0 < e1; e0 += 32) {
     const int n = min(32, e1 - e0);
     int row = -1;
     float2 ml = make_float2(-INFINITY, 0.f);
@@ -1057,12 +1058,22 @@ extern "C" kv_status paged_latent_decode_attn(
       info->n_row_items > info->n_tile_items ||
       (info->n_row_items > 0) != (info->n_row_warp_items > 0) ||
       (info->n_row_items < info->n_tile_items) != (info->n_tile_wide_items > 0) ||
-      info->n_merge_rows < 0 || info->n_merge_rows > nb || info->partial_rows < 0)
+      info->n_merge_rows < 0 || info->n_merge_rows > nb || info->partial_rows < 0 ||
+      info->latent_rows != nb * Hq)
     return fail(KV_ERR_INVALID_ARG, "plan info does not match the step");
   const size_t need = pkv::ws_total(info->partial_rows, rank);
   if (ws_bytes < need || (size_t)info->workspace_bytes != need)
     return fail(KV_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", ws_bytes,
                 need);
+  const int64_t off_item = pkv::kPlanHeaderInts;
+  const int64_t off_pair = off_item + 8 * (int64_t)info->n_tile_items;
+  const int64_t off_few = off_pair + info->n_tile_wide_items + 1;
+  const int64_t off_merge = off_few + info->n_row_warp_items + 1;
+  const int64_t off_ptr = off_merge + info->n_merge_rows;
+  const int64_t off_ent = off_ptr + nb + 1;
+  if (info->plan_ints < off_ent || info->plan_ints > INT32_MAX ||
+      (info->plan_ints - off_ent) % 4 != 0)
+    return fail(KV_ERR_INVALID_ARG, "plan info does not match the step");
   CUtensorMap tk, tv, tr, tq, tq_all;
   if (kv_status s = lat::make_latent_map(&tk, c_pool, num_blocks, lat::kKDim / 64))
     return s;
@@ -1073,12 +1084,6 @@ extern "C" kv_status paged_latent_decode_attn(
   if (kv_status s = lat::make_rows_map(&tq, q, q_rows, rank + rope_dim, 16)) return s;
   if (kv_status s = lat::make_rows_map(&tq_all, q, q_rows, rank + rope_dim, 128))
     return s;
-  const int64_t off_item = pkv::kPlanHeaderInts;
-  const int64_t off_pair = off_item + 8 * (int64_t)info->n_tile_items;
-  const int64_t off_few = off_pair + info->n_tile_wide_items + 1;
-  const int64_t off_merge = off_few + info->n_row_warp_items + 1;
-  const int64_t off_ptr = off_merge + info->n_merge_rows;
-  const int64_t off_ent = off_ptr + nb + 1;
   auto* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = (cudaStream_t)stream;
   lat::Params p;
@@ -1130,6 +1135,7 @@ extern "C" kv_status paged_latent_decode_attn(
     m.n = info->n_merge_rows;
     m.nb = nb;
     m.Hq = Hq;
+    m.n_csr = (int)((info->plan_ints - off_ent) / 4);
     m.partial_rows = p.partial_rows;
     const int64_t warps = (int64_t)m.n * Hq;
     e = pkv::launch_early(lat::latent_merge_kernel, (int)((warps + 7) / 8), 256, 0,

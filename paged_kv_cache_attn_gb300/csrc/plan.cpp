@@ -284,7 +284,7 @@ extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
   info->workspace_bytes = (int64_t)pkv::ws_total(prow, d);
   info->n_row_items = (int32_t)row_items.size();
   info->n_row_warp_items = n_warp_items;
-  info->reserved = 0;
+  info->latent_rows = 0;
   info->n_tile_items = (int32_t)tile_items.size();
   info->n_merge_rows = nb;
   info->chunk_blocks = chunk_rows;

@@ -262,6 +262,7 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
   info->chunk_blocks =
       (int32_t)std::min<int64_t>(INT32_MAX, chunk / kTileCost * kTileBlocks);
   info->flags = flags;
+  info->latent_rows = nb * Hq;
   if (!plan) return KV_OK;
   if (plan_cap < total)
     return fail(KV_ERR_INVALID_ARG, "plan_cap %lld < %lld", (long long)plan_cap,

@@ -105,3 +105,26 @@ def test_prefill_bits_do_not_depend_on_which_pair_takes_an_item():
         differ += not torch.equal(s.out.view(torch.int16), first.view(torch.int16))
     assert B.kv_check_device_status(s.ws) == (0, 0)
     assert differ == 0
+
+
+@pytest.mark.parametrize("value", [1 << 20, (1 << 31) - 1, -1, -(1 << 31)])
+def test_merge_lists_out_of_range_are_reported(value):
+    w = forked(320, [50, 50, 70], 16)
+    c = H.Cache(w, kv_dtype="latent")
+    bt = c.batch().upload()
+    q = queries(3, 16, 4)
+    out = torch.empty((3, 16, 512), dtype=torch.bfloat16, device="cuda")
+    bt.decode(q, out)
+    assert bt.device_status() == (0, 0)
+    good = out.clone()
+    i = bt.info
+    ptr = 16 + 8 * i.n_tile_items + i.n_tile_wide_items + i.n_row_warp_items + 2 + \
+        i.n_merge_rows
+    bt.dev["plan"][ptr + 2] = value              # branch 1's end, branch 2's start
+    out[:] = 3
+    bt.decode(q, out)
+    code, detail = bt.device_status()
+    assert code == B.KV_ERR_DEVICE and detail in (-2, -3)
+    assert torch.equal(out[0], good[0])
+    assert (out[1:] == 3).all()
+    c.close()

@@ -123,3 +123,17 @@ def test_appends_of_no_tokens_do_nothing(with_q):
                                 4, P, P, a["off"], 0, a["nb"], 2, 4, 1, 128, ws,
                                 block_size=a["block_size"])
         assert e.value.code == B.KV_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("nb,Hq", [(3, 16), (5, 16), (4, 8), (4, 17), (8, 16)])
+def test_a_plan_of_another_batch_is_refused(nb, Hq):
+    """A step of 4 branches and 16 heads, called as one of others."""
+    lens = [200, 170, 300, 165]
+    plan, info = B.paged_decode_plan(4, 16, 1, 512, 20, lens, [[0, 4, 0, 10]], 152,
+                                     B.KV_PLAN_LATENT)
+    assert info.n_merge_rows == 4
+    with pytest.raises(B.KVError) as e:
+        B.paged_latent_decode_attn(P, P, P, 1000, P, P, None, 0, nb, 20, Hq, 0.1, P,
+                                   P, info, P, info.workspace_bytes)
+    assert e.value.code == B.KV_ERR_INVALID_ARG
+    assert "does not match" in str(e.value)
