@@ -654,7 +654,8 @@ kv_status paged_latent_prefill_plan(int32_t nb, int32_t Hq, int64_t num_blocks,
  * total = sum of q_lens (0: nothing to do, q and out may be NULL).  w_kv
  * [Hq][256][512] bf16.  out [total][Hq][128] bf16.  c_pool, r_pool: this layer's
  * latent pools.  rank must be 512, rope_dim 64, head_dim 128.  Keys and values
- * are rounded to bf16 once, as cached ones are.  plan: a device copy of paged_latent_prefill_plan's,
+ * are rounded to bf16 once, as cached ones are.  A token whose latent or key is
+ * not finite reaches only the queries that see it.  plan: a device copy of paged_latent_prefill_plan's,
  * *info its host info; workspace: device, >= info->workspace_bytes, 256-byte
  * aligned, no initial contents needed.  Rows behind the last query are left as
  * they were.  All launches are on `stream` (capturable); status as for

@@ -33,8 +33,9 @@
 // heads run at 1.6 PFLOP/s, 1.5 when repeated without a pause.
 //
 // Tokens past a row's position are replaced by -inf before the maximum; values
-// of slots past a branch's length are written as zeros by the expansion, and
-// blocks past the tile's range take no part in PV.
+// of slots past a branch's length, and those of tokens whose latents are not
+// finite, are written as zeros by the expansion, and blocks past the tile's range
+// take no part in PV.
 
 #include <algorithm>
 #include <cmath>
@@ -234,9 +235,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) tc::remote_arrive(tc::map_rank(smem_u32(&sh.d_empty[b]), 0));
         }
+        // A latent with an infinity or a NaN makes every value expanded from it one
+        // (w x inf, 0 included).  Rows that do not see the token have weight 0, and
+        // 0 x NaN would be theirs too: zeros instead.  Those that see it have NaN
+        // from its keys.
+        float least = fabsf(__uint_as_float(v[0]));  // NaN if all are
+#pragma unroll
+        for (int k = 1; k < 32; ++k) least = fminf(least, fabsf(__uint_as_float(v[k])));
+        const bool none = zero || (wg == 1 && !(least < INFINITY));
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          w[k] = zero ? 0u
+          w[k] = none ? 0u
                       : pack_bf16(__uint_as_float(v[2 * k]),
                                   __uint_as_float(v[2 * k + 1]));
         put_rows(turn, w, lane, [&](int rr) -> uint8_t* {

@@ -128,3 +128,32 @@ def test_merge_lists_out_of_range_are_reported(value):
     assert torch.equal(out[0], good[0])
     assert (out[1:] == 3).all()
     c.close()
+
+
+@pytest.mark.parametrize("what", ["nan", "inf", "key"])
+def test_a_bad_token_reaches_only_the_rows_that_see_it(what):
+    """A latent with a NaN or an infinity, or a position key with a NaN: the queries
+    before that token get the bits that they have without it, those from it on NaN."""
+    from test_gpu_latent_prefill import Step
+    s = Step([700, 200, 160], [700, 40, 0], 3, shared=160, seed=22)
+    s.run()
+    s.check()
+    good = s.out.clone()
+    for t in (0, 15, 300, 511, 699):
+        blk, slot = int(s.tables[0][t // 16]), t % 16
+        keep = s.c[blk, slot].clone(), s.r[blk, slot].clone()
+        if what == "key":
+            s.r[blk, slot, 5] = float("nan")
+        else:
+            s.c[blk, slot, 77] = float(what)
+        s.out[:] = 3
+        s.run()
+        assert B.kv_check_device_status(s.ws) == (0, 0)
+        sees = torch.arange(s.n, device="cuda") >= t
+        sees[700:] = t < 160                  # the other branch shares 160 tokens
+        got, want = s.out[:s.n], good[:s.n]
+        assert torch.equal(got[~sees].view(torch.int16), want[~sees].view(torch.int16))
+        assert got[sees].isnan().all()
+        s.c[blk, slot], s.r[blk, slot] = keep
+    s.run()
+    assert torch.equal(s.out.view(torch.int16), good.view(torch.int16))
