@@ -655,11 +655,11 @@ kv_status paged_latent_prefill_plan(int32_t nb, int32_t Hq, int64_t num_blocks,
  * [Hq][256][512] bf16.  out [total][Hq][128] bf16.  c_pool, r_pool: this layer's
  * latent pools.  rank must be 512, rope_dim 64, head_dim 128.  Keys and values
  * are rounded to bf16 once, as cached ones are.  A token whose latent or key is
- * not finite reaches only the queries that see it.  plan: a device copy of paged_latent_prefill_plan's,
- * *info its host info; workspace: device, >= info->workspace_bytes, 256-byte
- * aligned, no initial contents needed.  Rows behind the last query are left as
- * they were.  All launches are on `stream` (capturable); status as for
- * paged_decode_attn.  Errors: INVALID_ARG, CUDA. */
+ * not finite reaches only the queries that see it.  plan: a device copy of
+ * paged_latent_prefill_plan's, *info its host info; workspace: device, >=
+ * info->workspace_bytes, 256-byte aligned, no initial contents needed.  Rows
+ * behind the last query are left as they were.  All launches are on `stream`
+ * (capturable); status as for paged_decode_attn.  Errors: INVALID_ARG, CUDA. */
 kv_status paged_latent_prefill_attn(
     const void* q, const void* c_pool, const void* r_pool, int64_t num_blocks,
     const void* w_kv, int32_t total, int32_t nb, int32_t Hq, int32_t rank,
