@@ -47,7 +47,7 @@ typedef int32_t kv_status;
 
 #define KV_OK 0
 #define KV_ERR_OOM 1          /* pool has too few free blocks ([TRM] §6 MemoryError),
-                                or no host memory for a latent plan */
+                                or no host memory for a plan */
 #define KV_ERR_INVALID_ARG 2  /* bad size, pointer, layout or plan */
 #define KV_ERR_NOT_FOUND 3    /* unknown or already-freed branch ([TRM] §6 KeyError) */
 #define KV_ERR_CUDA 4         /* a CUDA runtime call failed */
@@ -506,7 +506,7 @@ typedef struct kv_decode_plan_info {
  * size splits).  flags: KV_PLAN_*.  With KV_PLAN_LATENT (Hkv = 1, head_dim =
  * 512): n_tile_items = work items, n_tile_wide_items = the pairs of CTAs that
  * run them, n_merge_rows = branches whose partial results are merged, the
- * other counts 0.  Errors: INVALID_ARG. */
+ * other counts 0.  Errors: INVALID_ARG, OOM. */
 kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
                             int32_t head_dim, int32_t block_size,
                             int32_t max_blocks, const int32_t* seq_lens,
@@ -636,7 +636,7 @@ kv_status paged_latent_decode_attn(
  * workspace_bytes, n_row_items = distinct blocks of the step (each expanded
  * once, 8 KB of workspace a head), n_tile_items = query tiles a head,
  * n_merge_rows = query rows.  num_sms: as for paged_decode_plan.  Errors:
- * INVALID_ARG (lengths, a block id outside the pool). */
+ * INVALID_ARG (lengths, a block id outside the pool), OOM. */
 kv_status paged_latent_prefill_plan(int32_t nb, int32_t Hq, int64_t num_blocks,
                                     int32_t max_blocks, const int32_t* tables,
                                     const int32_t* seq_lens,

@@ -48,17 +48,11 @@ int32_t pick_chunk(const std::vector<Unit>& units, bool tile, int Hkv,
   }
 }
 
-}  // namespace
-
-extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
-                                       int32_t d, int32_t B,
-                                       int32_t max_blocks,
-                                       const int32_t* seq_lens,
-                                       const int32_t* groups, int32_t n_groups,
-                                       int32_t num_sms, int32_t flags,
-                                       int32_t* plan, int64_t plan_cap,
-                                       kv_decode_plan_info* info) {
-  pkv::clear_error();
+kv_status decode_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d, int32_t B,
+                      int32_t max_blocks, const int32_t* seq_lens,
+                      const int32_t* groups, int32_t n_groups, int32_t num_sms,
+                      int32_t flags, int32_t* plan, int64_t plan_cap,
+                      kv_decode_plan_info* info) {
   if (!info || !seq_lens) return fail(KV_ERR_INVALID_ARG, "null argument");
   if (nb < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
     return fail(KV_ERR_INVALID_ARG, "bad nb/Hq/Hkv (%d/%d/%d)", nb, Hq, Hkv);
@@ -149,15 +143,10 @@ extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
       shared_end[b] = end;
     }
   }
-  if (latent) {
-    try {
-      return pkv::latent_plan(nb, Hq, max_blocks, nblk.data(), groups,
-                              use_groups ? n_groups : 0, shared_end.data(),
-                              num_sms, flags, plan, plan_cap, info);
-    } catch (const std::bad_alloc&) {
-      return fail(KV_ERR_OOM, "no host memory for the plan");
-    }
-  }
+  if (latent)
+    return pkv::latent_plan(nb, Hq, max_blocks, nblk.data(), groups,
+                            use_groups ? n_groups : 0, shared_end.data(), num_sms,
+                            flags, plan, plan_cap, info);
   for (int32_t b = 0; b < nb; ++b) {
     if (shared_end[b] < nblk[b])
       units.push_back({b, G, shared_end[b], nblk[b], 1, false, false});
@@ -329,6 +318,25 @@ extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
     ent[4 * k + 3] = t.e.r_hi;
   }
   return KV_OK;
+}
+
+}  // namespace
+
+extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
+                                       int32_t d, int32_t B,
+                                       int32_t max_blocks,
+                                       const int32_t* seq_lens,
+                                       const int32_t* groups, int32_t n_groups,
+                                       int32_t num_sms, int32_t flags,
+                                       int32_t* plan, int64_t plan_cap,
+                                       kv_decode_plan_info* info) {
+  pkv::clear_error();
+  try {
+    return decode_plan(nb, Hq, Hkv, d, B, max_blocks, seq_lens, groups, n_groups,
+                       num_sms, flags, plan, plan_cap, info);
+  } catch (const std::bad_alloc&) {
+    return fail(KV_ERR_OOM, "no host memory for the plan");
+  }
 }
 
 extern "C" kv_status paged_decode_attn_workspace_size(

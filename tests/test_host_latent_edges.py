@@ -137,3 +137,30 @@ def test_a_plan_of_another_batch_is_refused(nb, Hq):
                                    P, info, P, info.workspace_bytes)
     assert e.value.code == B.KV_ERR_INVALID_ARG
     assert "does not match" in str(e.value)
+
+
+NO_MEMORY = """
+import resource, numpy as np
+from paged_kv_cache_attn_gb300 import binding as B
+n = 40_000_000
+lens = np.full(n, 5, np.int32)
+groups = np.zeros((0, 4), np.int32)
+used = int(open("/proc/self/statm").read().split()[0]) * 4096
+resource.setrlimit(resource.RLIMIT_AS, (used + (64 << 20), used + (64 << 20)))
+try:
+    B.paged_decode_plan(n, 1, 1, {d}, 1, lens, groups, 152, {flags})
+except B.KVError as e:
+    print("refused", e.code)
+"""
+
+
+@pytest.mark.parametrize("d,flags", [(512, B.KV_PLAN_LATENT), (128, 0)])
+def test_decode_plan_without_host_memory(d, flags):
+    """A plan that finds no memory is an error, not the end of the process."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(B.__file__)))
+    r = subprocess.run([sys.executable, "-c", NO_MEMORY.format(d=d, flags=flags)],
+                       cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.stdout.split() == ["refused", str(B.KV_ERR_OOM)], r.stderr[-2000:]
