@@ -481,7 +481,9 @@ typedef struct kv_decode_plan_info {
   int32_t n_tile_items;    /* work items of the tcgen05 kernels (the first
                               n_tile_wide_items of up to 256 rows, the rest
                               of up to 128) */
-  int32_t n_merge_rows;    /* nb (one merge per branch and kv-head) */
+  int32_t n_merge_rows;    /* nb (one merge per branch and kv-head); latent
+                              steps: branches with partial results; prefills:
+                              query rows */
   int32_t chunk_blocks;    /* blocks per split-KV item */
   int32_t n_tile_wide_items; /* tcgen05 items of up to 256 rows: segments of
                                 more than 128 rows (bf16), two M-tiles per
@@ -504,9 +506,12 @@ typedef struct kv_decode_plan_info {
  * the plan to host `plan` (plan_cap int32 entries; pass plan = NULL to query
  * the size in info->plan_ints).  num_sms = the device's SM count (used to
  * size splits).  flags: KV_PLAN_*.  With KV_PLAN_LATENT (Hkv = 1, head_dim =
- * 512): n_tile_items = work items, n_tile_wide_items = the pairs of CTAs that
- * run them, n_merge_rows = branches whose partial results are merged, the
- * other counts 0.  Errors: INVALID_ARG, OOM. */
+ * 512): n_tile_items = all work items, the last n_row_items of them of at most 16
+ * query rows; n_tile_wide_items = lists of the former for pairs of CTAs,
+ * n_row_warp_items = lists of the latter for single CTAs (either may be 0);
+ * n_merge_rows = branches whose partial results are merged; latent_rows = nb x
+ * Hq, by which paged_latent_decode_attn knows its plan.  Errors: INVALID_ARG,
+ * OOM. */
 kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
                             int32_t head_dim, int32_t block_size,
                             int32_t max_blocks, const int32_t* seq_lens,
@@ -635,7 +640,7 @@ kv_status paged_latent_decode_attn(
  * host `plan` (plan = NULL: the size in info->plan_ints) and fills info:
  * workspace_bytes, n_row_items = distinct blocks of the step (each expanded
  * once, 8 KB of workspace a head), n_tile_items = query tiles a head,
- * n_merge_rows = query rows.  num_sms: as for paged_decode_plan.  Errors:
+ * n_merge_rows = query rows.  num_sms is not used.  Errors:
  * INVALID_ARG (lengths, a block id outside the pool), OOM. */
 kv_status paged_latent_prefill_plan(int32_t nb, int32_t Hq, int64_t num_blocks,
                                     int32_t max_blocks, const int32_t* tables,

@@ -74,6 +74,7 @@ using tc::fence_before_sync;
 using tc::idesc;
 using tc::map_rank;
 using tc::mbar_wait_cluster;
+using tc::put_rows;
 using tc::remote_arrive;
 using tc::remote_store16;
 using tc::remote_store4;
@@ -675,10 +676,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           remote_arrive(map_rank(smem_u32(&bars.fin_empty[f]), 0));
         }
       }
-      // A warp turns 32 rows x 64 bytes at a time in its 2 KB of shared memory
-      // (16-byte pieces swizzled by the row), so that a store covers whole
-      // sectors of eight rows instead of 16-byte pieces of 32 (128 rows of
-      // partial results took 10 us that way).
       const int wrow = (warp & 3) * 32;          // the warp's first row
       if (wrow < it.nrows) {
         uint8_t* turn = smem + kOffTurn + warp * 2048;
@@ -691,22 +688,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   p.o + ((int64_t)it.prow_base + wrow) * kRank + wg * (kRank / 2));
         const int pitch = direct ? kRank * 2 : kRank * 4;  // bytes of a row
         auto put = [&](const uint32_t (&w)[16]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(
-                turn + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = k * 8 + (lane >> 2), c = lane & 3;
-            const uint4 x = *reinterpret_cast<const uint4*>(
-                turn + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
-            if (rr < n)
-              *reinterpret_cast<uint4*>(dst + (int64_t)rr * pitch + c * 16) = x;
-          }
+          put_rows(turn, w, lane, [&](int rr) -> uint8_t* {
+            return rr < n ? dst + (int64_t)rr * pitch : nullptr;
+          });
           dst += 64;
-          __syncwarp();
         };
 #pragma unroll 1
         for (int c = 0; c < kRank / 2; c += 32) {
@@ -915,8 +900,8 @@ struct MergeArgs {
 __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  // Launched while the attention kernel runs; its results are complete and
-  // visible from here on.
+  // Its launch overlaps the end of the attention kernel (which lets nothing start
+  // beside it but the other one); results are complete and visible from here on.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (w >= (int64_t)a.n * a.Hq) return;
   const int b = a.branches[w / a.Hq], r = (int)(w % a.Hq);
@@ -925,7 +910,6 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
   // rows' loads depend on nothing of one another.
   float m = -INFINITY, l = 0.f;
   float4 acc[4] = {};
-  bool any = false;
   int e0 = a.csr_ptr[b], e1 = a.csr_ptr[b + 1];
   if (e0 < 0 || e1 > a.n_csr) e0 = e1;
   for (; e0 < e1; e0 += 32) {
@@ -940,7 +924,6 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
         ml = a.ml[row];
       }
     }
-    any |= __any_sync(0xffffffffu, row >= 0);
     float m_new = fmaxf(m, ml.x);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1)
@@ -978,7 +961,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const MergeArgs a) {
       }
     }
   }
-  if (!any) {
+  if (l == 0.f) {  // no entry
     if (lane == 0) record_status(a.status, KV_ERR_DEVICE, -1 - b);
     return;
   }
@@ -1087,8 +1070,6 @@ extern "C" kv_status paged_latent_decode_attn(
   auto* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = (cudaStream_t)stream;
   lat::Params p;
-  p.c_pool = static_cast<const uint8_t*>(c_pool);
-  p.r_pool = static_cast<const uint8_t*>(r_pool);
   p.tables = block_tables;
   p.seq_lens = seq_lens;
   p.items = reinterpret_cast<const pkv::WorkItem*>(plan + off_item);

@@ -9,8 +9,9 @@
 // so a tile is loaded once (the kernel for many rows loads it into two SMs), and
 // O^T takes 64 columns of tensor memory.  Per 64 tokens 36 products of 32 cycles
 // (M = 64) and 16 of 45 (M = 128), measured: 1.0 us, against 1.65 us that HBM takes
-// to bring 72 KB to every SM.  That is the bound; three stages of 64 tokens (144 KB
-// in flight while one is computed on) keep it fed.  16 contexts of 32768 tokens with
+// to bring 72 KB to every SM.  That is the bound; three stages of 64 tokens (128 KB
+// of latents in flight while one is computed on, and 8 KB of position keys once S's
+// products have released their stage) keep it fed.  16 contexts of 32768 tokens with
 // 16 heads: 106 us with the merge, 5.7 TB/s (on pairs of SMs, as items of more rows
 // run, 124); stages of 48 tokens, which leave room for two of position keys, took
 // 133: the step from tile to tile costs more than the wait.

@@ -11,8 +11,6 @@ constexpr int kRank = KV_LATENT_RANK;
 constexpr int kFewRows = kLatentFewRows;
 
 struct Params {
-  const uint8_t* c_pool;
-  const uint8_t* r_pool;
   const int32_t* tables;
   const int32_t* seq_lens;
   const WorkItem* items;

@@ -227,8 +227,8 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
       const int32_t a = std::max(u.row0, b * Hq);
       const int32_t e = std::min<int64_t>(row1, (int64_t)b * Hq + Hq);
       merge.push_back({u.branch0 + b,
-                       {(int32_t)(prow + (a - u.row0)), u.nrows, a - b * Hq,
-                        e - b * Hq}});
+                       {(int32_t)(prow + (a - u.row0)), 0,  // one kv-head: no stride
+                        a - b * Hq, e - b * Hq}});
     }
     prow += u.nrows;
     if (prow > INT32_MAX / 2)

@@ -64,8 +64,8 @@ kv_status prefill_plan(int32_t nb, int32_t Hq, int64_t num_blocks,
                        L - n + r, (int32_t)off});
     row += n;
   }
-  // The tiles of one head run longest first; the hardware hands them out in
-  // this order, so the last ones to start are short.
+  // Longest first: the persistent pairs take the tiles of a group of heads in this
+  // order, so that the last ones to start are short.
   std::stable_sort(tiles.begin(), tiles.end(),
                    [](const pkv::PrefillTile& x, const pkv::PrefillTile& y) {
                      return x.pos0 + x.nrows > y.pos0 + y.nrows;
