@@ -259,28 +259,6 @@ __device__ __forceinline__ void l2_prefetch_2d(const CUtensorMap* tm, int x, int
                : "memory");
 }
 
-// 32 rows x 64 bytes of a warp (lane = row, w = its 16 words) out to dst(row)
-// (null: not stored) through 2 KB of shared memory, 16-byte pieces swizzled by the
-// row, so that a store covers whole sectors of eight rows instead of 16-byte pieces
-// of 32 (128 rows of a decode item's partial results took 10 us that way, 4 now).
-template <typename Dst>
-__device__ __forceinline__ void put_rows(uint8_t* turn, const uint32_t (&w)[16],
-                                         int lane, Dst dst) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<uint4*>(turn + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int rr = k * 8 + (lane >> 2), c = lane & 3;
-    const uint4 x = *reinterpret_cast<const uint4*>(
-        turn + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
-    if (uint8_t* d = dst(rr)) *reinterpret_cast<uint4*>(d + c * 16) = x;
-  }
-  __syncwarp();
-}
-
 // Named barriers over `n` threads (whole warps), combining a predicate.
 __device__ __forceinline__ bool bar_and(int id, int n, bool v) {
   uint32_t r;
