@@ -40,9 +40,13 @@
 //
 // Measured: 1.7 us a 128-token tile and pair of SMs (1.13 us of products).  The
 // latents pass from L2 twice, as K into one SM and as V into the other: 272 KB a
-// tile, 12 TB/s over all SMs, near to what L2 gave a kernel that does nothing else
-// (13.9).  An item's end costs 128 rows 4 us (256 KB of partial results; an SM
-// stores 29 bytes a cycle, by bulk copies too), a step's start 5 to 7 us.
+// tile, 12 TB/s over all SMs while all are in the tile loop, near to what L2 gave a
+// kernel that does nothing else (13.9).  An item's end costs 128 rows 4 us (256 KB of
+// partial results; an SM stores 29 bytes a cycle, by bulk copies too), a step's start
+// 5 to 7 us.  These fixed costs bound a step of 64 branches of 512 to 4096 tokens with
+// 128 heads: its 1250 tiles are 29 us of the 56 that 73 pairs take here, with the
+// starts and ends of 106 items and 10112 partial rows in the rest; over those 56 us
+// nothing is saturated (L2 6.3 TB/s, DRAM 3.4, tensor pipe 32%).
 // Prefetches of K or of the position keys into L2 changed nothing or made it
 // slower.
 //

@@ -22,15 +22,18 @@
 // work items (a tile of 256 query rows and a head) as they come.  Each CTA has 128
 // of the rows and loads half of every key tile of 128 tokens (64 tokens of K, 64
 // columns of V), which leaves room for four stages of each: with whole tiles in
-// one CTA, V had one stage and its load (1.3 us) lay on every tile's path (2.4 us
-// a tile of 256 rows and 128 keys on an SM; 1.4 us here, 1.25 of them products).
+// one CTA, V had one stage and its load (1.3 us) lay on every tile's path (a tile of
+// 256 rows and 128 keys took 2.4 us of one SM; here 0.70 us of two, 1410 cycles, 1280
+// of them products).
 // The rows' two warpgroups take the key tiles in turn, each with its own maximum,
 // sum and O, joined at the item's end.  TMEM: S (128 columns), P of the two
 // warpgroups (2 x 64, bf16 pairs), O of the two (2 x 128).  QK(j) may overwrite S
 // once it has been read, which the rows do while PV(j - 2) runs; the softmax of a
 // tile (a thread a row, base 2, lazy maximum, two columns to an instruction) lies
 // behind the products of two others.  Bound by power: 1 x 8192 tokens with 32
-// heads run at 1.6 PFLOP/s, 1.5 when repeated without a pause.
+// heads run at 1.65 PFLOP/s, 1.55 when repeated without a pause.  Tiles of 256 rows
+// waste what a chunk's last one does not fill: 13 of them for 2698 rows in six chunks
+// are 19% padding.
 //
 // Tokens past a row's position are replaced by -inf before the maximum; values
 // of slots past a branch's length, and those of tokens whose latents are not

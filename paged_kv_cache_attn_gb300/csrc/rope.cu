@@ -12,9 +12,12 @@
 // Every value is read once and written once, so the calls are bound by HBM on
 // prompts and by the launch and one chain of dependent loads (offsets, length,
 // table entry, table row) on a decode step.  Measured: 4 prompts of 4096 tokens
-// with 64 + 8 + 8 heads of 128 in 117 us (5.8 TB/s), five of about 2000 latent
-// tokens with 16 heads' queries in 18.5 us (3.7 TB/s, two waves of that chain),
-// steps of 64 and of 128 branches in 6.2 us.
+// with 64 + 8 + 8 heads of 128 in 118 us (5.7 TB/s), five of about 2000 latent
+// tokens with 16 heads' queries in 18.5 us (3.7 TB/s: 1279 CTAs, three an SM at 80
+// registers, are 2.8 waves, and every warp of each goes through that chain for its
+// token), steps of 64 (bf16) and of 128 branches (latent) in 6.2 us, a step of 64
+// branches into an e4m3 pool in 8.3 us (the chain, then a warp's maximum, the block's
+// scale and the codes).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -680,8 +683,11 @@ kv_status rope_append_impl(
     // A decode step's tokens each begin a write: one CTA a token, and the
     // queries in the same launch.  In a chunk about every sixteenth does; the
     // queries are most of the bytes then and take a launch of their own, which
-    // keeps twice the warps on an SM and runs beside the other (24 chunks of 37
-    // to 701 tokens: 73 us in one launch, 58 us one after the other).
+    // keeps twice the warps on an SM and may start before the other has ended (24
+    // chunks of 37 to 701 tokens: 73 us in one launch, 58 us one after the other,
+    // 50.5 so).  The two take 30.0 and 27.6 us alone, so they overlap by 7 us only:
+    // four CTAs of 128 threads at 128 registers are an SM's whole register file, and
+    // the queries' CTAs find room when the last of those leave.
     a.window = off ? 16 : 1;
     const bool own_launch = off != nullptr && q != nullptr;
     a.q_ctas = q && !own_launch
