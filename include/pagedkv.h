@@ -495,7 +495,8 @@ typedef struct kv_decode_plan_info {
                                per warp; the others take a whole CTA.  Latent
                                steps: the lists of items of few rows
                                (n_tile_wide_items: the lists of the others) */
-  int32_t latent_rows;     /* latent decode steps: nb x Hq; others 0 */
+  int32_t latent_rows;     /* latent decode steps: nb x Hq; chunk plans: Hq,
+                              Hkv and head_dim in one; others 0 */
 } kv_decode_plan_info;
 
 /* Host half of a decode step: split the step into work items.
@@ -671,6 +672,62 @@ kv_status paged_latent_prefill_attn(
     int32_t rope_dim, int32_t head_dim, int32_t block_size, float scale,
     void* out, const int32_t* plan, const kv_decode_plan_info* info,
     void* workspace, size_t ws_bytes, void* stream);
+
+/* Host half of chunk attention: new tokens of each branch (a prompt, a chunk of
+ * one, drafted tokens, one token) attend to the branch's cached tokens in a bf16 or
+ * e4m3 pool.  tables (host, [nb][max_blocks]), seq_lens, q_lens (host, nb): branch
+ * b's q_lens[b] newest tokens (0: not in the step) are the queries, seq_lens[b] its
+ * cached tokens with them included, written to the pool beforehand (kv_append,
+ * paged_rope_append).  Hq a multiple of Hkv, at most 32767 and 128 Hkv; Hkv at most
+ * 2047.  flags: 0, or KV_PLAN_KV_E4M3 for an e4m3 pool.  Writes the plan to host
+ * `plan` (plan = NULL: the size in info->plan_ints) and fills info:
+ * workspace_bytes, n_merge_rows = query tokens, n_tile_items = work items a
+ * kv-head, chunk_blocks = blocks of an item at most, n_tile_wide_items = tiles whose
+ * keys are cut into several items, partial_rows = their partial rows, n_row_items =
+ * distinct blocks (e4m3: each widened to bf16 once, 64 head_dim bytes of workspace
+ * a kv-head; bf16: 0).  num_sms = the device's SM count (0: 152), which decides
+ * about the cuts and thereby the last bits of the result.  One plan serves every
+ * layer of a step.  Errors: INVALID_ARG (lengths, heads, flags, a block id outside
+ * the pool), OOM. */
+kv_status paged_chunk_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                           int64_t num_blocks, int32_t max_blocks,
+                           const int32_t* tables, const int32_t* seq_lens,
+                           const int32_t* q_lens, int32_t num_sms, int32_t flags,
+                           int32_t* plan, int64_t plan_cap,
+                           kv_decode_plan_info* info);
+
+/* Attention of new tokens over a paged bf16 pool, one layer:
+ *   out[i][h] = sum_{t <= p(i)} softmax_t(scale * q[i][h] . K_t) V_t,
+ * p(i) = seq_lens[b] - q_lens[b] + i the position of the branch's i-th query (it
+ * sees itself and everything before), K_t and V_t the branch's token t of kv-head
+ * h / (Hq / Hkv).  q [total][Hq][head_dim] bf16, q_stride values between tokens (a
+ * multiple of 8, no less than Hq * head_dim: a slice of a fused projection needs no
+ * copy), branches in order, total = sum of q_lens (0: nothing to do, q and out may
+ * be NULL).  out [total][Hq][head_dim] bf16, contiguous; rows behind the last query
+ * are left as they were.  k_pool, v_pool: this layer's pools.  Slots past a
+ * branch's length may hold anything.  A key or value that is not finite reaches
+ * only the queries that see its token.  Scores, maxima, sums and O are fp32; the
+ * weights are rounded to bf16.  plan: a device copy of paged_chunk_plan's, *info
+ * its host info; workspace: device, >= info->workspace_bytes (at least 256 bytes),
+ * 256-byte aligned, no initial contents needed, not shared by calls that may
+ * overlap.  All launches are on `stream` (capturable); status as for
+ * paged_decode_attn.  Errors: INVALID_ARG, CUDA. */
+kv_status paged_chunk_attn(const void* q, int64_t q_stride, const void* k_pool,
+                           const void* v_pool, int64_t num_blocks, int32_t total,
+                           int32_t nb, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                           int32_t block_size, float scale, void* out,
+                           const int32_t* plan, const kv_decode_plan_info* info,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* The same over an e4m3 pool (plan made with KV_PLAN_KV_E4M3), computed from the
+ * stored values: the step's distinct blocks are first widened to bf16 in the
+ * workspace, exactly (values below 2^-126 lose bits). */
+kv_status paged_chunk_attn_e4m3(
+    const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
+    const void* kv_scales, int64_t num_blocks, int32_t total, int32_t nb, int32_t Hq,
+    int32_t Hkv, int32_t head_dim, int32_t block_size, float scale, void* out,
+    const int32_t* plan, const kv_decode_plan_info* info, void* workspace,
+    size_t ws_bytes, void* stream);
 
 /* paged_decode_attn without a caller workspace.  The pages have no
  * counterpart: this exists for callers that cannot allocate device memory

@@ -188,6 +188,19 @@ _SIGS = {
                                               C.c_int32, _i32p, _i32p, _i32p,
                                               C.c_int32, _i32p, C.c_int64,
                                               C.POINTER(kv_decode_plan_info)]),
+    "paged_chunk_plan": (C.c_int32, [C.c_int32] * 4 +
+                         [C.c_int64, C.c_int32, _i32p, _i32p, _i32p, C.c_int32,
+                          C.c_int32, _i32p, C.c_int64,
+                          C.POINTER(kv_decode_plan_info)]),
+    "paged_chunk_attn": (C.c_int32, [_vp, C.c_int64, _vp, _vp, C.c_int64] +
+                         [C.c_int32] * 6 +
+                         [C.c_float, _vp, _vp, C.POINTER(kv_decode_plan_info),
+                          _vp, C.c_size_t, _vp]),
+    "paged_chunk_attn_e4m3": (C.c_int32, [_vp, C.c_int64, _vp, _vp, _vp,
+                                          C.c_int64] + [C.c_int32] * 6 +
+                              [C.c_float, _vp, _vp,
+                               C.POINTER(kv_decode_plan_info), _vp, C.c_size_t,
+                               _vp]),
     "paged_latent_prefill_attn": (C.c_int32, [_vp, _vp, _vp, C.c_int64, _vp] +
                                   [C.c_int32] * 7 +
                                   [C.c_float, _vp, _vp,
@@ -691,6 +704,58 @@ def paged_latent_prefill_attn(q, c_pool, r_pool, num_blocks, w_kv, total, nb,
         Hq, KV_LATENT_RANK, KV_LATENT_ROPE, KV_LATENT_HEAD, block_size, scale,
         _ptr(out), _ptr(plan), C.byref(info), _ptr(workspace), ws_bytes,
         _stream(stream)))
+
+
+def paged_chunk_plan(nb, Hq, Hkv, head_dim, num_blocks, tables, seq_lens, q_lens,
+                     num_sms=0, flags=0):
+    """Host plan (int32 array) and its info; tables [nb][max_blocks]."""
+    t = _i32(tables).reshape(nb, -1)
+    lens, qn = _i32(seq_lens), _i32(q_lens)
+    if len(lens) < nb or len(qn) < nb:
+        raise KVError(KV_ERR_INVALID_ARG, "seq_lens and q_lens: nb entries")
+    info = kv_decode_plan_info()
+
+    def call(plan, cap):
+        _check(_lib.paged_chunk_plan(
+            nb, Hq, Hkv, head_dim, num_blocks, t.shape[1], _as_i32p(t),
+            _as_i32p(lens), _as_i32p(qn), num_sms, flags, plan, cap,
+            C.byref(info)))
+
+    call(None, 0)
+    plan = np.zeros(info.plan_ints, dtype=np.int32)
+    call(_as_i32p(plan), len(plan))
+    return plan, info
+
+
+def _whole_rows(t, width, total):
+    """Pointer of a contiguous bf16 tensor of at least `total` tokens."""
+    ptr, stride = _token_rows(t, width, total)
+    if t is not None and stride != width:
+        raise KVError(KV_ERR_INVALID_ARG, f"expected contiguous tokens of {width} "
+                                          f"values, got strides {t.stride()}")
+    return ptr
+
+
+def paged_chunk_attn(q, k_pool, v_pool, num_blocks, total, nb, Hq, Hkv, head_dim,
+                     scale, out, plan, info, workspace, ws_bytes, stream=None,
+                     block_size=16):
+    """q [total][Hq][head_dim], the distance between tokens free; out contiguous."""
+    _check(_lib.paged_chunk_attn(
+        *_token_rows(q, Hq * head_dim, total), _ptr(k_pool), _ptr(v_pool),
+        num_blocks, total, nb, Hq, Hkv, head_dim, block_size, scale,
+        _whole_rows(out, Hq * head_dim, total), _ptr(plan), C.byref(info),
+        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def paged_chunk_attn_e4m3(q, k_pool, v_pool, kv_scales, num_blocks, total, nb, Hq,
+                          Hkv, head_dim, scale, out, plan, info, workspace,
+                          ws_bytes, stream=None, block_size=16):
+    """As paged_chunk_attn, over an e4m3 pool."""
+    _check(_lib.paged_chunk_attn_e4m3(
+        *_token_rows(q, Hq * head_dim, total), _ptr(k_pool), _ptr(v_pool),
+        _ptr(kv_scales), num_blocks, total, nb, Hq, Hkv, head_dim, block_size,
+        scale, _whole_rows(out, Hq * head_dim, total), _ptr(plan), C.byref(info),
+        _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def paged_decode_attn_noalloc(q, k_pool, v_pool, num_blocks, block_tables,

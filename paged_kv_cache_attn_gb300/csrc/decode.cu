@@ -483,14 +483,14 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 
 kv_status encode_bf16_map(CUtensorMap* tm, const void* base, int rank,
                           const cuuint64_t* dims, const cuuint64_t* strides,
-                          const cuuint32_t* box) {
+                          const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
   auto enc = get_encode();
   if (!enc) return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r =
       enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
           const_cast<void*>(base), dims, strides, box, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
@@ -699,6 +699,8 @@ static kv_status decode_impl(
                                          : "plan was made for an e4m3 pool");
   if (info->flags & (KV_PLAN_LATENT | pkv::kPrefillPlan))
     return fail(KV_ERR_INVALID_ARG, "plan was made for a latent pool");
+  if (info->flags & pkv::kChunkPlan)
+    return fail(KV_ERR_INVALID_ARG, "the plan is one of paged_chunk_plan");
   if (info->n_tile_items != 0 && d != 128)
     return fail(KV_ERR_INVALID_ARG, "tensor-core tiles need head_dim 128");
   if (info->n_tile_wide_items < 0 ||

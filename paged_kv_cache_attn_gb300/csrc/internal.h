@@ -136,6 +136,38 @@ inline size_t prefill_workspace(int64_t slots, int Hq) {
   return kStatusBytes + 2 * prefill_half(slots, Hq);
 }
 
+// A work item of chunk attention: query tokens [row0, row0 + ntok) of the batch,
+// the first at position pos0 of its branch, whose table is slots[table ..), against
+// key tiles [key_begin, key_end).  partial < 0: the item has all of its rows' keys
+// and writes their output; else its rows go to partial rows partial + head *
+// ntok * G .. of the workspace.
+struct ChunkItem {
+  int32_t row0, ntok, pos0, table, key_begin, key_end, partial, pad;
+};
+static_assert(sizeof(ChunkItem) == 32, "ChunkItem is 8 int32");
+// Query tokens whose keys are cut into `pieces` items; piece i's partial rows
+// start at partial + i * ntok * Hq.
+struct ChunkMerge {
+  int32_t row0, ntok, partial, pieces;
+};
+constexpr int32_t kChunkPlanMagic = 0x31434B50;  // "PKC1"
+constexpr int32_t kChunkPlan = 64;  // info.flags of a chunk plan
+constexpr int kChunkRows = 128;     // rows (tokens x heads) of a CTA
+constexpr int kChunkKeys = 128;     // tokens of a key tile
+// What info.latent_rows of a chunk plan holds, by which a step knows its plan.
+inline int32_t chunk_mark(int32_t Hq, int32_t Hkv, int32_t d) {
+  return Hq * 65536 + Hkv * 2 + (d == 128);
+}
+kv_status chunk_heads_ok(int32_t Hq, int32_t Hkv, int32_t d);  // plan_chunk.cpp
+// Workspace: the status block, (m, l) pairs and o rows of the partial results,
+// then the distinct blocks of an e4m3 step widened to bf16 (keys, values).
+inline size_t chunk_half(int64_t slots, int Hkv, int d) {
+  return (size_t)slots * Hkv * 16 * d * 2;
+}
+inline size_t chunk_workspace(int64_t partial_rows, int64_t slots, int Hkv, int d) {
+  return ws_total(partial_rows, d) + 2 * chunk_half(slots, Hkv, d);
+}
+
 // Device status word (first 16 bytes of the workspace).
 struct DeviceStatus {
   uint32_t code;    // 0, KV_ERR_DEVICE or KV_ERR_TIMEOUT (first recorded)

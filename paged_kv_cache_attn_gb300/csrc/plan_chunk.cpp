@@ -1,0 +1,219 @@
+// Host half of chunk attention (paged_chunk_plan): tiles of query tokens, cut
+// along the keys where there are too few of them for the GPU.
+//
+// A tile is up to 2 floor(128 / G) tokens of one branch with the G query heads
+// of a kv-head: floor(128 / G) tokens x G heads on each CTA of a pair.
+//
+// Plan (int32): header; for e4m3 pools the distinct blocks in order of first use;
+// the branches' tables (physical blocks, or indices into the distinct ones); one
+// descriptor of 8 per work item and kv-head, longest key ranges first; one of 4
+// per tile whose key range is cut.
+
+#include <algorithm>
+#include <cstring>
+#include <new>
+
+#include "internal.h"
+
+using pkv::fail;
+
+namespace {
+
+constexpr int kKeys = pkv::kChunkKeys;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Tile {
+  int32_t row0, ntok, pos0, table;
+  int32_t keys() const { return (pos0 + ntok - 1) / kKeys + 1; }  // key tiles
+};
+
+// Key tiles of a work item at most.  An item costs about as much as kItem more
+// key tiles (its first loads, the last products, the joining of the rows), a cut
+// one kPartial on top (the partial rows out, and in again), and the merge kMerge
+// once: with them the longest item or the mean of the pairs, whichever is more, is
+// least.
+int32_t pick_cut(const std::vector<Tile>& tiles, int32_t Hkv, int32_t pairs) {
+  constexpr double kItem = 3, kPartial = 1.5, kMerge = 5;
+  int32_t longest = 1;
+  for (const Tile& t : tiles) longest = std::max(longest, t.keys());
+  int32_t best = longest;
+  double least = 1e300;
+  for (int32_t cut = longest; cut >= 1; cut = cut * 3 / 4) {
+    double total = 0, top = 0;
+    int64_t n = 0;
+    for (const Tile& t : tiles) {
+      const int64_t pieces = ceil_div(t.keys(), cut);
+      const double each = (double)ceil_div(t.keys(), pieces) + kItem +
+                          (pieces > 1 ? kPartial : 0.);
+      total += (double)(t.keys() + pieces * (kItem + (pieces > 1 ? kPartial : 0.))) *
+               Hkv;
+      top = std::max(top, each);
+      n += pieces * Hkv;
+    }
+    double cost = std::max(top, total / pairs);
+    // Few items of a kind go by whole rounds.
+    if (n < 4ll * pairs) cost = std::max(cost, ceil_div(n, pairs) * (total / n));
+    if (cut < longest) cost += kMerge;
+    if (cost < least) {
+      least = cost;
+      best = cut;
+    }
+    // Already a small part of what the pairs have to do.
+    if (top * 8 < total / pairs) break;
+  }
+  return best;
+}
+
+kv_status chunk_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d,
+                     int64_t num_blocks, int32_t max_blocks, const int32_t* tables,
+                     const int32_t* seq_lens, const int32_t* q_lens,
+                     int32_t num_sms, int32_t flags, int32_t* plan,
+                     int64_t plan_cap, kv_decode_plan_info* info) {
+  if (!info || !tables || !seq_lens || !q_lens)
+    return fail(KV_ERR_INVALID_ARG, "null argument");
+  if (kv_status s = pkv::chunk_heads_ok(Hq, Hkv, d)) return s;
+  if (nb < 1 || max_blocks < 1)
+    return fail(KV_ERR_INVALID_ARG, "bad nb/max_blocks (%d/%d)", nb, max_blocks);
+  if (num_blocks < 1 || num_blocks > (int64_t)INT32_MAX / 16 / Hkv)
+    return fail(KV_ERR_INVALID_ARG, "num_blocks out of range");
+  if (flags & ~KV_PLAN_KV_E4M3)
+    return fail(KV_ERR_INVALID_ARG, "unknown plan flags 0x%x", flags);
+  const bool e4m3 = flags & KV_PLAN_KV_E4M3;
+  if (num_sms <= 0) num_sms = 152;
+  const int32_t pairs = std::clamp(num_sms / 2, 1, 4096);
+  const int32_t G = Hq / Hkv, step = 2 * (pkv::kChunkRows / G);
+
+  std::vector<int32_t> uniq, slots;
+  std::vector<Tile> whole;
+  std::vector<int32_t> slot_of(e4m3 ? num_blocks : 0, -1);
+  int64_t row = 0;
+  for (int32_t b = 0; b < nb; ++b) {
+    const int32_t L = seq_lens[b], n = q_lens[b];
+    if (n < 0 || L < n || (int64_t)L > (int64_t)max_blocks * 16)
+      return fail(KV_ERR_INVALID_ARG, "branch %d: q_lens %d, seq_lens %d, at most "
+                                      "%lld tokens", b, n, L,
+                  (long long)max_blocks * 16);
+    if (n == 0) continue;
+    if (row + n > INT32_MAX / 2)
+      return fail(KV_ERR_INVALID_ARG, "too many query rows");
+    const int64_t off = (int64_t)slots.size();
+    const int32_t nblk = (int32_t)(((int64_t)L + 15) / 16);
+    if (off + nblk > INT32_MAX / 4)
+      return fail(KV_ERR_INVALID_ARG, "tables too large for one plan");
+    for (int32_t k = 0; k < nblk; ++k) {
+      const int32_t phys = tables[(int64_t)b * max_blocks + k];
+      if (phys < 0 || phys >= num_blocks)
+        return fail(KV_ERR_INVALID_ARG, "branch %d: block %d is %d, outside the "
+                                        "pool", b, k, phys);
+      if (e4m3 && slot_of[phys] < 0) {
+        slot_of[phys] = (int32_t)uniq.size();
+        uniq.push_back(phys);
+      }
+      slots.push_back(e4m3 ? slot_of[phys] : phys);
+    }
+    for (int32_t r = 0; r < n; r += step)
+      whole.push_back({(int32_t)(row + r), std::min(step, n - r), L - n + r,
+                       (int32_t)off});
+    row += n;
+  }
+  const int32_t cut = whole.empty() ? 1 : pick_cut(whole, Hkv, pairs);
+  std::vector<pkv::ChunkItem> items;
+  std::vector<pkv::ChunkMerge> merges;
+  int64_t partial = 0;
+  for (const Tile& t : whole) {
+    const int32_t keys = t.keys();
+    const int32_t pieces = (int32_t)ceil_div(keys, cut);
+    const int64_t rows = (int64_t)t.ntok * Hq;  // of a piece
+    if (pieces > 1)
+      merges.push_back({t.row0, t.ntok, (int32_t)partial, pieces});
+    for (int32_t i = 0; i < pieces; ++i) {
+      items.push_back({t.row0, t.ntok, t.pos0, t.table,
+                       (int32_t)((int64_t)keys * i / pieces),
+                       (int32_t)((int64_t)keys * (i + 1) / pieces),
+                       pieces > 1 ? (int32_t)partial : -1, 0});
+      if (pieces > 1) partial += rows;
+      if (partial > INT32_MAX / 4)
+        return fail(KV_ERR_INVALID_ARG, "step too large for one plan");
+    }
+  }
+  // Longest first: the persistent pairs take the items in this order, so that the
+  // last ones to start are short.
+  std::stable_sort(items.begin(), items.end(),
+                   [](const pkv::ChunkItem& x, const pkv::ChunkItem& y) {
+                     return x.key_end - x.key_begin > y.key_end - y.key_begin;
+                   });
+  const int64_t U = (int64_t)uniq.size();
+  if ((int64_t)items.size() * Hkv > INT32_MAX / 2 || U * Hkv > INT32_MAX / 16)
+    return fail(KV_ERR_INVALID_ARG, "step too large for one plan");
+  const int64_t off_slots = pkv::kPlanHeaderInts + U;
+  const int64_t off_items = off_slots + (int64_t)slots.size();
+  const int64_t off_merges = off_items + 8 * (int64_t)items.size();
+  const int64_t total = off_merges + 4 * (int64_t)merges.size();
+  if (total > INT32_MAX) return fail(KV_ERR_INVALID_ARG, "plan too large");
+  std::memset(info, 0, sizeof *info);
+  info->plan_ints = total;
+  info->partial_rows = partial;
+  info->workspace_bytes = (int64_t)pkv::chunk_workspace(partial, U, Hkv, d);
+  info->n_row_items = (int32_t)U;
+  info->n_tile_items = (int32_t)items.size();
+  info->n_merge_rows = (int32_t)row;
+  info->chunk_blocks = cut * (kKeys / 16);
+  info->n_tile_wide_items = (int32_t)merges.size();
+  info->n_row_warp_items = (int32_t)slots.size();
+  info->flags = pkv::kChunkPlan | flags;
+  info->latent_rows = pkv::chunk_mark(Hq, Hkv, d);
+  if (!plan) return KV_OK;
+  if (plan_cap < total)
+    return fail(KV_ERR_INVALID_ARG, "plan_cap %lld < %lld", (long long)plan_cap,
+                (long long)total);
+  std::fill(plan, plan + pkv::kPlanHeaderInts, 0);
+  plan[pkv::H_MAGIC] = pkv::kChunkPlanMagic;
+  plan[pkv::H_NB] = nb;
+  plan[pkv::H_HQ] = Hq;
+  plan[pkv::H_HKV] = Hkv;
+  plan[pkv::H_D] = d;
+  plan[pkv::H_N_ROW_ITEMS] = (int32_t)U;
+  plan[pkv::H_N_TILE_ITEMS] = (int32_t)items.size();
+  plan[pkv::H_OFF_TILE_ITEMS] = (int32_t)off_items;
+  plan[pkv::H_PARTIAL_ROWS] = (int32_t)partial;
+  plan[pkv::H_CHUNK] = info->chunk_blocks;
+  plan[pkv::H_FLAGS] = info->flags;
+  plan[pkv::H_TOTAL] = (int32_t)total;
+  std::copy(uniq.begin(), uniq.end(), plan + pkv::kPlanHeaderInts);
+  std::copy(slots.begin(), slots.end(), plan + off_slots);
+  if (!items.empty())
+    std::memcpy(plan + off_items, items.data(), items.size() * sizeof items[0]);
+  if (!merges.empty())
+    std::memcpy(plan + off_merges, merges.data(), merges.size() * sizeof merges[0]);
+  return KV_OK;
+}
+
+}  // namespace
+
+namespace pkv {
+
+kv_status chunk_heads_ok(int32_t Hq, int32_t Hkv, int32_t d) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq > 32767 || Hkv > 2047)
+    return fail(KV_ERR_INVALID_ARG, "bad Hq/Hkv (%d/%d)", Hq, Hkv);
+  if (Hq / Hkv > kChunkRows)
+    return fail(KV_ERR_INVALID_ARG, "more than %d query heads a kv-head", kChunkRows);
+  if (d != 64 && d != 128) return fail(KV_ERR_INVALID_ARG, "head_dim must be 64 or 128");
+  return KV_OK;
+}
+
+}  // namespace pkv
+
+extern "C" kv_status paged_chunk_plan(
+    int32_t nb, int32_t Hq, int32_t Hkv, int32_t head_dim, int64_t num_blocks,
+    int32_t max_blocks, const int32_t* tables, const int32_t* seq_lens,
+    const int32_t* q_lens, int32_t num_sms, int32_t flags, int32_t* plan,
+    int64_t plan_cap, kv_decode_plan_info* info) {
+  pkv::clear_error();
+  try {
+    return chunk_plan(nb, Hq, Hkv, head_dim, num_blocks, max_blocks, tables,
+                      seq_lens, q_lens, num_sms, flags, plan, plan_cap, info);
+  } catch (const std::bad_alloc&) {
+    return fail(KV_ERR_OOM, "no host memory for the plan");
+  }
+}

@@ -11,11 +11,12 @@
 
 namespace pkv {
 
-// A tiled map over bf16 data with 128-byte swizzle and zero fill (decode.cu).
-// strides: bytes, rank - 1 of them.
+// A tiled map over bf16 data with zero fill (decode.cu).  strides: bytes,
+// rank - 1 of them.
 kv_status encode_bf16_map(CUtensorMap* tm, const void* base, int rank,
                           const cuuint64_t* dims, const cuuint64_t* strides,
-                          const cuuint32_t* box);
+                          const cuuint32_t* box,
+                          CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // Allow `kernel` `bytes` of dynamic shared memory on the current device, once
 // per device (`done`: a bit per device, one word per kernel).
