@@ -89,6 +89,10 @@ typedef int32_t kv_status;
 #define KV_ROPE_HALVES 0 /* (j, j + rot_dim / 2) */
 #define KV_ROPE_PAIRS 1  /* (2 j, 2 j + 1) */
 
+/* Type of the logits of kv_beam_select. */
+#define KV_LOGITS_BF16 0
+#define KV_LOGITS_F32 1
+
 typedef struct kv_pool kv_pool; /* opaque */
 
 typedef struct kv_pool_desc {
@@ -222,6 +226,19 @@ kv_status kv_fork_branches(kv_pool* pool, int32_t parent, int32_t n,
  * Errors: NOT_FOUND (unknown or already freed; the page's listing ignores
  * unknown ids silently, this library reports them). */
 kv_status kv_free(kv_pool* pool, int32_t id);
+
+/* A beam step's branches: beam i of the next step continues branch
+ * ids[parents[i]] (parents[i] = -1: no beam, out_ids[i] = -1), as kv_beam_select
+ * picks them.  The first beam of a parent keeps the parent's branch, further ones
+ * are forks of it (copy-on-write as kv_fork_branch, in the order of the beams, one
+ * copy launch on `stream`); then the branches of `ids` that no beam continues are
+ * freed as kv_free, in list order.  The forks' blocks are taken before those are
+ * returned.  ids: host, n live branches, each once; parents, out_ids: host, n_out
+ * entries.  All or nothing.  Errors: NOT_FOUND, OOM, INVALID_ARG (a parent out of
+ * range, a branch twice, a fork of a spilled branch), CUDA. */
+kv_status kv_beam_reorder(kv_pool* pool, int32_t n, const int32_t* ids,
+                          int32_t n_out, const int32_t* parents, int32_t* out_ids,
+                          void* stream);
 
 /* Release every live branch of id's subtree, post-order, children in
  * creation order (id itself may already be freed).  out_freed_ids: host,
@@ -728,6 +745,132 @@ kv_status paged_chunk_attn_e4m3(
     int32_t Hkv, int32_t head_dim, int32_t block_size, float scale, void* out,
     const int32_t* plan, const kv_decode_plan_info* info, void* workspace,
     size_t ws_bytes, void* stream);
+
+/* ---- decode over selected blocks ------------------------------------------ */
+
+/* Bounds of blocks' keys, by which paged_select_blocks scores them.  For each
+ * (block, kv-head), over the block's cached keys k of that head:
+ *   lo[c] = floor(min k[c] / 2^e),  hi[c] = ceil(max k[c] / 2^e),
+ * e the smallest integer in [-60, 40] with max|k| <= 127 * 2^e, both cut to +-127
+ * (which only keys above 127 * 2^40 meet).  bounds: device int8
+ * [num_blocks][Hkv][2][head_dim] (lo, then hi), 16-byte aligned; bound_scales:
+ * device fp32 [num_blocks][Hkv], 2^e (a block with a key that is not finite:
+ * infinity, lo and hi 0).  One pair of arrays a layer, the caller's.
+ * A call brings the blocks up to date that hold new tokens of the step, written
+ * before (kv_append, paged_rope_append): branch b's new tokens are its last
+ * row_offsets[b + 1] - row_offsets[b] of seq_lens[b] (row_offsets[0] = 0,
+ * row_offsets[nb] = total; NULL: one new token a branch, total = nb).  Other blocks'
+ * bounds are left as they were.  Blocks keep their bounds when they are forked,
+ * indexed or shared; a branch whose blocks were copied (a fork inside a block) or
+ * moved (kv_restore) has its bounds again after a call with those blocks' tokens as
+ * new ones (a copied block is the branch's last, which is always selected, until
+ * the branch grows past it and has had such a call).  block_tables, seq_lens,
+ * workspace and status: as for paged_rope_append (>= 256 bytes, zeroed once by the
+ * caller).  total = 0 does nothing.  Launches only.  Errors: INVALID_ARG, CUDA. */
+kv_status paged_key_bounds(const void* k_pool, int64_t num_blocks,
+                           const int32_t* block_tables, const int32_t* seq_lens,
+                           const int32_t* row_offsets, int32_t total, int32_t nb,
+                           int32_t max_blocks, int32_t Hkv, int32_t head_dim,
+                           int32_t block_size, void* bounds, float* bound_scales,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* The same for an e4m3 pool, of the stored values. */
+kv_status paged_key_bounds_e4m3(
+    const void* k_pool, const void* kv_scales, int64_t num_blocks,
+    const int32_t* block_tables, const int32_t* seq_lens, const int32_t* row_offsets,
+    int32_t total, int32_t nb, int32_t max_blocks, int32_t Hkv, int32_t head_dim,
+    int32_t block_size, void* bounds, float* bound_scales, void* workspace,
+    size_t ws_bytes, void* stream);
+
+/* Workspace of paged_select_blocks, which holds the blocks' scores. */
+kv_status paged_select_blocks_workspace_size(int32_t nb, int32_t max_blocks,
+                                             int32_t Hkv, size_t* out_bytes);
+
+/* The n_sel blocks that each (branch, kv-head) attends to in a decode step: the
+ * first n_first and the last n_last blocks of the branch, and of the others those
+ * with the highest scores, ties to the lower block; all blocks of a branch that has
+ * no more than n_sel.  With every query head q of the group as whole numbers
+ * n[c] = round(q[c] / 2^eq) (to even, at most 127, eq by the rule of the bounds; a
+ * head with a value that is not finite: zeros), a block's score is
+ *   max over heads of 2^eq * 2^e * sum_c max(n[c] lo[c], n[c] hi[c]),
+ * exact, an upper bound on the products of n with the block's keys; infinity where
+ * bound_scales is.  n_last >= 1, n_first + n_last <= n_sel; Hq / Hkv at most 128; nb
+ * and Hkv at most 65535.
+ * q [nb][Hq][head_dim] bf16; block_tables [nb][max_blocks], seq_lens [nb] as for
+ * paged_decode_attn; bounds, bound_scales: this layer's.  Outputs, device int32:
+ * sel (nullable) [nb][Hkv][n_sel]: the branch's logical blocks, ascending, then -1;
+ * sel_tables [nb * Hkv][n_sel] and sel_lens [nb * Hkv]: the same as
+ * paged_selected_attn reads it, for this layer or another one whose pool has the
+ * same blocks.  workspace: device, 256-byte aligned, no initial contents needed, not
+ * shared by calls that may overlap.  A block id outside the pool or a length outside
+ * [1, 16 max_blocks] is recorded in the status word.  Launches only.  Errors:
+ * INVALID_ARG, CUDA. */
+kv_status paged_select_blocks(
+    const void* q, const void* bounds, const float* bound_scales, int64_t num_blocks,
+    const int32_t* block_tables, const int32_t* seq_lens, int32_t nb,
+    int32_t max_blocks, int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t block_size,
+    int32_t n_sel, int32_t n_first, int32_t n_last, int32_t* sel, int32_t* sel_tables,
+    int32_t* sel_lens, void* workspace, size_t ws_bytes, void* stream);
+
+/* Host half of a decode step over selected blocks: paged_decode_plan for nb * Hkv
+ * branches of one kv-head, whose lengths follow from seq_lens (host, the step's)
+ * and n_sel.  flags: 0 or KV_PLAN_KV_E4M3.  Errors: INVALID_ARG, OOM. */
+kv_status paged_selected_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                              int32_t block_size, int32_t max_blocks,
+                              const int32_t* seq_lens, int32_t n_sel,
+                              int32_t num_sms, int32_t flags, int32_t* plan,
+                              int64_t plan_cap, kv_decode_plan_info* info);
+
+/* paged_decode_attn over the selected blocks alone: out[b][h] attends to the tokens
+ * of sel_tables' blocks for (b, h / (Hq / Hkv)).  plan, info: paged_selected_plan's
+ * for this nb, Hq, Hkv, head_dim and n_sel and the seq_lens of the selection.
+ * Everything else (q, pools, out, workspace, status, errors) as for
+ * paged_decode_attn. */
+kv_status paged_selected_attn(
+    const void* q, const void* k_pool, const void* v_pool, int64_t num_blocks,
+    const int32_t* sel_tables, const int32_t* sel_lens, int32_t nb, int32_t Hq,
+    int32_t Hkv, int32_t head_dim, int32_t block_size, int32_t n_sel, float scale,
+    void* out, const int32_t* plan, const kv_decode_plan_info* info, void* workspace,
+    size_t ws_bytes, void* stream);
+
+/* The same over an e4m3 pool (plan made with KV_PLAN_KV_E4M3). */
+kv_status paged_selected_attn_e4m3(
+    const void* q, const void* k_pool, const void* v_pool, const void* kv_scales,
+    int64_t num_blocks, const int32_t* sel_tables, const int32_t* sel_lens,
+    int32_t nb, int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t block_size,
+    int32_t n_sel, float scale, void* out, const int32_t* plan,
+    const kv_decode_plan_info* info, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- beam selection ------------------------------------------------------- */
+
+/* Workspace of kv_beam_select. */
+kv_status kv_beam_select_workspace_size(int32_t n_groups, int32_t beams,
+                                        int32_t vocab, int32_t n_out,
+                                        size_t* out_bytes);
+
+/* Beam search's selection: of every group of `beams` beams the n_out continuations
+ * (beam, token) with the highest
+ *   scores[beam] + logits[beam][token] - log sum_t exp logits[beam][t],
+ * in descending order, ties to the lower beam, then the lower token.  logits:
+ * device, n_groups * beams rows of `vocab` values of logits_type (KV_LOGITS_*),
+ * row_stride values apart, any alignment; scores: device fp32 [n_groups * beams],
+ * sums of log probabilities so far (-infinity or NaN: no such beam).  A logit of
+ * -infinity or NaN is a token that cannot follow; a beam with a logit of +infinity,
+ * or none that can follow, has no continuation.  Outputs, device
+ * [n_groups][n_out]: out_scores fp32, out_parents int32 (the beam's place in its
+ * group), out_tokens int32; where there are fewer continuations, -infinity, -1 and
+ * -1.  The sums are fp32 in parts of 8 or 32 logits and 64 bits across them, the
+ * results 64 bits (rounded to fp32 once): beams whose results differ by less than
+ * about 1e-7 may change places.  n_out in [1, 128]; beams in [1, 1024]; n_groups *
+ * beams at most 65535.  workspace: device, 256-byte aligned, no initial contents
+ * needed, not shared by calls that may overlap.  Launches only.  kv_beam_reorder
+ * takes the parents (of one group) to the pool's branches.  Errors: INVALID_ARG,
+ * CUDA. */
+kv_status kv_beam_select(const void* logits, int32_t logits_type, int64_t row_stride,
+                         const float* scores, int32_t n_groups, int32_t beams,
+                         int32_t vocab, int32_t n_out, float* out_scores,
+                         int32_t* out_parents, int32_t* out_tokens, void* workspace,
+                         size_t ws_bytes, void* stream);
 
 /* paged_decode_attn without a caller workspace.  The pages have no
  * counterpart: this exists for callers that cannot allocate device memory

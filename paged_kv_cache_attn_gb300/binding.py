@@ -42,6 +42,8 @@ KV_LATENT_ROPE = 64
 KV_LATENT_HEAD = 128
 KV_ROPE_HALVES = 0
 KV_ROPE_PAIRS = 1
+KV_LOGITS_BF16 = 0
+KV_LOGITS_F32 = 1
 
 _NAMES = {0: "OK", 1: "OOM", 2: "INVALID_ARG", 3: "NOT_FOUND", 4: "CUDA",
           5: "DEVICE", 6: "TIMEOUT", 7: "INTERNAL"}
@@ -188,6 +190,33 @@ _SIGS = {
                                               C.c_int32, _i32p, _i32p, _i32p,
                                               C.c_int32, _i32p, C.c_int64,
                                               C.POINTER(kv_decode_plan_info)]),
+    "kv_beam_reorder": (C.c_int32, [_vp, C.c_int32, _i32p, C.c_int32, _i32p,
+                                    _i32p, _vp]),
+    "kv_beam_select_workspace_size": (C.c_int32, [C.c_int32] * 4 +
+                                      [C.POINTER(C.c_size_t)]),
+    "kv_beam_select": (C.c_int32, [_vp, C.c_int32, C.c_int64, _vp] +
+                       [C.c_int32] * 4 + [_vp, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "paged_key_bounds": (C.c_int32, [_vp, C.c_int64, _vp, _vp, _vp] +
+                         [C.c_int32] * 6 + [_vp, _vp, _vp, C.c_size_t, _vp]),
+    "paged_key_bounds_e4m3": (C.c_int32, [_vp, _vp, C.c_int64, _vp, _vp, _vp] +
+                              [C.c_int32] * 6 + [_vp, _vp, _vp, C.c_size_t, _vp]),
+    "paged_select_blocks_workspace_size": (C.c_int32, [C.c_int32] * 3 +
+                                           [C.POINTER(C.c_size_t)]),
+    "paged_select_blocks": (C.c_int32, [_vp, _vp, _vp, C.c_int64, _vp, _vp] +
+                            [C.c_int32] * 9 + [_vp, _vp, _vp, _vp, C.c_size_t,
+                                               _vp]),
+    "paged_selected_plan": (C.c_int32, [C.c_int32] * 6 +
+                            [_i32p, C.c_int32, C.c_int32, C.c_int32, _i32p,
+                             C.c_int64, C.POINTER(kv_decode_plan_info)]),
+    "paged_selected_attn": (C.c_int32, [_vp, _vp, _vp, C.c_int64, _vp, _vp] +
+                            [C.c_int32] * 6 +
+                            [C.c_float, _vp, _vp, C.POINTER(kv_decode_plan_info),
+                             _vp, C.c_size_t, _vp]),
+    "paged_selected_attn_e4m3": (C.c_int32, [_vp, _vp, _vp, _vp, C.c_int64, _vp,
+                                             _vp] + [C.c_int32] * 6 +
+                                 [C.c_float, _vp, _vp,
+                                  C.POINTER(kv_decode_plan_info), _vp, C.c_size_t,
+                                  _vp]),
     "paged_chunk_plan": (C.c_int32, [C.c_int32] * 4 +
                          [C.c_int64, C.c_int32, _i32p, _i32p, _i32p, C.c_int32,
                           C.c_int32, _i32p, C.c_int64,
@@ -756,6 +785,126 @@ def paged_chunk_attn_e4m3(q, k_pool, v_pool, kv_scales, num_blocks, total, nb, H
         _ptr(kv_scales), num_blocks, total, nb, Hq, Hkv, head_dim, block_size,
         scale, _whole_rows(out, Hq * head_dim, total), _ptr(plan), C.byref(info),
         _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def paged_key_bounds(k_pool, num_blocks, block_tables, seq_lens, row_offsets, total,
+                     nb, max_blocks, Hkv, head_dim, bounds, bound_scales, workspace,
+                     stream=None, block_size=16):
+    """bounds: int8 [num_blocks][Hkv][2][head_dim]; bound_scales: fp32
+    [num_blocks][Hkv]; workspace: a zeroed uint8 tensor of >= 256 bytes."""
+    _check(_lib.paged_key_bounds(
+        _ptr(k_pool), num_blocks, _ptr(block_tables), _ptr(seq_lens),
+        _ptr(row_offsets), total, nb, max_blocks, Hkv, head_dim, block_size,
+        _ptr(bounds), _ptr(bound_scales), _ptr(workspace), workspace.numel(),
+        _stream(stream)))
+
+
+def paged_key_bounds_e4m3(k_pool, kv_scales, num_blocks, block_tables, seq_lens,
+                          row_offsets, total, nb, max_blocks, Hkv, head_dim, bounds,
+                          bound_scales, workspace, stream=None, block_size=16):
+    """As paged_key_bounds, of an e4m3 pool."""
+    _check(_lib.paged_key_bounds_e4m3(
+        _ptr(k_pool), _ptr(kv_scales), num_blocks, _ptr(block_tables),
+        _ptr(seq_lens), _ptr(row_offsets), total, nb, max_blocks, Hkv, head_dim,
+        block_size, _ptr(bounds), _ptr(bound_scales), _ptr(workspace),
+        workspace.numel(), _stream(stream)))
+
+
+def paged_select_blocks_workspace_size(nb, max_blocks, Hkv) -> int:
+    out = C.c_size_t()
+    _check(_lib.paged_select_blocks_workspace_size(nb, max_blocks, Hkv,
+                                                   C.byref(out)))
+    return out.value
+
+
+def paged_select_blocks(q, bounds, bound_scales, num_blocks, block_tables, seq_lens,
+                        nb, max_blocks, Hq, Hkv, head_dim, n_sel, n_first, n_last,
+                        sel, sel_tables, sel_lens, workspace, stream=None,
+                        block_size=16):
+    """sel (or None) [nb][Hkv][n_sel], sel_tables [nb * Hkv][n_sel], sel_lens
+    [nb * Hkv]: int32."""
+    _check(_lib.paged_select_blocks(
+        _ptr(q), _ptr(bounds), _ptr(bound_scales), num_blocks, _ptr(block_tables),
+        _ptr(seq_lens), nb, max_blocks, Hq, Hkv, head_dim, block_size, n_sel,
+        n_first, n_last, _ptr(sel), _ptr(sel_tables), _ptr(sel_lens),
+        _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def paged_selected_plan(nb, Hq, Hkv, head_dim, max_blocks, seq_lens, n_sel,
+                        num_sms=0, flags=0, block_size=16):
+    """Host plan (int32 array) and its info."""
+    lens = _i32(seq_lens)
+    if len(lens) < nb:
+        raise KVError(KV_ERR_INVALID_ARG, "seq_lens: nb entries")
+    info = kv_decode_plan_info()
+
+    def call(plan, cap):
+        _check(_lib.paged_selected_plan(
+            nb, Hq, Hkv, head_dim, block_size, max_blocks, _as_i32p(lens), n_sel,
+            num_sms, flags, plan, cap, C.byref(info)))
+
+    call(None, 0)
+    plan = np.zeros(info.plan_ints, dtype=np.int32)
+    call(_as_i32p(plan), len(plan))
+    return plan, info
+
+
+def paged_selected_attn(q, k_pool, v_pool, num_blocks, sel_tables, sel_lens, nb, Hq,
+                        Hkv, head_dim, n_sel, scale, out, plan, info, workspace,
+                        ws_bytes, stream=None, block_size=16):
+    _check(_lib.paged_selected_attn(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), num_blocks, _ptr(sel_tables),
+        _ptr(sel_lens), nb, Hq, Hkv, head_dim, block_size, n_sel, scale, _ptr(out),
+        _ptr(plan), C.byref(info), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def paged_selected_attn_e4m3(q, k_pool, v_pool, kv_scales, num_blocks, sel_tables,
+                             sel_lens, nb, Hq, Hkv, head_dim, n_sel, scale, out,
+                             plan, info, workspace, ws_bytes, stream=None,
+                             block_size=16):
+    _check(_lib.paged_selected_attn_e4m3(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(kv_scales), num_blocks,
+        _ptr(sel_tables), _ptr(sel_lens), nb, Hq, Hkv, head_dim, block_size, n_sel,
+        scale, _ptr(out), _ptr(plan), C.byref(info), _ptr(workspace), ws_bytes,
+        _stream(stream)))
+
+
+def kv_beam_select_workspace_size(n_groups, beams, vocab, n_out) -> int:
+    out = C.c_size_t()
+    _check(_lib.kv_beam_select_workspace_size(n_groups, beams, vocab, n_out,
+                                              C.byref(out)))
+    return out.value
+
+
+def kv_beam_select(logits, scores, n_groups, beams, n_out, out_scores, out_parents,
+                   out_tokens, workspace, stream=None):
+    """logits: bf16 or fp32 [n_groups * beams][vocab], the distance between rows
+    free."""
+    bf16, f32 = _types()
+    rows = n_groups * beams
+    if logits.dim() != 2 or logits.shape[0] < rows or logits.dtype not in (bf16, f32) \
+            or logits.stride(1) != 1 and logits.shape[1] > 1:
+        raise KVError(KV_ERR_INVALID_ARG,
+                      f"expected bf16 or fp32 [{rows}][vocab], got "
+                      f"{tuple(logits.shape)} of {logits.dtype}, strides "
+                      f"{logits.stride()}")
+    vocab = logits.shape[1]
+    _check(_lib.kv_beam_select(
+        _ptr(logits), KV_LOGITS_F32 if logits.dtype is f32 else KV_LOGITS_BF16,
+        logits.stride(0) if logits.shape[0] > 1 else vocab, _ptr(scores), n_groups,
+        beams, vocab, n_out, _ptr(out_scores), _ptr(out_parents), _ptr(out_tokens),
+        _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def kv_beam_reorder(h, ids, parents, stream=None) -> list:
+    """The branches of the next step's beams; parents: places in ids, or -1."""
+    ids, parents = _i32(ids), _i32(parents)
+    out = np.full(max(len(parents), 1), -1, dtype=np.int32)
+    _check(_lib.kv_beam_reorder(
+        h, len(ids), _as_i32p(ids) if len(ids) else None, len(parents),
+        _as_i32p(parents) if len(parents) else None, _as_i32p(out),
+        _stream(stream)))
+    return out[:len(parents)].tolist()
 
 
 def paged_decode_attn_noalloc(q, k_pool, v_pool, num_blocks, block_tables,

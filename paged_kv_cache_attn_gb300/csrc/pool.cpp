@@ -16,6 +16,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstring>
+#include <new>
 #include <numeric>
 
 #include "internal.h"
@@ -450,6 +451,104 @@ extern "C" kv_status kv_free(kv_pool* p, int32_t id) {
   if (kv_status s = get_live(p, id, &nd)) return s;
   release_node(p, *nd);
   return KV_OK;
+}
+
+static kv_status beam_reorder(kv_pool* p, int32_t n, const int32_t* ids,
+                              int32_t n_out, const int32_t* parents,
+                              int32_t* out_ids, void* stream) {
+  if (n < 0 || n_out < 0 || (n > 0 && !ids) || (n_out > 0 && (!parents || !out_ids)))
+    return fail(KV_ERR_INVALID_ARG, "bad beam lists");
+  std::vector<int32_t> sorted(ids, ids + n);
+  std::sort(sorted.begin(), sorted.end());
+  for (int32_t i = 0; i < n; ++i) {
+    Node* nd;
+    if (kv_status s = get_live(p, ids[i], &nd)) return s;
+    if (i > 0 && sorted[i] == sorted[i - 1])
+      return fail(KV_ERR_INVALID_ARG, "branch %d is listed twice", sorted[i]);
+  }
+  // The first beam of a parent keeps its branch; the others are forks.
+  const int32_t B = p->block_size;
+  std::vector<int32_t> result(n_out, -1), src, dst, children(n, 0);
+  std::vector<char> used(n, 0);
+  std::vector<Node> forks;
+  const size_t first = p->nodes.size();
+  for (int32_t i = 0; i < n_out; ++i) {
+    const int32_t k = parents[i];
+    if (k == -1) continue;
+    if (k < -1 || k >= n)
+      return fail(KV_ERR_INVALID_ARG, "parents[%d] = %d outside [-1, %d)", i, k, n);
+    const Node& pn = p->nodes[ids[k]];
+    if (!used[k]) {
+      used[k] = 1;
+      result[i] = ids[k];
+      continue;
+    }
+    if (pn.spilled)
+      return fail(KV_ERR_INVALID_ARG, "branch %d is spilled: restore it first", ids[k]);
+    if (first + forks.size() + 1 > (size_t)INT32_MAX)
+      return fail(KV_ERR_INVALID_ARG, "branch id space exhausted");
+    const int32_t full = pn.seq_len / B;
+    Node c;
+    c.parent = ids[k];
+    c.depth = pn.depth + 1;
+    c.inherited = full;
+    c.seq_len = pn.seq_len;
+    c.table.reserve(full + 1);
+    c.table.assign(pn.table.begin(), pn.table.begin() + full);
+    if (pn.seq_len % B != 0) {
+      if (dst.size() >= p->free_stack.size())
+        return fail(KV_ERR_OOM, "the beams' forks need more copy-on-write blocks than "
+                                "the %zu free", p->free_stack.size());
+      src.push_back(pn.table[full]);
+      dst.push_back(p->free_stack[p->free_stack.size() - 1 - dst.size()]);
+      c.table.push_back(dst.back());
+    }
+    ++children[k];
+    result[i] = (int32_t)(first + forks.size());
+    forks.push_back(std::move(c));
+  }
+  // What the commit needs room for, before anything changes (growing as push_back
+  // would, so that a long search does not copy its nodes every step).
+  auto room = [](auto& v, size_t more) {
+    if (v.capacity() < v.size() + more)
+      v.reserve(std::max(v.size() + more, 2 * v.capacity()));
+  };
+  room(p->nodes, forks.size());
+  for (int32_t k = 0; k < n; ++k) room(p->nodes[ids[k]].children, children[k]);
+  p->free_stack.reserve(p->num_blocks);
+  p->host_free.reserve(p->host_slots);
+  if (p->has_data() && !src.empty()) {
+    const pkv::PoolBufs dev{p->k_pool, p->v_pool, p->kv_scales, p->num_blocks};
+    const int err = pkv::launch_block_move(
+        dev, dev, p->num_layers, p->k_bytes(), p->v_bytes(), p->scale_bytes(),
+        src.data(), dst.data(), (int)src.size(), stream);
+    if (err) return fail(KV_ERR_CUDA, "copy-on-write launch failed (cuda %d)", err);
+  }
+  for (Node& c : forks) {
+    for (int32_t k = 0; k < c.inherited; ++k) p->ref[c.table[k]] += 1;
+    if ((int32_t)c.table.size() > c.inherited) {
+      p->ref[c.table.back()] = 1;
+      p->free_stack.pop_back();
+    }
+    p->nodes[c.parent].children.push_back((int32_t)p->nodes.size());
+    p->nodes.push_back(std::move(c));
+  }
+  for (int32_t k = 0; k < n; ++k)
+    if (!used[k]) release_node(p, p->nodes[ids[k]]);
+  std::copy(result.begin(), result.end(), out_ids);
+  return KV_OK;
+}
+
+extern "C" kv_status kv_beam_reorder(kv_pool* p, int32_t n, const int32_t* ids,
+                                     int32_t n_out, const int32_t* parents,
+                                     int32_t* out_ids, void* stream) {
+  pkv::clear_error();
+  if (!p) return fail(KV_ERR_INVALID_ARG, "null pool");
+  try {
+    return beam_reorder(p, n, ids, n_out, parents, out_ids, stream);
+  } catch (const std::bad_alloc&) {
+    return fail(KV_ERR_OOM, "no host memory for the beams");
+  }
 }
 
 static void free_subtree_rec(kv_pool* p, int32_t id, std::vector<int32_t>* freed) {
