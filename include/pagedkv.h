@@ -699,9 +699,10 @@ kv_status paged_latent_prefill_attn(
  * 2047.  flags: 0, or KV_PLAN_KV_E4M3 for an e4m3 pool.  Writes the plan to host
  * `plan` (plan = NULL: the size in info->plan_ints) and fills info:
  * workspace_bytes, n_merge_rows = query tokens, n_tile_items = work items a
- * kv-head, chunk_blocks = blocks of an item at most, n_tile_wide_items = tiles whose
- * keys are cut into several items, partial_rows = their partial rows, n_row_items =
- * distinct blocks (e4m3: each widened to bf16 once, 64 head_dim bytes of workspace
+ * kv-head (n_tile_wide_items of them of more than 128 rows, tokens x heads),
+ * chunk_blocks = blocks of an item at most, n_row_warp_items = tiles whose keys are
+ * cut into several items, partial_rows = their partial rows, n_row_items = distinct
+ * blocks (e4m3: each widened to bf16 once, 64 head_dim bytes of workspace
  * a kv-head; bf16: 0).  num_sms = the device's SM count (0: 152), which decides
  * about the cuts and thereby the last bits of the result.  One plan serves every
  * layer of a step.  Errors: INVALID_ARG (lengths, heads, flags, a block id outside

@@ -2,14 +2,16 @@
 // along the keys where there are too few of them for the GPU.
 //
 // A tile is up to 2 floor(128 / G) tokens of one branch with the G query heads
-// of a kv-head: floor(128 / G) tokens x G heads on each CTA of a pair.
+// of a kv-head: floor(128 / G) tokens x G heads on each CTA of a pair, or on a single
+// CTA where it has no more.
 //
 // Plan (int32): header; for e4m3 pools the distinct blocks in order of first use;
 // the branches' tables (physical blocks, or indices into the distinct ones); one
-// descriptor of 8 per work item and kv-head, longest key ranges first; one of 4
-// per tile whose key range is cut.
+// descriptor of 8 per work item of a kv-head (tiles for pairs first, in each kind
+// longest key ranges first); one of 4 per tile whose key range is cut.
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <new>
 
@@ -31,35 +33,34 @@ struct Tile {
 // Key tiles of a work item at most.  An item costs about as much as kItem more
 // key tiles (its first loads, the last products, the joining of the rows), a cut
 // one kPartial on top (the partial rows out, and in again), and the merge kMerge
-// once: with them the longest item or the mean of the pairs, whichever is more, is
-// least.
-int32_t pick_cut(const std::vector<Tile>& tiles, int32_t Hkv, int32_t pairs) {
+// once: with them the longest item or the mean of the units (pairs of SMs, and single
+// ones for tiles of no more than a CTA's tokens), whichever is more, is least.
+int32_t pick_cut(const std::vector<Tile>& tiles, int32_t Hkv, int32_t ctok,
+                 int32_t pairs) {
   constexpr double kItem = 3, kPartial = 1.5, kMerge = 5;
   int32_t longest = 1;
   for (const Tile& t : tiles) longest = std::max(longest, t.keys());
   int32_t best = longest;
   double least = 1e300;
   for (int32_t cut = longest; cut >= 1; cut = cut * 3 / 4) {
-    double total = 0, top = 0;
-    int64_t n = 0;
+    double total = 0, n = 0, top = 0;  // in pairs
     for (const Tile& t : tiles) {
       const int64_t pieces = ceil_div(t.keys(), cut);
-      const double each = (double)ceil_div(t.keys(), pieces) + kItem +
-                          (pieces > 1 ? kPartial : 0.);
-      total += (double)(t.keys() + pieces * (kItem + (pieces > 1 ? kPartial : 0.))) *
-               Hkv;
-      top = std::max(top, each);
-      n += pieces * Hkv;
+      const double fixed = kItem + (pieces > 1 ? kPartial : 0.);
+      const double share = (t.ntok <= ctok ? 0.5 : 1.) * Hkv;
+      total += (t.keys() + pieces * fixed) * share;
+      n += pieces * share;
+      top = std::max(top, (double)ceil_div(t.keys(), pieces) + fixed);
     }
     double cost = std::max(top, total / pairs);
     // Few items of a kind go by whole rounds.
-    if (n < 4ll * pairs) cost = std::max(cost, ceil_div(n, pairs) * (total / n));
+    if (n < 4. * pairs) cost = std::max(cost, std::ceil(n / pairs) * (total / n));
     if (cut < longest) cost += kMerge;
     if (cost < least) {
       least = cost;
       best = cut;
     }
-    // Already a small part of what the pairs have to do.
+    // Already a small part of what there is to do.
     if (top * 8 < total / pairs) break;
   }
   return best;
@@ -117,7 +118,7 @@ kv_status chunk_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d,
                        (int32_t)off});
     row += n;
   }
-  const int32_t cut = whole.empty() ? 1 : pick_cut(whole, Hkv, pairs);
+  const int32_t cut = whole.empty() ? 1 : pick_cut(whole, Hkv, step / 2, pairs);
   std::vector<pkv::ChunkItem> items;
   std::vector<pkv::ChunkMerge> merges;
   int64_t partial = 0;
@@ -137,12 +138,19 @@ kv_status chunk_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d,
         return fail(KV_ERR_INVALID_ARG, "step too large for one plan");
     }
   }
-  // Longest first: the persistent pairs take the items in this order, so that the
-  // last ones to start are short.
+  // Tiles for pairs, then those of no more than a CTA's tokens; longest first: the
+  // persistent CTAs take the items in this order, so that the last ones to start are
+  // short.
+  const int32_t ctok = step / 2;
   std::stable_sort(items.begin(), items.end(),
-                   [](const pkv::ChunkItem& x, const pkv::ChunkItem& y) {
+                   [ctok](const pkv::ChunkItem& x, const pkv::ChunkItem& y) {
+                     const bool wx = x.ntok > ctok, wy = y.ntok > ctok;
+                     if (wx != wy) return wx;
                      return x.key_end - x.key_begin > y.key_end - y.key_begin;
                    });
+  const auto n_wide = std::count_if(
+      items.begin(), items.end(),
+      [ctok](const pkv::ChunkItem& x) { return x.ntok > ctok; });
   const int64_t U = (int64_t)uniq.size();
   if ((int64_t)items.size() * Hkv > INT32_MAX / 2 || U * Hkv > INT32_MAX / 16)
     return fail(KV_ERR_INVALID_ARG, "step too large for one plan");
@@ -159,8 +167,8 @@ kv_status chunk_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d,
   info->n_tile_items = (int32_t)items.size();
   info->n_merge_rows = (int32_t)row;
   info->chunk_blocks = cut * (kKeys / 16);
-  info->n_tile_wide_items = (int32_t)merges.size();
-  info->n_row_warp_items = (int32_t)slots.size();
+  info->n_tile_wide_items = (int32_t)n_wide;
+  info->n_row_warp_items = (int32_t)merges.size();
   info->flags = pkv::kChunkPlan | flags;
   info->latent_rows = pkv::chunk_mark(Hq, Hkv, d);
   if (!plan) return KV_OK;
