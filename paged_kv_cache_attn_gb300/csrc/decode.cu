@@ -409,8 +409,12 @@ struct MergeParams {
   int64_t partial_rows;
 };
 
-// One warp per (branch, q-head).
-template <int D>
+// One warp per (branch, q-head).  kAhead entries of the branch's list are fetched at
+// a time, then joined in order (the same operations for every kAhead).  With few
+// rows each entry's three dependent loads are all there is to wait for: 16 entries
+// a row and 64 rows 13 us one at a time, 4 us eight at a time; with many rows other
+// warps cover them, and one at a time is as fast.
+template <int D, int kAhead>
 __global__ void __launch_bounds__(256) lse_merge_kernel(const MergeParams p) {
   constexpr int V = D / 32;  // values per lane
   const int gw = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -424,28 +428,44 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(const MergeParams p) {
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (int e = e0; e < e1; ++e) {
-    const MergeEntry me = p.csr[e];
-    if (r < me.r_lo || r >= me.r_hi) continue;
-    const int64_t row = me.base + (int64_t)g * me.stride + (r - me.r_lo);
-    if (row < 0 || row >= p.partial_rows) continue;
-    const float2 ml = p.ml[row];
-    const float* src = p.o + (int64_t)row * D + lane * V;
-    float v[V];
-    if constexpr (V == 4) {
-      const float4 t = *reinterpret_cast<const float4*>(src);
-      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-    } else {
-      const float2 t = *reinterpret_cast<const float2*>(src);
-      v[0] = t.x; v[1] = t.y;
-    }
-    const float m_new = fmaxf(m, ml.x);
-    const float a = m == -INFINITY ? 0.f : ex2(m - m_new);  // first entry: 0
-    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m_new);
-    lsum = lsum * a + w * ml.y;
+  for (int e = e0; e < e1; e += kAhead) {
+    int64_t row[kAhead];
+    float2 ml[kAhead];
+    float v[kAhead][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = acc[i] * a + w * v[i];
-    m = m_new;
+    for (int k = 0; k < kAhead; ++k) {
+      row[k] = -1;
+      if (e + k < e1) {
+        const MergeEntry me = p.csr[e + k];
+        if (r >= me.r_lo && r < me.r_hi)
+          row[k] = me.base + (int64_t)g * me.stride + (r - me.r_lo);
+        if (row[k] >= p.partial_rows) row[k] = -1;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (row[k] < 0) continue;
+      ml[k] = p.ml[row[k]];
+      const float* src = p.o + row[k] * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(src);
+        v[k][0] = t.x; v[k][1] = t.y; v[k][2] = t.z; v[k][3] = t.w;
+      } else {
+        const float2 t = *reinterpret_cast<const float2*>(src);
+        v[k][0] = t.x; v[k][1] = t.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (row[k] < 0) continue;
+      const float m_new = fmaxf(m, ml[k].x);
+      const float a = m == -INFINITY ? 0.f : ex2(m - m_new);  // first entry: 0
+      const float w = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - m_new);
+      lsum = lsum * a + w * ml[k].y;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = acc[i] * a + w * v[k][i];
+      m = m_new;
+    }
   }
   const float inv = 1.f / lsum;
   __nv_bfloat16* dst = p.out + ((int64_t)b * p.Hq + h) * D + lane * V;
@@ -568,10 +588,15 @@ cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv,
   return cudaGetLastError();
 }
 
+constexpr int kFewMergeRows = 1024;  // fewer than a warp on every scheduler and a half
+
 template <int D>
 cudaError_t launch_merge(const MergeParams& mp, cudaStream_t stream) {
   const int warps = mp.nb * mp.Hq;
-  lse_merge_kernel<D><<<(warps + 7) / 8, 256, 0, stream>>>(mp);
+  if (warps <= kFewMergeRows)
+    lse_merge_kernel<D, 8><<<(warps + 7) / 8, 256, 0, stream>>>(mp);
+  else
+    lse_merge_kernel<D, 1><<<(warps + 7) / 8, 256, 0, stream>>>(mp);
   return cudaGetLastError();
 }
 

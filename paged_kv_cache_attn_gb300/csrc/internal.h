@@ -184,6 +184,13 @@ kv_status latent_plan(int32_t nb, int32_t Hq, int32_t max_blocks,
                       int32_t num_sms, int32_t flags, int32_t* plan,
                       int64_t plan_cap, kv_decode_plan_info* info);
 
+// paged_decode_plan for branches without segments and one kv-head, with split-KV
+// items of at most row_blocks blocks (plan.cpp).
+kv_status decode_plan_of_rows(int32_t nb, int32_t Hq, int32_t d, int32_t max_blocks,
+                              const int32_t* seq_lens, int32_t num_sms, int32_t flags,
+                              int32_t row_blocks, int32_t* plan, int64_t plan_cap,
+                              kv_decode_plan_info* info);
+
 // ---- kernel launchers (state_kernels.cu, decode kernels) -------------------
 // Copy appended K/V rows into their slots.  dst_blocks[i] = physical block of
 // logical block first_lblock + i; rows are tokens [tok0, tok0 + n) of the

@@ -51,8 +51,8 @@ int32_t pick_chunk(const std::vector<Unit>& units, bool tile, int Hkv,
 kv_status decode_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d, int32_t B,
                       int32_t max_blocks, const int32_t* seq_lens,
                       const int32_t* groups, int32_t n_groups, int32_t num_sms,
-                      int32_t flags, int32_t* plan, int64_t plan_cap,
-                      kv_decode_plan_info* info) {
+                      int32_t flags, int32_t row_blocks, int32_t* plan,
+                      int64_t plan_cap, kv_decode_plan_info* info) {
   if (!info || !seq_lens) return fail(KV_ERR_INVALID_ARG, "null argument");
   if (nb < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
     return fail(KV_ERR_INVALID_ARG, "bad nb/Hq/Hkv (%d/%d/%d)", nb, Hq, Hkv);
@@ -170,7 +170,8 @@ kv_status decode_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d, int32_t B,
     block_work += (int64_t)(u.blk_end - u.blk_begin) *
                   ceil_div(u.rows, rows_per(u)) * Hkv;
   }
-  const int32_t chunk_rows = pick_chunk(units, false, Hkv, num_sms, 128);
+  const int32_t chunk_rows =
+      row_blocks > 0 ? row_blocks : pick_chunk(units, false, Hkv, num_sms, 128);
   const int32_t chunk_tile =
       any_rows ? (int32_t)std::min<int64_t>(
                      INT32_MAX, std::max<int64_t>(8, block_work / num_sms))
@@ -322,6 +323,18 @@ kv_status decode_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d, int32_t B,
 
 }  // namespace
 
+namespace pkv {
+
+kv_status decode_plan_of_rows(int32_t nb, int32_t Hq, int32_t d, int32_t max_blocks,
+                              const int32_t* seq_lens, int32_t num_sms, int32_t flags,
+                              int32_t row_blocks, int32_t* plan, int64_t plan_cap,
+                              kv_decode_plan_info* info) {
+  return decode_plan(nb, Hq, 1, d, 16, max_blocks, seq_lens, nullptr, 0, num_sms,
+                     flags | KV_PLAN_IGNORE_GROUPS, row_blocks, plan, plan_cap, info);
+}
+
+}  // namespace pkv
+
 extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
                                        int32_t d, int32_t B,
                                        int32_t max_blocks,
@@ -333,7 +346,7 @@ extern "C" kv_status paged_decode_plan(int32_t nb, int32_t Hq, int32_t Hkv,
   pkv::clear_error();
   try {
     return decode_plan(nb, Hq, Hkv, d, B, max_blocks, seq_lens, groups, n_groups,
-                       num_sms, flags, plan, plan_cap, info);
+                       num_sms, flags, 0, plan, plan_cap, info);
   } catch (const std::bad_alloc&) {
     return fail(KV_ERR_OOM, "no host memory for the plan");
   }

@@ -276,16 +276,48 @@ constexpr int kWarps = 8;
 constexpr int kWarpBlocks = 32;                       // blocks a warp scores
 constexpr int kCtaBlocks = kWarps * kWarpBlocks;
 
-// grid (block ranges, Hkv, nb).  The heads are the 16 rows of the products, eight
-// blocks their columns; lane 4 n + t has bytes [16 t + 64 j, + 16) of block n's
-// record, which are its columns of four products in any order that the queries'
-// fragments share.
+// A query head as whole numbers of at most 127 times a power of two, by one warp: its
+// f16 values to dst, the power returned (-1: no such head, all zeros).
 template <int D>
-__global__ void __launch_bounds__(256) score_kernel(const SelectParams p) {
+__device__ __forceinline__ float quantise(const __nv_bfloat16* src, bool there,
+                                          __half* dst, int lane) {
+  constexpr int V = D / 32;
+  float x[V], amax = 0.f;
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    x[i] = there ? __bfloat162float(src[lane * V + i]) : 0.f;
+    odd |= !(fabsf(x[i]) < INFINITY);
+    amax = fmaxf(amax, fabsf(x[i]));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  odd = __any_sync(0xffffffffu, odd);
+  const int e = bound_exponent(amax);
+  const float inv = pow2f(-e);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    dst[lane * V + i] = __float2half_rn(
+        odd ? 0.f : fminf(fmaxf(rintf(x[i] * inv), -127.f), 127.f));
+  return there ? (odd ? 0.f : pow2f(e)) : -1.f;
+}
+
+// grid (block ranges, Hkv, nb).  Up to 16 heads are the rows of the products, eight
+// blocks their columns; lane 4 n + t has bytes [16 t + 64 j, + 16) of block n's record,
+// which are its columns of four products in any order that the queries' fragments
+// share.  A warp has 16 blocks' records in flight at a time (4 KB at D = 128), asked
+// for before the queries are quantised.  kFew: at most 8 heads, kept in registers (the
+// rows after them are zeros); else 16 at a time from shared memory.
+template <int D, bool kFew>
+__global__ void __launch_bounds__(256, kFew ? 2 : 1)
+    score_kernel(const SelectParams p) {
   constexpr int kRow = D + 8;  // a head's f16 values in shared memory
-  __shared__ __align__(16) __half qs[kMaxG * kRow];
-  __shared__ float qe[kMaxG];
+  __shared__ __align__(16) __half qs[(kFew ? 8 : kMaxG) * kRow];
+  __shared__ float qe[kFew ? 8 : kMaxG];
   const int b = blockIdx.z, h = blockIdx.y;
+  if (blockIdx.x == 0 && b == 0 && h == 0 && threadIdx.x == 0)
+    *p.status = DeviceStatus{};  // the next kernel records
   const int L = p.seq_lens[b];
   const int nblk = L < 1 || L > (int64_t)p.max_blocks * 16 ? 0 : (L + 15) / 16;
   // A branch of few blocks has them all.
@@ -293,116 +325,111 @@ __global__ void __launch_bounds__(256) score_kernel(const SelectParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blk0 = blockIdx.x * kCtaBlocks + warp * kWarpBlocks;
   const int32_t* table = p.tables + (int64_t)b * p.max_blocks;
+  // A block id outside the pool (recorded by the next kernel) has no score.
   int phys = -1;
-  if (blk0 + lane < nblk) {
-    phys = table[blk0 + lane];
-    if (phys < 0 || phys >= p.num_blocks) {
-      record_status(p.status, KV_ERR_DEVICE, phys);
-      phys = -1;
+  if (blk0 + lane < nblk) phys = table[blk0 + lane];
+  if (phys >= p.num_blocks) phys = -1;
+  const int n = lane >> 2, t = lane & 3;
+  constexpr int kJ = 2 * D / 64;  // 64-byte parts of a record
+  uint4 rec[2][kJ];
+  auto fetch = [&](int half) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int ph = __shfl_sync(0xffffffffu, phys, half * 16 + i * 8 + n);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.bounds + ((int64_t)max(ph, 0) * p.Hkv + h) * (2 * D));
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) rec[i][j] = src[j * 4 + t];
     }
-  }
-  // Queries: a warp quantises a head at a time; heads of the last 16 that there
-  // are not are zeros.
-  const int G = p.G, rows = (G + 15) & ~15;
+  };
+  fetch(0);
+  const float my_scale =
+      phys >= 0 ? p.bound_scales[(int64_t)phys * p.Hkv + h] : 0.f;
+  const int G = p.G, rows = kFew ? 8 : (G + 15) & ~15;
   for (int g = warp; g < rows; g += kWarps) {
-    constexpr int V = D / 32;
-    float x[V], amax = 0.f;
-    bool odd = false;
-    const __nv_bfloat16* src =
-        p.q + ((int64_t)b * p.Hq + (int64_t)h * G + min(g, G - 1)) * D + lane * V;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      x[i] = g < G ? __bfloat162float(src[i]) : 0.f;
-      odd |= !(fabsf(x[i]) < INFINITY);
-      amax = fmaxf(amax, fabsf(x[i]));
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    odd = __any_sync(0xffffffffu, odd);
-    const int e = bound_exponent(amax);
-    const float inv = pow2f(-e);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float n = odd ? 0.f : fminf(fmaxf(rintf(x[i] * inv), -127.f), 127.f);
-      qs[g * kRow + lane * V + i] = __float2half_rn(n);
-    }
-    if (lane == 0) qe[g] = g < G ? (odd ? 0.f : pow2f(e)) : -1.f;
+    const float e = quantise<D>(
+        p.q + ((int64_t)b * p.Hq + (int64_t)h * G + min(g, G - 1)) * D, g < G,
+        qs + g * kRow, lane);
+    if (lane == 0) qe[g] = e;
   }
   __syncthreads();
   if (blk0 >= nblk) return;
-  const int n = lane >> 2, t = lane & 3;
-  constexpr int kJ = 2 * D / 64;  // 64-byte parts of a record
-  uint4 rec[4][kJ];
+  // The least values meet the queries' negative numbers, the largest the positive
+  // ones.
+  auto fragment = [&](int g, int j, uint32_t (&f)[8]) {
+    const __half* src = qs + g * kRow + (j * 64) % D + t * 16;
+    const uint4 v0 = *reinterpret_cast<const uint4*>(src);
+    const uint4 v1 = *reinterpret_cast<const uint4*>(src + 8);
+    const uint32_t v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int ph = __shfl_sync(0xffffffffu, phys, i * 8 + n);
-    const uint4* src = reinterpret_cast<const uint4*>(
-        p.bounds + ((int64_t)max(ph, 0) * p.Hkv + h) * (2 * D));
+    for (int k = 0; k < 8; ++k)
+      f[k] = j < kJ / 2 ? min2h(v[k], 0u) : max2h(v[k], 0u);
+  };
+  uint32_t few[kFew ? kJ : 1][8];
+  if constexpr (kFew) {
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) rec[i][j] = src[j * 4 + t];
-  }
-  const float my_scale =
-      phys >= 0 ? p.bound_scales[(int64_t)phys * p.Hkv + h] : 0.f;
-  float best[4][2];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) best[i][0] = best[i][1] = -INFINITY;
-  for (int g0 = 0; g0 < rows; g0 += 16) {
-    float acc[4][4] = {};
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      // The least values meet the queries' negative numbers, the largest the
-      // positive ones.
-      const int col = (j * 64) % D + t * 16;
-      const bool neg = j < kJ / 2;
-      uint32_t f[2][8];
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const __half* src = qs + (g0 + z * 8 + n) * kRow + col;
-        const uint4 v0 = *reinterpret_cast<const uint4*>(src);
-        const uint4 v1 = *reinterpret_cast<const uint4*>(src + 8);
-        const uint32_t v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[z][k] = neg ? min2h(v[k], 0u) : max2h(v[k], 0u);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {rec[i][j].x, rec[i][j].y, rec[i][j].z, rec[i][j].w};
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          uint32_t b0, b1;
-          bytes_to_f16(w[s], b0, b1);
-          const uint32_t a[4] = {f[0][2 * s], f[1][2 * s], f[0][2 * s + 1],
-                                 f[1][2 * s + 1]};
-          mma_f16(acc[i], a, b0, b1);
-        }
-      }
-    }
-    const float e0 = qe[g0 + n], e1 = qe[g0 + 8 + n];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const float s0 = e0 < 0.f ? -INFINITY : acc[i][z] * e0;
-        const float s1 = e1 < 0.f ? -INFINITY : acc[i][2 + z] * e1;
-        best[i][z] = fmaxf(best[i][z], fmaxf(s0, s1));
-      }
+    for (int j = 0; j < kJ; ++j) fragment(n, j, few[j]);
   }
   float* dst = p.scores + ((int64_t)b * p.Hkv + h) * p.stride;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      float s = best[i][z];
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1)
-        s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
-      const float sc = __shfl_sync(0xffffffffu, my_scale, i * 8 + 2 * t + z);
-      const int blk = blk0 + i * 8 + 2 * t + z;
-      // (+ 0 makes a zero positive.)
-      if (n == 0 && blk < nblk)
-        dst[blk] = sc == INFINITY ? INFINITY : s * sc + 0.f;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    if (half > 0) {
+      if (blk0 + 16 >= nblk) break;
+      fetch(1);
     }
+    float best[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) best[i][0] = best[i][1] = -INFINITY;
+#pragma unroll 1
+    for (int g0 = 0; g0 < rows; g0 += 16) {
+      float acc[2][4] = {};
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        uint32_t f[2][8];
+        if constexpr (!kFew) {
+          fragment(g0 + n, j, f[0]);
+          fragment(g0 + 8 + n, j, f[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w[4] = {rec[i][j].x, rec[i][j].y, rec[i][j].z, rec[i][j].w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint32_t b0, b1;
+            bytes_to_f16(w[s], b0, b1);
+            const uint32_t a[4] = {kFew ? few[kFew ? j : 0][2 * s] : f[0][2 * s],
+                                   kFew ? 0u : f[1][2 * s],
+                                   kFew ? few[kFew ? j : 0][2 * s + 1] : f[0][2 * s + 1],
+                                   kFew ? 0u : f[1][2 * s + 1]};
+            mma_f16(acc[i], a, b0, b1);
+          }
+        }
+      }
+      const float e0 = qe[g0 + n], e1 = kFew ? -1.f : qe[g0 + 8 + n];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float s0 = e0 < 0.f ? -INFINITY : acc[i][z] * e0;
+          const float s1 = e1 < 0.f ? -INFINITY : acc[i][2 + z] * e1;
+          best[i][z] = fmaxf(best[i][z], fmaxf(s0, s1));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        float s = best[i][z];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+          s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
+        const int at = half * 16 + i * 8 + 2 * t + z;
+        const float sc = __shfl_sync(0xffffffffu, my_scale, at);
+        // (+ 0 makes a zero positive.)
+        if (n == 0 && blk0 + at < nblk)
+          dst[blk0 + at] = sc == INFINITY ? INFINITY : s * sc + 0.f;
+      }
+  }
 }
 
 // ---- selection --------------------------------------------------------------------
@@ -412,110 +439,205 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-constexpr int kPickThreads = 256, kPickWarps = 8;
+constexpr int kBuckets = 1024;
 
-// A CTA for each (branch, kv-head): the n_sel-th largest key digit by digit (8
-// bits), then the blocks above it and the first of those equal to it, in order.
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectParams p) {
-  __shared__ uint32_t hist[kPickWarps][256];
-  __shared__ uint32_t sh_digit, sh_left;
-  __shared__ int above[kPickWarps], equal[kPickWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int row = blockIdx.x, b = row / p.Hkv, h = row % p.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Inclusive sums over the CTA's threads; `sh`: 32 entries.
+template <int T>
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();  // sh may still be read
+  if (lane == 31) sh[warp] = v;
+  __syncthreads();
+  uint32_t w = lane < T / 32 ? sh[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  return v + (warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
+}
+
+// A CTA for each (branch, kv-head): which blocks are among the n_sel.  A thread has
+// eight blocks' keys at a time (a branch of up to 8 T blocks in registers).  The keys'
+// range is cut into 1024 buckets and the one that holds the last key wanted becomes
+// the range, until it is wanted whole (nearly always after two passes: scores spread
+// over their range) or holds one key, of whose blocks the first are taken.
+template <int T>
+__global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
+  __shared__ uint32_t hist[kBuckets], sums[32];
+  __shared__ uint32_t sh_lo, sh_hi, sh_bucket, sh_left, sh_count;
+  const int row = blockIdx.x, b = row / p.Hkv, h = row % p.Hkv, tid = threadIdx.x;
   const int L = p.seq_lens[b];
   const int32_t* table = p.tables + (int64_t)b * p.max_blocks;
   int32_t* sel = p.sel ? p.sel + (int64_t)row * p.n_sel : nullptr;
   int32_t* out = p.sel_tables + (int64_t)row * p.n_sel;
   const bool bad = L < 1 || L > (int64_t)p.max_blocks * 16;
-  if (bad && threadIdx.x == 0) record_status(p.status, KV_ERR_DEVICE, L);
   const int nblk = bad ? 0 : (L + 15) / 16;
   const int count = min(nblk, p.n_sel);
+  if (tid == 0) {
+    sh_lo = 0xffffffffu;
+    sh_hi = 0;
+  }
+  // Scores, and a cleared status word.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (bad && tid == 0) record_status(p.status, KV_ERR_DEVICE, L);
+  if (h == 0)
+    for (int i = tid; i < nblk; i += T) {
+      const int phys = table[i];
+      if (phys < 0 || phys >= p.num_blocks)
+        record_status(p.status, KV_ERR_DEVICE, phys);
+    }
   auto put = [&](int at, int blk) {
     const int phys = table[blk];
     const bool in = phys >= 0 && phys < p.num_blocks;
-    if (!in) record_status(p.status, KV_ERR_DEVICE, phys);
     if (sel) sel[at] = blk;
     out[at] = in ? (int)(phys * (int64_t)p.Hkv + h) : -1;
   };
-  if (threadIdx.x == 0)
+  if (tid == 0)
     p.sel_lens[row] = count > 0 ? 16 * (count - 1) + (L - 16 * (nblk - 1)) : 0;
-  for (int i = count + threadIdx.x; i < p.n_sel; i += kPickThreads) {
+  for (int i = count + tid; i < p.n_sel; i += T) {
     if (sel) sel[i] = -1;
     out[i] = -1;
   }
   if (nblk <= p.n_sel) {
-    for (int i = threadIdx.x; i < nblk; i += kPickThreads) put(i, i);
+    for (int i = tid; i < nblk; i += T) put(i, i);
     return;
   }
   const float* scores = p.scores + (int64_t)row * p.stride;
-  auto key = [&](int i) -> uint32_t {
-    if (i < p.n_first || i >= nblk - p.n_last) return 0xffffffffu;
-    return ordered(scores[i]);
-  };
-  // The digits of the n_sel-th largest key; `left`: how many of the keys that begin
-  // with the digits so far are wanted.
-  uint32_t prefix = 0, left = (uint32_t)p.n_sel;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < kPickWarps * 256; i += kPickThreads)
-      (&hist[0][0])[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < nblk; i += kPickThreads) {
-      const uint32_t k = key(i);
-      if (shift == 24 || (k >> (shift + 8)) == prefix)
-        atomicAdd(&hist[warp][(k >> shift) & 255], 1u);
-    }
-    __syncthreads();
-    // Thread t: keys of digit 255 - t, and of all above it.
-    uint32_t n = 0;
-    for (int w = 0; w < kPickWarps; ++w) n += hist[w][255 - threadIdx.x];
-    uint32_t sum = n;
+  // Keys of blocks base + 8 tid ..; 0 where there is none, all ones where the block
+  // is taken in any case.
+  auto load = [&](int base, uint32_t (&k)[8]) {
+    const int i0 = base + 8 * tid;
+    float x[8];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
+    for (int i = 0; i < 8; i += 4) {
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + i < nblk) y = *reinterpret_cast<const float4*>(scores + i0 + i);
+      x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
     }
-    if (lane == 31) above[warp] = (int)sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      k[i] = i0 + i >= nblk                                    ? 0u
+             : i0 + i < p.n_first || i0 + i >= nblk - p.n_last ? 0xffffffffu
+                                                               : ordered(x[i]);
+  };
+  uint32_t first[8];
+  load(0, first);
+  // f(key, block) for all blocks.
+  auto each = [&](auto&& f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f(first[i], 8 * tid + i);
+    for (int base = 8 * T; base < nblk; base += 8 * T) {
+      uint32_t k[8];
+      load(base, k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f(k[i], base + 8 * tid + i);
+    }
+  };
+  // [lo, hi]: where the last key wanted is; left: how many of its keys are wanted.
+  uint32_t lo = 0xffffffffu, hi = 0, left = (uint32_t)(p.n_sel - p.n_first - p.n_last);
+  bool whole = left == 0;  // the range is wanted whole (or nothing of it)
+  if (whole) {
+    lo = 0xffffffffu;
+    hi = 0xffffffffu;
+  } else {
+    uint32_t a = 0xffffffffu, z = 0;
+    each([&](uint32_t k, int) {
+      if (k != 0 && k != 0xffffffffu) {
+        a = min(a, k);
+        z = max(z, k);
+      }
+    });
+    a = __reduce_min_sync(0xffffffffu, a);
+    z = __reduce_max_sync(0xffffffffu, z);
     __syncthreads();
-    for (int w = 0; w < warp; ++w) sum += (uint32_t)above[w];
-    if (sum >= left && sum - n < left) {
-      sh_digit = 255 - threadIdx.x;
-      sh_left = left - (sum - n);
+    if ((tid & 31) == 0) {
+      atomicMin(&sh_lo, a);
+      atomicMax(&sh_hi, z);
     }
     __syncthreads();
-    prefix = prefix << 8 | sh_digit;
+    lo = sh_lo;
+    hi = sh_hi;
+  }
+  while (!whole && lo < hi) {
+    // Keys (of finite scores and infinity) span less than 2^32.
+    const int shift = max(0, 32 - __clz(hi - lo) - 10);
+    for (int i = tid; i < kBuckets; i += T) hist[i] = 0;
+    __syncthreads();
+    each([&](uint32_t k, int) {
+      if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> shift], 1u);
+    });
+    __syncthreads();
+    // Thread t: buckets from the top.
+    constexpr int kPer = kBuckets / T;
+    uint32_t mine[kPer], all = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      mine[i] = hist[kBuckets - 1 - (tid * kPer + i)];
+      all += mine[i];
+    }
+    uint32_t above = block_scan<T>(all, sums) - all;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (above < left && above + mine[i] >= left) {
+        sh_bucket = kBuckets - 1 - (tid * kPer + i);
+        sh_left = left - above;
+        sh_count = mine[i];
+      }
+      above += mine[i];
+    }
+    __syncthreads();
+    lo += sh_bucket << shift;
+    hi = min(hi, lo + ((1u << shift) - 1));
     left = sh_left;
+    whole = sh_count == left;
+  }
+  // Blocks above the range, and of the range's all or the first `left`.
+  uint32_t n_above = 0, n_equal = 0;  // before this thread's
+  auto place = [&](const uint32_t (&k)[8], int base) {
+    uint32_t mine = 0;  // blocks taken, and of the range (in the upper half)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = k[i] >= lo && k[i] <= hi && k[i] != 0xffffffffu;
+      const bool up = k[i] > hi || k[i] == 0xffffffffu || (in && whole);
+      mine += up ? 1u : in ? 0x10000u : 0u;
+    }
+    const uint32_t sum = block_scan<T>(mine, sums);
+    uint32_t a = n_above + (sum & 0xffffu) - (mine & 0xffffu);
+    uint32_t e = n_equal + (sum >> 16) - (mine >> 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = k[i] >= lo && k[i] <= hi && k[i] != 0xffffffffu;
+      const bool up = k[i] > hi || k[i] == 0xffffffffu || (in && whole);
+      if (up) {
+        put((int)(a + min(e, left)), base + 8 * tid + i);
+        ++a;
+      } else if (in) {
+        if (e < left) put((int)(a + e), base + 8 * tid + i);
+        ++e;
+      }
+    }
+    // The CTA's total, for the blocks after these.
     __syncthreads();
-  }
-  // Each warp a run of blocks: counts, then places.
-  const int run = ((nblk + kPickWarps - 1) / kPickWarps + 31) & ~31;
-  const int i0 = warp * run, i1 = min(i0 + run, nblk);
-  int n_above = 0, n_equal = 0;
-  for (int i = i0; i < i1; i += 32) {
-    const uint32_t k = i + lane < i1 ? key(i + lane) : 0;
-    n_above += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && k > prefix));
-    n_equal += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && k == prefix));
-  }
-  if (lane == 0) {
-    above[warp] = n_above;
-    equal[warp] = n_equal;
-  }
-  __syncthreads();
-  n_above = n_equal = 0;
-  for (int w = 0; w < warp; ++w) {
-    n_above += above[w];
-    n_equal += equal[w];
-  }
-  const uint32_t below = (1u << lane) - 1;
-  for (int i = i0; i < i1; i += 32) {
-    const uint32_t k = i + lane < i1 ? key(i + lane) : 0;
-    const uint32_t m1 = __ballot_sync(0xffffffffu, i + lane < i1 && k > prefix);
-    const uint32_t m2 = __ballot_sync(0xffffffffu, i + lane < i1 && k == prefix);
-    const int a = n_above + __popc(m1 & below), e = n_equal + __popc(m2 & below);
-    const bool mine = (m1 >> lane & 1) || ((m2 >> lane & 1) && e < (int)left);
-    if (mine) put(a + min(e, (int)left), i + lane);
-    n_above += __popc(m1);
-    n_equal += __popc(m2);
+    if (tid == T - 1) {
+      sh_lo = n_above + (sum & 0xffffu);
+      sh_hi = n_equal + (sum >> 16);
+    }
+    __syncthreads();
+    n_above = sh_lo;
+    n_equal = sh_hi;
+  };
+  if (whole) left = 0;
+  place(first, 0);
+  for (int base = 8 * T; base < nblk; base += 8 * T) {
+    uint32_t k[8];
+    load(base, k);
+    place(k, base);
   }
 }
 
@@ -614,6 +736,40 @@ kv_status virtual_batch(int32_t nb, int32_t Hq, int32_t Hkv, int64_t num_blocks)
   return KV_OK;
 }
 
+// Blocks of a split-KV item.  All branches are about as long as the selection, so
+// that items go by rounds of the CTAs that run at once: 256 branches of 128 blocks as
+// 512 items of 64 left 56 for a second round (56 us), as 768 of 43 they take 46.  An
+// item costs about as much as kItem more blocks (its table entries and first loads), a
+// piece of a branch kPiece (the merge's).
+int32_t pick_cut(const std::vector<int32_t>& lens, int32_t G, int32_t num_sms) {
+  constexpr double kItem = 14, kPiece = 1;
+  const int64_t slots = (int64_t)kSplitCtasPerSm * num_sms;
+  int32_t longest = 1, best = 1;
+  for (const int32_t L : lens) longest = std::max(longest, (L + 15) / 16);
+  double least = 1e300;
+  // From items of a whole branch (at most 256 blocks) down.
+  for (int32_t cut = std::min(longest, 256); cut >= 8 || cut == std::min(longest, 256);
+       cut = cut * 3 / 4) {
+    int64_t n = 0;
+    double total = 0;
+    for (const int32_t L : lens) {
+      const int64_t blocks = (L + 15) / 16;
+      const int64_t pieces = (blocks + cut - 1) / cut * ((G + kRowTile - 1) / kRowTile);
+      n += pieces;
+      total += blocks * ((G + kRowTile - 1) / kRowTile) + pieces * kItem;
+    }
+    const double rounds = (double)((n + slots - 1) / slots);
+    const double cost = std::max(std::min<double>(cut, longest) + kItem,
+                                 n < 6 * slots ? rounds * (total / n) : total / slots) +
+                        kPiece * ((longest + cut - 1) / cut);
+    if (cost < least) {
+      least = cost;
+      best = cut;
+    }
+  }
+  return best;
+}
+
 }  // namespace sel
 }  // namespace pkv
 
@@ -709,19 +865,28 @@ extern "C" kv_status paged_select_blocks(
   p.n_sel = n_sel;
   p.n_first = n_first;
   p.n_last = n_last;
-  S::clear_kernel<<<1, 32, 0, st>>>(p.status);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && max_blocks > n_sel) {
+  if (max_blocks > n_sel) {
     const dim3 grid((unsigned)((max_blocks + S::kCtaBlocks - 1) / S::kCtaBlocks),
                     (unsigned)Hkv, (unsigned)nb);
-    if (head_dim == 128)
-      S::score_kernel<128><<<grid, 256, 0, st>>>(p);
+    if (head_dim == 128 && p.G <= 8)
+      S::score_kernel<128, true><<<grid, 256, 0, st>>>(p);
+    else if (head_dim == 128)
+      S::score_kernel<128, false><<<grid, 256, 0, st>>>(p);
+    else if (p.G <= 8)
+      S::score_kernel<64, true><<<grid, 256, 0, st>>>(p);
     else
-      S::score_kernel<64><<<grid, 256, 0, st>>>(p);
-    e = cudaGetLastError();
+      S::score_kernel<64, false><<<grid, 256, 0, st>>>(p);
+  } else {
+    S::clear_kernel<<<1, 32, 0, st>>>(p.status);
   }
+  cudaError_t e = cudaGetLastError();
+  // As many threads as hold a branch's keys at once.
   if (e == cudaSuccess)
-    e = pkv::launch_early(S::pick_kernel, nb * Hkv, S::kPickThreads, 0, st, p);
+    e = max_blocks <= 2048
+            ? pkv::launch_early(S::pick_kernel<256>, nb * Hkv, 256, 0, st, p)
+        : max_blocks <= 4096
+            ? pkv::launch_early(S::pick_kernel<512>, nb * Hkv, 512, 0, st, p)
+            : pkv::launch_early(S::pick_kernel<1024>, nb * Hkv, 1024, 0, st, p);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "block selection: %s", cudaGetErrorString(e));
   return KV_OK;
@@ -753,9 +918,10 @@ extern "C" kv_status paged_selected_plan(int32_t nb, int32_t Hq, int32_t Hkv,
       const int32_t cut = nblk > n_sel ? (nblk - n_sel) * 16 : 0;
       std::fill_n(lens.begin() + (size_t)b * Hkv, Hkv, L - cut);
     }
-    return paged_decode_plan(nb * Hkv, Hq / Hkv, 1, head_dim, block_size, n_sel,
-                             lens.data(), nullptr, 0, num_sms,
-                             flags | KV_PLAN_IGNORE_GROUPS, plan, plan_cap, info);
+    return pkv::decode_plan_of_rows(
+        nb * Hkv, Hq / Hkv, head_dim, n_sel, lens.data(), num_sms, flags,
+        pkv::sel::pick_cut(lens, Hq / Hkv, num_sms > 0 ? num_sms : 152), plan, plan_cap,
+        info);
   } catch (const std::bad_alloc&) {
     return fail(KV_ERR_OOM, "no host memory for the plan");
   }
