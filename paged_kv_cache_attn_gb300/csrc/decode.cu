@@ -594,7 +594,7 @@ template <int D>
 cudaError_t launch_merge(const MergeParams& mp, cudaStream_t stream) {
   const int warps = mp.nb * mp.Hq;
   if (warps <= kFewMergeRows)
-    lse_merge_kernel<D, 8><<<(warps + 7) / 8, 256, 0, stream>>>(mp);
+    lse_merge_kernel<D, 16><<<(warps + 7) / 8, 256, 0, stream>>>(mp);
   else
     lse_merge_kernel<D, 1><<<(warps + 7) / 8, 256, 0, stream>>>(mp);
   return cudaGetLastError();

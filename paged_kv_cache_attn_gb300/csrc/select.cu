@@ -126,16 +126,22 @@ __device__ __forceinline__ void tile_bounds(const BoundsParams& p, int64_t tile,
       }
     }
   }
+  // Joined over the rows' lanes, each step leaving a lane half of its pairs: those of
+  // its chunk from pair `at` on.
+  int at = 0;
 #pragma unroll
-  for (int o = kChunks; o < 32; o <<= 1) {
+  for (int o = kChunks, n = kPairs / 2; o < 32; o <<= 1, n >>= 1) {
+    const bool up = lane & o;
 #pragma unroll
-    for (int k = 0; k < kPairs; ++k) {
-      const uint32_t a = __shfl_xor_sync(0xffffffffu, lo[k], o);
-      const uint32_t b = __shfl_xor_sync(0xffffffffu, hi[k], o);
-      lo[k] = E4M3 ? min2h(lo[k], a) : min2(lo[k], a);
-      hi[k] = E4M3 ? max2h(hi[k], b) : max2(hi[k], b);
+    for (int k = 0; k < n; ++k) {
+      const uint32_t a = __shfl_xor_sync(0xffffffffu, up ? lo[k] : lo[k + n], o);
+      const uint32_t b = __shfl_xor_sync(0xffffffffu, up ? hi[k] : hi[k + n], o);
+      lo[k] = E4M3 ? min2h(up ? lo[k + n] : lo[k], a) : min2(up ? lo[k + n] : lo[k], a);
+      hi[k] = E4M3 ? max2h(up ? hi[k + n] : hi[k], b) : max2(up ? hi[k + n] : hi[k], b);
     }
+    at += up ? n : 0;
   }
+  constexpr int kLeft = kPairs / kRows;
   auto value = [&](uint32_t w, int half) {
     if (E4M3) {
       const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w));
@@ -146,40 +152,35 @@ __device__ __forceinline__ void tile_bounds(const BoundsParams& p, int64_t tile,
   float amax = 0.f;
   bool odd = false;
 #pragma unroll
-  for (int k = 0; k < kPairs; ++k)
+  for (int k = 0; k < kLeft; ++k)
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
       const float a = fabsf(value(lo[k], z)), b = fabsf(value(hi[k], z));
       odd |= !(a < INFINITY) || !(b < INFINITY);
       amax = fmaxf(amax, fmaxf(a, b));
     }
-#pragma unroll
-  for (int o = 1; o < kChunks; o <<= 1)
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  // (Not negative: ordered as whole numbers.)
+  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
   odd = __any_sync(0xffffffffu, odd);
   const int e = bound_exponent(amax);
   const float inv = pow2f(-e);
-  // The first lanes of a row's chunks write the least, the next the largest.
-  const bool upper = r0 == 1;
-  uint32_t out[kPer / 4];
+  uint32_t out[2] = {0, 0};
 #pragma unroll
-  for (int k = 0; k < kPer / 4; ++k) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int z = 0; z < 4; ++z) {
-      const float v = value((upper ? hi : lo)[2 * k + z / 2], z & 1) * inv;
-      float n = upper ? ceilf(v) : floorf(v);
-      n = odd ? 0.f : fminf(fmaxf(n, -127.f), 127.f);
-      w |= (uint32_t)((int)n & 0xff) << (8 * z);
-    }
-    out[k] = w;
+  for (int k = 0; k < 2 * kLeft; ++k) {
+    const float l = fmaxf(floorf(value(lo[k / 2], k & 1) * inv), -127.f);
+    const float u = fminf(ceilf(value(hi[k / 2], k & 1) * inv), 127.f);
+    // (Above -127 and below 127 too, where keys are beyond the exponents.)
+    out[0] |= (uint32_t)((int)fminf(l, 127.f) & 0xff) << (8 * k);
+    out[1] |= (uint32_t)((int)fmaxf(u, -127.f) & 0xff) << (8 * k);
   }
-  if (r0 < 2) {
-    int8_t* dst = p.bounds + tile * (2 * D) + r0 * D + c * kPer;
-    if constexpr (E4M3)
-      *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+  if (odd) out[0] = out[1] = 0;
+  int8_t* dst = p.bounds + tile * (2 * D) + c * kPer + 2 * at;
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    if constexpr (kLeft == 2)
+      *reinterpret_cast<uint32_t*>(dst + z * D) = out[z];
     else
-      *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+      *reinterpret_cast<uint16_t*>(dst + z * D) = (uint16_t)out[z];
   }
   // A block with a value that is not finite has a score above all others.
   if (lane == 0) p.bound_scales[tile] = odd ? INFINITY : pow2f(e);
@@ -273,8 +274,6 @@ __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
 }
 
 constexpr int kWarps = 8;
-constexpr int kWarpBlocks = 32;                       // blocks a warp scores
-constexpr int kCtaBlocks = kWarps * kWarpBlocks;
 
 // A query head as whole numbers of at most 127 times a power of two, by one warp: its
 // f16 values to dst, the power returned (-1: no such head, all zeros).
@@ -303,15 +302,17 @@ __device__ __forceinline__ float quantise(const __nv_bfloat16* src, bool there,
   return there ? (odd ? 0.f : pow2f(e)) : -1.f;
 }
 
-// grid (block ranges, Hkv, nb).  Up to 16 heads are the rows of the products, eight
-// blocks their columns; lane 4 n + t has bytes [16 t + 64 j, + 16) of block n's record,
-// which are its columns of four products in any order that the queries' fragments
-// share.  A warp has 16 blocks' records in flight at a time (4 KB at D = 128), asked
-// for before the queries are quantised.  kFew: at most 8 heads, kept in registers (the
-// rows after them are zeros); else 16 at a time from shared memory.
-template <int D, bool kFew>
+// grid (block ranges, Hkv, nb); a warp has kSteps x 16 consecutive blocks.  Up to 16
+// heads are the rows of the products, eight blocks their columns; lane 4 n + t has
+// bytes [16 t + 64 j, + 16) of block n's record, which are its columns of four products
+// in any order that the queries' fragments share.  The records of 16 blocks (4 KB at
+// D = 128) are in flight while those before are used, the first while the queries are
+// quantised.  kFew: at most 8 heads, kept in registers (the rows after them are zeros);
+// else 16 at a time from shared memory.
+template <int D, bool kFew, int kSteps>
 __global__ void __launch_bounds__(256, kFew ? 2 : 1)
     score_kernel(const SelectParams p) {
+  constexpr int kWarpBlocks = 16 * kSteps, kCtaBlocks = kWarps * kWarpBlocks;
   constexpr int kRow = D + 8;  // a head's f16 values in shared memory
   __shared__ __align__(16) __half qs[(kFew ? 8 : kMaxG) * kRow];
   __shared__ float qe[kFew ? 8 : kMaxG];
@@ -326,25 +327,33 @@ __global__ void __launch_bounds__(256, kFew ? 2 : 1)
   const int blk0 = blockIdx.x * kCtaBlocks + warp * kWarpBlocks;
   const int32_t* table = p.tables + (int64_t)b * p.max_blocks;
   // A block id outside the pool (recorded by the next kernel) has no score.
-  int phys = -1;
-  if (blk0 + lane < nblk) phys = table[blk0 + lane];
-  if (phys >= p.num_blocks) phys = -1;
+  constexpr int kIds = (kSteps + 1) / 2;
+  int phys[kIds];
+#pragma unroll
+  for (int i = 0; i < kIds; ++i) {
+    phys[i] = -1;
+    if (blk0 + i * 32 + lane < nblk) phys[i] = table[blk0 + i * 32 + lane];
+    if (phys[i] >= p.num_blocks) phys[i] = -1;
+  }
   const int n = lane >> 2, t = lane & 3;
   constexpr int kJ = 2 * D / 64;  // 64-byte parts of a record
-  uint4 rec[2][kJ];
-  auto fetch = [&](int half) {
+  uint4 rec[2][2][kJ];
+  auto fetch = [&](int step) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int ph = __shfl_sync(0xffffffffu, phys, half * 16 + i * 8 + n);
+      const int ph =
+          __shfl_sync(0xffffffffu, phys[step / 2], (step & 1) * 16 + i * 8 + n);
       const uint4* src = reinterpret_cast<const uint4*>(
           p.bounds + ((int64_t)max(ph, 0) * p.Hkv + h) * (2 * D));
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) rec[i][j] = src[j * 4 + t];
+      for (int j = 0; j < kJ; ++j) rec[step & 1][i][j] = src[j * 4 + t];
     }
   };
   fetch(0);
-  const float my_scale =
-      phys >= 0 ? p.bound_scales[(int64_t)phys * p.Hkv + h] : 0.f;
+  float scales[kIds];
+#pragma unroll
+  for (int i = 0; i < kIds; ++i)
+    scales[i] = phys[i] >= 0 ? p.bound_scales[(int64_t)phys[i] * p.Hkv + h] : 0.f;
   const int G = p.G, rows = kFew ? 8 : (G + 15) & ~15;
   for (int g = warp; g < rows; g += kWarps) {
     const float e = quantise<D>(
@@ -371,12 +380,10 @@ __global__ void __launch_bounds__(256, kFew ? 2 : 1)
     for (int j = 0; j < kJ; ++j) fragment(n, j, few[j]);
   }
   float* dst = p.scores + ((int64_t)b * p.Hkv + h) * p.stride;
-#pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-    if (half > 0) {
-      if (blk0 + 16 >= nblk) break;
-      fetch(1);
-    }
+#pragma unroll
+  for (int step = 0; step < kSteps; ++step) {
+    if (blk0 + step * 16 >= nblk) break;
+    if (step + 1 < kSteps) fetch(step + 1);
     float best[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) best[i][0] = best[i][1] = -INFINITY;
@@ -392,7 +399,8 @@ __global__ void __launch_bounds__(256, kFew ? 2 : 1)
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t w[4] = {rec[i][j].x, rec[i][j].y, rec[i][j].z, rec[i][j].w};
+          const uint4 x = rec[step & 1][i][j];
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             uint32_t b0, b1;
@@ -423,8 +431,8 @@ __global__ void __launch_bounds__(256, kFew ? 2 : 1)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)
           s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
-        const int at = half * 16 + i * 8 + 2 * t + z;
-        const float sc = __shfl_sync(0xffffffffu, my_scale, at);
+        const int at = step * 16 + i * 8 + 2 * t + z;
+        const float sc = __shfl_sync(0xffffffffu, scales[step / 2], at & 31);
         // (+ 0 makes a zero positive.)
         if (n == 0 && blk0 + at < nblk)
           dst[blk0 + at] = sc == INFINITY ? INFINITY : s * sc + 0.f;
@@ -483,20 +491,25 @@ __global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
     sh_lo = 0xffffffffu;
     sh_hi = 0;
   }
+  // This thread's blocks' ids, of the first 8 T (older than the kernel before).
+  int ids[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ids[i] = 8 * tid + i < nblk ? table[8 * tid + i] : 0;
   // Scores, and a cleared status word.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (bad && tid == 0) record_status(p.status, KV_ERR_DEVICE, L);
-  if (h == 0)
-    for (int i = tid; i < nblk; i += T) {
-      const int phys = table[i];
-      if (phys < 0 || phys >= p.num_blocks)
-        record_status(p.status, KV_ERR_DEVICE, phys);
-    }
-  auto put = [&](int at, int blk) {
-    const int phys = table[blk];
+  auto check = [&](int phys) {
     const bool in = phys >= 0 && phys < p.num_blocks;
+    if (!in && h == 0) record_status(p.status, KV_ERR_DEVICE, phys);
+    return in;
+  };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (!check(ids[i])) ids[i] = -1;
+  }
+  auto put_id = [&](int at, int blk, int phys) {
     if (sel) sel[at] = blk;
-    out[at] = in ? (int)(phys * (int64_t)p.Hkv + h) : -1;
+    out[at] = phys >= 0 ? (int)(phys * (int64_t)p.Hkv + h) : -1;
   };
   if (tid == 0)
     p.sel_lens[row] = count > 0 ? 16 * (count - 1) + (L - 16 * (nblk - 1)) : 0;
@@ -504,8 +517,26 @@ __global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
     if (sel) sel[i] = -1;
     out[i] = -1;
   }
+  auto load_ids = [&](int base, int (&id)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = base + 8 * tid + i;
+      id[i] = at < nblk ? table[at] : 0;
+      if (!check(id[i])) id[i] = -1;
+    }
+  };
   if (nblk <= p.n_sel) {
-    for (int i = tid; i < nblk; i += T) put(i, i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (8 * tid + i < nblk) put_id(8 * tid + i, 8 * tid + i, ids[i]);
+    for (int base = 8 * T; base < nblk; base += 8 * T) {
+      load_ids(base, ids);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = base + 8 * tid + i;
+        if (at < nblk) put_id(at, at, ids[i]);
+      }
+    }
     return;
   }
   const float* scores = p.scores + (int64_t)row * p.stride;
@@ -599,7 +630,7 @@ __global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
   }
   // Blocks above the range, and of the range's all or the first `left`.
   uint32_t n_above = 0, n_equal = 0;  // before this thread's
-  auto place = [&](const uint32_t (&k)[8], int base) {
+  auto place = [&](const uint32_t (&k)[8], const int (&id)[8], int base) {
     uint32_t mine = 0;  // blocks taken, and of the range (in the upper half)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -615,10 +646,10 @@ __global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
       const bool in = k[i] >= lo && k[i] <= hi && k[i] != 0xffffffffu;
       const bool up = k[i] > hi || k[i] == 0xffffffffu || (in && whole);
       if (up) {
-        put((int)(a + min(e, left)), base + 8 * tid + i);
+        put_id((int)(a + min(e, left)), base + 8 * tid + i, id[i]);
         ++a;
       } else if (in) {
-        if (e < left) put((int)(a + e), base + 8 * tid + i);
+        if (e < left) put_id((int)(a + e), base + 8 * tid + i, id[i]);
         ++e;
       }
     }
@@ -633,11 +664,12 @@ __global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
     n_equal = sh_hi;
   };
   if (whole) left = 0;
-  place(first, 0);
+  place(first, ids, 0);
   for (int base = 8 * T; base < nblk; base += 8 * T) {
     uint32_t k[8];
     load(base, k);
-    place(k, base);
+    load_ids(base, ids);
+    place(k, ids, base);
   }
 }
 
@@ -646,6 +678,25 @@ __global__ void clear_kernel(DeviceStatus* status) {
 }
 
 // ---- host side --------------------------------------------------------------------
+
+// Longer runs of blocks a warp where there are still two rounds of CTAs (two run at
+// once on an SM).
+template <int D>
+void launch_scores(const SelectParams& p, cudaStream_t st) {
+  const int64_t ctas = (int64_t)((p.max_blocks + 511) / 512) * p.Hkv * p.nb;
+  const int steps = ctas >= 2 * 2 * 152 ? 4 : 2;
+  const int blocks = kWarps * 16 * steps;
+  const dim3 grid((unsigned)((p.max_blocks + blocks - 1) / blocks), (unsigned)p.Hkv,
+                  (unsigned)p.nb);
+  if (p.G <= 8 && steps == 4)
+    score_kernel<D, true, 4><<<grid, 256, 0, st>>>(p);
+  else if (p.G <= 8)
+    score_kernel<D, true, 2><<<grid, 256, 0, st>>>(p);
+  else if (steps == 4)
+    score_kernel<D, false, 4><<<grid, 256, 0, st>>>(p);
+  else
+    score_kernel<D, false, 2><<<grid, 256, 0, st>>>(p);
+}
 
 int score_stride(int max_blocks) { return (max_blocks + 31) & ~31; }
 
@@ -866,16 +917,10 @@ extern "C" kv_status paged_select_blocks(
   p.n_first = n_first;
   p.n_last = n_last;
   if (max_blocks > n_sel) {
-    const dim3 grid((unsigned)((max_blocks + S::kCtaBlocks - 1) / S::kCtaBlocks),
-                    (unsigned)Hkv, (unsigned)nb);
-    if (head_dim == 128 && p.G <= 8)
-      S::score_kernel<128, true><<<grid, 256, 0, st>>>(p);
-    else if (head_dim == 128)
-      S::score_kernel<128, false><<<grid, 256, 0, st>>>(p);
-    else if (p.G <= 8)
-      S::score_kernel<64, true><<<grid, 256, 0, st>>>(p);
+    if (head_dim == 128)
+      S::launch_scores<128>(p, st);
     else
-      S::score_kernel<64, false><<<grid, 256, 0, st>>>(p);
+      S::launch_scores<64>(p, st);
   } else {
     S::clear_kernel<<<1, 32, 0, st>>>(p.status);
   }
