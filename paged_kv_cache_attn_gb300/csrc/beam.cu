@@ -4,21 +4,26 @@
 // ties to the lower beam, then the lower token.  Bound by the logits' bytes: they are
 // read once.
 //
-// First kernel: a CTA has a piece of one beam's logits in registers.  Its maximum and
-// its sum of exponentials go out, and its n highest logits (of one beam the order of
-// y is that of x): the n-th highest of the threads' maxima bounds them from below, is
-// found to within a few by bisection over counts, and leaves a few candidates, which
-// are ranked against each other.  Second kernel: a CTA per group joins the sums in
-// 64 bits and picks the n highest y of the pieces' candidates the same way.
+// First kernel: a CTA streams a piece of one beam's logits through registers, a step of
+// up to 4096 at a time, and each thread adds up exponentials.
+// Of one beam the order of y is that of x: the CTA keeps candidates for the n highest
+// logits, and of what comes in only logits above a bar that n of those before reach.
+// The bar is taken from the threads' maxima of a step (a value that at least n of them
+// reach, and not many more, by bisection over counts).  Nearly all of a row lies below
+// it and costs no more than its sum and one barrier a step.  Second kernel: a CTA per
+// group joins the sums in 64 bits and picks the n highest y of the pieces' candidates.
 //
-// y is computed in 64 bits from fp32 sums of exponentials (a thread's 8 or 32 of
-// them; across threads and pieces in 64 bits), about 1e-7 from exact, so that beams
-// are hardly ever ordered otherwise than exactly.
+// y is computed in 64 bits from sums of at most 16 exponentials in fp32 (added up with
+// what each addition rounds off, and across threads in 64 bits: 64-bit operations are
+// issued one lane pair a cycle here, and an addition a thread and step bounded the
+// kernel), about 1e-7 from exact, so that beams are hardly ever ordered otherwise than
+// exactly.
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
-#include "device_common.cuh"
+#include "prefill.cuh"
 #include "tensor_map.h"
 
 namespace pkv {
@@ -27,7 +32,10 @@ namespace beam {
 constexpr int kThreads = 256;
 constexpr int kMaxOut = 128;
 constexpr int kMaxBeams = 1024;
-constexpr int kCand = 1024;  // candidates in shared memory; more: one at a time
+constexpr int kRound = 4 * 152;                   // CTAs of the first kernel at once
+constexpr int kMaxParts = 3 * kRound;             // beams x pieces of a group
+constexpr int kCand = 768;   // candidates in shared memory; more: one at a time
+constexpr float kHeadroom = 40.f;  // of logits above the reference of a sum
 
 struct Stat {
   double sum;  // of exponentials of logits less `top`
@@ -62,7 +70,6 @@ __device__ __forceinline__ uint64_t ordered(double x) {
 }
 
 constexpr uint32_t kNone32 = 0x007fffffu;  // ordered(-inf): no candidate
-constexpr uint64_t kNone64 = 0x000fffffffffffffull;
 
 // A value that at least n threads' `mine` reach, and not many more; `floor` (the
 // least a candidate has) where fewer do.  All threads call it; `lo` and `hi`: the
@@ -114,203 +121,488 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) {
   return __bfloat162float(x);
 }
 
-// E: logits of a thread.
+// The n highest of c <= kCand keys to best, in order (0 where there are fewer).  Of
+// many, a bar that n of the threads' highest keys reach leaves few to be ranked.  `floor`: a logit
+// that all of them reach.
+__device__ __forceinline__ void pick_best(const uint64_t* cand, int c, int n, float floor,
+                                          uint64_t* few, uint64_t* best, uint32_t* sh,
+                                          int* count) {
+  const int tid = threadIdx.x;
+  const uint64_t* from = cand;
+  int k = c;
+  if (c > kThreads) {
+    uint64_t own[kCand / kThreads], top = 0;
+#pragma unroll
+    for (int i = 0; i < kCand / kThreads; ++i) {
+      const int at = tid + i * kThreads;
+      own[i] = at < c ? cand[at] : 0;
+      top = max(top, own[i]);
+    }
+    const uint32_t mine = (uint32_t)(top >> 32);
+    uint32_t lo, hi;
+    range(mine, sh, lo, hi);
+    const uint32_t bar =
+        threshold(mine, lo, hi, max(ordered(floor), kNone32 + 1), n);
+    if (tid == 0) *count = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kCand / kThreads; ++i)
+      if ((uint32_t)(own[i] >> 32) >= bar) few[atomicAdd(count, 1)] = own[i];
+    __syncthreads();
+    from = few;
+    k = *count;
+  }
+  for (int i = tid; i < n; i += kThreads) best[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < k; i += kThreads) {
+    const uint64_t a = from[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < k; ++j) rank += from[j] > a;
+    if (rank < n) best[rank] = a;
+  }
+  __syncthreads();
+}
+
+// e^x in 64 bits for x <= 0: x / ln 2 split into a whole number and at most half of one
+// either way, its Taylor series to the 11th power (2e-14 relative).  Few operations:
+// 64-bit ones are issued one lane pair a cycle here, and this kernel waits for each.
+__device__ __forceinline__ double exp_of(double x) {
+  x = fmax(x, -700.);
+  const double k = rint(x * 1.4426950408889634);
+  const double r = fma(k, -0.6931471805599453, x);
+  double y = 1. / 39916800.;
+#pragma unroll
+  for (int i = 10; i >= 0; --i) {
+    constexpr double inv[11] = {1., 1., 1. / 2, 1. / 6, 1. / 24, 1. / 120, 1. / 720,
+                                1. / 5040, 1. / 40320, 1. / 362880, 1. / 3628800};
+    y = fma(y, r, inv[i]);
+  }
+  return y * __longlong_as_double((long long)((int)k + 1023) << 52);
+}
+
+// log s in 64 bits, from the 32-bit one by a Newton step (and the next term):
+// log s = y + log(s e^-y).  s >= 1e-30.
+__device__ __forceinline__ double log_of(double s) {
+  // s = f 2^k, so that the exponential's argument is small.
+  const long long bits = __double_as_longlong(s);
+  const int k = (int)(bits >> 52) - 1023;
+  const double f = __longlong_as_double((bits & 0xfffffffffffffll) | 1023ll << 52);
+  const float y = logf((float)f);  // in [0, ln 2]
+  const double d = fma(f, exp_of(-(double)y), -1.);
+  return fma((double)k, 0.6931471805599453, (double)y + fma(-.5 * d, d, d));
+}
+
+// E: logits of a thread in a step.
 template <typename T, int E>
-__global__ void __launch_bounds__(kThreads) piece_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) piece_kernel(const Params p) {
   constexpr int VE = 16 / sizeof(T), NV = E / VE;
-  __shared__ uint64_t cand[kCand];
+  __shared__ uint64_t cand[kCand], few[kCand], best[kMaxOut];
   __shared__ uint32_t sh[64];
   __shared__ double sums[kThreads / 32];
-  __shared__ int count;
+  __shared__ int count, few_count;
   __shared__ unsigned long long top;
-  const int row = blockIdx.y, piece = blockIdx.x, tid = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int row = blockIdx.y, piece = blockIdx.x, tid = threadIdx.x, n = p.n;
   if (!(p.scores[row] > -INFINITY)) return;  // no beam
   const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
   // Vectors start on 16-byte borders, the first at or before the row's start.
   const int off = (int)((uintptr_t)x % 16 / sizeof(T));
-  const int64_t v0 = (int64_t)piece * (kThreads * NV) + tid;
-  float f[NV][VE];
+  const int64_t vectors = ((int64_t)p.vocab + off + VE - 1) / VE;
+  const int64_t v_begin = vectors * piece / p.pieces;
+  const int64_t v_end = vectors * (piece + 1) / p.pieces;
+  if (tid == 0) count = 0;
+  __syncthreads();
+  // The sum so far of exponentials of logits less m, the first step's maximum.  It
+  // moves, in a thread alone, only where a logit lies far above it.
+  float m = -INFINITY, ref = -INFINITY;
+  float sum_hi = 0.f, sum_lo = 0.f;  // the sum and what its additions have rounded off
+  float bar = -INFINITY;  // what comes in is a candidate above it
+  int bound = 0;          // candidates at most
+  int fresh = 0;          // threads that have brought some since the bar rose
+  bool picked = false;    // `best` holds the n highest of them
+  // Each thread's vectors of the next two steps are on their way to its own places in
+  // shared memory (32 KB a CTA, 128 KB an SM: with one step in registers the loads'
+  // latency, 1.9 us under load, kept an SM at 29 GB/s).  Vectors that reach over the
+  // row's ends are read value by value.
+  extern __shared__ __align__(16) uint4 ring[];  // [2][NV][kThreads]
+  auto inside = [&](int64_t v) {
+    const int64_t e = v * VE - off;
+    return v < v_end && e >= 0 && e + VE <= p.vocab;
+  };
+  constexpr int kStep = kThreads * NV;
+  // Nothing of a step reaches over the row's or the piece's ends.
+  auto whole = [&](int64_t step) {
+    return step * VE >= off && step + kStep <= v_end &&
+           (step + kStep) * VE - off <= p.vocab;
+  };
+  const uint32_t mine_at = smem_u32(ring + tid);
+  constexpr int kPlace = kThreads * 16;  // bytes between a thread's vectors
+  auto copy = [&](uint32_t dst, const T* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src)
+                 : "memory");
+  };
+  auto issue = [&](int64_t step, int slot) {
+    const uint32_t dst = mine_at + slot * (NV * kPlace);
+    const T* src = x + ((step + tid) * VE - off);
+    if (whole(step)) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t e = (v0 + (int64_t)i * kThreads) * VE - off;
-    if (e >= 0 && e + VE <= p.vocab) {
-      const uint4 raw = __ldcs(reinterpret_cast<const uint4*>(x + e));
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-      for (int k = 0; k < VE; ++k) {
-        if (sizeof(T) == 4)
-          f[i][k] = __uint_as_float(w[k % 4]);
-        else
-          f[i][k] = __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
-      }
+      for (int i = 0; i < NV; ++i) copy(dst + i * kPlace, src + i * (kThreads * VE));
     } else {
 #pragma unroll
-      for (int k = 0; k < VE; ++k)
-        f[i][k] = e + k >= 0 && e + k < p.vocab ? to_float(x[e + k]) : -INFINITY;
+      for (int i = 0; i < NV; ++i)
+        if (inside(step + tid + i * kThreads))
+          copy(dst + i * kPlace, src + i * (kThreads * VE));
     }
-  }
-  float m = -INFINITY;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto fetch = [&](float (&f)[NV][VE], int64_t step, int slot) {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const uint32_t src = mine_at + slot * (NV * kPlace);
+    const bool all = whole(step);
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      if (all || inside(step + tid + i * kThreads)) {
+        const uint4 raw = lds128(src + i * kPlace);
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-    for (int k = 0; k < VE; ++k) {
-      f[i][k] = fmaxf(f[i][k], -INFINITY);  // NaN counts as -inf
-      m = fmaxf(m, f[i][k]);
+        for (int k = 0; k < VE; ++k) {
+          if (sizeof(T) == 4)
+            f[i][k] = __uint_as_float(w[k % 4]);
+          else
+            f[i][k] = __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+        }
+      } else {
+        const int64_t v = step + tid + i * kThreads, e = v * VE - off;
+#pragma unroll
+        for (int k = 0; k < VE; ++k)
+          f[i][k] = v < v_end && e + k >= 0 && e + k < p.vocab ? to_float(x[e + k])
+                                                              : -INFINITY;
+      }
     }
-  const uint32_t mine = ordered(m);
-  uint32_t lo, hi;
-  range(mine, sh, lo, hi);
-  const float top_x = unordered(hi);
-  float s = 0.f;
-  if (top_x > -INFINITY) {
+  };
+  auto process = [&](float (&f)[NV][VE], int64_t step, int slot) {
+    const int64_t v0 = step + tid;
+    float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < VE; ++k) s += ex2((f[i][k] - top_x) * 1.4426950408889634f);
-  }
-  double sum = s;
+      for (int k = 0; k < VE; ++k) {
+        mx = fmaxf(mx, f[i][k]);  // (passes over NaN)
+      }
+    // (This step's values are in registers: its place is free.)
+    const int over = __syncthreads_count(mx > bar);
+    issue(step + 2 * kStep, slot);
+    uint32_t lo = 0, hi = 0;  // least and largest of the threads' maxima
+    // (Of a first step with logits m is -inf in every thread.)
+    if (over > n || (over > 0 && bar == -INFINITY)) {
+      range(ordered(mx), sh, lo, hi);
+      if (m == -INFINITY) m = ref = unordered(hi);
+    }
+    if (mx > m + kHeadroom) {
+      const double y = ((double)sum_hi + sum_lo) * exp_of((double)m - mx);
+      sum_hi = (float)y;
+      sum_lo = (float)(y - sum_hi);
+      m = mx;
+    }
+    if (m > -INFINITY) {
+      // Two at a time; where one is not a number, again without it.
+      const uint64_t neg = tc::pack2(-m, -m);
+      const uint64_t scale = tc::pack2(1.4426950408889634f, 1.4426950408889634f);
+      uint64_t s2 = 0;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((tid & 31) == 0) sums[tid >> 5] = sum;
-  if (tid == 0) count = 0;
-  const int n = p.n;
-  const uint32_t bar = threshold(mine, lo, hi, kNone32 + 1, n);
-  const int64_t slot = (int64_t)row * p.pieces + piece;
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < VE; k += 2) {
+          float y, z;
+          tc::unpack2(tc::fma2(tc::add2(tc::pack2(f[i][k], f[i][k + 1]), neg), scale, 0),
+                      y, z);
+          s2 = tc::add2(s2, tc::pack2(ex2(y), ex2(z)));
+        }
+      float y, z;
+      tc::unpack2(s2, y, z);
+      float s = y + z;
+      if (s != s) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int k = 0; k < VE; ++k) {
+            if (f[i][k] != f[i][k]) f[i][k] = -INFINITY;
+            s += ex2((f[i][k] - m) * 1.4426950408889634f);
+          }
+      }
+      const float to = sum_hi + s, part = to - sum_hi;
+      sum_lo += (sum_hi - (to - part)) + (s - part);
+      sum_hi = to;
+    }
+    if (over == 0) return;
+    // Candidates: above the bar; where more than n threads have some, from a value
+    // on that n of them reach, which is a bar for what comes later.
+    float from = bar;
+    bool equal = false;
+    int before = 0;
+    fresh += over;
+    picked = false;
+    const bool many = fresh > n || bound + over * E > kCand;
+    if (many) {
+      if (over > n) {
+        from = unordered(threshold(ordered(mx), lo, hi, ordered(bar) + 1, n));
+        equal = true;
+      }
+      __syncthreads();
+      before = count;
+      __syncthreads();
+    }
+    // Higher logits first, then lower tokens.
+    auto key = [&](int i, int k) {
+      const uint32_t token = (uint32_t)((v0 + i * kThreads) * VE - off + k);
+      return (uint64_t)ordered(f[i][k]) << 32 | (0xffffffffu - token);
+    };
+    // Few lanes have any, and those one, as a rule: which, without branches, then
+    // theirs alone.
+    if (mx > from || (equal && mx == from)) {
+      uint32_t mask = 0;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const float y = f[j / VE][j % VE];
+        mask |= (y > from || (equal && y == from) ? 1u : 0u) << j;
+      }
+      while (mask) {
+        const int j = __ffs(mask) - 1;
+        mask &= mask - 1;
+        float y = f[0][0];
+#pragma unroll
+        for (int k = 1; k < E; ++k) y = j == k ? f[k / VE][k % VE] : y;
+        const uint32_t token =
+            (uint32_t)((v0 + j / VE * kThreads) * VE - off + j % VE);
+        const int at = atomicAdd(&count, 1);
+        if (at < kCand) cand[at] = (uint64_t)ordered(y) << 32 | (0xffffffffu - token);
+      }
+    }
+    bound += over * E;
+    if (equal) bar = from;
+    if (!many) return;
+    __syncthreads();
+    int c = count;
+    __syncthreads();
+    if (c > kCand) {
+      // Many equal logits: the n highest of this step one at a time, behind the
+      // candidates there were, or the n highest of those (there are more than n).
+      if (before + n > kCand) {
+        pick_best(cand, before, n, bar, few, best, sh, &few_count);
+        for (int i = tid; i < n; i += kThreads) cand[i] = best[i];
+        before = n;
+        __syncthreads();
+      }
+      uint64_t last = ~0ull;
+      for (int r = 0; r < n; ++r) {
+        uint64_t most = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int k = 0; k < VE; ++k) {
+            const uint64_t a = key(i, k);
+            if (a < last && a > most) most = a;
+          }
+        if (tid == 0) top = 0;
+        __syncthreads();
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+          most = max(most, (uint64_t)__shfl_xor_sync(0xffffffffu, most, o));
+        if ((tid & 31) == 0) atomicMax(&top, (unsigned long long)most);
+        __syncthreads();
+        last = top;
+        if (tid == 0) cand[before + r] = last;
+        __syncthreads();
+      }
+      c = before + n;
+    }
+    if (c > n) {
+      // The n highest so far: the lowest of them is the bar.
+      pick_best(cand, c, n, bar, few, best, sh, &few_count);
+      for (int i = tid; i < n; i += kThreads) cand[i] = best[i];
+      bar = fmaxf(bar, unordered((uint32_t)(best[n - 1] >> 32)));
+      c = n;
+      picked = true;
+    }
+    __syncthreads();
+    if (tid == 0) count = c;
+    bound = c;
+    fresh = 0;
+    __syncthreads();
+  };
+  issue(v_begin, 0);
+  issue(v_begin + kStep, 1);
+  int slot = 0;
+  for (int64_t step = v_begin; step < v_end; step += kStep, slot ^= 1) {
+    float f[NV][VE];
+    fetch(f, step, slot);
+    process(f, step, slot);
+  }
+  // Threads that have moved their reference (rare): back to a common one.
+  if (__syncthreads_or(m != ref)) {
+    uint32_t lo, hi;
+    range(ordered(m), sh, lo, hi);
+    ref = unordered(hi);
+    const double y =
+        m > -INFINITY ? ((double)sum_hi + sum_lo) * exp_of((double)m - ref) : 0.;
+    sum_hi = (float)y;
+    sum_lo = (float)(y - sum_hi);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, sum_hi, o);
+    sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, o);
+    // (The larger first.)
+    const float a = fmaxf(sum_hi, y), b = fminf(sum_hi, y);
+    sum_hi = a + b;
+    sum_lo += b - (sum_hi - a);
+  }
+  if ((tid & 31) == 0) sums[tid >> 5] = (double)sum_hi + sum_lo;
+  __syncthreads();
+  const int64_t at = (int64_t)row * p.pieces + piece;
   if (tid == 0) {
     double all = 0;
     for (int w = 0; w < kThreads / 32; ++w) all += sums[w];
-    p.stats[slot] = Stat{all, top_x, 0.f};
+    p.stats[at] = Stat{all, ref, 0.f};
   }
-  auto token = [&](int i, int k) {
-    return (uint32_t)((v0 + (int64_t)i * kThreads) * VE - off + k);
-  };
-  // Higher logits first, then lower tokens.
-  auto key = [&](int i, int k) {
-    return (uint64_t)ordered(f[i][k]) << 32 | (0xffffffffu - token(i, k));
-  };
-  if (mine >= bar) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < VE; ++k)
-        if (ordered(f[i][k]) >= bar) {
-          const int at = atomicAdd(&count, 1);
-          if (at < kCand) cand[at] = key(i, k);
-        }
-  }
-  __syncthreads();
-  const int c = count;
-  uint2* out = p.entries + slot * n;
-  if (c <= kCand) {
-    for (int i = tid; i < c; i += kThreads) {
-      const uint64_t a = cand[i];
-      int rank = 0;
-      for (int j = 0; j < c; ++j) rank += cand[j] > a;
-      if (rank < n) out[rank] = make_uint2((uint32_t)(a >> 32), ~(uint32_t)a);
-    }
-    for (int i = c + tid; i < n; i += kThreads) out[i] = make_uint2(0, 0);
-    return;
-  }
-  // Many equal logits: one at a time (c > n of them).
-  uint64_t last = ~0ull;
-  for (int r = 0; r < n; ++r) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < VE; ++k) {
-        const uint64_t a = key(i, k);
-        if (a < last && a > best) best = a;
-      }
-    if (tid == 0) top = 0;
-    __syncthreads();
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-      best = max(best, (uint64_t)__shfl_xor_sync(0xffffffffu, best, o));
-    if ((tid & 31) == 0) atomicMax(&top, (unsigned long long)best);
-    __syncthreads();
-    last = top;
-    if (tid == 0) out[r] = make_uint2((uint32_t)(last >> 32), ~(uint32_t)last);
-    __syncthreads();
-  }
+  // (Picked already where nothing came after.)
+  if (!picked) pick_best(cand, count, n, bar, few, best, sh, &few_count);
+  uint2* out = p.entries + at * n;
+  for (int i = tid; i < n; i += kThreads)
+    out[i] = best[i] ? make_uint2((uint32_t)(best[i] >> 32), ~(uint32_t)best[i])
+                     : make_uint2(0, 0);
 }
 
 struct Cand {
-  uint64_t y;    // ordered
-  int64_t flat;  // beam x vocab + token
+  uint64_t y;   // ordered
+  uint64_t at;  // beam, and token in the lower half
 };
 
+__device__ __forceinline__ double value_of(uint64_t y) {
+  return __longlong_as_double(
+      (long long)(y & 0x8000000000000000ull ? y ^ 0x8000000000000000ull : ~y));
+}
+
 __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
-  return a.y > b.y || (a.y == b.y && a.flat < b.flat);
+  return a.y > b.y || (a.y == b.y && a.at < b.at);
 }
 
 __global__ void __launch_bounds__(kThreads) group_kernel(const Params p) {
   __shared__ Cand cand[kCand];
+  __shared__ int which[kCand];
   // log sum exp(x - top), NaN: no continuations.  Kept apart from the highest logit,
   // so that logits of any size cancel before the score is added.
-  __shared__ double log_sum[kMaxBeams];
-  __shared__ float top[kMaxBeams];
-  __shared__ uint64_t sh[64];
+  __shared__ double log_sum[kMaxBeams], parts[kMaxParts];
+  __shared__ uint32_t top[kMaxBeams];  // highest logit, ordered
+  __shared__ uint32_t largest;  // |score| + |log sum| of the beams, at most
+  __shared__ uint32_t sh[64];
   __shared__ Cand best_of[kThreads / 32];
   __shared__ int count;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int group = blockIdx.x, tid = threadIdx.x, lane = tid & 31, n = p.n;
-  for (int b = tid >> 5; b < p.beams; b += kThreads / 32) {
-    const int64_t row = (int64_t)group * p.beams + b;
-    const float score = p.scores[row];
-    double out = NAN;
-    if (score > -INFINITY) {
-      const Stat* st = p.stats + row * p.pieces;
-      float m = -INFINITY;
-      for (int i = lane; i < p.pieces; i += 32) m = fmaxf(m, st[i].top);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      double s = 0;
-      if (m > -INFINITY && m < INFINITY)
-        for (int i = lane; i < p.pieces; i += 32)
-          if (st[i].top > -INFINITY) s += st[i].sum * exp((double)st[i].top - m);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (s > 0) out = log(s);
-      if (lane == 0) top[b] = m;
-    }
-    if (lane == 0) log_sum[b] = out;
-  }
-  if (tid == 0) count = 0;
-  __syncthreads();
+  const int64_t row0 = (int64_t)group * p.beams;
   const int per = p.pieces * n, total = p.beams * per;
   const uint2* entries = p.entries + (int64_t)group * total;
-  const float* scores = p.scores + (int64_t)group * p.beams;
-  auto get = [&](int i) {
+  const float* scores = p.scores + row0;
+  // A thread's first entries, and the first of its pieces' sums, asked for together.
+  constexpr int kOwn = 8;
+  uint2 own[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i)
+    own[i] = tid + i * kThreads < total ? entries[tid + i * kThreads] : make_uint2(0, 0);
+  for (int b = tid; b < p.beams; b += kThreads) top[b] = kNone32;
+  if (tid == 0) {
+    count = 0;
+    largest = 0;
+  }
+  __syncthreads();
+  // (Beams that are not there have no sums.)
+  Stat st{0, -INFINITY, 0};
+  auto sum_of = [&](int i) {
+    return scores[i / p.pieces] > -INFINITY ? p.stats[row0 * p.pieces + i]
+                                            : Stat{0, -INFINITY, 0};
+  };
+  const int sums = p.beams * p.pieces;
+  if (tid < sums) st = sum_of(tid);
+  for (int i = tid; i < sums; i += kThreads)
+    atomicMax(&top[i / p.pieces], ordered((i == tid ? st : sum_of(i)).top));
+  __syncthreads();
+  for (int i = tid; i < sums; i += kThreads) {
+    const Stat x = i == tid ? st : sum_of(i);
+    const float m = unordered(top[i / p.pieces]);
+    // A logit of +infinity: no continuations.
+    parts[i] = !(x.top > -INFINITY) || m == INFINITY ? 0.
+               : x.top == m                          ? x.sum
+                                                     : x.sum * exp_of((double)x.top - m);
+  }
+  __syncthreads();
+  for (int b = tid; b < p.beams; b += kThreads) {
+    double s[4] = {0, 0, 0, 0};
+    for (int i = 0; i < p.pieces; i += 4)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k < p.pieces) s[k] += parts[b * p.pieces + i + k];
+    const double all = (s[0] + s[1]) + (s[2] + s[3]);
+    const double l = all > 0 ? log_of(all) : NAN;
+    log_sum[b] = l;
+    if (all > 0) atomicMax(&largest, __float_as_uint(fabsf(scores[b]) + fabsf((float)l)));
+  }
+  __syncthreads();
+  auto get = [&](const uint2& e, int i) {
     const int b = i / per;
     const double l = log_sum[b];
-    if (isnan(l)) return Cand{0, 0};
-    const uint2 e = entries[i];
-    if (e.x == 0) return Cand{0, 0};
-    const double y = (double)scores[b] + (((double)unordered(e.x) - top[b]) - l);
+    if (e.x == 0 || isnan(l)) return Cand{0, 0};
+    const double y =
+        (double)scores[b] + (((double)unordered(e.x) - unordered(top[b])) - l);
     if (!(y > -INFINITY)) return Cand{0, 0};
-    return Cand{ordered(y), (int64_t)b * p.vocab + e.y};
+    return Cand{ordered(y), (uint64_t)b << 32 | e.y};
   };
-  uint64_t mine = 0, lo, hi;
-  for (int i = tid; i < total; i += kThreads) mine = max(mine, get(i).y);
-  range(mine, sh, lo, hi);
-  const uint64_t bar = threshold(mine, lo, hi, kNone64 + 1, n);
-  if (mine >= bar)
-    for (int i = tid; i < total; i += kThreads) {
-      const Cand a = get(i);
-      if (a.y >= bar) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kCand) cand[at] = a;
-      }
-    }
+  // The same in fp32, off by less than 2^-21 (|score| + |log sum| + |x - top|), the
+  // last at most the first two and |y|: a bar on these, lowered by that twice (and a
+  // half more), leaves few results to be computed in 64 bits.
+  auto near = [&](const uint2& e, int i) {
+    const int b = min(i, total - 1) / per;
+    const float l = (float)log_sum[b];
+    if (e.x == 0 || l != l) return -INFINITY;
+    return fmaxf(scores[b] + ((unordered(e.x) - unordered(top[b])) - l), -FLT_MAX);
+  };
+  float near_own[kOwn], most = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    near_own[i] = near(own[i], tid + i * kThreads);
+    most = fmaxf(most, near_own[i]);
+  }
+  for (int i = tid + kOwn * kThreads; i < total; i += kThreads)
+    most = fmaxf(most, near(entries[i], i));
+  uint32_t lo, hi;
+  range(ordered(most), sh, lo, hi);
+  float bar = unordered(threshold(ordered(most), lo, hi, kNone32, n));
+  bar -= (fabsf(bar) + 2.f * __uint_as_float(largest)) * 0x1p-19f;
+  if (!(bar > -INFINITY)) bar = -INFINITY;  // (fewer than n, or no finite margin)
+  auto add = [&](int i, float y) {
+    if (y < bar || y == -INFINITY || i >= total) return;
+    const int at = atomicAdd(&count, 1);
+    if (at < kCand) which[at] = i;
+  };
+  if (most >= bar) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) add(tid + i * kThreads, near_own[i]);
+    for (int i = tid + kOwn * kThreads; i < total; i += kThreads)
+      add(i, near(entries[i], i));
+  }
+  __syncthreads();
+  // Those in 64 bits.
+  for (int i = tid; i < min(count, kCand); i += kThreads)
+    cand[i] = get(entries[which[i]], which[i]);
   __syncthreads();
   const int c = count;
   auto put = [&](int rank, const Cand& a) {
     const int64_t at = (int64_t)group * n + rank;
-    const uint64_t u = a.y & 0x8000000000000000ull ? a.y ^ 0x8000000000000000ull : ~a.y;
-    p.out_scores[at] = (float)__longlong_as_double((long long)u);
-    p.out_parents[at] = (int32_t)(a.flat / p.vocab);
-    p.out_tokens[at] = (int32_t)(a.flat % p.vocab);
+    p.out_scores[at] = (float)value_of(a.y);
+    p.out_parents[at] = (int32_t)(a.at >> 32);
+    p.out_tokens[at] = (int32_t)a.at;
   };
   for (int i = c + tid; i < n; i += kThreads) {
     const int64_t at = (int64_t)group * n + i;
@@ -327,17 +619,17 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const Params p) {
     return;
   }
   // Many equal sums: one at a time (c > n of them).
-  Cand last{~0ull, -1};
+  Cand last{~0ull, 0};
   for (int r = 0; r < n; ++r) {
     Cand best{0, 0};
     for (int i = tid; i < total; i += kThreads) {
-      const Cand a = get(i);
+      const Cand a = get(entries[i], i);
       if (a.y && before(last, a) && before(a, best)) best = a;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       const Cand a{__shfl_xor_sync(0xffffffffu, best.y, o),
-                   __shfl_xor_sync(0xffffffffu, best.flat, o)};
+                   __shfl_xor_sync(0xffffffffu, best.at, o)};
       if (before(a, best)) best = a;
     }
     if (lane == 0) best_of[tid >> 5] = best;
@@ -350,16 +642,22 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const Params p) {
   }
 }
 
-// Logits of a piece: 8192, or 2048 where those would be fewer than two waves of
-// pieces (three CTAs of them an SM).
-int piece_size(int64_t rows, int vocab) {
-  return rows * ((vocab + 8191) / 8192) < 2 * 3 * 152 ? 2048 : 8192;
-}
-
-// Pieces of a row, with vectors that start up to 7 values before it.
+// Pieces of a row, of 2048 logits at least: one to three rounds of CTAs (four on an
+// SM), whichever is filled best.
 int64_t n_pieces(int64_t rows, int vocab) {
-  const int size = piece_size(rows, vocab);
-  return ((int64_t)vocab + 7 + size - 1) / size;
+  const int64_t most = ((int64_t)vocab + 2047) / 2048;
+  int64_t best = 1;
+  double filled = 0;
+  for (int64_t rounds = 1; rounds <= 3; ++rounds) {
+    const int64_t p = std::clamp<int64_t>(rounds * kRound / rows, 1, most);
+    const int64_t r = (rows * p + kRound - 1) / kRound;
+    const double f = (double)(rows * p) / (double)(r * kRound);
+    if (f > filled * 1.02) {
+      filled = f;
+      best = p;
+    }
+  }
+  return best;
 }
 
 kv_status sizes_ok(int32_t n_groups, int32_t beams, int32_t vocab, int32_t n_out) {
@@ -440,15 +738,17 @@ extern "C" kv_status kv_beam_select(const void* logits, int32_t logits_type,
   p.beams = beams;
   cudaStream_t st = (cudaStream_t)stream;
   const dim3 grid((unsigned)p.pieces, (unsigned)rows);
-  const bool big = W::piece_size(rows, vocab) == 8192;
+  const bool big = vocab / p.pieces > 4096;  // steps of 4096 logits, else of 2048
+  // (Below the 48 KB that need no opting in.)
+  const int ring = 2 * W::kThreads * (big ? 16 : 8) * (f32 ? 4 : 2);
   if (f32 && big)
-    W::piece_kernel<float, 32><<<grid, W::kThreads, 0, st>>>(p);
+    W::piece_kernel<float, 16><<<grid, W::kThreads, ring, st>>>(p);
   else if (f32)
-    W::piece_kernel<float, 8><<<grid, W::kThreads, 0, st>>>(p);
+    W::piece_kernel<float, 8><<<grid, W::kThreads, ring, st>>>(p);
   else if (big)
-    W::piece_kernel<__nv_bfloat16, 32><<<grid, W::kThreads, 0, st>>>(p);
+    W::piece_kernel<__nv_bfloat16, 16><<<grid, W::kThreads, ring, st>>>(p);
   else
-    W::piece_kernel<__nv_bfloat16, 8><<<grid, W::kThreads, 0, st>>>(p);
+    W::piece_kernel<__nv_bfloat16, 8><<<grid, W::kThreads, ring, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
     e = pkv::launch_early(W::group_kernel, n_groups, W::kThreads, 0, st, p);
