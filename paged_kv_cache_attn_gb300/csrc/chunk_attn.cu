@@ -1184,10 +1184,13 @@ kv_status run(const void* q, int64_t q_stride, const void* k_pool,
   p.G = Hq / Hkv;
   p.total = total;
   p.scale_log2 = scale * 1.4426950408889634f;
-  // Heads whose keys and values the pairs share L2 for (shared blocks count as
-  // often as branches hold them).
-  p.heads = (int)std::clamp<int64_t>((48ll << 20) / ((int64_t)p.n_slots * 16 * d * 4),
-                                     1, Hkv);
+  // Heads whose items run at a time: all of them where their keys and values fit L2
+  // together (then the longest items of all heads come first), else as many as do
+  // (shared blocks count as often as branches hold them).
+  const int64_t head_bytes = (int64_t)p.n_slots * 16 * d * 4;
+  p.heads = head_bytes * Hkv <= (96ll << 20)
+                ? Hkv
+                : (int)std::clamp<int64_t>((48ll << 20) / head_bytes, 1, Hkv);
   if (e4m3) {
     const int ctas = (U * Hkv + 7) / 8;
     auto* k8 = static_cast<const uint8_t*>(k_pool);

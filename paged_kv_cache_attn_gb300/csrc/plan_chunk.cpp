@@ -11,9 +11,11 @@
 // longest key ranges first); one of 4 per tile whose key range is cut.
 
 #include <algorithm>
-#include <cmath>
 #include <cstring>
+#include <functional>
 #include <new>
+#include <queue>
+#include <utility>
 
 #include "internal.h"
 
@@ -30,40 +32,84 @@ struct Tile {
   int32_t keys() const { return (pos0 + ntok - 1) / kKeys + 1; }  // key tiles
 };
 
-// Key tiles of a work item at most.  An item costs about as much as kItem more
-// key tiles (its first loads, the last products, the joining of the rows), a cut
-// one kPartial on top (the partial rows out, and in again), and the merge kMerge
-// once: with them the longest item or the mean of the units (pairs of SMs, and single
-// ones for tiles of no more than a CTA's tokens), whichever is more, is least.
-int32_t pick_cut(const std::vector<Tile>& tiles, int32_t Hkv, int32_t ctok,
-                 int32_t pairs) {
-  constexpr double kItem = 3, kPartial = 1.5, kMerge = 5;
-  int32_t longest = 1;
-  for (const Tile& t : tiles) longest = std::max(longest, t.keys());
-  int32_t best = longest;
-  double least = 1e300;
-  for (int32_t cut = longest; cut >= 1; cut = cut * 3 / 4) {
-    double total = 0, n = 0, top = 0;  // in pairs
-    for (const Tile& t : tiles) {
-      const int64_t pieces = ceil_div(t.keys(), cut);
-      const double fixed = kItem + (pieces > 1 ? kPartial : 0.);
-      const double share = (t.ntok <= ctok ? 0.5 : 1.) * Hkv;
-      total += (t.keys() + pieces * fixed) * share;
-      n += pieces * share;
-      top = std::max(top, (double)ceil_div(t.keys(), pieces) + fixed);
+// When the persistent CTAs would be done, in pair tiles (a key tile of an item on a
+// pair of SMs, 0.58 us), with the items' order the kernels take them in.  Measured:
+// a single CTA takes a key tile in 0.55 of that, an item costs either about kItem on
+// top (its first loads, the last products, the joining of the rows), a cut kPartial
+// more (the partial rows out, and in again), the merge kMerge once.
+struct Cost {
+  static constexpr double kSingle = 0.55, kItem = 5, kPartial = 1.5, kMerge = 5;
+  int32_t Hkv, ctok, pairs;
+
+  // Tiles before `from` (of the sorted list) uncut, the others in pieces of at most
+  // `cut`.
+  double finish(const std::vector<Tile>& tiles, size_t from, int32_t cut) const {
+    // Durations of each kind, with how many items there are of each.
+    std::vector<std::pair<double, int64_t>> wide, narrow;
+    bool any_cut = false;
+    for (size_t i = 0; i < tiles.size(); ++i) {
+      const int32_t keys = tiles[i].keys();
+      const int64_t pieces = i < from ? 1 : ceil_div(keys, cut);
+      any_cut |= pieces > 1;
+      const bool w = tiles[i].ntok > ctok;
+      const double each = (double)keys / pieces * (w ? 1. : kSingle) + kItem +
+                          (pieces > 1 ? kPartial : 0.);
+      (w ? wide : narrow).push_back({each, pieces * Hkv});
     }
-    double cost = std::max(top, total / pairs);
-    // Few items of a kind go by whole rounds.
-    if (n < 4. * pairs) cost = std::max(cost, std::ceil(n / pairs) * (total / n));
-    if (cut < longest) cost += kMerge;
-    if (cost < least) {
-      least = cost;
-      best = cut;
+    auto longer = [](auto& x, auto& y) { return x.first > y.first; };
+    std::sort(wide.begin(), wide.end(), longer);
+    std::sort(narrow.begin(), narrow.end(), longer);
+    // Pairs, then the SMs of each as it is done.
+    using Heap = std::priority_queue<double, std::vector<double>, std::greater<double>>;
+    Heap on_pairs(std::greater<double>(), std::vector<double>(pairs, 0.));
+    double end = 0;
+    auto run = [&](Heap& heap, const auto& items) {
+      for (const auto& x : items)
+        for (int64_t k = 0; k < x.second; ++k) {
+          const double t = heap.top() + x.first;
+          heap.pop();
+          heap.push(t);
+          end = std::max(end, t);
+        }
+    };
+    run(on_pairs, wide);
+    Heap on_sms;
+    for (; !on_pairs.empty(); on_pairs.pop()) {
+      on_sms.push(on_pairs.top());
+      on_sms.push(on_pairs.top());
     }
-    // Already a small part of what there is to do.
-    if (top * 8 < total / pairs) break;
+    run(on_sms, narrow);
+    return end + (any_cut ? kMerge : 0.);
   }
-  return best;
+};
+
+// Where the keys of tiles (sorted, most keys first) are cut: from which tile on, and
+// into pieces of how many key tiles at most.  Uncut, all in pieces, or only those that
+// come after the last whole round of the pairs, whichever is done first.  Steps of
+// more than eight rounds of items even out by themselves.
+void pick_cut(const std::vector<Tile>& tiles, int32_t Hkv, int32_t ctok, int32_t pairs,
+              size_t* from, int32_t* cut) {
+  *from = tiles.size();
+  *cut = 1;
+  if (tiles.empty() || (int64_t)tiles.size() * Hkv > 8ll * pairs) return;
+  const Cost cost{Hkv, ctok, pairs};
+  const int32_t longest = tiles.front().keys();
+  double least = cost.finish(tiles, tiles.size(), 1) * 0.97;  // cuts have to pay
+  auto attempt = [&](size_t f, int32_t c) {
+    const double t = cost.finish(tiles, f, c);
+    if (t < least) {
+      least = t;
+      *from = f;
+      *cut = c;
+    }
+  };
+  const size_t round = std::max<int64_t>(pairs / Hkv, 1);
+  const size_t rest = tiles.size() / round * round;  // tiles of whole rounds
+  for (int32_t c = longest * 3 / 4; c >= 2; c = c * 3 / 4) {
+    attempt(0, c);
+    if (rest > 0 && rest < tiles.size()) attempt(rest, c);
+    if (rest > round) attempt(rest - round, c);
+  }
 }
 
 kv_status chunk_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d,
@@ -118,13 +164,19 @@ kv_status chunk_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d,
                        (int32_t)off});
     row += n;
   }
-  const int32_t cut = whole.empty() ? 1 : pick_cut(whole, Hkv, step / 2, pairs);
+  std::stable_sort(whole.begin(), whole.end(),
+                   [](const Tile& x, const Tile& y) { return x.keys() > y.keys(); });
+  size_t cut_from;
+  int32_t cut, most = 0;
+  pick_cut(whole, Hkv, step / 2, pairs, &cut_from, &cut);
   std::vector<pkv::ChunkItem> items;
   std::vector<pkv::ChunkMerge> merges;
   int64_t partial = 0;
-  for (const Tile& t : whole) {
+  for (size_t k = 0; k < whole.size(); ++k) {
+    const Tile& t = whole[k];
     const int32_t keys = t.keys();
-    const int32_t pieces = (int32_t)ceil_div(keys, cut);
+    const int32_t pieces = k < cut_from ? 1 : (int32_t)ceil_div(keys, cut);
+    most = std::max(most, (keys - 1) / pieces + 1);
     const int64_t rows = (int64_t)t.ntok * Hq;  // of a piece
     if (pieces > 1)
       merges.push_back({t.row0, t.ntok, (int32_t)partial, pieces});
@@ -166,7 +218,7 @@ kv_status chunk_plan(int32_t nb, int32_t Hq, int32_t Hkv, int32_t d,
   info->n_row_items = (int32_t)U;
   info->n_tile_items = (int32_t)items.size();
   info->n_merge_rows = (int32_t)row;
-  info->chunk_blocks = cut * (kKeys / 16);
+  info->chunk_blocks = most * (kKeys / 16);
   info->n_tile_wide_items = (int32_t)n_wide;
   info->n_row_warp_items = (int32_t)merges.size();
   info->flags = pkv::kChunkPlan | flags;
