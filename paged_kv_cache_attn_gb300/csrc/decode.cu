@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(128, 3)
   __shared__ __align__(8) uint64_t bars[C::kWarps][NS];
   __shared__ float m_sh[C::kWarps][16];
   __shared__ float l_sh[C::kWarps][16];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // where launched early
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -417,6 +418,7 @@ struct MergeParams {
 template <int D, int kAhead>
 __global__ void __launch_bounds__(256) lse_merge_kernel(const MergeParams p) {
   constexpr int V = D / 32;  // values per lane
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // where launched early
   const int gw = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (gw >= p.nb * p.Hq) return;
@@ -570,7 +572,7 @@ kv_status make_pool_map_tiles(CUtensorMap* tm, const void* pool, int64_t nh) {
 template <int D>
 cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv,
                          const SplitParams& sp, int n_items, int n_warp_items,
-                         cudaStream_t stream) {
+                         bool early, cudaStream_t stream) {
   if (n_warp_items < 0 || n_warp_items > n_items) return cudaErrorInvalidValue;
   const int n_long = n_items - n_warp_items;
   using C = SplitCfg<D, kStages>;
@@ -582,22 +584,34 @@ cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv,
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
+  const int grid = n_long + (n_warp_items + 3) / 4;
+  if (early)
+    return launch_early(splitkv_decode_kernel<D, kStages>, grid, 128, C::kSmem, stream,
+                        tk, tv, sp, n_long, n_items);
   splitkv_decode_kernel<D, kStages>
-      <<<n_long + (n_warp_items + 3) / 4, 128, C::kSmem, stream>>>(
-          tk, tv, sp, n_long, n_items);
+      <<<grid, 128, C::kSmem, stream>>>(tk, tv, sp, n_long, n_items);
   return cudaGetLastError();
 }
 
 constexpr int kFewMergeRows = 1024;  // fewer than a warp on every scheduler and a half
 
 template <int D>
-cudaError_t launch_merge(const MergeParams& mp, cudaStream_t stream) {
-  const int warps = mp.nb * mp.Hq;
+cudaError_t launch_merge(const MergeParams& mp, bool early, cudaStream_t stream) {
+  const int warps = mp.nb * mp.Hq, grid = (warps + 7) / 8;
+  if (early)
+    return warps <= kFewMergeRows
+               ? launch_early(lse_merge_kernel<D, 16>, grid, 256, 0, stream, mp)
+               : launch_early(lse_merge_kernel<D, 1>, grid, 256, 0, stream, mp);
   if (warps <= kFewMergeRows)
-    lse_merge_kernel<D, 16><<<(warps + 7) / 8, 256, 0, stream>>>(mp);
+    lse_merge_kernel<D, 16><<<grid, 256, 0, stream>>>(mp);
   else
-    lse_merge_kernel<D, 1><<<(warps + 7) / 8, 256, 0, stream>>>(mp);
+    lse_merge_kernel<D, 1><<<grid, 256, 0, stream>>>(mp);
   return cudaGetLastError();
+}
+
+__global__ void clear_status_kernel(DeviceStatus* status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0) *status = DeviceStatus{};
 }
 
 }  // namespace
@@ -605,7 +619,8 @@ cudaError_t launch_merge(const MergeParams& mp, cudaStream_t stream) {
 // Split-KV kernel over an e4m3 pool; defined in decode_e4m3.cu.
 cudaError_t launch_split_e4m3(const SplitParams& sp, const void* k8,
                               const void* v8, const void* scales, int n_items,
-                              int n_warp_items, int d, cudaStream_t stream);
+                              int n_warp_items, int d, bool early,
+                              cudaStream_t stream);
 
 // Tensor-core tile kernel over an e4m3 pool; defined in decode_tc_e4m3.cu.
 cudaError_t launch_tile_e4m3(const SplitParams& sp, const WorkItem* items,
@@ -701,7 +716,7 @@ static kv_status decode_impl(
     int32_t nb, int32_t max_blocks, int32_t Hq, int32_t Hkv, int32_t d,
     int32_t block_size, float scale, void* out, const int32_t* plan,
     const kv_decode_plan_info* info, void* workspace, size_t ws_bytes,
-    void* stream, const E4m3Append* pre = nullptr) {
+    void* stream, const E4m3Append* pre = nullptr, bool early = false) {
   (void)prefix_groups;
   if (!q || !k_pool || !v_pool || !block_tables || !seq_lens || !out ||
       !plan || !info || !workspace)
@@ -789,7 +804,12 @@ static kv_status decode_impl(
   const int off_ptr = off_tile + 8 * info->n_tile_items;
   const int off_ent = off_ptr + nb + 1;
 
-  cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(pkv::DeviceStatus), st);
+  // early: each kernel may be launched while the one before it in the stream still
+  // runs (and waits for it), the selection's among them.  Steps without tile items.
+  early = early && info->n_tile_items == 0;
+  cudaError_t e = early ? pkv::launch_early(pkv::clear_status_kernel, 1, 32, 0, st,
+                                            sp.status)
+                        : cudaMemsetAsync(ws, 0, sizeof(pkv::DeviceStatus), st);
   if (e != cudaSuccess) return fail(KV_ERR_CUDA, "memset: %s", cudaGetErrorString(e));
   if (pre) {
     const int err = pkv::launch_append_step_e4m3(
@@ -853,12 +873,12 @@ static kv_status decode_impl(
     if (e4m3)
       e = pkv::launch_split_e4m3(sp, k_pool, v_pool, kv_scales,
                                  info->n_row_items, info->n_row_warp_items, d,
-                                 st);
+                                 early, st);
     else
       e = d == 128 ? pkv::launch_split<128>(tk, tv, sp, info->n_row_items,
-                                            info->n_row_warp_items, st)
+                                            info->n_row_warp_items, early, st)
                    : pkv::launch_split<64>(tk, tv, sp, info->n_row_items,
-                                           info->n_row_warp_items, st);
+                                           info->n_row_warp_items, early, st);
     pkv::mark(3, st);
     if (e != cudaSuccess)
       return fail(KV_ERR_CUDA, "split-KV kernel: %s", cudaGetErrorString(e));
@@ -879,12 +899,29 @@ static kv_status decode_impl(
   mp.G = sp.G;
   mp.partial_rows = info->partial_rows;
   pkv::mark(4, st);
-  e = d == 128 ? pkv::launch_merge<128>(mp, st) : pkv::launch_merge<64>(mp, st);
+  e = d == 128 ? pkv::launch_merge<128>(mp, early, st)
+               : pkv::launch_merge<64>(mp, early, st);
   pkv::mark(5, st);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "merge kernel: %s", cudaGetErrorString(e));
   return KV_OK;
 }
+
+namespace pkv {
+
+kv_status decode_selected(const void* q, const void* k_pool, const void* v_pool,
+                          const void* kv_scales, int64_t num_blocks,
+                          const int32_t* tables, const int32_t* lens, int32_t nb,
+                          int32_t max_blocks, int32_t Hq, int32_t d,
+                          int32_t block_size, float scale, void* out,
+                          const int32_t* plan, const kv_decode_plan_info* info,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  return decode_impl(q, nullptr, nullptr, k_pool, v_pool, kv_scales, num_blocks, tables,
+                     lens, nullptr, 0, nb, max_blocks, Hq, 1, d, block_size, scale, out,
+                     plan, info, workspace, ws_bytes, stream, nullptr, true);
+}
+
+}  // namespace pkv
 
 extern "C" kv_status paged_decode_attn(
     const void* q, const void* k_pool, const void* v_pool, int64_t num_blocks,

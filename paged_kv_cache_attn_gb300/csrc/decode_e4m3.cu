@@ -37,6 +37,7 @@
 
 #include "device_common.cuh"
 #include "e4m3.cuh"
+#include "tensor_map.h"
 
 namespace pkv {
 
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(128, 3)
   __shared__ __align__(8) uint64_t bars[C::kWarps][NS];
   __shared__ float m_sh[C::kWarps][16];
   __shared__ float l_sh[C::kWarps][16];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // where launched early
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(128, 3)
 template <int D>
 cudaError_t launch_t(const SplitParams& sp, const void* k8, const void* v8,
                      const void* scales, int n_items, int n_warp_items,
-                     cudaStream_t stream) {
+                     bool early, cudaStream_t stream) {
   using C = E4m3Cfg<D, kE4m3Stages>;
   static bool attr_set = false;
   if (!attr_set) {
@@ -512,6 +514,17 @@ cudaError_t launch_t(const SplitParams& sp, const void* k8, const void* v8,
   const auto* k = static_cast<const uint8_t*>(k8);
   const auto* v = static_cast<const uint8_t*>(v8);
   const auto* s = static_cast<const float4*>(scales);
+  if (early) {
+    cudaError_t e = cudaSuccess;
+    if (n_long > 0)
+      e = launch_early(splitkv_e4m3_kernel<D, kE4m3Stages, false>, n_long, 128, C::kSmem,
+                       stream, sp, k, v, s, 0, n_items);
+    if (e == cudaSuccess && n_warp_items > 0)
+      e = launch_early(splitkv_e4m3_kernel<D, kE4m3Stages, true>,
+                       (n_warp_items + 3) / 4, 128, C::kSmem, stream, sp, k, v, s, n_long,
+                       n_items);
+    return e;
+  }
   if (n_long > 0)
     splitkv_e4m3_kernel<D, kE4m3Stages, false>
         <<<n_long, 128, C::kSmem, stream>>>(sp, k, v, s, 0, n_items);
@@ -526,10 +539,11 @@ cudaError_t launch_t(const SplitParams& sp, const void* k8, const void* v8,
 
 cudaError_t launch_split_e4m3(const SplitParams& sp, const void* k8,
                               const void* v8, const void* scales, int n_items,
-                              int n_warp_items, int d, cudaStream_t stream) {
-  return d == 128 ? launch_t<128>(sp, k8, v8, scales, n_items, n_warp_items,
+                              int n_warp_items, int d, bool early,
+                              cudaStream_t stream) {
+  return d == 128 ? launch_t<128>(sp, k8, v8, scales, n_items, n_warp_items, early,
                                   stream)
-                  : launch_t<64>(sp, k8, v8, scales, n_items, n_warp_items,
+                  : launch_t<64>(sp, k8, v8, scales, n_items, n_warp_items, early,
                                  stream);
 }
 

@@ -191,6 +191,16 @@ kv_status decode_plan_of_rows(int32_t nb, int32_t Hq, int32_t d, int32_t max_blo
                               int32_t row_blocks, int32_t* plan, int64_t plan_cap,
                               kv_decode_plan_info* info);
 
+// A decode step of such a plan, bf16 or (kv_scales not null) e4m3, whose kernels are
+// launched early (decode.cu).
+kv_status decode_selected(const void* q, const void* k_pool, const void* v_pool,
+                          const void* kv_scales, int64_t num_blocks,
+                          const int32_t* tables, const int32_t* lens, int32_t nb,
+                          int32_t max_blocks, int32_t Hq, int32_t d,
+                          int32_t block_size, float scale, void* out,
+                          const int32_t* plan, const kv_decode_plan_info* info,
+                          void* workspace, size_t ws_bytes, void* stream);
+
 // ---- kernel launchers (state_kernels.cu, decode kernels) -------------------
 // Copy appended K/V rows into their slots.  dst_blocks[i] = physical block of
 // logical block first_lblock + i; rows are tokens [tok0, tok0 + n) of the

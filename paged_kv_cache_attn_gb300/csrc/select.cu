@@ -980,10 +980,9 @@ extern "C" kv_status paged_selected_attn(
     size_t ws_bytes, void* stream) {
   pkv::clear_error();
   if (kv_status s = pkv::sel::virtual_batch(nb, Hq, Hkv, num_blocks)) return s;
-  return paged_decode_attn(q, k_pool, v_pool, num_blocks * Hkv, sel_tables, sel_lens,
-                           nullptr, 0, nb * Hkv, n_sel, Hq / Hkv, 1, head_dim,
-                           block_size, scale, out, plan, info, workspace, ws_bytes,
-                           stream);
+  return pkv::decode_selected(q, k_pool, v_pool, nullptr, num_blocks * Hkv, sel_tables,
+                              sel_lens, nb * Hkv, n_sel, Hq / Hkv, head_dim, block_size,
+                              scale, out, plan, info, workspace, ws_bytes, stream);
 }
 
 extern "C" kv_status paged_selected_attn_e4m3(
@@ -994,8 +993,9 @@ extern "C" kv_status paged_selected_attn_e4m3(
     const kv_decode_plan_info* info, void* workspace, size_t ws_bytes, void* stream) {
   pkv::clear_error();
   if (kv_status s = pkv::sel::virtual_batch(nb, Hq, Hkv, num_blocks)) return s;
-  return paged_decode_attn_e4m3(q, k_pool, v_pool, kv_scales, num_blocks * Hkv,
-                                sel_tables, sel_lens, nullptr, 0, nb * Hkv, n_sel,
-                                Hq / Hkv, 1, head_dim, block_size, scale, out, plan,
-                                info, workspace, ws_bytes, stream);
+  if (!kv_scales) return fail(KV_ERR_INVALID_ARG, "kv_scales required");
+  return pkv::decode_selected(q, k_pool, v_pool, kv_scales, num_blocks * Hkv,
+                              sel_tables, sel_lens, nb * Hkv, n_sel, Hq / Hkv,
+                              head_dim, block_size, scale, out, plan, info, workspace,
+                              ws_bytes, stream);
 }
