@@ -668,8 +668,6 @@ kv_status sizes_ok(int32_t n_groups, int32_t beams, int32_t vocab, int32_t n_out
     return fail(KV_ERR_INVALID_ARG, "n_out %d outside [1, %d]", n_out, kMaxOut);
   const int64_t rows = (int64_t)n_groups * beams;
   if (rows > 65535) return fail(KV_ERR_INVALID_ARG, "more than 65535 beams");
-  if (n_pieces(rows, vocab) * beams * n_out > INT32_MAX / 2)
-    return fail(KV_ERR_INVALID_ARG, "vocabulary too large");
   return KV_OK;
 }
 
