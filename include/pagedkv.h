@@ -860,7 +860,7 @@ kv_status kv_beam_select_workspace_size(int32_t n_groups, int32_t beams,
  * or none that can follow, has no continuation.  Outputs, device
  * [n_groups][n_out]: out_scores fp32, out_parents int32 (the beam's place in its
  * group), out_tokens int32; where there are fewer continuations, -infinity, -1 and
- * -1.  The sums are fp32 in parts of 8 or 16 logits and 64 bits across them, the
+ * -1.  The sums are fp32 in parts of 8 or 16 logits and pairs of fp32 across them, the
  * results 64 bits (rounded to fp32 once): beams whose results differ by less than
  * about 1e-7 may change places.  n_out in [1, 128]; beams in [1, 1024]; n_groups *
  * beams at most 65535.  workspace: device, 256-byte aligned, no initial contents

@@ -4,20 +4,22 @@
 // ties to the lower beam, then the lower token.  Bound by the logits' bytes: they are
 // read once.
 //
-// First kernel: a CTA streams a piece of one beam's logits through registers, a step of
-// up to 4096 at a time, and each thread adds up exponentials.
-// Of one beam the order of y is that of x: the CTA keeps candidates for the n highest
-// logits, and of what comes in only logits above a bar that n of those before reach.
-// The bar is taken from the threads' maxima of a step (a value that at least n of them
-// reach, and not many more, by bisection over counts).  Nearly all of a row lies below
-// it and costs no more than its sum and one barrier a step.  Second kernel: a CTA per
-// group joins the sums in 64 bits and picks the n highest y of the pieces' candidates.
+// First kernel: a CTA streams a piece of one beam's logits through shared memory, a step
+// of up to 4096 at a time; each thread adds up its exponentials and keeps the largest
+// logits of its steps, and waits for no other thread.  Of one beam the order of y is
+// that of x: at the end a value that n threads' largest logits reach (and not many
+// more, by bisection over counts) is a bar for the n highest, and the few groups of
+// logits whose largest reaches it are read again.  (With candidates kept as they came,
+// a barrier a step and a bar raised on the way, 32 x 16 beams of 128256 took 88 us, 21
+// instructions a logit; this takes 58 us, 4.5 TB/s.  Of the 53 us of the first kernel
+// some 6 are its ends: sums joined, the bar, groups read again from memory.)  Second
+// kernel: a CTA per group joins the sums and picks the n highest y of the pieces'
+// candidates.  1 x 8 beams of 32000 take 11 us, two launches of dependent steps.
 //
-// y is computed in 64 bits from sums of at most 16 exponentials in fp32 (added up with
-// what each addition rounds off, and across threads in 64 bits: 64-bit operations are
-// issued one lane pair a cycle here, and an addition a thread and step bounded the
-// kernel), about 1e-7 from exact, so that beams are hardly ever ordered otherwise than
-// exactly.
+// The sums are at most 16 exponentials in fp32, added up with what each addition rounds
+// off; y is computed in 64 bits, about 1e-7 from exact, so that beams are hardly ever
+// ordered otherwise than exactly.  References of the sums are whole numbers: what lies
+// between two of them is, too, and its exponential comes from a table.
 
 #include <algorithm>
 #include <cfloat>
@@ -33,13 +35,23 @@ constexpr int kThreads = 256;
 constexpr int kMaxOut = 128;
 constexpr int kMaxBeams = 1024;
 constexpr int kRound = 4 * 152;                   // CTAs of the first kernel at once
-constexpr int kMaxParts = 3 * kRound;             // beams x pieces of a group
-constexpr int kCand = 768;   // candidates in shared memory; more: one at a time
+constexpr int kCand = 768;   // candidates in shared memory; more: by their digits
+constexpr int kGroups = 16;  // groups of a thread's steps whose largest logits are kept
+constexpr int kList = 1024;  // groups to be read again, at most
 constexpr float kHeadroom = 40.f;  // of logits above the reference of a sum
 
+// Steps on their way to a CTA: 32 KB.
+template <typename T>
+constexpr int kRingSteps = sizeof(T) == 4 ? 2 : 4;
+
+// (Below the 48 KB that need no opting in; the candidates fit in.)
+template <typename T, int E>
+constexpr int kRingBytes = std::max((2 * kCand + kMaxOut) * 8 + kList * 2,
+                                    kRingSteps<T> * kThreads * E * (int)sizeof(T));
+
 struct Stat {
-  double sum;  // of exponentials of logits less `top`
-  float top, pad;
+  float sum, rest;  // of exponentials of logits less `top`, and what its rounding left
+  float top, pad;   // a whole number
 };
 
 struct Params {
@@ -51,7 +63,7 @@ struct Params {
   int32_t* out_parents;
   int32_t* out_tokens;
   int64_t stride;        // values between rows
-  int vocab, pieces, n, beams;
+  int vocab, pieces, n, beams, heads;
 };
 
 // Floats as unsigned numbers of the same order; -inf is 0x007fffff.
@@ -74,12 +86,12 @@ constexpr uint32_t kNone32 = 0x007fffffu;  // ordered(-inf): no candidate
 // A value that at least n threads' `mine` reach, and not many more; `floor` (the
 // least a candidate has) where fewer do.  All threads call it; `lo` and `hi`: the
 // least and largest of `mine`.
-template <typename Key>
-__device__ __forceinline__ Key threshold(Key mine, Key lo, Key hi, Key floor, int n) {
+__device__ __forceinline__ uint32_t threshold(uint32_t mine, uint32_t lo, uint32_t hi,
+                                              uint32_t floor, int n) {
   if (__syncthreads_count(mine >= floor) < n) return floor;
   lo = lo < floor ? floor : lo;
   while (hi - lo > 1) {
-    const Key mid = lo + (hi - lo) / 2;
+    const uint32_t mid = lo + (hi - lo) / 2;
     const int c = __syncthreads_count(mine >= mid);
     if (c >= n) {
       lo = mid;
@@ -91,25 +103,63 @@ __device__ __forceinline__ Key threshold(Key mine, Key lo, Key hi, Key floor, in
   return lo;
 }
 
-// Least and largest over the CTA.
-template <typename Key>
-__device__ __forceinline__ void range(Key mine, Key* sh, Key& lo, Key& hi) {
-  lo = hi = mine;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) {
-    sh[threadIdx.x >> 5] = lo;
-    sh[32 + (threadIdx.x >> 5)] = hi;
+// Least and largest over the CTA's 256 threads.
+__device__ __forceinline__ void range(uint32_t mine, uint32_t* sh, uint32_t& lo,
+                                      uint32_t& hi) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  lo = __reduce_min_sync(0xffffffffu, mine);
+  hi = __reduce_max_sync(0xffffffffu, mine);
+  if (lane == 0) {
+    sh[warp] = lo;
+    sh[kThreads / 32 + warp] = hi;
   }
   __syncthreads();
-  for (int w = 0; w < warps; ++w) {
-    lo = min(lo, sh[w]);
-    hi = max(hi, sh[32 + w]);
+  lo = __reduce_min_sync(0xffffffffu, sh[lane % (kThreads / 32)]);
+  hi = __reduce_max_sync(0xffffffffu, sh[kThreads / 32 + lane % (kThreads / 32)]);
+}
+
+struct Digits {
+  uint32_t hist[256];
+  uint64_t prefix;
+  int want;
+};
+
+// The n-th highest of the keys that `each` calls its argument with (whether there is
+// one, the key; whole warps), by digits of 8 bits from bit `top` down, of the keys that
+// begin with `prefix` (under `mask`): the least key of the n highest, or its first
+// digits where all keys that begin so are among them (n: 0 then, else which of the
+// keys equal to the result is the last).  All threads call it; 0 where there are fewer.
+template <typename Each>
+__device__ __forceinline__ uint64_t nth_key(Each each, int top, uint64_t prefix,
+                                         uint64_t mask, int& n, Digits& sh) {
+  const int tid = threadIdx.x;
+  for (int d = top; d >= 0; d -= 8) {
+    __syncthreads();
+    sh.hist[tid] = 0;
+    if (tid == 0) sh.want = -1;
+    __syncthreads();
+    each([&](bool in, uint64_t a) {
+      const int digit = in && (a & mask) == prefix ? (int)(a >> d & 255) : -1;
+      const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+      if (digit >= 0 && (tid & 31) == __ffs(peers) - 1)
+        atomicAdd(&sh.hist[digit], __popc(peers));
+    });
+    __syncthreads();
+    int above = 0;
+    for (int k = tid + 1; k < 256; ++k) above += sh.hist[k];
+    const int here = sh.hist[tid];
+    if (above < n && above + here >= n) {
+      sh.prefix = prefix | (uint64_t)tid << d;
+      sh.want = above + here == n ? 0 : n - above;
+    }
+    __syncthreads();
+    if (sh.want < 0) return 0;
+    prefix = sh.prefix;
+    n = sh.want;
+    mask |= 255ull << d;
+    if (n == 0) break;
   }
+  return prefix;
 }
 
 template <typename T>
@@ -154,19 +204,23 @@ __device__ __forceinline__ void pick_best(const uint64_t* cand, int c, int n, fl
   }
   for (int i = tid; i < n; i += kThreads) best[i] = 0;
   __syncthreads();
-  for (int i = tid; i < k; i += kThreads) {
-    const uint64_t a = from[i];
+  // Eight threads a key.
+  for (int i0 = 0; i0 < k; i0 += kThreads / 8) {
+    const int i = i0 + (tid >> 3);
+    const uint64_t a = i < k ? from[i] : 0;
     int rank = 0;
-#pragma unroll 4
-    for (int j = 0; j < k; ++j) rank += from[j] > a;
-    if (rank < n) best[rank] = a;
+    for (int j = tid & 7; j < k; j += 8) rank += from[j] > a;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (i < k && rank < n && (tid & 7) == 0) best[rank] = a;
   }
   __syncthreads();
 }
 
 // e^x in 64 bits for x <= 0: x / ln 2 split into a whole number and at most half of one
-// either way, its Taylor series to the 11th power (2e-14 relative).  Few operations:
-// 64-bit ones are issued one lane pair a cycle here, and this kernel waits for each.
+// either way, its Taylor series to the 11th power (2e-14 relative).  64-bit operations
+// take about 110 cycles each here: where a call waits for them they are few, and
+// tables, made while nothing else can be done, stand for this and the logarithm.
 __device__ __forceinline__ double exp_of(double x) {
   x = fmax(x, -700.);
   const double k = rint(x * 1.4426950408889634);
@@ -197,11 +251,12 @@ __device__ __forceinline__ double log_of(double s) {
 template <typename T, int E>
 __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const Params p) {
   constexpr int VE = 16 / sizeof(T), NV = E / VE;
-  __shared__ uint64_t cand[kCand], few[kCand], best[kMaxOut];
+  constexpr int kDepth = kRingSteps<T>;
   __shared__ uint32_t sh[64];
-  __shared__ double sums[kThreads / 32];
-  __shared__ int count, few_count;
-  __shared__ unsigned long long top;
+  __shared__ Digits digits;
+  __shared__ float2 sums[kThreads / 32];
+  __shared__ uint16_t group_max[kGroups][kThreads];
+  __shared__ int count, few_count, listed;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int row = blockIdx.y, piece = blockIdx.x, tid = threadIdx.x, n = p.n;
   if (!(p.scores[row] > -INFINITY)) return;  // no beam
@@ -211,30 +266,25 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const Params p) {
   const int64_t vectors = ((int64_t)p.vocab + off + VE - 1) / VE;
   const int64_t v_begin = vectors * piece / p.pieces;
   const int64_t v_end = vectors * (piece + 1) / p.pieces;
-  if (tid == 0) count = 0;
-  __syncthreads();
-  // The sum so far of exponentials of logits less m, the first step's maximum.  It
-  // moves, in a thread alone, only where a logit lies far above it.
-  float m = -INFINITY, ref = -INFINITY;
-  float sum_hi = 0.f, sum_lo = 0.f;  // the sum and what its additions have rounded off
-  float bar = -INFINITY;  // what comes in is a candidate above it
-  int bound = 0;          // candidates at most
-  int fresh = 0;          // threads that have brought some since the bar rose
-  bool picked = false;    // `best` holds the n highest of them
-  // Each thread's vectors of the next two steps are on their way to its own places in
+  constexpr int kStep = kThreads * NV;
+  const int steps = (int)((v_end - v_begin + kStep - 1) / kStep);
+  // Each thread's vectors of the next steps are on their way to its own places in
   // shared memory (32 KB a CTA, 128 KB an SM: with one step in registers the loads'
-  // latency, 1.9 us under load, kept an SM at 29 GB/s).  Vectors that reach over the
-  // row's ends are read value by value.
-  extern __shared__ __align__(16) uint4 ring[];  // [2][NV][kThreads]
+  // latency, 1.9 us under load, kept an SM at 29 GB/s), so that nothing of the stream
+  // waits for another thread.  Vectors that reach over the row's ends are read value
+  // by value.  What the candidates need lies there once the stream has ended.
+  extern __shared__ __align__(16) uint4 ring[];  // [kDepth][NV][kThreads]
+  uint64_t* cand = reinterpret_cast<uint64_t*>(ring);
+  uint64_t* few = cand + kCand;
+  uint64_t* best = few + kCand;
+  uint16_t* list = reinterpret_cast<uint16_t*>(best + kMaxOut);
   auto inside = [&](int64_t v) {
     const int64_t e = v * VE - off;
     return v < v_end && e >= 0 && e + VE <= p.vocab;
   };
-  constexpr int kStep = kThreads * NV;
   // Nothing of a step reaches over the row's or the piece's ends.
-  auto whole = [&](int64_t step) {
-    return step * VE >= off && step + kStep <= v_end &&
-           (step + kStep) * VE - off <= p.vocab;
+  auto whole = [&](int64_t v0) {
+    return v0 * VE >= off && v0 + kStep <= v_end && (v0 + kStep) * VE - off <= p.vocab;
   };
   const uint32_t mine_at = smem_u32(ring + tid);
   constexpr int kPlace = kThreads * 16;  // bytes between a thread's vectors
@@ -242,68 +292,89 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const Params p) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src)
                  : "memory");
   };
-  auto issue = [&](int64_t step, int slot) {
-    const uint32_t dst = mine_at + slot * (NV * kPlace);
-    const T* src = x + ((step + tid) * VE - off);
-    if (whole(step)) {
+  auto issue = [&](int64_t v0, int place) {
+    const uint32_t dst = mine_at + place * (NV * kPlace);
+    const T* src = x + ((v0 + tid) * VE - off);
+    if (whole(v0)) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) copy(dst + i * kPlace, src + i * (kThreads * VE));
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (inside(step + tid + i * kThreads))
+        if (inside(v0 + tid + i * kThreads))
           copy(dst + i * kPlace, src + i * (kThreads * VE));
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto fetch = [&](float (&f)[NV][VE], int64_t step, int slot) {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    const uint32_t src = mine_at + slot * (NV * kPlace);
-    const bool all = whole(step);
+  auto unpack = [&](const uint4& raw, float (&f)[VE]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (all || inside(step + tid + i * kThreads)) {
-        const uint4 raw = lds128(src + i * kPlace);
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-        for (int k = 0; k < VE; ++k) {
-          if (sizeof(T) == 4)
-            f[i][k] = __uint_as_float(w[k % 4]);
-          else
-            f[i][k] = __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
-        }
-      } else {
-        const int64_t v = step + tid + i * kThreads, e = v * VE - off;
-#pragma unroll
-        for (int k = 0; k < VE; ++k)
-          f[i][k] = v < v_end && e + k >= 0 && e + k < p.vocab ? to_float(x[e + k])
-                                                              : -INFINITY;
-      }
+    for (int k = 0; k < VE; ++k) {
+      if (sizeof(T) == 4)
+        f[k] = __uint_as_float(w[k % 4]);
+      else
+        f[k] = __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
     }
   };
-  auto process = [&](float (&f)[NV][VE], int64_t step, int slot) {
-    const int64_t v0 = step + tid;
+  auto one_by_one = [&](int64_t v, float (&f)[VE]) {
+    const int64_t e = v * VE - off;
+#pragma unroll
+    for (int k = 0; k < VE; ++k)
+      f[k] = v < v_end && e + k >= 0 && e + k < p.vocab ? to_float(x[e + k]) : -INFINITY;
+  };
+  // The sum so far of exponentials of logits less m, the whole number at the first
+  // step's maximum.  It moves, in a thread alone, only where a logit lies far above.
+  float m = -INFINITY, ref = -INFINITY;
+  float sum_hi = 0.f, sum_lo = 0.f;  // the sum and what its additions have rounded off
+  // Largest logit of this thread, and of a group of its steps.
+  float most = -INFINITY, of_group = -INFINITY;
+  const int width = (steps + kGroups - 1) / kGroups;  // steps of a group
+  int group = 0, in_group = 0;
+#pragma unroll
+  for (int k = 0; k < kDepth; ++k) issue(v_begin + (int64_t)k * kStep, k);
+  int place = 0;
+#pragma unroll 1
+  for (int step = 0; step < steps; ++step) {
+    const int64_t v0 = v_begin + (int64_t)step * kStep;
+    float f[NV][VE];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    {
+      const uint32_t src = mine_at + place * (NV * kPlace);
+      const bool all = whole(v0);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (all || inside(v0 + tid + i * kThreads))
+          unpack(lds128(src + i * kPlace), f[i]);
+        else
+          one_by_one(v0 + tid + i * kThreads, f[i]);
+      }
+    }
     float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < VE; ++k) {
-        mx = fmaxf(mx, f[i][k]);  // (passes over NaN)
-      }
+      for (int k = 0; k < VE; k += 2) mx = fmaxf(mx, fmaxf(f[i][k], f[i][k + 1]));
     // (This step's values are in registers: its place is free.)
-    const int over = __syncthreads_count(mx > bar);
-    issue(step + 2 * kStep, slot);
-    uint32_t lo = 0, hi = 0;  // least and largest of the threads' maxima
-    // (Of a first step with logits m is -inf in every thread.)
-    if (over > n || (over > 0 && bar == -INFINITY)) {
+    issue(v0 + (int64_t)kDepth * kStep, place);
+    place = place + 1 == kDepth ? 0 : place + 1;
+    if (step == 0) {
+      uint32_t lo, hi;
       range(ordered(mx), sh, lo, hi);
-      if (m == -INFINITY) m = ref = unordered(hi);
+      m = ref = rintf(unordered(hi));
+    }
+    most = fmaxf(most, mx);
+    of_group = fmaxf(of_group, mx);
+    if (++in_group == width) {
+      group_max[group++][tid] = (uint16_t)(ordered(of_group) >> 16);
+      of_group = -INFINITY;
+      in_group = 0;
     }
     if (mx > m + kHeadroom) {
-      const double y = ((double)sum_hi + sum_lo) * exp_of((double)m - mx);
+      const float to = rintf(mx);
+      const double y = ((double)sum_hi + sum_lo) * exp_of((double)m - to);
       sum_hi = (float)y;
       sum_lo = (float)(y - sum_hi);
-      m = mx;
+      m = to;
     }
     if (m > -INFINITY) {
       // Two at a time; where one is not a number, again without it.
@@ -336,110 +407,11 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const Params p) {
       sum_lo += (sum_hi - (to - part)) + (s - part);
       sum_hi = to;
     }
-    if (over == 0) return;
-    // Candidates: above the bar; where more than n threads have some, from a value
-    // on that n of them reach, which is a bar for what comes later.
-    float from = bar;
-    bool equal = false;
-    int before = 0;
-    fresh += over;
-    picked = false;
-    const bool many = fresh > n || bound + over * E > kCand;
-    if (many) {
-      if (over > n) {
-        from = unordered(threshold(ordered(mx), lo, hi, ordered(bar) + 1, n));
-        equal = true;
-      }
-      __syncthreads();
-      before = count;
-      __syncthreads();
-    }
-    // Higher logits first, then lower tokens.
-    auto key = [&](int i, int k) {
-      const uint32_t token = (uint32_t)((v0 + i * kThreads) * VE - off + k);
-      return (uint64_t)ordered(f[i][k]) << 32 | (0xffffffffu - token);
-    };
-    // Few lanes have any, and those one, as a rule: which, without branches, then
-    // theirs alone.
-    if (mx > from || (equal && mx == from)) {
-      uint32_t mask = 0;
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const float y = f[j / VE][j % VE];
-        mask |= (y > from || (equal && y == from) ? 1u : 0u) << j;
-      }
-      while (mask) {
-        const int j = __ffs(mask) - 1;
-        mask &= mask - 1;
-        float y = f[0][0];
-#pragma unroll
-        for (int k = 1; k < E; ++k) y = j == k ? f[k / VE][k % VE] : y;
-        const uint32_t token =
-            (uint32_t)((v0 + j / VE * kThreads) * VE - off + j % VE);
-        const int at = atomicAdd(&count, 1);
-        if (at < kCand) cand[at] = (uint64_t)ordered(y) << 32 | (0xffffffffu - token);
-      }
-    }
-    bound += over * E;
-    if (equal) bar = from;
-    if (!many) return;
-    __syncthreads();
-    int c = count;
-    __syncthreads();
-    if (c > kCand) {
-      // Many equal logits: the n highest of this step one at a time, behind the
-      // candidates there were, or the n highest of those (there are more than n).
-      if (before + n > kCand) {
-        pick_best(cand, before, n, bar, few, best, sh, &few_count);
-        for (int i = tid; i < n; i += kThreads) cand[i] = best[i];
-        before = n;
-        __syncthreads();
-      }
-      uint64_t last = ~0ull;
-      for (int r = 0; r < n; ++r) {
-        uint64_t most = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int k = 0; k < VE; ++k) {
-            const uint64_t a = key(i, k);
-            if (a < last && a > most) most = a;
-          }
-        if (tid == 0) top = 0;
-        __syncthreads();
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-          most = max(most, (uint64_t)__shfl_xor_sync(0xffffffffu, most, o));
-        if ((tid & 31) == 0) atomicMax(&top, (unsigned long long)most);
-        __syncthreads();
-        last = top;
-        if (tid == 0) cand[before + r] = last;
-        __syncthreads();
-      }
-      c = before + n;
-    }
-    if (c > n) {
-      // The n highest so far: the lowest of them is the bar.
-      pick_best(cand, c, n, bar, few, best, sh, &few_count);
-      for (int i = tid; i < n; i += kThreads) cand[i] = best[i];
-      bar = fmaxf(bar, unordered((uint32_t)(best[n - 1] >> 32)));
-      c = n;
-      picked = true;
-    }
-    __syncthreads();
-    if (tid == 0) count = c;
-    bound = c;
-    fresh = 0;
-    __syncthreads();
-  };
-  issue(v_begin, 0);
-  issue(v_begin + kStep, 1);
-  int slot = 0;
-  for (int64_t step = v_begin; step < v_end; step += kStep, slot ^= 1) {
-    float f[NV][VE];
-    fetch(f, step, slot);
-    process(f, step, slot);
   }
+  if (in_group > 0) group_max[group++][tid] = (uint16_t)(ordered(of_group) >> 16);
+  // (Nothing is on its way to the ring any more, which is used for other things.)
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (tid == 0) count = listed = 0;
   // Threads that have moved their reference (rare): back to a common one.
   if (__syncthreads_or(m != ref)) {
     uint32_t lo, hi;
@@ -449,26 +421,110 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const Params p) {
         m > -INFINITY ? ((double)sum_hi + sum_lo) * exp_of((double)m - ref) : 0.;
     sum_hi = (float)y;
     sum_lo = (float)(y - sum_hi);
+    __syncthreads();
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
+  auto join = [&](int o) {
     const float y = __shfl_xor_sync(0xffffffffu, sum_hi, o);
     sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, o);
     // (The larger first.)
     const float a = fmaxf(sum_hi, y), b = fminf(sum_hi, y);
     sum_hi = a + b;
     sum_lo += b - (sum_hi - a);
-  }
-  if ((tid & 31) == 0) sums[tid >> 5] = (double)sum_hi + sum_lo;
-  __syncthreads();
+  };
+#pragma unroll
+  for (int o = 16; o; o >>= 1) join(o);
+  if ((tid & 31) == 0) sums[tid >> 5] = make_float2(sum_hi, sum_lo);
+  // Candidates: logits from a value on that n threads' largest reach.  They lie in the
+  // groups whose largest reach it (compared by their upper halves), which are read
+  // again.
+  uint32_t lo, hi;
+  range(ordered(most), sh, lo, hi);
+  const uint32_t bar = threshold(ordered(most), lo, hi, kNone32 + 1, n);
   const int64_t at = (int64_t)row * p.pieces + piece;
-  if (tid == 0) {
-    double all = 0;
-    for (int w = 0; w < kThreads / 32; ++w) all += sums[w];
-    p.stats[at] = Stat{all, ref, 0.f};
+  if (tid < 32) {
+    sum_hi = sums[tid % (kThreads / 32)].x;
+    sum_lo = sums[tid % (kThreads / 32)].y;
+#pragma unroll
+    for (int o = kThreads / 64; o; o >>= 1) join(o);
+    if (tid == 0) p.stats[at] = Stat{sum_hi, sum_lo, ref, 0.f};
   }
-  // (Picked already where nothing came after.)
-  if (!picked) pick_best(cand, count, n, bar, few, best, sh, &few_count);
+  for (int g = 0; g < group; ++g)
+    if (group_max[g][tid] >= bar >> 16) {
+      const int i = atomicAdd(&listed, 1);
+      if (i < kList) list[i] = (uint16_t)(g * kThreads + tid);
+    }
+  __syncthreads();
+  auto vector = [&](int64_t v, float (&f)[VE]) {
+    if (inside(v))
+      unpack(__ldg(reinterpret_cast<const uint4*>(x + (v * VE - off))), f);
+    else
+      one_by_one(v, f);
+  };
+  // Higher logits first, then lower tokens.
+  auto key = [&](float y, int64_t v, int k) {
+    return (uint64_t)ordered(y) << 32 | (0xffffffffu - (uint32_t)(v * VE - off + k));
+  };
+  auto reaches = [&](float y) { return y == y && ordered(y) >= bar; };
+  const int groups = listed;
+  if (groups <= kList) {
+    for (int i = tid; i < groups * width; i += kThreads) {
+      const int e = list[i / width], step = e / kThreads * width + i % width;
+      if (step >= steps) continue;
+      const int64_t v = v_begin + (int64_t)step * kStep + e % kThreads;
+      float f[NV][VE];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) vector(v + j * kThreads, f[j]);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < VE; ++k)
+          if (reaches(f[j][k])) {
+            const int to = atomicAdd(&count, 1);
+            if (to < kCand) cand[to] = key(f[j][k], v + j * kThreads, k);
+          }
+    }
+  }
+  __syncthreads();
+  int c = count;
+  if (groups > kList || c > kCand) {
+    // Many equal logits, or few threads with any: the n-th highest key by its digits.
+    auto each = [&](auto&& f) {
+      auto of_vector = [&](int64_t v, bool there) {
+        float y[VE];
+        vector(there ? v : v_end, y);
+#pragma unroll
+        for (int k = 0; k < VE; ++k) f(reaches(y[k]), key(y[k], v, k));
+      };
+      if (groups <= kList) {
+        for (int i0 = 0; i0 < groups * width; i0 += kThreads) {
+          const int i = min(i0 + tid, groups * width - 1);
+          const int e = list[i / width], step = e / kThreads * width + i % width;
+          for (int j = 0; j < NV; ++j)
+            of_vector(v_begin + (int64_t)step * kStep + e % kThreads + j * kThreads,
+                      i0 + tid == i && step < steps);
+        }
+      } else {
+        for (int64_t v0 = v_begin; v0 < v_end; v0 += kThreads) of_vector(v0 + tid, true);
+      }
+    };
+    // Digits that all of them share: of the logits between the bar and the highest, and
+    // where those are equal, of the piece's tokens.
+    const int64_t first = max(v_begin * VE - off, (int64_t)0), end = v_end * VE - off;
+    const uint64_t high = (uint64_t)hi << 32 | (0xffffffffu - (uint32_t)first);
+    const uint64_t low = (uint64_t)bar << 32 | (0xffffffffu - (uint32_t)end);
+    const int top = (63 - __clzll((long long)(high ^ low))) & ~7;
+    const uint64_t mask = top == 56 ? 0 : ~0ull << (top + 8);
+    int last = n;
+    const uint64_t least = nth_key(each, top, high & mask, mask, last, digits);
+    if (tid == 0) count = 0;
+    __syncthreads();
+    each([&](bool in, uint64_t a) {
+      if (in && a >= least) cand[atomicAdd(&count, 1)] = a;
+    });
+    __syncthreads();
+    c = count;
+  }
+  pick_best(cand, c, n, unordered(bar), few, best, sh, &few_count);
   uint2* out = p.entries + at * n;
   for (int i = tid; i < n; i += kThreads)
     out[i] = best[i] ? make_uint2((uint32_t)(best[i] >> 32), ~(uint32_t)best[i])
@@ -489,110 +545,186 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
   return a.y > b.y || (a.y == b.y && a.at < b.at);
 }
 
+// A CTA for each group.  The tables are made while the pieces are still read.
 __global__ void __launch_bounds__(kThreads) group_kernel(const Params p) {
   __shared__ Cand cand[kCand];
   __shared__ int which[kCand];
-  // log sum exp(x - top), NaN: no continuations.  Kept apart from the highest logit,
-  // so that logits of any size cancel before the score is added.
-  __shared__ double log_sum[kMaxBeams], parts[kMaxParts];
-  __shared__ uint32_t top[kMaxBeams];  // highest logit, ordered
-  __shared__ uint32_t largest;  // |score| + |log sum| of the beams, at most
+  // Score less log sum exp(x - top), NaN: no continuations.  The highest reference is
+  // kept apart, so that logits of any size cancel before the score is added.
+  __shared__ double offset[kMaxBeams];
+  __shared__ float near_offset[kMaxBeams], top[kMaxBeams];
+  __shared__ double e_ones[32], e_32s[24];   // e^-k, e^-32k
+  __shared__ double log_at[65];              // log of c = 1 / (inverse of 1 + k / 64)
+  __shared__ uint32_t largest;  // |offset| of the beams, at most
   __shared__ uint32_t sh[64];
-  __shared__ Cand best_of[kThreads / 32];
+  __shared__ Digits digits;
   __shared__ int count;
+  const int group = blockIdx.x, tid = threadIdx.x, n = p.n;
+  auto inverse_at = [](int k) { return (double)(1.f / (1.f + (float)k * 0.015625f)); };
+  if (tid < 32) {
+    e_ones[tid] = exp_of(-(double)tid);
+  } else if (tid < 32 + 24) {
+    e_32s[tid - 32] = exp_of(-32. * (tid - 32));
+  } else if (tid >= 64 && tid < 64 + 65) {
+    log_at[tid - 64] = -log_of(inverse_at(tid - 64));
+  } else if (tid == 63) {
+    count = 0;
+    largest = 0;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int group = blockIdx.x, tid = threadIdx.x, lane = tid & 31, n = p.n;
   const int64_t row0 = (int64_t)group * p.beams;
   const int per = p.pieces * n, total = p.beams * per;
   const uint2* entries = p.entries + (int64_t)group * total;
   const float* scores = p.scores + row0;
-  // A thread's first entries, and the first of its pieces' sums, asked for together.
+  const Stat* stats = p.stats + row0 * p.pieces;
+  auto entry = [&](int i) { return i < total ? entries[i] : make_uint2(0, 0); };
+  const int turns = (total + kThreads - 1) / kThreads;
+  // A piece's entries come highest first: `1 << p.heads` of each, 2048 in all at most,
+  // are looked at first.  A thread has its share of several ranks.
   constexpr int kOwn = 8;
+  auto head = [&](int k) {
+    const int at = k * kThreads + ((tid + 37 * k) & (kThreads - 1));
+    const int rank = at & ((1 << p.heads) - 1);
+    return rank < n ? min((at >> p.heads) * n + rank, total) : total;
+  };
   uint2 own[kOwn];
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i)
-    own[i] = tid + i * kThreads < total ? entries[tid + i * kThreads] : make_uint2(0, 0);
-  for (int b = tid; b < p.beams; b += kThreads) top[b] = kNone32;
-  if (tid == 0) {
-    count = 0;
-    largest = 0;
+  for (int k = 0; k < kOwn; ++k) own[k] = entry(head(k));
+  __syncthreads();
+  // As many lanes a beam as it has pieces (a power of two, at most a warp).
+  int lanes = 1;
+  while (lanes < p.pieces && lanes < 32) lanes <<= 1;
+  for (int b0 = 0; b0 < p.beams; b0 += kThreads / lanes) {
+    const int b = b0 + tid / lanes, l = tid % lanes;
+    // (Beams that are not there have no sums.)
+    const float score = b < p.beams ? scores[b] : -INFINITY;
+    const Stat none{0.f, 0.f, -INFINITY, 0.f};
+    Stat first = b < p.beams && l < p.pieces ? stats[b * p.pieces + l] : none;
+    const bool there = score > -INFINITY;
+    if (!there) first = none;
+    float m = first.top;
+    for (int i = l + lanes; there && i < p.pieces; i += lanes)
+      m = fmaxf(m, stats[b * p.pieces + i].top);
+    for (int o = lanes >> 1; o; o >>= 1)
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // The references are whole numbers, and so is what lies between them.
+    auto part = [&](const Stat& x) {
+      const float d = m - x.top;
+      if (!(d < 700.f)) return 0.;
+      const int k = (int)d;
+      const double y = (double)x.sum + x.rest;
+      return k == 0 ? y : y * e_ones[k & 31] * e_32s[k >> 5];
+    };
+    double sum = part(first);
+    for (int i = l + lanes; there && i < p.pieces; i += lanes)
+      sum += part(stats[b * p.pieces + i]);
+    for (int o = lanes >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (l == 0 && b < p.beams) {
+      double at = NAN;
+      // (A logit of +infinity: no continuations.)
+      if (there && sum > 0 && m < INFINITY) {
+        // sum = f 2^e, log f = log c + log(1 + r), r = f / c - 1 within 2^-7: its
+        // series in fp32 is off by 2^-31.
+        const long long bits = __double_as_longlong(sum);
+        const double f = __longlong_as_double((bits & 0xfffffffffffffll) | 1023ll << 52);
+        const int k = (int)((bits >> 45 & 127) + 1) >> 1;
+        const float r = (float)fma(f, inverse_at(k), -1.);
+        const float series =
+            r * fmaf(r, fmaf(r, fmaf(r, fmaf(r, .2f, -.25f), 1.f / 3), -.5f), 1.f);
+        at = (double)score - (fma((double)((int)(bits >> 52) - 1023), 0.6931471805599453,
+                                  log_at[k]) + series);
+        atomicMax(&largest, __float_as_uint(fabsf((float)at)));
+      }
+      offset[b] = at;
+      near_offset[b] = (float)at;
+      top[b] = m;
+    }
   }
   __syncthreads();
-  // (Beams that are not there have no sums.)
-  Stat st{0, -INFINITY, 0};
-  auto sum_of = [&](int i) {
-    return scores[i / p.pieces] > -INFINITY ? p.stats[row0 * p.pieces + i]
-                                            : Stat{0, -INFINITY, 0};
-  };
-  const int sums = p.beams * p.pieces;
-  if (tid < sums) st = sum_of(tid);
-  for (int i = tid; i < sums; i += kThreads)
-    atomicMax(&top[i / p.pieces], ordered((i == tid ? st : sum_of(i)).top));
-  __syncthreads();
-  for (int i = tid; i < sums; i += kThreads) {
-    const Stat x = i == tid ? st : sum_of(i);
-    const float m = unordered(top[i / p.pieces]);
-    // A logit of +infinity: no continuations.
-    parts[i] = !(x.top > -INFINITY) || m == INFINITY ? 0.
-               : x.top == m                          ? x.sum
-                                                     : x.sum * exp_of((double)x.top - m);
-  }
-  __syncthreads();
-  for (int b = tid; b < p.beams; b += kThreads) {
-    double s[4] = {0, 0, 0, 0};
-    for (int i = 0; i < p.pieces; i += 4)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i + k < p.pieces) s[k] += parts[b * p.pieces + i + k];
-    const double all = (s[0] + s[1]) + (s[2] + s[3]);
-    const double l = all > 0 ? log_of(all) : NAN;
-    log_sum[b] = l;
-    if (all > 0) atomicMax(&largest, __float_as_uint(fabsf(scores[b]) + fabsf((float)l)));
-  }
-  __syncthreads();
+  // An entry's beam: i + 1/2 is exact, and at least 1 / (2 per) of a beam from the
+  // next whole number, which two roundings of at most total / per beams do not reach.
+  const float inv_per = 1.f / (float)per;
+  auto beam_of = [&](int i) { return (int)(((float)i + .5f) * inv_per); };
   auto get = [&](const uint2& e, int i) {
-    const int b = i / per;
-    const double l = log_sum[b];
-    if (e.x == 0 || isnan(l)) return Cand{0, 0};
-    const double y =
-        (double)scores[b] + (((double)unordered(e.x) - unordered(top[b])) - l);
+    const int b = beam_of(i);
+    const double at = offset[b];
+    if (e.x == 0 || isnan(at)) return Cand{0, 0};
+    const double y = at + ((double)unordered(e.x) - top[b]);
     if (!(y > -INFINITY)) return Cand{0, 0};
     return Cand{ordered(y), (uint64_t)b << 32 | e.y};
   };
-  // The same in fp32, off by less than 2^-21 (|score| + |log sum| + |x - top|), the
-  // last at most the first two and |y|: a bar on these, lowered by that twice (and a
-  // half more), leaves few results to be computed in 64 bits.
+  // The same in fp32, off by less than 2^-21 (|offset| + |x - top| + |y|), the second at
+  // most the others: a bar on these, lowered by that twice (and a half more), leaves
+  // few results to be computed in 64 bits.
   auto near = [&](const uint2& e, int i) {
-    const int b = min(i, total - 1) / per;
-    const float l = (float)log_sum[b];
-    if (e.x == 0 || l != l) return -INFINITY;
-    return fmaxf(scores[b] + ((unordered(e.x) - unordered(top[b])) - l), -FLT_MAX);
+    const int b = beam_of(min(i, total - 1));
+    const float at = near_offset[b];
+    if (e.x == 0 || at != at) return -INFINITY;
+    return fmaxf(at + (unordered(e.x) - top[b]), -FLT_MAX);
   };
   float near_own[kOwn], most = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    near_own[i] = near(own[i], tid + i * kThreads);
-    most = fmaxf(most, near_own[i]);
+  for (int k = 0; k < kOwn; ++k) {
+    near_own[k] = -INFINITY;
+    if (k * kThreads < (p.beams * p.pieces) << p.heads)
+      near_own[k] = near(own[k], head(k));
+    most = fmaxf(most, near_own[k]);
   }
-  for (int i = tid + kOwn * kThreads; i < total; i += kThreads)
-    most = fmaxf(most, near(entries[i], i));
   uint32_t lo, hi;
   range(ordered(most), sh, lo, hi);
-  float bar = unordered(threshold(ordered(most), lo, hi, kNone32, n));
-  bar -= (fabsf(bar) + 2.f * __uint_as_float(largest)) * 0x1p-19f;
-  if (!(bar > -INFINITY)) bar = -INFINITY;  // (fewer than n, or no finite margin)
+  auto lowered = [&](uint32_t key) {
+    float bar = unordered(key);
+    bar -= (fabsf(bar) + 2.f * __uint_as_float(largest)) * 0x1p-19f;
+    return bar > -INFINITY ? bar : -INFINITY;  // (fewer than n, or no finite margin)
+  };
+  float bar = lowered(threshold(ordered(most), lo, hi, kNone32, n));
   auto add = [&](int i, float y) {
-    if (y < bar || y == -INFINITY || i >= total) return;
+    if (y < bar || y == -INFINITY) return false;
     const int at = atomicAdd(&count, 1);
     if (at < kCand) which[at] = i;
+    return true;
   };
   if (most >= bar) {
+    uint32_t reached = 0;  // turns
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) add(tid + i * kThreads, near_own[i]);
-    for (int i = tid + kOwn * kThreads; i < total; i += kThreads)
-      add(i, near(entries[i], i));
+    for (int k = 0; k < kOwn; ++k)
+      if (add(head(k), near_own[k])) reached |= 1u << k;
+    // The last ones looked at of a piece: on, as far as they reach the bar.
+    if (1 << p.heads >= n) reached = 0;
+#pragma unroll 1
+    for (; reached; reached &= reached - 1) {
+      const int at = head(__ffs(reached) - 1), left = n - 1 - at % n;
+      if (n - left != 1 << p.heads) continue;
+      bool more = true;
+      for (int r = 1; more && r <= left; r += 4) {
+        float y[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          y[z] = r + z <= left ? near(entry(at + r + z), at + r + z) : -INFINITY;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) more = more && add(at + r + z, y[z]);
+      }
+    }
   }
   __syncthreads();
+  if (count > kCand) {
+    // The bar is too low: from the n-th highest of all.
+    int last = n;
+    const uint32_t nth = (uint32_t)nth_key(
+        [&](auto&& f) {
+          for (int k = 0; k < turns; ++k) {
+            const int i = k * kThreads + tid;
+            const float y = near(entry(i), i);
+            f(y > -INFINITY, ordered(y));
+          }
+        },
+        24, 0, 0, last, digits);
+    bar = lowered(nth);
+    if (tid == 0) count = 0;
+    __syncthreads();
+    for (int i = tid; i < total; i += kThreads) add(i, near(entries[i], i));
+    __syncthreads();
+  }
   // Those in 64 bits.
   for (int i = tid; i < min(count, kCand); i += kThreads)
     cand[i] = get(entries[which[i]], which[i]);
@@ -609,37 +741,50 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const Params p) {
     p.out_scores[at] = -INFINITY;
     p.out_parents[at] = p.out_tokens[at] = -1;
   }
-  if (c <= kCand) {
-    for (int i = tid; i < c; i += kThreads) {
-      const Cand a = cand[i];
+  auto rank_and_put = [&](int c) {
+    // Eight threads a result.
+    for (int i0 = 0; i0 < c; i0 += kThreads / 8) {
+      const int i = i0 + (tid >> 3);
+      const Cand a = i < c ? cand[i] : Cand{0, 0};
       int rank = 0;
-      for (int j = 0; j < c; ++j) rank += before(cand[j], a);
-      if (rank < n) put(rank, a);
+      for (int j = tid & 7; j < c; j += 8) rank += before(cand[j], a);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+      if (i < c && rank < n && (tid & 7) == 0) put(rank, a);
     }
+  };
+  if (c <= kCand) {
+    rank_and_put(c);
     return;
   }
-  // Many equal sums: one at a time (c > n of them).
-  Cand last{~0ull, 0};
-  for (int r = 0; r < n; ++r) {
-    Cand best{0, 0};
-    for (int i = tid; i < total; i += kThreads) {
-      const Cand a = get(entries[i], i);
-      if (a.y && before(last, a) && before(a, best)) best = a;
+  // Many equal results (c > n of them): the n-th highest, and of its equals the first.
+  auto each = [&](auto&& f) {
+    for (int k = 0; k < turns; ++k) {
+      const int i = k * kThreads + tid;
+      const uint2 e = entry(i);
+      const Cand a = near(e, i) >= bar ? get(e, min(i, total - 1)) : Cand{0, 0};
+      f(a);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const Cand a{__shfl_xor_sync(0xffffffffu, best.y, o),
-                   __shfl_xor_sync(0xffffffffu, best.at, o)};
-      if (before(a, best)) best = a;
-    }
-    if (lane == 0) best_of[tid >> 5] = best;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w)
-      if (before(best_of[w], best)) best = best_of[w];
-    last = best;
-    if (tid == 0) put(r, best);
-    __syncthreads();
-  }
+  };
+  int last = n;
+  const uint64_t y = nth_key(
+      [&](auto&& f) { each([&](const Cand& a) { f(a.y != 0, a.y); }); }, 56, 0, 0, last,
+      digits);
+  uint64_t at = 0;
+  if (last > 0)
+    at = nth_key(
+        [&](auto&& f) {
+          each([&](const Cand& a) { f(a.y == y, ~a.at & 0xffffffffffffull); });
+        },
+        40, 0, 0, last, digits);
+  if (tid == 0) count = 0;
+  __syncthreads();
+  each([&](const Cand& a) {
+    if (a.y > y || (a.y == y && (~a.at & 0xffffffffffffull) >= at))
+      cand[atomicAdd(&count, 1)] = a;
+  });
+  __syncthreads();
+  rank_and_put(count);
 }
 
 // Pieces of a row, of 2048 logits at least: one to three rounds of CTAs (four on an
@@ -734,19 +879,22 @@ extern "C" kv_status kv_beam_select(const void* logits, int32_t logits_type,
   p.vocab = vocab;
   p.n = n_out;
   p.beams = beams;
+  for (p.heads = 0; (2 << p.heads) * p.pieces * beams <= 2048 && 1 << p.heads < n_out;)
+    ++p.heads;
   cudaStream_t st = (cudaStream_t)stream;
   const dim3 grid((unsigned)p.pieces, (unsigned)rows);
   const bool big = vocab / p.pieces > 4096;  // steps of 4096 logits, else of 2048
-  // (Below the 48 KB that need no opting in.)
-  const int ring = 2 * W::kThreads * (big ? 16 : 8) * (f32 ? 4 : 2);
+  auto launch = [&](auto kernel, int ring) {
+    kernel<<<grid, W::kThreads, ring, st>>>(p);
+  };
   if (f32 && big)
-    W::piece_kernel<float, 16><<<grid, W::kThreads, ring, st>>>(p);
+    launch(W::piece_kernel<float, 16>, W::kRingBytes<float, 16>);
   else if (f32)
-    W::piece_kernel<float, 8><<<grid, W::kThreads, ring, st>>>(p);
+    launch(W::piece_kernel<float, 8>, W::kRingBytes<float, 8>);
   else if (big)
-    W::piece_kernel<__nv_bfloat16, 16><<<grid, W::kThreads, ring, st>>>(p);
+    launch(W::piece_kernel<__nv_bfloat16, 16>, W::kRingBytes<__nv_bfloat16, 16>);
   else
-    W::piece_kernel<__nv_bfloat16, 8><<<grid, W::kThreads, ring, st>>>(p);
+    launch(W::piece_kernel<__nv_bfloat16, 8>, W::kRingBytes<__nv_bfloat16, 8>);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
     e = pkv::launch_early(W::group_kernel, n_groups, W::kThreads, 0, st, p);

@@ -138,6 +138,49 @@ def test_sorted_and_reversed_logits():
     check(x.flip(1).contiguous(), s, 1, 3, 64)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("n", [5, 128])
+def test_rows_whose_candidates_lie_together(dtype, n):
+    """Equal logits all over a long row, and masked rows with one run of tokens that
+    may follow: more candidates than fit, of few threads or of all."""
+    V = 151936
+    x = torch.full((3, V), -math.inf, dtype=dtype, device="cuda")
+    x[0] = 0.25
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x[1, 70001:73001] = torch.randn(3000, generator=g, device="cuda").to(dtype)
+    x[2, 151000:] = -2.0
+    x[2, 5] = -1.0
+    s = torch.tensor([-1.0, -3.0, -2.0], device="cuda")
+    check(x, s, 1, 3, n)
+    check(x, s, 3, 1, n)
+    check(x[1:, 70000:], s[1:], 2, 1, n)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_equal_results_of_many_beams(dtype):
+    """More equal results than fit, over the beams of a group."""
+    x = torch.zeros(64, 40000, dtype=dtype, device="cuda")
+    x[:, 20000:] = -3.0
+    s = torch.zeros(64, device="cuda")
+    check(x, s, 2, 32, 128)
+    x[:, ::2] = 1.0
+    check(x, s, 2, 32, 60)
+    s[3::7] = 0.5
+    check(x, s, 2, 32, 60)
+    check(x[:1], s[:1], 1, 1, 128)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_logits_that_rise_along_the_row(dtype):
+    """References that move in some threads, by more than exponentials can hold."""
+    x = torch.randn(640, 20000, device="cuda") * 2
+    x += torch.arange(20000, device="cuda") // 1500 * 45.0
+    x[1::2, :9000] = -math.inf
+    x[2::4, 11000:] -= 900.0
+    s = torch.linspace(-3, -1, 640, device="cuda")
+    check(x.to(dtype), s, 160, 4, 12)
+
+
 def test_captured_and_same_every_time():
     x, s = make(6, 8, 32003, torch.bfloat16, 6)
     ws = torch.zeros(B.kv_beam_select_workspace_size(6, 8, 32003, 16),
