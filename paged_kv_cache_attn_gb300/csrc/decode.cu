@@ -329,6 +329,12 @@ __global__ void __launch_bounds__(128, 3)
   if (per_warp) {
     // The warp's own item: its state is the partial result.  Lane (gq, tq)
     // holds rows gq and gq + 8, columns 8 nt + 2 tq and + 1.
+    if (p.out) {
+      put_results<D>(p, it, lane, l_r[0], l_r[1], [&](int nt, int hr) {
+        return make_float2(o[nt][2 * hr], o[nt][2 * hr + 1]);
+      });
+      return;
+    }
     float* dst = p.o + (int64_t)it.prow_base * D;
 #pragma unroll
     for (int nt = 0; nt < D / 8; ++nt) {
@@ -381,6 +387,7 @@ __global__ void __launch_bounds__(128, 3)
         lstar += wgt[w] * l_sh[w][row];
       }
       float* dst = p.o + (int64_t)(it.prow_base + row) * D + c0;
+      const float inv = 1.f / lstar;
 #pragma unroll
       for (int c = 0; c < D / 8; c += 4) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -393,9 +400,15 @@ __global__ void __launch_bounds__(128, 3)
           acc.z += wgt[w] * v.z;
           acc.w += wgt[w] * v.w;
         }
-        *reinterpret_cast<float4*>(dst + c) = acc;
+        if (p.out)
+          *reinterpret_cast<uint2*>(p.out + result_row(p, it, row) * D + c0 + c) =
+              make_uint2(pack_bf16(acc.x * inv, acc.y * inv),
+                         pack_bf16(acc.z * inv, acc.w * inv));
+        else
+          *reinterpret_cast<float4*>(dst + c) = acc;
       }
-      if ((threadIdx.x & 7) == 0) p.ml[it.prow_base + row] = make_float2(mstar, lstar);
+      if (!p.out && (threadIdx.x & 7) == 0)
+        p.ml[it.prow_base + row] = make_float2(mstar, lstar);
     }
   }
 }
@@ -796,6 +809,11 @@ static kv_status decode_impl(
   sp.v_step = static_cast<const uint4*>(v_step);
   sp.k_pool = static_cast<uint4*>(const_cast<void*>(k_pool));
   sp.v_pool = static_cast<uint4*>(const_cast<void*>(v_pool));
+  // A step over selected blocks whose plan cuts nothing has nothing to merge.
+  const bool whole = early && info->n_tile_items == 0 && Hkv == 1 &&
+                     info->n_row_items ==
+                         (int64_t)nb * ((sp.G + pkv::kRowTile - 1) / pkv::kRowTile);
+  sp.out = whole ? static_cast<__nv_bfloat16*>(out) : nullptr;
 
   // The plan lives on the device; its layout is fixed by the host header
   // fields mirrored in *info.
@@ -888,6 +906,7 @@ static kv_status decode_impl(
     if (e != cudaSuccess)
       return fail(KV_ERR_CUDA, "join: %s", cudaGetErrorString(e));
   }
+  if (whole) return KV_OK;
   pkv::MergeParams mp;
   mp.csr_ptr = plan + off_ptr;
   mp.csr = reinterpret_cast<const pkv::MergeEntry*>(plan + off_ent);

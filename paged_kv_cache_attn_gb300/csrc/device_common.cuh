@@ -188,6 +188,9 @@ struct SplitParams {
   const uint4* v_step;
   uint4* k_pool;
   uint4* v_pool;
+  // Not null: every item has all keys of its rows and writes their results here
+  // ([nb][Hq][d], one kv-head); else partial rows.
+  __nv_bfloat16* out;
 };
 
 // A work item read from the (caller-uploaded) plan must stay inside the
@@ -201,6 +204,31 @@ __device__ __forceinline__ bool item_ok(const WorkItem& it,
          it.blk_begin < it.blk_end && it.blk_end <= p.max_blocks &&
          it.prow_base >= 0 &&
          (int64_t)it.prow_base + it.nrows <= p.partial_rows;
+}
+
+// Where an item's row goes in p.out.
+__device__ __forceinline__ int64_t result_row(const SplitParams& p, const WorkItem& it,
+                                              int row) {
+  return (int64_t)it.branch0 * p.Hq + it.row0 + row;
+}
+
+// The results of a warp's own item: lane (gq, tq) has of rows gq and gq + 8 (hr) the
+// columns 8 nt + 2 tq and + 1, value(nt, hr), and the rows' sums.
+template <int D, typename Value>
+__device__ __forceinline__ void put_results(const SplitParams& p, const WorkItem& it,
+                                            int lane, float l0, float l1, Value value) {
+  const int gq = lane >> 2, tq = lane & 3;
+#pragma unroll
+  for (int hr = 0; hr < 2; ++hr) {
+    if (gq + 8 * hr >= it.nrows) continue;
+    const float inv = 1.f / (hr ? l1 : l0);
+    __nv_bfloat16* dst = p.out + result_row(p, it, gq + 8 * hr) * D + 2 * tq;
+#pragma unroll
+    for (int nt = 0; nt < D / 8; ++nt) {
+      const float2 v = value(nt, hr);
+      *reinterpret_cast<uint32_t*>(dst + 8 * nt) = pack_bf16(v.x * inv, v.y * inv);
+    }
+  }
 }
 
 }  // namespace pkv

@@ -80,28 +80,43 @@ __device__ __forceinline__ uint32_t max2h(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Bounds of the first `valid` slots of one (block, head) tile, by one warp.  A lane
-// has kPer dimensions (16 bytes) of every kRows-th row.
+// A warp's part of a tile's keys: a lane has kPer dimensions (16 bytes) of every
+// kRows-th row.
+template <int D, bool E4M3>
+struct TileKeys {
+  static constexpr int kPer = E4M3 ? 16 : 8;
+  static constexpr int kChunks = D / kPer;      // 16-byte chunks of a row
+  static constexpr int kRows = 32 / kChunks;    // rows of a load
+  static constexpr int kLoads = 16 / kRows;
+  uint4 x[kLoads];
+  float scale;
+
+  __device__ __forceinline__ void load(const BoundsParams& p, int64_t tile, int valid,
+                                       int lane) {
+    const int c = lane % kChunks, r0 = lane / kChunks;
+    const uint8_t* src = p.k + tile * (16 * D * (E4M3 ? 1 : 2));
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      // Slots past the branch's length: its last token again.
+      const int t = min(i * kRows + r0, valid - 1);
+      const int at = E4M3 ? t * D + ((D == 128 ? c ^ (t & 7) : c) << 4)
+                          : (t * kChunks + c) * 16;
+      x[i] = *reinterpret_cast<const uint4*>(src + at);
+    }
+    scale = E4M3 ? p.scales[tile].x : 1.f;
+  }
+};
+
+// Bounds of one (block, head) tile, by one warp.
 template <int D, bool E4M3>
 __device__ __forceinline__ void tile_bounds(const BoundsParams& p, int64_t tile,
-                                            int valid, int lane) {
-  constexpr int kPer = E4M3 ? 16 : 8;
-  constexpr int kChunks = D / kPer;      // 16-byte chunks of a row
-  constexpr int kRows = 32 / kChunks;    // rows of a load
-  constexpr int kLoads = 16 / kRows;
-  const int c = lane % kChunks, r0 = lane / kChunks;
-  const uint8_t* src = p.k + tile * (16 * D * (E4M3 ? 1 : 2));
-  uint4 x[kLoads];
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    // Slots past the branch's length: its last token again.
-    const int t = min(i * kRows + r0, valid - 1);
-    const int at = E4M3 ? t * D + ((D == 128 ? c ^ (t & 7) : c) << 4)
-                        : (t * kChunks + c) * 16;
-    x[i] = *reinterpret_cast<const uint4*>(src + at);
-  }
-  float scale = 1.f;
-  if (E4M3) scale = p.scales[tile].x;
+                                            const TileKeys<D, E4M3>& keys, int lane) {
+  using K = TileKeys<D, E4M3>;
+  constexpr int kPer = K::kPer, kChunks = K::kChunks, kRows = K::kRows,
+                kLoads = K::kLoads;
+  const int c = lane % kChunks;
+  const auto& x = keys.x;
+  const float scale = keys.scale;
   // Pairs of dimensions, least and largest.
   constexpr int kPairs = kPer / 2;
   uint32_t lo[kPairs], hi[kPairs];
@@ -186,14 +201,18 @@ __device__ __forceinline__ void tile_bounds(const BoundsParams& p, int64_t tile,
   if (lane == 0) p.bound_scales[tile] = odd ? INFINITY : pow2f(e);
 }
 
-// A warp for each (run of new tokens, kv-head): every block that a token of the run
-// is the first new one of.  kRun: tokens of a run (steps of one token a branch: 1).
-template <int D, bool E4M3>
+// A warp for each (run of new tokens, kHeads kv-heads): every block that a token of the
+// run is the first new one of.  run: tokens of a run (steps of one token a branch: 1).
+// Finding a block takes four reads that wait for one another; with more tiles than warps
+// that run at once, a warp has four heads of each block, whose keys are in flight
+// together.
+template <int D, bool E4M3, int kHeads>
 __global__ void __launch_bounds__(256) bounds_kernel(const BoundsParams p, int run) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int64_t tok0 = w / p.Hkv * run;
-  const int h = (int)(w % p.Hkv);
+  const int per_run = (p.Hkv + kHeads - 1) / kHeads;
+  const int64_t tok0 = w / per_run * run;
+  const int h = (int)(w % per_run) * kHeads;
   if (tok0 >= p.total) return;
   const int end = (int)min(tok0 + run, (int64_t)p.total);
   int tok = (int)tok0, b = tok;
@@ -223,8 +242,15 @@ __global__ void __launch_bounds__(256) bounds_kernel(const BoundsParams p, int r
       if (phys < 0 || phys >= p.num_blocks) {
         if (lane == 0) record_status(p.status, KV_ERR_DEVICE, phys);
       } else {
-        tile_bounds<D, E4M3>(p, (int64_t)phys * p.Hkv + h,
-                             min(16, L - (int)(pos & ~15ll)), lane);
+        const int64_t tile = (int64_t)phys * p.Hkv + h;
+        const int valid = min(16, L - (int)(pos & ~15ll));
+        TileKeys<D, E4M3> keys[kHeads];
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+          if (i == 0 || h + i < p.Hkv) keys[i].load(p, tile + i, valid, lane);
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+          if (i == 0 || h + i < p.Hkv) tile_bounds<D, E4M3>(p, tile + i, keys[i], lane);
       }
     }
     if (!p.row_offsets) {
@@ -302,7 +328,7 @@ __device__ __forceinline__ float quantise(const __nv_bfloat16* src, bool there,
   return there ? (odd ? 0.f : pow2f(e)) : -1.f;
 }
 
-// grid (block ranges, Hkv, nb); a warp has kSteps x 16 consecutive blocks.  Up to 16
+// grid (Hkv, block ranges, nb); a warp has kSteps x 16 consecutive blocks.  Up to 16
 // heads are the rows of the products, eight blocks their columns; lane 4 n + t has
 // bytes [16 t + 64 j, + 16) of block n's record, which are its columns of four products
 // in any order that the queries' fragments share.  The records of 16 blocks (4 KB at
@@ -317,15 +343,15 @@ __global__ void __launch_bounds__(256, kFew ? 2 : 1)
   __shared__ __align__(16) __half qs[(kFew ? 8 : kMaxG) * kRow];
   __shared__ float qe[kFew ? 8 : kMaxG];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int b = blockIdx.z, h = blockIdx.y;
-  if (blockIdx.x == 0 && b == 0 && h == 0 && threadIdx.x == 0)
+  const int b = blockIdx.z, h = blockIdx.x, part = blockIdx.y;
+  if (part == 0 && b == 0 && h == 0 && threadIdx.x == 0)
     *p.status = DeviceStatus{};  // the next kernel records
   const int L = p.seq_lens[b];
   const int nblk = L < 1 || L > (int64_t)p.max_blocks * 16 ? 0 : (L + 15) / 16;
   // A branch of few blocks has them all.
-  if (nblk <= p.n_sel || blockIdx.x * kCtaBlocks >= nblk) return;
+  if (nblk <= p.n_sel || part * kCtaBlocks >= nblk) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int blk0 = blockIdx.x * kCtaBlocks + warp * kWarpBlocks;
+  const int blk0 = part * kCtaBlocks + warp * kWarpBlocks;
   const int32_t* table = p.tables + (int64_t)b * p.max_blocks;
   // A block id outside the pool (recorded by the next kernel) has no score.
   constexpr int kIds = (kSteps + 1) / 2;
@@ -689,7 +715,7 @@ void launch_scores(const SelectParams& p, cudaStream_t st) {
   const int64_t ctas = (int64_t)((p.max_blocks + 511) / 512) * p.Hkv * p.nb;
   const int steps = ctas >= 2 * 2 * 152 ? 4 : 2;
   const int blocks = kWarps * 16 * steps;
-  const dim3 grid((unsigned)((p.max_blocks + blocks - 1) / blocks), (unsigned)p.Hkv,
+  const dim3 grid((unsigned)p.Hkv, (unsigned)((p.max_blocks + blocks - 1) / blocks),
                   (unsigned)p.nb);
   if (p.G <= 8 && steps == 4)
     score_kernel<D, true, 4><<<grid, 256, 0, st>>>(p);
@@ -755,17 +781,24 @@ kv_status run_bounds(const void* k_pool, const void* kv_scales, bool e4m3,
   p.max_blocks = max_blocks;
   p.Hkv = Hkv;
   const int run = row_offsets ? 16 : 1;
-  const int64_t ctas = (((int64_t)total + run - 1) / run * Hkv + 7) / 8;
+  const int64_t runs = ((int64_t)total + run - 1) / run;
+  // Measured, of 8 kv-heads: 30000 tiles of 2 KB 20 -> 17 us (d = 128 e4m3), 14 -> 12
+  // (d = 64), 15.6 -> 11.3 (d = 64 e4m3); 12000 of them 9.7 -> 10.7.  Tiles of 4 KB are
+  // better one a warp (27 us, two at a time 32).
+  const int heads =
+      runs * Hkv > 64 * 152 * 2 && Hkv >= 4 && (d == 64 || e4m3) ? 4 : 1;
+  const int64_t ctas = (runs * ((Hkv + heads - 1) / heads) + 7) / 8;
   if (ctas > INT32_MAX) return fail(KV_ERR_INVALID_ARG, "too many tokens");
   cudaStream_t st = (cudaStream_t)stream;
+  auto launch = [&](auto kernel) { kernel<<<(unsigned)ctas, 256, 0, st>>>(p, run); };
   if (d == 128 && e4m3)
-    bounds_kernel<128, true><<<(unsigned)ctas, 256, 0, st>>>(p, run);
+    launch(heads == 1 ? bounds_kernel<128, true, 1> : bounds_kernel<128, true, 4>);
   else if (d == 128)
-    bounds_kernel<128, false><<<(unsigned)ctas, 256, 0, st>>>(p, run);
+    launch(bounds_kernel<128, false, 1>);
   else if (e4m3)
-    bounds_kernel<64, true><<<(unsigned)ctas, 256, 0, st>>>(p, run);
+    launch(heads == 1 ? bounds_kernel<64, true, 1> : bounds_kernel<64, true, 4>);
   else
-    bounds_kernel<64, false><<<(unsigned)ctas, 256, 0, st>>>(p, run);
+    launch(heads == 1 ? bounds_kernel<64, false, 1> : bounds_kernel<64, false, 4>);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "bounds kernel: %s", cudaGetErrorString(e));
@@ -790,16 +823,25 @@ kv_status virtual_batch(int32_t nb, int32_t Hq, int32_t Hkv, int64_t num_blocks)
   return KV_OK;
 }
 
-// Blocks of a split-KV item.  All branches are about as long as the selection, so
-// that items go by rounds of the CTAs that run at once: 256 branches of 128 blocks as
-// 512 items of 64 left 56 for a second round (56 us), as 768 of 43 they take 46.  An
-// item costs about as much as kItem more blocks (its table entries and first loads), a
-// piece of a branch kPiece (the merge's).
-int32_t pick_cut(const std::vector<int32_t>& lens, int32_t G, int32_t num_sms) {
+// Blocks of a split-KV item.  Nothing is cut, and there is no merge, where that leaves
+// work for the SMs: one item for most of them, of the e4m3 kernel, which needs more
+// warps, three for two (128 blocks each, 256 items bf16 45 us, cut in three 53; 192
+// items e4m3 44 us, in two 32), fewer of short ones (32 blocks, 80 items 10.1 us, cut in
+// four 12.4).  A little more than the CTAs that run at once are halved (480 items bf16
+// 99 -> 91 us, e4m3 86 -> 79).  Else all branches are about as long as the selection, so
+// that items go by rounds of the CTAs that run at once.  An item costs about as much as
+// kItem more blocks (its table entries and first loads), a piece of a branch kPiece (the
+// merge's).
+int32_t pick_cut(const std::vector<int32_t>& lens, int32_t G, bool e4m3,
+                 int32_t num_sms) {
   constexpr double kItem = 14, kPiece = 1;
   const int64_t slots = (int64_t)kSplitCtasPerSm * num_sms;
   int32_t longest = 1, best = 1;
   for (const int32_t L : lens) longest = std::max(longest, (L + 15) / 16);
+  const int64_t whole = (int64_t)lens.size() * ((G + kRowTile - 1) / kRowTile);
+  const double few = longest <= 32 ? 0.5 : e4m3 ? 1.6 : 0.8;
+  if (whole > slots && whole < slots + slots / 3) return (longest + 1) / 2;
+  if ((double)whole >= few * num_sms) return longest;
   double least = 1e300;
   // From items of a whole branch (at most 256 blocks) down.
   for (int32_t cut = std::min(longest, 256); cut >= 8 || cut == std::min(longest, 256);
@@ -968,8 +1010,9 @@ extern "C" kv_status paged_selected_plan(int32_t nb, int32_t Hq, int32_t Hkv,
     }
     return pkv::decode_plan_of_rows(
         nb * Hkv, Hq / Hkv, head_dim, n_sel, lens.data(), num_sms, flags,
-        pkv::sel::pick_cut(lens, Hq / Hkv, num_sms > 0 ? num_sms : 152), plan, plan_cap,
-        info);
+        pkv::sel::pick_cut(lens, Hq / Hkv, flags & KV_PLAN_KV_E4M3,
+                           num_sms > 0 ? num_sms : 152),
+        plan, plan_cap, info);
   } catch (const std::bad_alloc&) {
     return fail(KV_ERR_OOM, "no host memory for the plan");
   }

@@ -161,10 +161,10 @@ class Tree:
                     16 * n - (16 * nblk - int(self.lens[b]))
         return sel, st, sl
 
-    def attend(self, n_sel, sel, st, sl):
+    def attend(self, n_sel, sel, st, sl, sms=152):
         flags = B.KV_PLAN_KV_E4M3 if self.kv == "e4m3" else 0
         plan, info = B.paged_selected_plan(self.nb, self.Hq, self.Hkv, self.d,
-                                           self.mb, self.lens, n_sel, 152, flags)
+                                           self.mb, self.lens, n_sel, sms, flags)
         ws = torch.empty(info.workspace_bytes, dtype=torch.uint8, device="cuda")
         out = torch.empty_like(self.q)
         tail = (self.blocks, st, sl, self.nb, self.Hq, self.Hkv, self.d, n_sel,
@@ -189,6 +189,7 @@ class Tree:
                                      torch.full((G,), len(tok), device="cuda"))
                 err = (out[b, h * G:(h + 1) * G].double() - want).abs()
                 assert (err <= tol).all()
+        return out, info
 
 
 LENS = [1, 15, 16, 17, 33, 160, 161, 700, 15999]
@@ -210,6 +211,16 @@ def test_bounds_of_chunks(d, kv):
     token, whole branches."""
     t = Tree(2, 2, d, [40, 16, 5, 700, 33, 64, 1, 300, 18], kv)
     new = [7, 16, 0, 700, 1, 48, 1, 131, 2]
+    t.update(new)
+    t.check_bounds(new)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [128, 64])
+def test_bounds_of_long_prompts(d, kv):
+    """More tiles than warps, of kv-heads that do not come in fours."""
+    t = Tree(6, 6, d, [30001, 23, 25000], kv)
+    new = [29990, 9, 25000]
     t.update(new)
     t.check_bounds(new)
 
@@ -276,6 +287,26 @@ def test_selected_steps(Hq, Hkv, d, kv):
     t = Tree(Hq, Hkv, d, [1, 200, 2000, 4097, 16 * 24, 16 * 24 + 1, 9000], kv)
     t.exact_bounds()
     t.attend(24, *t.check_select(24, 2, 3))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (3, 1, 64), (40, 2, 128),
+                                      (17, 1, 64)])
+def test_plans_that_cut_and_that_do_not(Hq, Hkv, d, kv):
+    """Whole branches write their results themselves, a CTA or (up to 16 blocks) a warp
+    each; halves and more pieces are merged."""
+    for n_sel in (9, 40):
+        t = Tree(Hq, Hkv, d, [1, 30, 16 * 16, 16 * 17, 3000, 5001, 700], kv, seed=6)
+        t.exact_bounds()
+        picked = t.check_select(n_sel, 1, 2)
+        rows = t.nb * Hkv * -(-Hq // Hkv // 16)
+        counts = set()
+        for sms in (1, -(-rows * 2 // 7), 152):
+            out, info = t.attend(n_sel, *picked, sms=sms)
+            counts.add(info.n_row_items == rows)
+            again, _ = t.attend(n_sel, *picked, sms=sms)
+            assert torch.equal(out, again)
+        assert counts == {True, False} or n_sel == 9
 
 
 @pytest.mark.parametrize("n_sel,first,last", [(1, 0, 1), (2, 1, 1), (2, 0, 2),
