@@ -416,12 +416,6 @@ __global__ void __launch_bounds__(128, 3)
     // The warp's own item: its state is the partial result (O back to plain
     // units, x vref).  Lane (gq, tq) holds rows gq and gq + 8, columns
     // 8 nt + 2 tq and + 1.
-    if (p.out) {
-      put_results<D>(p, it, lane, l_r[0], l_r[1], [&](int nt, int hr) {
-        return make_float2(o[nt][2 * hr] * vref, o[nt][2 * hr + 1] * vref);
-      });
-      return;
-    }
     float* dst = p.o + (int64_t)it.prow_base * D;
 #pragma unroll
     for (int nt = 0; nt < D / 8; ++nt) {
@@ -476,7 +470,6 @@ __global__ void __launch_bounds__(128, 3)
         lstar += wgt[w] * l_sh[w][row];
       }
       float* dst = p.o + (int64_t)(it.prow_base + row) * D + c0;
-      const float inv = 1.f / lstar;
 #pragma unroll
       for (int c = 0; c < D / 8; c += 4) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -489,14 +482,9 @@ __global__ void __launch_bounds__(128, 3)
           acc.z += wgt[w] * v.z;
           acc.w += wgt[w] * v.w;
         }
-        if (p.out)
-          *reinterpret_cast<uint2*>(p.out + result_row(p, it, row) * D + c0 + c) =
-              make_uint2(pack_bf16(acc.x * inv, acc.y * inv),
-                         pack_bf16(acc.z * inv, acc.w * inv));
-        else
-          *reinterpret_cast<float4*>(dst + c) = acc;
+        *reinterpret_cast<float4*>(dst + c) = acc;
       }
-      if (!p.out && (threadIdx.x & 7) == 0)
+      if ((threadIdx.x & 7) == 0)
         p.ml[it.prow_base + row] = make_float2(mstar, lstar);
     }
   }

@@ -277,6 +277,7 @@ struct SelectParams {
   DeviceStatus* status;
   int64_t num_blocks;
   int nb, max_blocks, stride, Hq, Hkv, G, n_sel, n_first, n_last;
+  int heads;                   // of a CTA of the scores (G <= 8; else 1)
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4],
@@ -301,57 +302,93 @@ __device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
 
 constexpr int kWarps = 8;
 
-// A query head as whole numbers of at most 127 times a power of two, by one warp: its
-// f16 values to dst, the power returned (-1: no such head, all zeros).
+// Eight query heads (those from G on are zeros) as whole numbers of at most 127 times a
+// power of two, four lanes a head: their f16 values to dst, the powers to e (-1: no such
+// head).
 template <int D>
-__device__ __forceinline__ float quantise(const __nv_bfloat16* src, bool there,
-                                          __half* dst, int lane) {
-  constexpr int V = D / 32;
-  float x[V], amax = 0.f;
+__device__ __forceinline__ void quantise8(const __nv_bfloat16* q, int G, __half* dst,
+                                          int row, float* e, int lane) {
+  constexpr int V = D / 32;  // 16-byte pieces of a lane
+  const int g = lane >> 2, part = lane & 3;
+  uint4 w[V];
+  float amax = 0.f;
   bool odd = false;
+  auto value = [](uint32_t pair, int half) {
+    return __uint_as_float(half ? pair & 0xffff0000u : pair << 16);
+  };
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    x[i] = there ? __bfloat162float(src[lane * V + i]) : 0.f;
-    odd |= !(fabsf(x[i]) < INFINITY);
-    amax = fmaxf(amax, fabsf(x[i]));
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (g < G) w[i] = *reinterpret_cast<const uint4*>(q + g * D + (i * 4 + part) * 8);
+    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = fabsf(value(x[k / 2], k & 1));
+      odd |= !(a < INFINITY);
+      amax = fmaxf(amax, a);
+    }
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
+  for (int o = 1; o < 4; o <<= 1) {
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  odd = __any_sync(0xffffffffu, odd);
-  const int e = bound_exponent(amax);
-  const float inv = pow2f(-e);
+    odd |= __shfl_xor_sync(0xffffffffu, (int)odd, o) != 0;
+  }
+  const int ex = bound_exponent(amax);
+  const float inv = pow2f(-ex);
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    dst[lane * V + i] = __float2half_rn(
-        odd ? 0.f : fminf(fmaxf(rintf(x[i] * inv), -127.f), 127.f));
-  return there ? (odd ? 0.f : pow2f(e)) : -1.f;
+  for (int i = 0; i < V; ++i) {
+    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+        f[z] = odd ? 0.f
+                   : fminf(fmaxf(rintf(value(x[k], z) * inv), -127.f), 127.f);
+      const __half2 h = __floats2half2_rn(f[0], f[1]);
+      y[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(dst + g * row + (i * 4 + part) * 8) =
+        make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  if (part == 0) e[g] = g < G ? (odd ? 0.f : pow2f(ex)) : -1.f;
 }
 
-// grid (Hkv, block ranges, nb); a warp has kSteps x 16 consecutive blocks.  Up to 16
-// heads are the rows of the products, eight blocks their columns; lane 4 n + t has
-// bytes [16 t + 64 j, + 16) of block n's record, which are its columns of four products
-// in any order that the queries' fragments share.  The records of 16 blocks (4 KB at
-// D = 128) are in flight while those before are used, the first while the queries are
-// quantised.  kFew: at most 8 heads, kept in registers (the rows after them are zeros);
-// else 16 at a time from shared memory.
+// grid (block ranges, groups of p.heads kv-heads, nb); a warp has a head and kSteps x 16
+// consecutive blocks.  Up to 16 query heads are the rows of the products, eight blocks
+// their columns; lane 4 n + t has bytes [16 t + 64 j, + 16) of block n's record, which
+// are its columns of four products in any order that the queries' fragments share.  The
+// records of 16 blocks (4 KB at D = 128) are in flight while those before are used, the
+// first while the queries are quantised.
+// kFew: at most 8 query heads a kv-head, kept in registers (the rows after them are
+// zeros), and a CTA's warps have several kv-heads of the same blocks, whose records lie
+// side by side.  Else 16 query heads at a time from shared memory, one kv-head a CTA.
+// 32 x ~32000 tokens, 133 MB: 35 us; the reads alone 28, the products alone 26, with 16
+// warps an SM to run them beside each other.  (Through bulk copies to shared memory 37
+// us, 16-byte ones 39; 24 warps with one buffer and the queries in shared memory 32, but
+// 48 mixed branches 15 instead of 12.)
 template <int D, bool kFew, int kSteps>
-__global__ void __launch_bounds__(256, kFew ? 2 : 1)
+__global__ void __launch_bounds__(32 * kWarps, kFew ? 2 : 1)
     score_kernel(const SelectParams p) {
-  constexpr int kWarpBlocks = 16 * kSteps, kCtaBlocks = kWarps * kWarpBlocks;
+  constexpr int kWarpBlocks = 16 * kSteps;
   constexpr int kRow = D + 8;  // a head's f16 values in shared memory
-  __shared__ __align__(16) __half qs[(kFew ? 8 : kMaxG) * kRow];
-  __shared__ float qe[kFew ? 8 : kMaxG];
+  __shared__ __align__(16) __half qs[(kFew ? kWarps * 8 : kMaxG) * kRow];
+  __shared__ float qe_all[kFew ? kWarps * 8 : kMaxG];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int b = blockIdx.z, h = blockIdx.x, part = blockIdx.y;
-  if (part == 0 && b == 0 && h == 0 && threadIdx.x == 0)
+  const int b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && b == 0 && blockIdx.y == 0 && threadIdx.x == 0)
     *p.status = DeviceStatus{};  // the next kernel records
   const int L = p.seq_lens[b];
   const int nblk = L < 1 || L > (int64_t)p.max_blocks * 16 ? 0 : (L + 15) / 16;
+  const int heads = kFew ? p.heads : 1, ranges = kWarps / heads;
+  const int64_t cta_blocks = (int64_t)ranges * kWarpBlocks;
   // A branch of few blocks has them all.
-  if (nblk <= p.n_sel || part * kCtaBlocks >= nblk) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int blk0 = part * kCtaBlocks + warp * kWarpBlocks;
+  if (nblk <= p.n_sel || blockIdx.x * cta_blocks >= nblk) return;
+  const int h = blockIdx.y * heads + warp % heads;
+  const int blk0 = (int)(blockIdx.x * cta_blocks) + warp / heads * kWarpBlocks;
+  // (No barrier follows where kFew.)
+  if (kFew && (h >= p.Hkv || warp >= ranges * heads || blk0 >= nblk)) return;
   const int32_t* table = p.tables + (int64_t)b * p.max_blocks;
   // A block id outside the pool (recorded by the next kernel) has no score.
   constexpr int kIds = (kSteps + 1) / 2;
@@ -382,18 +419,22 @@ __global__ void __launch_bounds__(256, kFew ? 2 : 1)
   for (int i = 0; i < kIds; ++i)
     scales[i] = phys[i] >= 0 ? p.bound_scales[(int64_t)phys[i] * p.Hkv + h] : 0.f;
   const int G = p.G, rows = kFew ? 8 : (G + 15) & ~15;
-  for (int g = warp; g < rows; g += kWarps) {
-    const float e = quantise<D>(
-        p.q + ((int64_t)b * p.Hq + (int64_t)h * G + min(g, G - 1)) * D, g < G,
-        qs + g * kRow, lane);
-    if (lane == 0) qe[g] = e;
+  const __nv_bfloat16* q = p.q + ((int64_t)b * p.Hq + (int64_t)h * G) * D;
+  __half* const own = qs + (kFew ? warp * 8 * kRow : 0);
+  float* const qe = qe_all + (kFew ? warp * 8 : 0);
+  if constexpr (kFew) {
+    quantise8<D>(q, G, own, kRow, qe, lane);
+    __syncwarp();
+  } else {
+    for (int g = 8 * warp; g < rows; g += 8 * kWarps)
+      quantise8<D>(q + (int64_t)g * D, G - g, own + g * kRow, kRow, qe + g, lane);
+    __syncthreads();
+    if (blk0 >= nblk) return;
   }
-  __syncthreads();
-  if (blk0 >= nblk) return;
   // The least values meet the queries' negative numbers, the largest the positive
   // ones.
   auto fragment = [&](int g, int j, uint32_t (&f)[8]) {
-    const __half* src = qs + g * kRow + (j * 64) % D + t * 16;
+    const __half* src = own + g * kRow + (j * 64) % D + t * 16;
     const uint4 v0 = *reinterpret_cast<const uint4*>(src);
     const uint4 v1 = *reinterpret_cast<const uint4*>(src + 8);
     const uint32_t v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
@@ -524,18 +565,23 @@ __global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) ids[i] = 8 * tid + i < nblk ? table[8 * tid + i] : 0;
   // Scores, and a cleared status word.  (The scores' kernel lets this one start beside
-  // it: 1 x 131072 23.7 -> 22.7 us, 32 x ~32000 98 -> 97 us.)
+  // it.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (bad && tid == 0) record_status(p.status, KV_ERR_DEVICE, L);
-  auto check = [&](int phys) {
-    const bool in = phys >= 0 && phys < p.num_blocks;
-    if (!in && h == 0) record_status(p.status, KV_ERR_DEVICE, phys);
-    return in;
-  };
+  // Ids outside the pool (as unsigned numbers no less than its blocks): recorded, -1.
+  auto check = [&](int (&id)[8]) {
+    uint32_t most = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (!check(ids[i])) ids[i] = -1;
-  }
+    for (int i = 0; i < 8; ++i) most = max(most, (uint32_t)id[i]);
+    if (most < (uint32_t)p.num_blocks) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((uint32_t)id[i] >= (uint32_t)p.num_blocks) {
+        if (h == 0) record_status(p.status, KV_ERR_DEVICE, id[i]);
+        id[i] = -1;
+      }
+  };
+  check(ids);
   auto put_id = [&](int at, int blk, int phys) {
     if (sel) sel[at] = blk;
     out[at] = phys >= 0 ? (int)(phys * (int64_t)p.Hkv + h) : -1;
@@ -551,8 +597,8 @@ __global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
     for (int i = 0; i < 8; ++i) {
       const int at = base + 8 * tid + i;
       id[i] = at < nblk ? table[at] : 0;
-      if (!check(id[i])) id[i] = -1;
     }
+    check(id);
   };
   if (nblk <= p.n_sel) {
 #pragma unroll
@@ -581,10 +627,14 @@ __global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
       x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
     }
 #pragma unroll
+    for (int i = 0; i < 8; ++i) k[i] = ordered(x[i]);
+    if (i0 >= p.n_first && i0 + 8 <= nblk - p.n_last) return;  // nearly all threads
+#pragma unroll
     for (int i = 0; i < 8; ++i)
-      k[i] = i0 + i >= nblk                                    ? 0u
-             : i0 + i < p.n_first || i0 + i >= nblk - p.n_last ? 0xffffffffu
-                                                               : ordered(x[i]);
+      if (i0 + i >= nblk)
+        k[i] = 0;
+      else if (i0 + i < p.n_first || i0 + i >= nblk - p.n_last)
+        k[i] = 0xffffffffu;
   };
   uint32_t first[8];
   load(0, first);
@@ -659,29 +709,35 @@ __global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
   }
   // Blocks above the range, and of the range's all or the first `left`.
   uint32_t n_above = 0, n_equal = 0;  // before this thread's
+  // (Keys that are taken in any case lie above every score.)
+  const uint32_t from = whole ? lo : hi + 1;
   auto place = [&](const uint32_t (&k)[8], const int (&id)[8], int base) {
-    uint32_t mine = 0;  // blocks taken, and of the range (in the upper half)
+    uint32_t up = 0, in = 0;  // the thread's blocks that are taken, and of the range
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const bool in = k[i] >= lo && k[i] <= hi && k[i] != 0xffffffffu;
-      const bool up = k[i] > hi || k[i] == 0xffffffffu || (in && whole);
-      mine += up ? 1u : in ? 0x10000u : 0u;
+      up |= (k[i] >= from ? 1u : 0u) << i;
+      in |= (k[i] >= lo ? 1u : 0u) << i;
     }
+    in &= ~up;
+    const uint32_t mine = __popc(up) + (__popc(in) << 16);
     const uint32_t sum = block_scan<T>(mine, sums);
     uint32_t a = n_above + (sum & 0xffffu) - (mine & 0xffffu);
     uint32_t e = n_equal + (sum >> 16) - (mine >> 16);
+    // Few lanes have any, and those one or two, as a rule.
+    for (uint32_t rest = up | in; rest; rest &= rest - 1) {
+      const int i = __ffs(rest) - 1;
+      int phys = id[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool in = k[i] >= lo && k[i] <= hi && k[i] != 0xffffffffu;
-      const bool up = k[i] > hi || k[i] == 0xffffffffu || (in && whole);
-      if (up) {
-        put_id((int)(a + min(e, left)), base + 8 * tid + i, id[i]);
+      for (int z = 1; z < 8; ++z) phys = z == i ? id[z] : phys;
+      if (up >> i & 1) {
+        put_id((int)(a + min(e, left)), base + 8 * tid + i, phys);
         ++a;
-      } else if (in) {
-        if (e < left) put_id((int)(a + e), base + 8 * tid + i, id[i]);
+      } else {
+        if (e < left) put_id((int)(a + e), base + 8 * tid + i, phys);
         ++e;
       }
     }
+    if (nblk <= 8 * T) return;
     // The CTA's total, for the blocks after these.
     __syncthreads();
     if (tid == T - 1) {
@@ -711,20 +767,22 @@ __global__ void clear_kernel(DeviceStatus* status) {
 // Longer runs of blocks a warp where there are still two rounds of CTAs (two run at
 // once on an SM).
 template <int D>
-void launch_scores(const SelectParams& p, cudaStream_t st) {
+void launch_scores(SelectParams p, cudaStream_t st) {
   const int64_t ctas = (int64_t)((p.max_blocks + 511) / 512) * p.Hkv * p.nb;
   const int steps = ctas >= 2 * 2 * 152 ? 4 : 2;
-  const int blocks = kWarps * 16 * steps;
-  const dim3 grid((unsigned)p.Hkv, (unsigned)((p.max_blocks + blocks - 1) / blocks),
-                  (unsigned)p.nb);
+  const int groups = (p.Hkv + kWarps - 1) / kWarps;
+  p.heads = p.G <= 8 ? (p.Hkv + groups - 1) / groups : 1;
+  const int blocks = kWarps / p.heads * 16 * steps;
+  const dim3 grid((unsigned)((p.max_blocks + blocks - 1) / blocks),
+                  (unsigned)((p.Hkv + p.heads - 1) / p.heads), (unsigned)p.nb);
   if (p.G <= 8 && steps == 4)
-    score_kernel<D, true, 4><<<grid, 256, 0, st>>>(p);
+    score_kernel<D, true, 4><<<grid, 32 * kWarps, 0, st>>>(p);
   else if (p.G <= 8)
-    score_kernel<D, true, 2><<<grid, 256, 0, st>>>(p);
+    score_kernel<D, true, 2><<<grid, 32 * kWarps, 0, st>>>(p);
   else if (steps == 4)
-    score_kernel<D, false, 4><<<grid, 256, 0, st>>>(p);
+    score_kernel<D, false, 4><<<grid, 32 * kWarps, 0, st>>>(p);
   else
-    score_kernel<D, false, 2><<<grid, 256, 0, st>>>(p);
+    score_kernel<D, false, 2><<<grid, 32 * kWarps, 0, st>>>(p);
 }
 
 int score_stride(int max_blocks) { return (max_blocks + 31) & ~31; }
