@@ -287,13 +287,12 @@ def _check(status: int) -> None:
 
 def _ptr(x):
     """Device/host pointer of a torch tensor, numpy array, int or None."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
-    if isinstance(x, np.ndarray):
-        return x.ctypes.data
-    return x.data_ptr()
+    try:        # tensors first: a call has up to a dozen
+        return x.data_ptr()
+    except AttributeError:
+        return x.ctypes.data if isinstance(x, np.ndarray) else int(x)
 
 
 _current_stream = None     # once a call has found a GPU

@@ -808,8 +808,9 @@ static kv_status decode_impl(
   sp.v_pool = static_cast<uint4*>(const_cast<void*>(v_pool));
   // A step over selected blocks whose plan cuts nothing has nothing to merge.  (The e4m3
   // kernel with an end of that kind takes 38.7 us instead of 35 for 384 branches of up to
-  // 96 blocks, as much as the merge.)
-  const bool whole = early && !e4m3 && info->n_tile_items == 0 && Hkv == 1 &&
+  // 96 blocks, as much as the merge: for short ones only.)
+  const bool whole = early && (!e4m3 || info->chunk_blocks <= 32) &&
+                     info->n_tile_items == 0 && Hkv == 1 &&
                      info->n_row_items ==
                          (int64_t)nb * ((sp.G + pkv::kRowTile - 1) / pkv::kRowTile);
   sp.out = whole ? static_cast<__nv_bfloat16*>(out) : nullptr;

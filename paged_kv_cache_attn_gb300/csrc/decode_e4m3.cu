@@ -75,7 +75,8 @@ constexpr int kE4m3Stages = 4;
 // kPerWarp: every warp takes a (short) item of its own, item
 // item_base + 4 * blockIdx.x + warp, and writes its partial rows itself; a
 // separate instantiation so that the CTA-wide one keeps its registers.
-template <int D, int NS, bool kPerWarp>
+// kWhole: items have all keys of their rows (p.out).
+template <int D, int NS, bool kPerWarp, bool kWhole>
 __global__ void __launch_bounds__(128, 3)
     splitkv_e4m3_kernel(const SplitParams p, const uint8_t* __restrict__ k8,
                         const uint8_t* __restrict__ v8,
@@ -416,6 +417,12 @@ __global__ void __launch_bounds__(128, 3)
     // The warp's own item: its state is the partial result (O back to plain
     // units, x vref).  Lane (gq, tq) holds rows gq and gq + 8, columns
     // 8 nt + 2 tq and + 1.
+    if constexpr (kWhole) {
+      put_results<D>(p, it, lane, l_r[0], l_r[1], [&](int nt, int hr) {
+        return make_float2(o[nt][2 * hr] * vref, o[nt][2 * hr + 1] * vref);
+      });
+      return;
+    }
     float* dst = p.o + (int64_t)it.prow_base * D;
 #pragma unroll
     for (int nt = 0; nt < D / 8; ++nt) {
@@ -470,6 +477,7 @@ __global__ void __launch_bounds__(128, 3)
         lstar += wgt[w] * l_sh[w][row];
       }
       float* dst = p.o + (int64_t)(it.prow_base + row) * D + c0;
+      const float inv = 1.f / lstar;
 #pragma unroll
       for (int c = 0; c < D / 8; c += 4) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -482,9 +490,14 @@ __global__ void __launch_bounds__(128, 3)
           acc.z += wgt[w] * v.z;
           acc.w += wgt[w] * v.w;
         }
-        *reinterpret_cast<float4*>(dst + c) = acc;
+        if constexpr (kWhole)
+          *reinterpret_cast<uint2*>(p.out + result_row(p, it, row) * D + c0 + c) =
+              make_uint2(pack_bf16(acc.x * inv, acc.y * inv),
+                         pack_bf16(acc.z * inv, acc.w * inv));
+        else
+          *reinterpret_cast<float4*>(dst + c) = acc;
       }
-      if ((threadIdx.x & 7) == 0)
+      if (!kWhole && (threadIdx.x & 7) == 0)
         p.ml[it.prow_base + row] = make_float2(mstar, lstar);
     }
   }
@@ -497,41 +510,33 @@ cudaError_t launch_t(const SplitParams& sp, const void* k8, const void* v8,
                      const void* scales, int n_items, int n_warp_items,
                      bool early, cudaStream_t stream) {
   using C = E4m3Cfg<D, kE4m3Stages>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(
-        splitkv_e4m3_kernel<D, kE4m3Stages, false>,
-        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(splitkv_e4m3_kernel<D, kE4m3Stages, true>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               C::kSmem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static std::atomic<uint64_t> opted[4];
+  const bool whole = sp.out != nullptr;
+  auto* const long_kernel = whole ? splitkv_e4m3_kernel<D, kE4m3Stages, false, true>
+                                  : splitkv_e4m3_kernel<D, kE4m3Stages, false, false>;
+  auto* const warp_kernel = whole ? splitkv_e4m3_kernel<D, kE4m3Stages, true, true>
+                                  : splitkv_e4m3_kernel<D, kE4m3Stages, true, false>;
+  cudaError_t e = opt_in_smem(long_kernel, C::kSmem, opted[whole]);
+  if (e == cudaSuccess) e = opt_in_smem(warp_kernel, C::kSmem, opted[2 + whole]);
+  if (e != cudaSuccess) return e;
   if (n_warp_items < 0 || n_warp_items > n_items) return cudaErrorInvalidValue;
   const int n_long = n_items - n_warp_items;
   const auto* k = static_cast<const uint8_t*>(k8);
   const auto* v = static_cast<const uint8_t*>(v8);
   const auto* s = static_cast<const float4*>(scales);
   if (early) {
-    cudaError_t e = cudaSuccess;
     if (n_long > 0)
-      e = launch_early(splitkv_e4m3_kernel<D, kE4m3Stages, false>, n_long, 128, C::kSmem,
-                       stream, sp, k, v, s, 0, n_items);
+      e = launch_early(long_kernel, n_long, 128, C::kSmem, stream, sp, k, v, s, 0, n_items);
     if (e == cudaSuccess && n_warp_items > 0)
-      e = launch_early(splitkv_e4m3_kernel<D, kE4m3Stages, true>,
-                       (n_warp_items + 3) / 4, 128, C::kSmem, stream, sp, k, v, s, n_long,
-                       n_items);
+      e = launch_early(warp_kernel, (n_warp_items + 3) / 4, 128, C::kSmem, stream, sp, k, v,
+                       s, n_long, n_items);
     return e;
   }
   if (n_long > 0)
-    splitkv_e4m3_kernel<D, kE4m3Stages, false>
-        <<<n_long, 128, C::kSmem, stream>>>(sp, k, v, s, 0, n_items);
+    long_kernel<<<n_long, 128, C::kSmem, stream>>>(sp, k, v, s, 0, n_items);
   if (n_warp_items > 0)
-    splitkv_e4m3_kernel<D, kE4m3Stages, true>
-        <<<(n_warp_items + 3) / 4, 128, C::kSmem, stream>>>(sp, k, v, s,
-                                                            n_long, n_items);
+    warp_kernel<<<(n_warp_items + 3) / 4, 128, C::kSmem, stream>>>(sp, k, v, s, n_long,
+                                                                  n_items);
   return cudaGetLastError();
 }
 

@@ -189,7 +189,7 @@ struct SplitParams {
   uint4* k_pool;
   uint4* v_pool;
   // Not null: every item has all keys of its rows and writes their results here
-  // ([nb][Hq][d], one kv-head; bf16 pools); else partial rows.
+  // ([nb][Hq][d], one kv-head); else partial rows.
   __nv_bfloat16* out;
 };
 
