@@ -307,7 +307,8 @@ def _find_current_stream():
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is None:
         return lambda: torch.cuda.current_stream().cuda_stream
-    device = torch.cuda.current_device
+    torch.cuda.init()
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     return lambda: raw(device())
 
 

@@ -865,50 +865,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Joins the partial rows of cut tiles: a warp for each (token, head).
+// Joins the partial rows of cut tiles: a warp for each (token, head), in turn.  Eight
+// pieces are fetched at a time, then joined in order: one at a time each waited for the
+// one before: 1 token with 8 heads on
+// 60000 cached ones 46 us, now 25; 64 heads on 4000 16.7, now 13.3.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const ChunkMerge* merges,
                                                    const Params p) {
   constexpr int V = D / 32;  // values per lane
+  constexpr int kAhead = 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const ChunkMerge m = merges[blockIdx.x];
   const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);  // (head, token, head of G)
+  const int first = blockIdx.y * 8 + (threadIdx.x >> 5);  // (head, token, head of G)
   const int64_t stride = (int64_t)m.ntok * p.Hq;
   if (m.ntok < 1 || m.row0 < 0 || m.row0 > p.total - m.ntok || m.pieces < 1 ||
       m.partial < 0 || m.partial + stride * m.pieces > p.partial_rows) {
-    if (row == 0 && lane == 0) record_status(p.status, KV_ERR_DEVICE, m.partial);
+    if (first == 0 && lane == 0) record_status(p.status, KV_ERR_DEVICE, m.partial);
     return;
   }
-  if (row >= stride) return;
-  const int h = row / (m.ntok * p.G), rest = row % (m.ntok * p.G);
-  float top = -INFINITY, sum = 0.f, acc[V];
+  for (int row = first; row < stride; row += gridDim.y * 8) {
+    const int h = row / (m.ntok * p.G), rest = row % (m.ntok * p.G);
+    float top = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (int k = 0; k < m.pieces; ++k) {
-    const int64_t at = m.partial + k * stride + row;
-    const float2 ml = p.ml[at];
-    float v[V];
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int k0 = 0; k0 < m.pieces; k0 += kAhead) {
+      float2 ml[kAhead];
+      float v[kAhead][V];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (k0 + k >= m.pieces) break;
+        const int64_t at = m.partial + (k0 + k) * stride + row;
+        ml[k] = p.ml[at];
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+          *reinterpret_cast<float2*>(v[k] + i) =
+              *reinterpret_cast<const float2*>(p.o + at * D + lane * V + i);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (k0 + k >= m.pieces) break;
+        const float m_new = fmaxf(top, ml[k].x);
+        const float a = top == -INFINITY ? 0.f : ex2(top - m_new);
+        const float w = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - m_new);
+        sum = sum * a + w * ml[k].y;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = acc[i] * a + w * v[k][i];
+        top = m_new;
+      }
+    }
+    const float inv = 1.f / sum;
+    __nv_bfloat16* dst =
+        p.out +
+        ((int64_t)(m.row0 + rest / p.G) * p.Hq + h * p.G + rest % p.G) * D + lane * V;
 #pragma unroll
     for (int i = 0; i < V; i += 2)
-      *reinterpret_cast<float2*>(v + i) =
-          *reinterpret_cast<const float2*>(p.o + at * D + lane * V + i);
-    const float m_new = fmaxf(top, ml.x);
-    const float a = top == -INFINITY ? 0.f : ex2(top - m_new);
-    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m_new);
-    sum = sum * a + w * ml.y;
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = acc[i] * a + w * v[i];
-    top = m_new;
+      *reinterpret_cast<uint32_t*>(dst + i) =
+          pack_bf16(acc[i] * inv, acc[i + 1] * inv);
   }
-  const float inv = 1.f / sum;
-  __nv_bfloat16* dst =
-      p.out +
-      ((int64_t)(m.row0 + rest / p.G) * p.Hq + h * p.G + rest % p.G) * D + lane * V;
-#pragma unroll
-  for (int i = 0; i < V; i += 2)
-    *reinterpret_cast<uint32_t*>(dst + i) =
-        pack_bf16(acc[i] * inv, acc[i + 1] * inv);
 }
 
 // An e4m3 step's distinct blocks as bf16 [slot][Hkv][16][D], a warp for each
@@ -1086,8 +1100,10 @@ kv_status launch_all(const CUtensorMap& tq, const void* k, const void* v, Params
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
+  // No more CTAs than run at once: most tiles have fewer rows than they could.
+  const int64_t most = (2 * (kM / p.G) * (int64_t)p.Hq + 7) / 8;
   cfg.gridDim = dim3((unsigned)n_merges,
-                     (unsigned)((2 * (kM / p.G) * (int64_t)p.Hq + 7) / 8));
+                     (unsigned)std::clamp<int64_t>(4 * 152 / n_merges, 1, most));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cfg.attrs = &early;
