@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const Params p) {
   __shared__ float2 sums[kThreads / 32];
   __shared__ uint16_t group_max[kGroups][kThreads];
   __shared__ int count, few_count, listed;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int row = blockIdx.y, piece = blockIdx.x, tid = threadIdx.x, n = p.n;
   if (!(p.scores[row] > -INFINITY)) return;  // no beam
@@ -885,17 +886,13 @@ extern "C" kv_status kv_beam_select(const void* logits, int32_t logits_type,
   const dim3 grid((unsigned)p.pieces, (unsigned)rows);
   const bool big = vocab / p.pieces > 4096;  // steps of 4096 logits, else of 2048
   auto launch = [&](auto kernel, int ring) {
-    kernel<<<grid, W::kThreads, ring, st>>>(p);
+    return pkv::launch_early(kernel, grid, W::kThreads, ring, st, p);
   };
-  if (f32 && big)
-    launch(W::piece_kernel<float, 16>, W::kRingBytes<float, 16>);
-  else if (f32)
-    launch(W::piece_kernel<float, 8>, W::kRingBytes<float, 8>);
-  else if (big)
-    launch(W::piece_kernel<__nv_bfloat16, 16>, W::kRingBytes<__nv_bfloat16, 16>);
-  else
-    launch(W::piece_kernel<__nv_bfloat16, 8>, W::kRingBytes<__nv_bfloat16, 8>);
-  cudaError_t e = cudaGetLastError();
+  using bf16 = __nv_bfloat16;
+  cudaError_t e = f32 && big ? launch(W::piece_kernel<float, 16>, W::kRingBytes<float, 16>)
+                  : f32      ? launch(W::piece_kernel<float, 8>, W::kRingBytes<float, 8>)
+                  : big      ? launch(W::piece_kernel<bf16, 16>, W::kRingBytes<bf16, 16>)
+                             : launch(W::piece_kernel<bf16, 8>, W::kRingBytes<bf16, 8>);
   if (e == cudaSuccess)
     e = pkv::launch_early(W::group_kernel, n_groups, W::kThreads, 0, st, p);
   if (e != cudaSuccess)

@@ -996,6 +996,7 @@ __global__ void __launch_bounds__(256)
 // ---- host side ------------------------------------------------------------------
 
 __global__ void clear_kernel(DeviceStatus* status, int* next) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x != 0) return;
   *status = DeviceStatus{};
   next[0] = next[1] = 0;
@@ -1180,8 +1181,7 @@ kv_status run(const void* q, int64_t q_stride, const void* k_pool,
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "chunk attention: %s", cudaGetErrorString(e));
-  clear_kernel<<<1, 32, 0, st>>>(p.status, p.next);
-  e = cudaGetLastError();
+  e = launch_early(clear_kernel, 1, 32, 0, st, p.status, p.next);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "chunk attention: %s", cudaGetErrorString(e));
   if (total == 0) return KV_OK;

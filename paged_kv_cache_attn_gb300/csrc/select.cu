@@ -208,6 +208,7 @@ __device__ __forceinline__ void tile_bounds(const BoundsParams& p, int64_t tile,
 // together.
 template <int D, bool E4M3, int kHeads>
 __global__ void __launch_bounds__(256) bounds_kernel(const BoundsParams p, int run) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int per_run = (p.Hkv + kHeads - 1) / kHeads;
@@ -375,6 +376,8 @@ __global__ void __launch_bounds__(32 * kWarps, kFew ? 2 : 1)
   constexpr int kRow = D + 8;  // a head's f16 values in shared memory
   __shared__ __align__(16) __half qs[(kFew ? kWarps * 8 : kMaxG) * kRow];
   __shared__ float qe_all[kFew ? kWarps * 8 : kMaxG];
+  // (Both kernels of a selection may start early; the second reads the tables at once.)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && b == 0 && blockIdx.y == 0 && threadIdx.x == 0)
@@ -759,6 +762,8 @@ __global__ void __launch_bounds__(T) pick_kernel(const SelectParams p) {
 }
 
 __global__ void clear_kernel(DeviceStatus* status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) *status = DeviceStatus{};
 }
 
@@ -767,7 +772,7 @@ __global__ void clear_kernel(DeviceStatus* status) {
 // Longer runs of blocks a warp where there are still two rounds of CTAs (two run at
 // once on an SM).
 template <int D>
-void launch_scores(SelectParams p, cudaStream_t st) {
+cudaError_t launch_scores(SelectParams p, cudaStream_t st) {
   const int64_t ctas = (int64_t)((p.max_blocks + 511) / 512) * p.Hkv * p.nb;
   const int steps = ctas >= 2 * 2 * 152 ? 4 : 2;
   const int groups = (p.Hkv + kWarps - 1) / kWarps;
@@ -775,14 +780,10 @@ void launch_scores(SelectParams p, cudaStream_t st) {
   const int blocks = kWarps / p.heads * 16 * steps;
   const dim3 grid((unsigned)((p.max_blocks + blocks - 1) / blocks),
                   (unsigned)((p.Hkv + p.heads - 1) / p.heads), (unsigned)p.nb);
-  if (p.G <= 8 && steps == 4)
-    score_kernel<D, true, 4><<<grid, 32 * kWarps, 0, st>>>(p);
-  else if (p.G <= 8)
-    score_kernel<D, true, 2><<<grid, 32 * kWarps, 0, st>>>(p);
-  else if (steps == 4)
-    score_kernel<D, false, 4><<<grid, 32 * kWarps, 0, st>>>(p);
-  else
-    score_kernel<D, false, 2><<<grid, 32 * kWarps, 0, st>>>(p);
+  auto launch = [&](auto kernel) { return launch_early(kernel, grid, 32 * kWarps, 0, st, p); };
+  if (p.G <= 8)
+    return launch(steps == 4 ? score_kernel<D, true, 4> : score_kernel<D, true, 2>);
+  return launch(steps == 4 ? score_kernel<D, false, 4> : score_kernel<D, false, 2>);
 }
 
 int score_stride(int max_blocks) { return (max_blocks + 31) & ~31; }
@@ -848,16 +849,15 @@ kv_status run_bounds(const void* k_pool, const void* kv_scales, bool e4m3,
   const int64_t ctas = (runs * ((Hkv + heads - 1) / heads) + 7) / 8;
   if (ctas > INT32_MAX) return fail(KV_ERR_INVALID_ARG, "too many tokens");
   cudaStream_t st = (cudaStream_t)stream;
-  auto launch = [&](auto kernel) { kernel<<<(unsigned)ctas, 256, 0, st>>>(p, run); };
-  if (d == 128 && e4m3)
-    launch(heads == 1 ? bounds_kernel<128, true, 1> : bounds_kernel<128, true, 4>);
-  else if (d == 128)
-    launch(bounds_kernel<128, false, 1>);
-  else if (e4m3)
-    launch(heads == 1 ? bounds_kernel<64, true, 1> : bounds_kernel<64, true, 4>);
-  else
-    launch(heads == 1 ? bounds_kernel<64, false, 1> : bounds_kernel<64, false, 4>);
-  const cudaError_t e = cudaGetLastError();
+  auto launch = [&](auto kernel) {
+    return launch_early(kernel, (unsigned)ctas, 256, 0, st, p, run);
+  };
+  const cudaError_t e =
+      d == 128 && e4m3
+          ? launch(heads == 1 ? bounds_kernel<128, true, 1> : bounds_kernel<128, true, 4>)
+      : d == 128 ? launch(bounds_kernel<128, false, 1>)
+      : e4m3     ? launch(heads == 1 ? bounds_kernel<64, true, 1> : bounds_kernel<64, true, 4>)
+                 : launch(heads == 1 ? bounds_kernel<64, false, 1> : bounds_kernel<64, false, 4>);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "bounds kernel: %s", cudaGetErrorString(e));
   return KV_OK;
@@ -1019,15 +1019,10 @@ extern "C" kv_status paged_select_blocks(
   p.n_sel = n_sel;
   p.n_first = n_first;
   p.n_last = n_last;
-  if (max_blocks > n_sel) {
-    if (head_dim == 128)
-      S::launch_scores<128>(p, st);
-    else
-      S::launch_scores<64>(p, st);
-  } else {
-    S::clear_kernel<<<1, 32, 0, st>>>(p.status);
-  }
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = max_blocks <= n_sel
+                      ? pkv::launch_early(S::clear_kernel, 1, 32, 0, st, p.status)
+                  : head_dim == 128 ? S::launch_scores<128>(p, st)
+                                    : S::launch_scores<64>(p, st);
   // As many threads as hold a branch's keys at once.
   if (e == cudaSuccess)
     e = max_blocks <= 2048

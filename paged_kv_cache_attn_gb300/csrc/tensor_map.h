@@ -36,13 +36,13 @@ cudaError_t opt_in_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
 // Launch a kernel that may start before the one ahead of it in the stream has
 // ended (it waits for that by griddepcontrol.wait).
 template <typename... Formal, typename... Args>
-cudaError_t launch_early(void (*kernel)(Formal...), int grid, int block, int smem,
+cudaError_t launch_early(void (*kernel)(Formal...), dim3 grid, int block, int smem,
                          cudaStream_t st, const Args&... args) {
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)block);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
