@@ -788,18 +788,24 @@ __global__ void __launch_bounds__(kThreads) group_kernel(const Params p) {
   rank_and_put(count);
 }
 
-// Pieces of a row, of 2048 logits at least: one to three rounds of CTAs (four on an
-// SM), whichever is filled best.
+// Pieces of a row, of 2048 logits at least and for three rounds of CTAs (four on an SM)
+// at most: those that are done first.  A round costs about 5 us (its first reads, the
+// bar, the groups read again), and the logits either the time of a CTA's share, 0.15 us
+// a thousand where reads' latency counts, or that of their bytes.  (By how full the
+// rounds are alone, 203 beams of 19163 went in eight pieces and three rounds, 32 us;
+// in two 14.6.)
 int64_t n_pieces(int64_t rows, int vocab) {
-  const int64_t most = ((int64_t)vocab + 2047) / 2048;
+  const int64_t most = std::min(((int64_t)vocab + 2047) / 2048,
+                                std::max<int64_t>(3 * kRound / rows, 1));
+  const double bytes_us = (double)rows * vocab * 4 / 6e6;
   int64_t best = 1;
-  double filled = 0;
-  for (int64_t rounds = 1; rounds <= 3; ++rounds) {
-    const int64_t p = std::clamp<int64_t>(rounds * kRound / rows, 1, most);
-    const int64_t r = (rows * p + kRound - 1) / kRound;
-    const double f = (double)(rows * p) / (double)(r * kRound);
-    if (f > filled * 1.02) {
-      filled = f;
+  double least = 1e300;
+  for (int64_t p = 1; p <= most; ++p) {
+    const double rounds = (double)((rows * p + kRound - 1) / kRound);
+    const double us =
+        rounds * 5 + std::max(rounds * (double)vocab / (double)p * 0.15e-3, bytes_us);
+    if (us < least * 0.98) {
+      least = us;
       best = p;
     }
   }
@@ -886,7 +892,7 @@ extern "C" kv_status kv_beam_select(const void* logits, int32_t logits_type,
   const dim3 grid((unsigned)p.pieces, (unsigned)rows);
   const bool big = vocab / p.pieces > 4096;  // steps of 4096 logits, else of 2048
   auto launch = [&](auto kernel, int ring) {
-    return pkv::launch_early(kernel, grid, W::kThreads, ring, st, p);
+    return pkv::launch_early<true>(kernel, grid, W::kThreads, ring, st, p);
   };
   using bf16 = __nv_bfloat16;
   cudaError_t e = f32 && big ? launch(W::piece_kernel<float, 16>, W::kRingBytes<float, 16>)
@@ -894,7 +900,7 @@ extern "C" kv_status kv_beam_select(const void* logits, int32_t logits_type,
                   : big      ? launch(W::piece_kernel<bf16, 16>, W::kRingBytes<bf16, 16>)
                              : launch(W::piece_kernel<bf16, 8>, W::kRingBytes<bf16, 8>);
   if (e == cudaSuccess)
-    e = pkv::launch_early(W::group_kernel, n_groups, W::kThreads, 0, st, p);
+    e = pkv::launch_early<true>(W::group_kernel, n_groups, W::kThreads, 0, st, p);
   if (e != cudaSuccess)
     return fail(KV_ERR_CUDA, "beam selection: %s", cudaGetErrorString(e));
   return KV_OK;

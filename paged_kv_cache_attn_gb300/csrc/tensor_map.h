@@ -34,20 +34,25 @@ cudaError_t opt_in_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
 }
 
 // Launch a kernel that may start before the one ahead of it in the stream has
-// ended (it waits for that by griddepcontrol.wait).
-template <typename... Formal, typename... Args>
+// ended (it waits for that by griddepcontrol.wait).  kMostShared: with four fifths of
+// an SM's memory as shared memory.  An SM changes that share only when nothing runs on
+// it: kernels that want different ones do not run beside each other (beams' groups
+// behind 180 CTAs of their pieces 5 us late).
+template <bool kMostShared = false, typename... Formal, typename... Args>
 cudaError_t launch_early(void (*kernel)(Formal...), dim3 grid, int block, int smem,
                          cudaStream_t st, const Args&... args) {
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attrs[2]{};
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+  attrs[1].val.sharedMemCarveout = 80;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)block);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = kMostShared ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -208,6 +208,54 @@ def test_captured_and_same_every_time():
     check(x, s, 6, 8, 16)
 
 
+def test_behind_a_join_of_streams():
+    """Logits that another stream makes, late, eager and captured: the first launch
+    starts early, but reads nothing before."""
+    x, s = make(4, 4, 30000, torch.float32, 9)
+    slow = torch.randn(4096, 4096, device="cuda")
+    logits, scores = torch.empty_like(x), torch.empty_like(s)
+    ws = torch.empty(B.kv_beam_select_workspace_size(4, 4, 30000, 8), dtype=torch.uint8,
+                     device="cuda")
+    out = (torch.empty(4, 8, device="cuda"),
+           torch.empty(4, 8, dtype=torch.int32, device="cuda"),
+           torch.empty(4, 8, dtype=torch.int32, device="cuda"))
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            torch.mm(slow, slow)
+            logits.copy_(x)
+        scores.copy_(s)
+        here.wait_stream(side)
+        B.kv_beam_select(logits, scores, 4, 4, 8, *out, ws)
+        logits.fill_(0.0)
+        scores.fill_(-1.0)
+
+    def good():
+        torch.cuda.synchronize()
+        ref = want(x, s, 4, 4, 8)
+        assert torch.equal(out[1], ref[1]) and torch.equal(out[2], ref[2])
+        for o in out:
+            o.zero_()
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        step()
+        good()
+        step()
+    good()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+        step()
+    for _ in range(3):
+        graph.replay()
+        graph.replay()
+        good()
+
+
 def test_a_search_on_the_pool():
     """Steps of a beam search: selection, the branches reordered with their caches,
     the new tokens appended, each beam's cache that of its own tokens."""

@@ -257,6 +257,35 @@ def test_captured(kv):
     assert B.kv_check_device_status(s.ws) == (0, 0)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_behind_work_of_other_streams(kv):
+    """Queries that another stream makes, late, captured: the first launch starts early,
+    but what reads them does not."""
+    s = Step(8, 2, 128, [(2000, 5), (30, 200), (0, 1)], kv, seed=18)
+    q, out = torch.zeros_like(s.q), torch.empty_like(s.q)
+    slow = torch.randn(4096, 4096, device="cuda")
+    s.call(s.q, out)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want, n = out.clone(), 3
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            here = torch.cuda.current_stream()
+            side.wait_stream(here)
+            with torch.cuda.stream(side):
+                torch.mm(slow, slow)
+                q.copy_(s.q)
+            here.wait_stream(side)
+            s.call(q, out)
+            q.fill_(0.0)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_two_layers_with_one_plan():
     s = Step(8, 2, 128, [(200, 30), (0, 17)], seed=14)
     first = s.run().clone()
