@@ -131,7 +131,7 @@ struct Digits {
 // keys equal to the result is the last).  All threads call it; 0 where there are fewer.
 template <typename Each>
 __device__ __forceinline__ uint64_t nth_key(Each each, int top, uint64_t prefix,
-                                         uint64_t mask, int& n, Digits& sh) {
+                                            uint64_t mask, int& n, Digits& sh) {
   const int tid = threadIdx.x;
   for (int d = top; d >= 0; d -= 8) {
     __syncthreads();
@@ -172,8 +172,8 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) {
 }
 
 // The n highest of c <= kCand keys to best, in order (0 where there are fewer).  Of
-// many, a bar that n of the threads' highest keys reach leaves few to be ranked.  `floor`: a logit
-// that all of them reach.
+// many, a bar that n of the threads' highest keys reach leaves few to be ranked.
+// `floor`: a logit that all of them reach.
 __device__ __forceinline__ void pick_best(const uint64_t* cand, int c, int n, float floor,
                                           uint64_t* few, uint64_t* best, uint32_t* sh,
                                           int* count) {
